@@ -72,6 +72,9 @@ typedef struct nvfp4_kv_cache {
   int32_t head_dim;
 } nvfp4_kv_cache;
 
+/* The most sequences of one attention call. */
+#define NVFP4_ATTENTION_MAX_SEQUENCES 8192
+
 /* A batch of sequences over a cache.  Sequence s holds its first kv_lens[s]
  * keys in the pages block_table[s][0..], key j in slot j % page_size of page
  * block_table[s][j / page_size].  Its new tokens are rows q_starts[s] to

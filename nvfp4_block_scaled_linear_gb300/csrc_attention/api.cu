@@ -15,7 +15,7 @@ __global__ void read_attention_error_kernel(int clear) {
       clear ? atomicExch(&g_attention_error, 0u) : atomicOr(&g_attention_error, 0u);
 }
 
-constexpr int kMaxDevices = 64;
+using nvfp4::attn::kMaxDevices;
 struct Slot {
   bool ready = false, supported = false;
   nvfp4::attn::Device d;
@@ -58,6 +58,7 @@ int check_seqs(const nvfp4_sequences* s, bool queries) {
   if (!s || s->count < 0 || s->table_width <= 0) return NVFP4_ERR_INVALID;
   if (s->count > 0 && (!s->block_table || !s->kv_lens)) return NVFP4_ERR_INVALID;
   if (queries && s->count > 0 && (!s->q_starts || s->max_q_len < 0)) return NVFP4_ERR_INVALID;
+  if (queries && s->count > NVFP4_ATTENTION_MAX_SEQUENCES) return NVFP4_ERR_SHAPE;
   return NVFP4_OK;
 }
 
@@ -124,6 +125,7 @@ int device(Device* out) {
       cudaGetLastError();
       return NVFP4_ERR_DEVICE;
     }
+    s.d.id = dev;
     s.d.num_sms = sms;
     s.d.err = static_cast<unsigned int*>(err);
     s.ready = true;

@@ -1,7 +1,13 @@
 // attend.cu -- attention of new tokens over the paged cache, one warp per
 // token and query head: the plain order of the formula with a running
 // maximum and sum, every key row read from the cache as it is needed.
-#include "common.cuh"
+#include <algorithm>
+#include <cstring>
+#include <mutex>
+
+#include <cudaTypedefs.h>
+
+#include "attend.cuh"
 
 namespace nvfp4 {
 namespace attn {
@@ -75,9 +81,76 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const Attend p) {
 
 }  // namespace
 
-int64_t attend_workspace(int, const Device&) { return 16; }
+int64_t attend_workspace(int head_dim, const Device& d) {
+  return attend_warp_workspace(head_dim, d);
+}
 
-int run_attend(const Attend& p, const Device&, cudaStream_t stream) {
+// Encoding a tensor map costs microseconds of host time, so encoded maps are
+// kept in a small direct-mapped cache.  The key holds every encoding input,
+// so a hit is always valid.
+bool page_map(CUtensorMap* map, const Cache& c, bool values, int inner, int rows) {
+  struct Key {
+    const void* base;
+    int64_t pages, stride[3];
+    int page_size, heads, dim, e4m3, inner, rows;
+  };
+  struct Slot {
+    Key key;
+    CUtensorMap map;
+  };
+  static Slot slots[64];
+  static std::mutex mutex;
+  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  const int64_t* st = values ? c.vs : c.ks;
+  Key key;
+  std::memset(&key, 0, sizeof(key));
+  key.base = values ? c.v : c.k;
+  key.pages = c.pages;
+  for (int i = 0; i < 3; ++i) key.stride[i] = st[i];
+  key.page_size = c.page_size, key.heads = c.heads, key.dim = c.dim, key.e4m3 = c.e4m3;
+  key.inner = inner, key.rows = rows;
+  uint64_t h = reinterpret_cast<uintptr_t>(key.base) >> 4;
+  h ^= uint64_t(c.pages) * 0x9E3779B97F4A7C15ull ^ uint64_t(inner) << 9 ^ uint64_t(rows) << 17;
+  h ^= h >> 29;
+  std::lock_guard<std::mutex> lock(mutex);
+  Slot& slot = slots[h % 64];
+  if (std::memcmp(&slot.key, &key, sizeof(key)) != 0) {
+    if (!encode) {
+      void* fn = nullptr;
+      cudaDriverEntryPointQueryResult q;
+      if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                           &q) != cudaSuccess ||
+          q != cudaDriverEntryPointSuccess || !fn) {
+        cudaGetLastError();
+        return false;
+      }
+      encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    }
+    const int size = c.e4m3 ? 1 : 2;
+    const cuuint64_t dims[4] = {cuuint64_t(c.dim), cuuint64_t(c.page_size), cuuint64_t(c.heads),
+                                cuuint64_t(c.pages)};
+    const cuuint64_t strides[3] = {cuuint64_t(st[1] * size), cuuint64_t(st[2] * size),
+                                   cuuint64_t(st[0] * size)};
+    const cuuint32_t box[4] = {cuuint32_t(inner), cuuint32_t(rows), 1, 1};
+    const cuuint32_t unit[4] = {1, 1, 1, 1};
+    CUtensorMap fresh;
+    if (encode(&fresh, c.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+               const_cast<void*>(key.base), dims, strides, box, unit,
+               CU_TENSOR_MAP_INTERLEAVE_NONE,
+               inner * size == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return false;
+    slot.key = key;
+    slot.map = fresh;
+  }
+  *map = slot.map;
+  return true;
+}
+
+int run_attend(const Attend& p, const Device& d, cudaStream_t stream) {
+  const int64_t rows = int64_t(std::max(1, p.max_q_len)) * p.group;
+  if (rows <= 64) return run_attend_warp(static_cast<int>(rows), p, d, stream);
   const int64_t blocks = (int64_t(p.seqs.tokens) * p.q_heads * 32 + kThreads - 1) / kThreads;
   if (blocks > INT32_MAX) return NVFP4_ERR_SHAPE;
   auto* kernel = p.cache.dim == 256   ? attend_kernel<256>

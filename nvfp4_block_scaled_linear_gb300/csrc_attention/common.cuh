@@ -7,6 +7,7 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/nvfp4_attention.h"
@@ -76,7 +77,10 @@ __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w 
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
 // ---------------------------------------------------------------- host side
+constexpr int kMaxDevices = 64;
+
 struct Device {
+  int id = 0;
   int num_sms = 0;
   unsigned int* err = nullptr;
 };
@@ -103,6 +107,19 @@ int launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_
     cudaGetLastError();
     return NVFP4_ERR_LAUNCH;
   }
+  return NVFP4_OK;
+}
+
+// Let `kernel` use `bytes` of dynamic shared memory, once per device.
+template <typename Kernel>
+int allow_smem(Kernel kernel, int bytes, const Device& d, std::atomic<bool> (&ready)[kMaxDevices]) {
+  if (ready[d.id].load(std::memory_order_acquire)) return NVFP4_OK;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return NVFP4_ERR_LAUNCH;
+  }
+  ready[d.id].store(true, std::memory_order_release);
   return NVFP4_OK;
 }
 
