@@ -40,8 +40,9 @@
 extern "C" {
 #endif
 
-/* bf16 [tokens, heads, head_dim] on the device; strides in elements, each a
- * multiple of 8; data 16-byte aligned. */
+/* bf16 [tokens, heads, head_dim] on the device; strides in elements, each
+ * positive and a multiple of 8 (that of a dimension of one is not read); data
+ * 16-byte aligned. */
 typedef struct nvfp4_heads {
   void* data;
   int64_t token_stride;
@@ -127,6 +128,7 @@ int nvfp4_qk_norm_rope(const nvfp4_heads* q, const nvfp4_heads* k, const nvfp4_h
  * sums are fp32; the weights are rounded to the cache's operand type (bf16,
  * or f16 over an E4M3 cache) before they meet the values; out is rounded
  * once to bf16.
+ *   scale        positive and finite.
  *   q, out       bf16 [tokens, q_heads, head_dim] heads; q_heads a multiple
  *                of cache->kv_heads, at most 128 times it.
  *   lse          fp32 [tokens, q_heads], or NULL.

@@ -154,7 +154,7 @@ def _heads(t, name, tokens, heads, dim, device):
     a, b, c = t.stride()
     if c != 1 and dim > 1:
         raise ValueError("the last dimension of %s must be dense" % name)
-    return _Heads(t.data_ptr(), a if tokens > 1 else 0, b if heads > 1 else 0)
+    return _Heads(t.data_ptr(), a, b)
 
 
 def _flat(t, name, dtype, shape, device):

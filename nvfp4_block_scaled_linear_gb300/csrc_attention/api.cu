@@ -1,7 +1,9 @@
 // api.cu -- the C ABI of include/nvfp4_attention.h: validation on the host,
 // the per-device set-up and the attention error word.
 #include <climits>
+#include <cmath>
 #include <mutex>
+#include <utility>
 
 #include "common.cuh"
 
@@ -25,11 +27,16 @@ std::mutex g_device_mutex;
 
 bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 
-int check_heads(const nvfp4_heads* h) {
+// A stride counts only where its dimension has more than one element.
+int check_heads(const nvfp4_heads* h, int64_t tokens, int64_t count) {
   if (!h || !h->data) return NVFP4_ERR_INVALID;
   if (misaligned(h->data)) return NVFP4_ERR_MISALIGNED;
-  if (h->token_stride < 0 || h->head_stride < 0) return NVFP4_ERR_INVALID;
-  if (h->token_stride % 8 != 0 || h->head_stride % 8 != 0) return NVFP4_ERR_MISALIGNED;
+  for (const auto& [stride, size] : {std::pair(h->token_stride, tokens), {h->head_stride, count}}) {
+    if (size <= 1) continue;
+    if (stride <= 0) return NVFP4_ERR_INVALID;
+    if (stride % 8 != 0) return NVFP4_ERR_MISALIGNED;
+    if (stride >= (int64_t(1) << 38)) return NVFP4_ERR_SHAPE;     // the copy engine's limit
+  }
   return NVFP4_OK;
 }
 
@@ -69,9 +76,10 @@ int check_groups(int64_t tokens, int32_t q_heads, int32_t kv_heads) {
   return NVFP4_OK;
 }
 
-nvfp4::attn::Heads heads(const nvfp4_heads* h) {
+nvfp4::attn::Heads heads(const nvfp4_heads* h, int64_t tokens, int64_t count, int dim) {
   if (!h) return {};
-  return {static_cast<__nv_bfloat16*>(h->data), h->token_stride, h->head_stride};
+  return {static_cast<__nv_bfloat16*>(h->data), tokens > 1 ? h->token_stride : dim * count,
+          count > 1 ? h->head_stride : dim};
 }
 
 nvfp4::attn::Cache cache_of(const nvfp4_kv_cache* c) {
@@ -169,17 +177,19 @@ int nvfp4_qk_norm_rope(const nvfp4_heads* q, const nvfp4_heads* k, const nvfp4_h
     if (misaligned(cos_sin)) return NVFP4_ERR_MISALIGNED;
   }
   if (tokens == 0) return NVFP4_OK;
-  for (const nvfp4_heads* h : {q, k, q_out, cache ? v : k_out})
-    if (const int st = check_heads(h)) return st;
+  for (const nvfp4_heads* h : {q, q_out})
+    if (const int st = check_heads(h, tokens, q_heads)) return st;
+  for (const nvfp4_heads* h : {k, cache ? v : k_out})
+    if (const int st = check_heads(h, tokens, kv_heads)) return st;
   if (cache && !slots) return NVFP4_ERR_INVALID;
   Device d;
   if (const int st = device(&d)) return st;
   NormRope p{};
-  p.q = heads(q);
-  p.k = heads(k);
-  p.v = heads(v);
-  p.q_out = heads(q_out);
-  p.k_out = heads(k_out);
+  p.q = heads(q, tokens, q_heads, head_dim);
+  p.k = heads(k, tokens, kv_heads, head_dim);
+  p.v = heads(v, tokens, kv_heads, head_dim);
+  p.q_out = heads(q_out, tokens, q_heads, head_dim);
+  p.k_out = heads(k_out, tokens, kv_heads, head_dim);
   p.q_weight = static_cast<const __nv_bfloat16*>(q_weight);
   p.k_weight = static_cast<const __nv_bfloat16*>(k_weight);
   p.cos_sin = cos_sin;
@@ -212,17 +222,18 @@ int nvfp4_paged_attention(const nvfp4_heads* q, int64_t tokens, int32_t q_heads,
   if (const int st = check_cache(cache)) return st;
   if (const int st = check_groups(tokens, q_heads, cache->kv_heads)) return st;
   if (const int st = check_seqs(seqs, true)) return st;
+  if (!(scale > 0.f && scale < INFINITY)) return NVFP4_ERR_INVALID;
   if (tokens == 0 || seqs->count == 0) return NVFP4_OK;
-  if (const int st = check_heads(q)) return st;
-  if (const int st = check_heads(out)) return st;
+  if (const int st = check_heads(q, tokens, q_heads)) return st;
+  if (const int st = check_heads(out, tokens, q_heads)) return st;
   if (!workspace) return NVFP4_ERR_INVALID;
   if (misaligned(workspace)) return NVFP4_ERR_MISALIGNED;
   Device d;
   if (const int st = device(&d)) return st;
   if (workspace_bytes < attend_workspace(cache->head_dim, d)) return NVFP4_ERR_TOO_LARGE;
   Attend p{};
-  p.q = heads(q);
-  p.out = heads(out);
+  p.q = heads(q, tokens, q_heads, cache->head_dim);
+  p.out = heads(out, tokens, q_heads, cache->head_dim);
   p.cache = cache_of(cache);
   p.seqs = seqs_of(seqs, tokens, cache->page_size);
   p.q_heads = q_heads;
@@ -242,18 +253,18 @@ int nvfp4_attention_mass(const nvfp4_heads* q, int64_t tokens, int32_t q_heads,
   if (const int st = check_cache(cache)) return st;
   if (const int st = check_groups(tokens, q_heads, cache->kv_heads)) return st;
   if (const int st = check_seqs(seqs, true)) return st;
-  if (room <= 0) return NVFP4_ERR_INVALID;
+  if (room <= 0 || !(scale > 0.f && scale < INFINITY)) return NVFP4_ERR_INVALID;
   if (room > INT_MAX) return NVFP4_ERR_SHAPE;
   if (seqs->count == 0) return NVFP4_OK;
   if (!out) return NVFP4_ERR_INVALID;
   if (tokens > 0) {
-    if (const int st = check_heads(q)) return st;
+    if (const int st = check_heads(q, tokens, q_heads)) return st;
     if (!lse) return NVFP4_ERR_INVALID;
   }
   Device d;
   if (const int st = device(&d)) return st;
   Mass p{};
-  p.q = heads(q);
+  p.q = heads(q, tokens, q_heads, cache->head_dim);
   p.cache = cache_of(cache);
   p.seqs = seqs_of(seqs, tokens, cache->page_size);
   p.q_heads = q_heads;

@@ -13,6 +13,10 @@ namespace attn {
 // that width) by `rows` slots.
 bool page_map(CUtensorMap* map, const Cache& c, bool values, int inner, int rows);
 
+// Tensor map of the queries, dimensions (element, head, token), for boxes of 64
+// elements by one group of heads by `tokens` tokens.
+bool query_map(CUtensorMap* map, const Attend& a, int tokens);
+
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar,
                                             int32_t c0, int32_t c1, int32_t c2, int32_t c3) {
   asm volatile(
@@ -26,6 +30,10 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
 // rows: query rows of one key/value head in the longest sequence, at most 64.
 int run_attend_warp(int rows, const Attend& p, const Device& d, cudaStream_t stream);
 int64_t attend_warp_workspace(int head_dim, const Device& d);
+
+// rows: as above, any number.
+int run_attend_tc(int64_t rows, const Attend& p, const Device& d, cudaStream_t stream);
+int64_t attend_tc_workspace(int head_dim, const Device& d);
 
 }  // namespace attn
 }  // namespace nvfp4

@@ -674,7 +674,7 @@ int run(const Attend& p, const Device& d, cudaStream_t stream) {
     return NVFP4_ERR_LAUNCH;
   const Plan plan{std::max(1, C::kRows / p.group), kUnit, 4};
   const int ctas = d.num_sms * C::kCtas;
-  const Parts parts(p.workspace, ctas, C::kRows, kDim);
+  const Parts parts(p.workspace, ctas, C::kRows, 1, kDim);
   if (const int st = launch(kernel, dim3(ctas), dim3(kThreads), C::kSmem, stream, tm_k, tm_v, p,
                             plan, parts))
     return st;

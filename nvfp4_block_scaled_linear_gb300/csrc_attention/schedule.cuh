@@ -187,13 +187,15 @@ struct Parts {
   int4* note;             // {flags, s, h, tile} of part 1's item
   float* lse2;            // [ctas][2][rows]
   float* out;             // [ctas][2][rows][dim]
-  int rows, dim;
+  int tile_rows, rows;    // of one MMA tile (whole tokens from its first row on), of all
+  int dim;
 
-  __host__ __device__ Parts(void* base, int ctas, int rows_, int dim_)
+  Parts(void* base, int ctas, int tile_rows_, int tiles, int dim_)
       : note(static_cast<int4*>(base)),
         lse2(reinterpret_cast<float*>(note + ctas)),
-        out(lse2 + int64_t(ctas) * 2 * rows_),
-        rows(rows_),
+        out(lse2 + int64_t(ctas) * 2 * tile_rows_ * tiles),
+        tile_rows(tile_rows_),
+        rows(tile_rows_ * tiles),
         dim(dim_) {}
   __device__ int64_t row(int cta, int part, int r) const {
     return (int64_t(cta) * 2 + part) * rows + r;
