@@ -16,9 +16,9 @@ namespace {
 // so a hit is always valid.
 struct MapKey {
   const void* base;
-  uint64_t dims[4], strides[3];
-  uint32_t box[4];
-  int32_t rank, bytes;       // bytes of an element
+  uint64_t dims[5], strides[4];
+  uint32_t box[5];
+  int32_t rank, bytes, zero; // bytes of an element
 };
 struct MapSlot {
   MapKey key;
@@ -52,11 +52,11 @@ bool encode(CUtensorMap* map, const MapKey& key) {
       }
       g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     }
-    cuuint64_t dims[4], strides[3];
-    cuuint32_t box[4];
-    const cuuint32_t unit[4] = {1, 1, 1, 1};
-    for (int i = 0; i < 4; ++i) dims[i] = key.dims[i], box[i] = key.box[i];
-    for (int i = 0; i < 3; ++i) strides[i] = key.strides[i];
+    cuuint64_t dims[5], strides[4];
+    cuuint32_t box[5];
+    const cuuint32_t unit[5] = {1, 1, 1, 1, 1};
+    for (int i = 0; i < 5; ++i) dims[i] = key.dims[i], box[i] = key.box[i];
+    for (int i = 0; i < 4; ++i) strides[i] = key.strides[i];
     CUtensorMap fresh;
     if (g_encode(&fresh,
                  key.bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
@@ -76,17 +76,19 @@ bool encode(CUtensorMap* map, const MapKey& key) {
 
 }  // namespace
 
-bool page_map(CUtensorMap* map, const Cache& c, bool values, int inner, int rows) {
+bool page_map(CUtensorMap* map, const Cache& c, bool values, int inner, int rows, int chunks) {
   const int64_t* st = values ? c.vs : c.ks;
   const int size = c.e4m3 ? 1 : 2;
   MapKey key;
   std::memset(&key, 0, sizeof(key));
   key.base = values ? c.v : c.k;
-  key.rank = 4;
+  key.rank = 5;
   key.bytes = size;
-  key.dims[0] = c.dim, key.dims[1] = c.page_size, key.dims[2] = c.heads, key.dims[3] = c.pages;
-  key.strides[0] = st[1] * size, key.strides[1] = st[2] * size, key.strides[2] = st[0] * size;
-  key.box[0] = inner, key.box[1] = rows, key.box[2] = 1, key.box[3] = 1;
+  key.dims[0] = inner, key.dims[1] = c.page_size, key.dims[2] = c.dim / inner;
+  key.dims[3] = c.heads, key.dims[4] = c.pages;
+  key.strides[0] = st[1] * size, key.strides[1] = inner * size;
+  key.strides[2] = st[2] * size, key.strides[3] = st[0] * size;
+  key.box[0] = inner, key.box[1] = rows, key.box[2] = chunks, key.box[3] = 1, key.box[4] = 1;
   return encode(map, key);
 }
 

@@ -8,22 +8,24 @@
 namespace nvfp4 {
 namespace attn {
 
-// Tensor map of the cache's key or value pages, dimensions (element, slot,
-// head, page), for boxes of `inner` elements (64 or 128 bytes, swizzled to
-// that width) by `rows` slots.
-bool page_map(CUtensorMap* map, const Cache& c, bool values, int inner, int rows);
+// Tensor map of the cache's key or value pages, dimensions (element of a
+// chunk, slot, chunk, head, page), for boxes of `rows` slots by `chunks` chunks
+// of `inner` elements (64 or 128 bytes, swizzled to that width): chunk after
+// chunk in shared memory, each `rows` rows of that width.
+bool page_map(CUtensorMap* map, const Cache& c, bool values, int inner, int rows, int chunks);
 
 // Tensor map of the queries, dimensions (element, head, token), for boxes of 64
 // elements by one group of heads by `tokens` tokens.
 bool query_map(CUtensorMap* map, const Attend& a, int tokens);
 
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar,
-                                            int32_t c0, int32_t c1, int32_t c2, int32_t c3) {
+__device__ __forceinline__ void tma_load_page(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                              int32_t chunk, int32_t slot, int32_t head,
+                                              int32_t page) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_addr(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(c0), "r"(c1), "r"(c2),
-      "r"(c3)
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(0), "r"(slot), "r"(chunk),
+      "r"(head), "r"(page)
       : "memory");
 }
 

@@ -578,35 +578,42 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
         if (it >= C::kSlots)
           ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], ((it / C::kSlots) & 1) ^ 1, abort_flag));
         if (ok && lane == 0) mbar_arrive_expect_tx(&full[s], bytes);
-        __syncwarp();
         return s;
       };
+      // One lane issues: a copy's operands are warp-uniform registers, and
+      // copies from several lanes took some 250 cycles each.
       auto copy_k = [&](const Walk& w, const Pages& g) {
         const int n = __popc(__ballot_sync(0xffffffffu, g.page >= 0));
         for (int h = 0; h < C::kPieces; ++h, ++it) {
           const int s = next_slot(n * p.box_rows * 128);
           if (!ok) return;
-          if (g.page >= 0)
-            tma_load_4d(ring + s * C::kSlotBytes + lane * p.box_rows * 128, &tm_k, &full[s], h * 64,
-                        g.in_page, w.r.h, g.page);
-          __syncwarp();
+          for (int i = 0; i < k_boxes; ++i) {
+            const int page = __shfl_sync(0xffffffffu, g.page, i);
+            const int in_page = __shfl_sync(0xffffffffu, g.in_page, i);
+            if (lane == 0 && page >= 0)
+              tma_load_page(ring + s * C::kSlotBytes + i * p.box_rows * 128, &tm_k, &full[s], h,
+                            in_page, w.r.h, page);
+          }
         }
       };
       auto copy_v = [&](const Walk& w, const Pages& g) {
+        const int v_chunks = v_boxes == 1 ? C::kPieces : 1;         // of one copy
         for (int h = 0; h < C::kPieces; ++h, ++it) {
-          // lane: 64-column piece lane / 8, rows lane % 8 of v_boxes
-          const int row = h * C::kVKeys + (lane & 7) * v_rows;      // of the block
-          const int from = row / p.box_rows & 31;
-          const int page = __shfl_sync(0xffffffffu, g.page, from);
-          const int in_page = __shfl_sync(0xffffffffu, g.in_page, from) + row % p.box_rows;
-          const bool mine = (lane & 7) < v_boxes && lane >> 3 < C::kPieces && page >= 0;
-          const int n = __popc(__ballot_sync(0xffffffffu, mine));
-          const int s = next_slot(n * v_rows * 128);
+          int n = 0;
+          for (int i = 0; i < v_boxes; ++i)
+            n += __shfl_sync(0xffffffffu, g.page, (h * C::kVKeys + i * v_rows) / p.box_rows) >= 0;
+          const int s = next_slot(n * C::kPieces * v_rows * 128);
           if (!ok) return;
-          if (mine)
-            tma_load_4d(ring + s * C::kSlotBytes + (lane >> 3) * C::kVChunk + (lane & 7) * v_rows * 128,
-                        &tm_v, &full[s], (lane >> 3) * 64, in_page, w.r.h, page);
-          __syncwarp();
+          for (int i = 0; i < v_boxes; ++i) {
+            const int row = h * C::kVKeys + i * v_rows;             // of the block
+            const int from = row / p.box_rows;
+            const int page = __shfl_sync(0xffffffffu, g.page, from);
+            const int in_page = __shfl_sync(0xffffffffu, g.in_page, from) + row - from * p.box_rows;
+            if (lane == 0 && page >= 0)
+              for (int ch = 0; ch < C::kPieces; ch += v_chunks)
+                tma_load_page(ring + s * C::kSlotBytes + ch * C::kVChunk + i * v_rows * 128, &tm_v,
+                              &full[s], ch, in_page, w.r.h, page);
+          }
         }
       };
       // in the order of the products: with one tile V0 after K1, with two after K0
@@ -905,8 +912,9 @@ int run(const Attend& a, const Device& d, cudaStream_t stream) {
   while (p.box_rows < kN && a.cache.page_size % (2 * p.box_rows) == 0) p.box_rows *= 2;
   CUtensorMap tm_q{}, tm_k{}, tm_v{};
   if (!kE4m3 && (!query_map(&tm_q, a, p.tile_tokens) ||
-                 !page_map(&tm_k, a.cache, false, 64, p.box_rows) ||
-                 !page_map(&tm_v, a.cache, true, 64, std::min(p.box_rows, C::kVKeys))))
+                 !page_map(&tm_k, a.cache, false, 64, p.box_rows, 1) ||
+                 !page_map(&tm_v, a.cache, true, 64, std::min(p.box_rows, C::kVKeys),
+                           p.box_rows >= C::kVKeys ? C::kPieces : 1)))
     return NVFP4_ERR_LAUNCH;
   if (const int st = launch(kernel, dim3(d.num_sms), dim3(C::kThreads), C::kSmem, stream, tm_q,
                             tm_k, tm_v, p))

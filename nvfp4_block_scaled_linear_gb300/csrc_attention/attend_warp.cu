@@ -42,6 +42,9 @@ struct Cfg {
   static constexpr int kRowBytes = kDim * kEsz;
   static constexpr int kChunkBytes = kRowBytes < 128 ? kRowBytes : 128;
   static constexpr int kChunks = kRowBytes / kChunkBytes;
+  // a unit: chunk after chunk, each 16 rows of kChunkBytes
+  static constexpr int kUnitBytes = kUnit * kRowBytes;
+  static constexpr int kUnitChunk = kUnit * kChunkBytes;
   static constexpr int kSlotBytes = kSlotKeys * kRowBytes;
   static constexpr int kRows = 16 * kR;
   static constexpr int kQPitch = kDim * 2 + 16;
@@ -215,16 +218,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<kDim, kE4m3, kR>::kCtas)
                             mbar_wait(&empty[slot], ((it / C::kSlots) & 1) ^ 1, abort_flag));
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(&full[slot], units * kUnit * C::kRowBytes);
-          __syncwarp();
-          // lane: unit lane / 4 (of this slot), chunk lane % 4
-          const int lu = lane >> 2 & 3, ch = lane & 3;
-          const int pg = __shfl_sync(0xffffffffu, page, half * 4 + lu);
-          const int ip = __shfl_sync(0xffffffffu, in_page, half * 4 + lu);
-          if (lane < 16 && lu < units && ch < C::kChunks)
-            tma_load_4d(smem + slot * C::kSlotBytes + ch * kSlotKeys * C::kChunkBytes +
-                            lu * kUnit * C::kChunkBytes,
-                        is_v ? &tm_v : &tm_k, &full[slot], ch * (C::kChunkBytes / C::kEsz), ip,
-                        w.r.h, pg);
+          // one lane issues: a copy's operands are warp-uniform registers, and
+          // copies from several lanes took some 250 cycles each
+          for (int lu = 0; lu < units; ++lu) {
+            const int pg = __shfl_sync(0xffffffffu, page, half * 4 + lu);
+            const int ip = __shfl_sync(0xffffffffu, in_page, half * 4 + lu);
+            if (lane == 0)
+              tma_load_page(smem + slot * C::kSlotBytes + lu * C::kUnitBytes, is_v ? &tm_v : &tm_k,
+                            &full[slot], 0, ip, w.r.h, pg);
+          }
         }
       }
     }
@@ -346,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<kDim, kE4m3, kR>::kCtas)
           mbar_wait(&full[si % C::kSlots], (si / C::kSlots) & 1, abort_flag);
           __syncwarp();
           const uint32_t base = ring + (si % C::kSlots) * C::kSlotBytes +
-                                (warp & 3) * kUnit * C::kChunkBytes;
+                                (warp & 3) * C::kUnitBytes;
           if (kE4m3) {
 #pragma unroll
             for (int cc = 0; cc < kDim / 64; ++cc) {
@@ -355,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<kDim, kE4m3, kR>::kCtas)
               for (int j = 0; j < 2; ++j) {
                 const int row = j * 8 + g;
                 if (C::kChunkBytes == 128)
-                  kc[j] = lds128(base + (cc >> 1) * kSlotKeys * 128 + row * 128 +
+                  kc[j] = lds128(base + (cc >> 1) * C::kUnitChunk + row * 128 +
                                  (((2 * t + (cc & 1)) ^ g) << 4));
                 else
                   kc[j] = lds128(base + row * 64 + ((t ^ (row >> 1 & 3)) << 4));
@@ -390,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<kDim, kE4m3, kR>::kCtas)
             for (int ks = 0; ks < kSteps; ++ks) {
               uint32_t b[4];
               const int c16 = ks * 2 + (mi & 1);
-              ldsm_x4(row + (c16 >> 3) * kSlotKeys * 128 + (((c16 & 7) ^ r8) << 4), b);
+              ldsm_x4(row + (c16 >> 3) * C::kUnitChunk + (((c16 & 7) ^ r8) << 4), b);
 #pragma unroll
               for (int rt = 0; rt < kR; ++rt) {
                 uint32_t a[4];
@@ -481,19 +483,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<kDim, kE4m3, kR>::kCtas)
             const int u = half * 4 + lu;
             if (u >= n) break;
             uint32_t b[kNt][2];
+            const uint32_t unit = base + lu * C::kUnitBytes;
             if (kE4m3) {
               // columns 8 kNt warp + kNt g + i of keys 2t, 2t+1, 2t+8, 2t+9
               uint32_t c4[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const int row = lu * 16 + 2 * t + (i & 1) + 8 * (i >> 1);
+                const int row = 2 * t + (i & 1) + 8 * (i >> 1);
                 const int byte = warp * (8 * kNt) + kNt * g;
                 uint32_t a;
                 if (C::kChunkBytes == 128)
-                  a = base + (byte >> 7) * kSlotKeys * 128 + row * 128 +
+                  a = unit + (byte >> 7) * C::kUnitChunk + row * 128 +
                       ((((byte >> 4) & 7) ^ (row & 7)) << 4) + (byte & 15);
                 else
-                  a = base + row * 64 + (((byte >> 4) ^ (row >> 1 & 3)) << 4) + (byte & 15);
+                  a = unit + row * 64 + (((byte >> 4) ^ (row >> 1 & 3)) << 4) + (byte & 15);
                 c4[i] = kNt == 4 ? lds32(a) : kNt == 2 ? lds16(a) : lds8(a);
               }
 #pragma unroll
@@ -509,16 +512,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<kDim, kE4m3, kR>::kCtas)
               }
             } else {
               const int mi = lane >> 3, r8 = lane & 7;
-              const uint32_t row = base + (lu * 16 + (mi & 1) * 8 + r8) * 128;
+              const uint32_t row = unit + ((mi & 1) * 8 + r8) * 128;
               if (kNt == 1) {
-                const uint32_t a = base + (lu * 16 + (mi & 1) * 8 + r8) * 128 + ((warp ^ r8) << 4);
-                ldsm_x2_t(a, b[0][0], b[0][1]);
+                ldsm_x2_t(row + ((warp ^ r8) << 4), b[0][0], b[0][1]);
               } else {
 #pragma unroll
                 for (int i = 0; i < kNt / 2; ++i) {
                   const int c16 = warp * kNt + 2 * i + (mi >> 1);
                   uint32_t r4[4];
-                  ldsm_x4_t(row + (c16 >> 3) * kSlotKeys * 128 + (((c16 & 7) ^ r8) << 4), r4);
+                  ldsm_x4_t(row + (c16 >> 3) * C::kUnitChunk + (((c16 & 7) ^ r8) << 4), r4);
                   b[2 * i][0] = r4[0], b[2 * i][1] = r4[1];
                   b[(2 * i + 1) % kNt][0] = r4[2], b[(2 * i + 1) % kNt][1] = r4[3];
                 }
@@ -669,8 +671,8 @@ int run(const Attend& p, const Device& d, cudaStream_t stream) {
   if (const int st = allow_smem(kernel, C::kSmem, d, ready)) return st;
   CUtensorMap tm_k, tm_v;
   constexpr int inner = C::kChunkBytes / C::kEsz;
-  if (!page_map(&tm_k, p.cache, false, inner, kUnit) ||
-      !page_map(&tm_v, p.cache, true, inner, kUnit))
+  if (!page_map(&tm_k, p.cache, false, inner, kUnit, C::kChunks) ||
+      !page_map(&tm_v, p.cache, true, inner, kUnit, C::kChunks))
     return NVFP4_ERR_LAUNCH;
   const Plan plan{std::max(1, C::kRows / p.group), kUnit, 4};
   const int ctas = d.num_sms * C::kCtas;
