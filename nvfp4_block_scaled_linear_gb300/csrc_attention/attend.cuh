@@ -8,6 +8,22 @@
 namespace nvfp4 {
 namespace attn {
 
+// Wait for the phase with the given parity; given up after 2^31 clock ticks
+// (about a second), or at once when another wait of the block was, with
+// `abort_flag` set and false returned.  Little code, since it is inlined in
+// every role of kernels that have to stay within the instruction cache.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  const uint32_t t0 = static_cast<uint32_t>(clock());
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort_flag || static_cast<uint32_t>(clock()) - t0 > 0x7FFFFFFFu) {
+      *abort_flag = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
 // Tensor map of the cache's key or value pages, dimensions (element of a
 // chunk, slot, chunk, head, page), for boxes of `rows` slots by `chunks` chunks
 // of `inner` elements (64 or 128 bytes, swizzled to that width): chunk after

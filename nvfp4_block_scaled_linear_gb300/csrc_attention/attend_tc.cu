@@ -43,32 +43,36 @@ namespace attn {
 namespace {
 
 constexpr int kM = 128;                       // rows of a tile
-constexpr int kN = 128;                       // keys of a block (one unit)
+constexpr int kBlockShift = 7;
+constexpr int kN = 1 << kBlockShift;          // keys of a block (one unit)
 constexpr float kSlack = 8.f;                 // growth of log2 of a weight before rescaling
+constexpr int kItems = 4;                     // item descriptors in flight
 constexpr int kQFactors = 4;                  // items whose row factors are held
 constexpr int kDirty = 8;                     // items whose `dirty` note is held: more than the ring's
 
 template <int kDim, bool kE4m3, int kTiles>
 struct Cfg {
   static constexpr int kThreads = kE4m3 ? 512 : 384;
-  // A slot holds 16 KB: 64 of head_dim of all keys of a K block, or all of
-  // head_dim of some keys of a V block (64 columns by 64 columns).  Small
-  // slots are refilled as soon as a few MMAs are done with them: at head_dim
-  // 256 the ring is little more than one block deep.
-  static constexpr int kPieces = kDim / 64;                    // slots of one K (or V) block
-  static constexpr int kSlotBytes = kN * 128;
-  static constexpr int kVKeys = kN / kPieces;                  // keys of a V slot
-  static constexpr int kVChunk = kVKeys * 128;                 // bytes of 64 columns of it
+  // A slot holds up to 32 KB: 128 of head_dim of all keys of a K block, or all
+  // of head_dim of some keys of a V block, in chunks of 64 columns.
+  static constexpr int kSlotBytes = std::min(kDim * kN * 2, 32 * 1024);
+  static constexpr int kPieces = kDim * kN * 2 / kSlotBytes;   // slots of one K (or V) block
+  static constexpr int kKChunks = kDim / 64 / kPieces;         // of a K slot
+  static constexpr int kKChunk = kN * 128;                     // bytes of one of them
+  static constexpr int kVChunks = kDim / 64;                   // of a V slot
+  static constexpr int kVKeys = kN / kPieces;
+  static constexpr int kVChunk = kVKeys * 128;
   static constexpr int kQTile = kM * kDim * 2;
   static constexpr int kQBytes = kTiles * kQTile;
-  static constexpr int kMaxSlots = 12;
-  static constexpr int kBars = 3 * kMaxSlots + 19;
+  static constexpr int kMaxSlots = 8;
+  static constexpr int kBars = 3 * kMaxSlots + 21 + 2 * kItems;
   static constexpr int kBarOff = 0;
-  static constexpr int kMaxOff = (kBarOff + kBars * 8 + 8 + kDirty * 4 + 15) / 16 * 16;   // running maxima
+  static constexpr int kItemOff = (kBarOff + kBars * 8 + 8 + kDirty * 4 + 15) / 16 * 16;  // descriptors
+  static constexpr int kMaxOff = kItemOff + kItems * 32;                                   // running maxima
   static constexpr int kSumOff = kMaxOff + (kTiles == 1 ? kM * 4 : 0);        // row sums
-  static constexpr int kFacOff = kSumOff + (kTiles == 1 ? 2 * kM * 4 : 0);    // Q row factors
+  static constexpr int kFacOff = kSumOff + (kTiles == 1 ? kM * 4 : 0);    // Q row factors
   static constexpr int kRowOff = kFacOff + (kE4m3 ? kQFactors * kTiles * kM * 4 : 0);
-  static constexpr int kFixed = kRowOff + (kE4m3 ? 2 * kN * 8 : 0);
+  static constexpr int kFixed = kRowOff + (kE4m3 ? 2 * kN * 8 : 4 * 8 * 8);
   static constexpr int kBudget = 227 * 1024 - 1024 - kFixed - kQBytes;
   static constexpr int kSlots = std::min(kMaxSlots, kBudget / kSlotBytes);
   static constexpr int kSmem = kQBytes + kSlots * kSlotBytes + kFixed + 1024;
@@ -80,16 +84,31 @@ struct Cfg {
   static_assert(kS + 2 * kN <= 512, "TMEM");
 };
 
-// MN-major operand (d contiguous): 64 d per 128-byte row, 8-key groups 1024 B
-// apart, the next 64 d `lbo` bytes on.
-__device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t addr, uint32_t lbo) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((addr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
+// Shared-memory matrix descriptors, 128-byte swizzled rows, 8-row groups 1024
+// bytes apart: the high word is the same for all, the low word the start
+// address (in 16 bytes) and, for the MN-major V (d contiguous), the distance
+// of the next 64 columns.  Advancing along k adds to the low word.
+constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
+  return (addr >> 4) | (lbo >> 4) << 16;
+}
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t id,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(id), "r"(accumulate), "r"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t id,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "r"(b_lo), "r"(id), "r"(accumulate), "r"(kDescHi)
+      : "memory");
 }
 
 template <bool kE4m3>
@@ -117,6 +136,15 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
+}
+
+__device__ __forceinline__ void tmem_st_16cols(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 
 template <int kRegs>
@@ -157,34 +185,74 @@ __device__ __forceinline__ uint32_t finite_mask(uint32_t w) {
   return ((w & e) == e ? 0u : 0xFFFFu) | ((w & (e << 16)) == (e << 16) ? 0u : 0xFFFF0000u);
 }
 
+// A position in the ring of slots, and the parity of its turn.
+template <int kSlots>
+struct Ring {
+  int slot = 0;
+  uint32_t par = 0;
+  __device__ void next() {
+    if (++slot == kSlots) slot = 0, par ^= 1u;
+  }
+};
+
 struct TcParams {
   Attend a;
   Plan plan;
   Parts parts;
   int tile_tokens;          // tokens of one 128-row tile
-  int box_rows;             // slots of one page copy
+  int box_shift;            // log2 of the slots of one page copy
 };
 
-// The blocks of a CTA's range in order, tile by tile where a block serves two.
-template <int kTiles>
-struct Steps {
-  Walk w;
-  int b = 0, x = 0;           // block of the item, tile
-  int item = 0;               // ordinal of the item in this CTA
-  __device__ Steps(const Range& r, const TcParams& p) : w(r, p.a.seqs, p.plan, p.a.err) {}
-  __device__ bool more() const { return w.more(); }
+// One item of the CTA's range, as the scheduling lane publishes it to the other
+// warps (the code that finds the next item exists once: inlined in every role
+// it made the kernel larger than the instruction cache, and every role's
+// steps several times slower).
+struct alignas(16) Item {
+  int s, h, q0, q_len, kv_len;
+  int tok0;                   // first token, of the sequence's new ones
+  int key0;                   // first key
+  int blocks;                 // 0: the end of the range; kBegins, kEnds in its top bits
+  __device__ int count() const { return blocks & 0x0FFFFFFF; }
+  // keys that every token sees, that the last token sees
+  __device__ int least() const { return max(0, kv_len - q_len + tok0 + 1); }
+  __device__ int seen(const Plan& p) const {
+    return max(0, kv_len - q_len + min(q_len, tok0 + p.tile_tokens));
+  }
+};
+constexpr int kBegins = 1 << 30, kEnds = 1 << 29;
+
+struct Items {
+  Item* ring;
+  uint64_t* full;
+  uint64_t* empty;
+  volatile int* abort_flag;
+  // Item i, or false at the end (or when waiting for it was given up).
+  __device__ bool get(int i, Item& it) const {
+    const bool ok = wait(&full[i % kItems], i / kItems & 1, abort_flag);
+    const int4* src = reinterpret_cast<const int4*>(&ring[i % kItems]);
+    reinterpret_cast<int4*>(&it)[0] = src[0];
+    reinterpret_cast<int4*>(&it)[1] = src[1];
+    if (!ok) it.blocks = 0;
+    return it.blocks != 0;
+  }
+  // One role is done with item i.
+  __device__ void release(int i) const { mbar_arrive(&empty[i % kItems]); }
+};
+
+// A role's place in the sequence of blocks.
+struct Place {
+  Item it;
+  int item = 0, b = 0;
+  bool live;
+  __device__ void start(const Items& items) { live = items.get(0, it); }
   __device__ bool first() const { return b == 0; }
-  __device__ bool last() const { return b + 1 == w.count; }
-  __device__ void next(const TcParams& p) {
-    if (kTiles == 2 && x == 0) {
-      x = 1;
-      return;
-    }
-    x = 0;
-    if (++b < w.count) return;
+  __device__ bool last() const { return b + 1 == it.count(); }
+  // To the next block; true where it is another item's.
+  __device__ bool next(const Items& items) {
+    if (++b < it.count()) return false;
     b = 0;
-    ++item;
-    w.next(p.a.seqs, p.a.cache.heads, p.plan, p.a.err);
+    live = items.get(++item, it);
+    return true;
   }
 };
 
@@ -209,6 +277,10 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
   uint64_t* q_full = m_ready + 8;
   uint64_t* q_empty = q_full + 1;
   uint64_t* mma_done = q_empty + 1;               // every product issued has completed
+  uint64_t* pair = mma_done + 1;                  // both softmax groups (kTiles == 1)
+  uint64_t* widen = pair + 1;                     // the widening warps (e4m3)
+  const Items items{reinterpret_cast<Item*>(fixed + C::kItemOff), widen + 1, widen + 1 + kItems,
+                    reinterpret_cast<volatile int*>(full + C::kBars)};
   volatile int* abort_flag = reinterpret_cast<volatile int*>(full + C::kBars);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(full + C::kBars) + 1;
   volatile int* dirty = reinterpret_cast<volatile int*>(full + C::kBars) + 2;  // item ordinal + 1
@@ -234,6 +306,13 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
     mbar_init(q_full, kE4m3 ? 3 : 1);
     mbar_init(q_empty, 1);
     mbar_init(mma_done, 1);
+    mbar_init(pair, 8);
+    mbar_init(widen, 4);
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&items.full[i], 1);
+      // softmax warps, MMA, and the copying and checking (or Q and widening) warps
+      mbar_init(&items.empty[i], 8 + 1 + (kE4m3 ? 2 + 4 : 2));
+    }
     *abort_flag = 0;
     for (int i = 0; i < kDirty; ++i) dirty[i] = 0;
     fence_mbar_init();
@@ -251,17 +330,25 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
   griddep_launch_dependents();
   // the range, in scratch that the ring's first copies will overwrite
   const Range range =
-      find_range(a.seqs, a.cache.heads, p.plan, static_cast<int>(blockIdx.x),
-                 static_cast<int>(gridDim.x), reinterpret_cast<RangeSmem*>(ring), a.err);
+      find_range(a.seqs, a.cache.heads, p.plan, blockIdx.x,
+                 gridDim.x, reinterpret_cast<RangeSmem*>(ring), a.err);
   fence_proxy_async_smem();
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
 
-  // Keys that every token of the item sees, and that its last one does.
-  auto least_of = [&](const Walk& w) {
-    return max(0, w.seq.kv_len - w.seq.q_len + w.r.tile * p.plan.tile_tokens + 1);
+  // The scheduling lane: item i, or the end, to all other warps; false at the end.
+  auto publish = [&](const Walk& w, int i) {
+    if (i >= kItems && !wait(&items.empty[i % kItems], (i / kItems & 1) ^ 1, abort_flag))
+      return false;
+    Item it{};
+    if (w.more())
+      it = Item{w.r.s, w.r.h, w.seq.q0, w.seq.q_len, w.seq.kv_len, w.r.tile * p.plan.tile_tokens,
+                w.r.unit0 * kN, w.count | (w.begins() ? kBegins : 0) | (w.ends() ? kEnds : 0)};
+    items.ring[i % kItems] = it;
+    mbar_arrive(&items.full[i % kItems]);
+    return w.more();
   };
 
   if (warp < 8) {
@@ -277,19 +364,27 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
     int4 note = make_int4(0, 0, 0, 0);
     int step = 0;                                     // of both buffers (kTiles == 1)
     int uses = 0;                                     // of buffer x
-    int item = 0;
-    for (Walk w(range, a.seqs, p.plan, a.err); w.more();
-         w.next(a.seqs, a.cache.heads, p.plan, a.err), ++item) {
-      const SeqInfo seq = w.seq;
-      const int ti = w.r.tile * p.plan.tile_tokens + (kTiles == 2 ? x * p.tile_tokens : 0) + tok;
-      const bool valid = tok < p.tile_tokens && ti < seq.q_len;
-      const int lim = valid ? max(0, seq.kv_len - seq.q_len + ti + 1) : 0;
+    uint32_t pair_par = 0;
+    auto meet = [&]() {                               // both groups
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pair);
+      wait(pair, pair_par, abort_flag);
+      __syncwarp();
+      pair_par ^= 1u;
+    };
+    Item it;
+    for (int item = 0; items.get(item, it); ++item) {
+      __syncwarp();
+      const int ti = it.tok0 + (kTiles == 2 ? x * p.tile_tokens : 0) + tok;
+      const bool valid = tok < p.tile_tokens && ti < it.q_len;
+      const int lim = valid ? max(0, it.kv_len - it.q_len + ti + 1) : 0;
+      const int count = it.count();
       float c = a.scale * 1.44269504088896f;
-      if (kE4m3 && a.cache.k_scale) c *= a.cache.k_scale[w.r.h];
+      if (kE4m3 && a.cache.k_scale) c *= a.cache.k_scale[it.h];
       float m = -INFINITY, l = 0.f;                   // of the blocks that this thread saw
-      for (int b = 0; b < w.count; ++b, ++step) {
+      for (int b = 0; b < count; ++b, ++step) {
         if (kTiles == 1 && (step & 1) != x) continue;
-        mbar_wait(&s_full[x], uses & 1, abort_flag);
+        wait(&s_full[x], uses & 1, abort_flag);
         __syncwarp();
         tc_fence_after_sync();
         if (kE4m3 && (b == 0 || (kTiles == 1 && b == 1)))
@@ -298,7 +393,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_ld_32cols(t_s + i * 32, s[i]);
         tmem_ld_wait();
-        const int seen = lim - (w.r.unit0 + b) * kN;  // of this block, by this row
+        const int seen = lim - it.key0 - b * kN;      // of this block, by this row
         if (__any_sync(0xffffffffu, seen < kN)) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -320,7 +415,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
         if (b > 0) {
           float prev = m;
           if (kTiles == 1) {
-            mbar_wait(&m_ready[(x ^ 1) * 4 + quad], ((step - 1) >> 1) & 1, abort_flag);
+            wait(&m_ready[(x ^ 1) * 4 + quad], ((step - 1) >> 1) & 1, abort_flag);
             __syncwarp();
             prev = run_max[row];
           }
@@ -328,9 +423,9 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
           if (__any_sync(0xffffffffu, now - prev > kSlack)) {
             // the accumulator, complete up to the block before
             if (kTiles == 1)
-              mbar_wait(&pv_done[x ^ 1], ((step - 1) >> 1) & 1, abort_flag);
+              wait(&pv_done[x ^ 1], ((step - 1) >> 1) & 1, abort_flag);
             else
-              mbar_wait(&pv_done[x], (uses - 1) & 1, abort_flag);
+              wait(&pv_done[x], (uses - 1) & 1, abort_flag);
             __syncwarp();
             tc_fence_after_sync();
             const float alpha = prev == -INFINITY ? 0.f : ex2(prev - now);
@@ -360,17 +455,17 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
         const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-          uint32_t w16[32];
+        for (int i = 0; i < 4; ++i) {
+          uint32_t w16[16];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const uint32_t* sj = &s[i + (j >> 4)][2 * (j & 15)];
-            float2 e = fma2(make_float2(__uint_as_float(sj[0]), __uint_as_float(sj[1])), c2, b2);
+          for (int j = 0; j < 16; ++j) {
+            float2 e = fma2(make_float2(__uint_as_float(s[i][2 * j]), __uint_as_float(s[i][2 * j + 1])),
+                            c2, b2);
             e.x = ex2(e.x), e.y = ex2(e.y);
             sum[j & 1] = add2(sum[j & 1], e);
             w16[j] = kE4m3 ? f32x2_to_f16x2(e.x, e.y) : f32x2_to_bf16x2(e.x, e.y);
           }
-          tmem_st_32cols(t_s + i * 16, w16);
+          tmem_st_16cols(t_s + i * 16, w16);
         }
         sum[0] = add2(sum[0], sum[1]);
         l += sum[0].x + sum[0].y;
@@ -381,30 +476,34 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
         ++uses;
       }
       // ---- the row's sum, and the result
-      const bool whole = w.begins() && w.ends();
-      const int part = w.begins() ? 1 : 0;
+      const bool whole = (it.blocks & kBegins) && (it.blocks & kEnds);
+      const int part = it.blocks & kBegins ? 1 : 0;
       if (!whole) {
-        flags |= part ? kPart1 : kPart0 | (w.ends() ? kPart0Ends : 0);
-        if (part) note = make_int4(0, w.r.s, w.r.h, w.r.tile);
+        flags |= part ? kPart1 : kPart0 | (it.blocks & kEnds ? kPart0Ends : 0);
+        if (part) note = make_int4(0, it.s, it.h, it.tok0 / p.plan.tile_tokens);
       }
       if (kTiles == 1) {
         // the last product with either buffer, whose weights both groups gave
-        mbar_wait(&pv_done[(step - 1) & 1], ((step - 1) >> 1) & 1, abort_flag);
+        wait(&pv_done[(step - 1) & 1], ((step - 1) >> 1) & 1, abort_flag);
         __syncwarp();
         const float now = run_max[row];               // of the last block
-        row_sum[x * kM + row] = m == -INFINITY ? l : l * ex2(m - now);
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        l = row_sum[row] + row_sum[kM + row];
+        if (m != -INFINITY) l *= ex2(m - now);
+        meet();                                       // both groups have read it
+        float* mine = x ? row_sum : run_max;
+        const float* other = x ? run_max : row_sum;
+        mine[row] = l;
+        meet();
+        l = x ? other[row] + l : l + other[row];
         m = now;
       } else {
-        mbar_wait(&pv_done[x], (uses - 1) & 1, abort_flag);
+        wait(&pv_done[x], (uses - 1) & 1, abort_flag);
         __syncwarp();
       }
       tc_fence_after_sync();
-      const float vs = kE4m3 && a.cache.v_scale ? a.cache.v_scale[w.r.h] : 1.f;
+      const float vs = kE4m3 && a.cache.v_scale ? a.cache.v_scale[it.h] : 1.f;
       const float inv = l == 0.f ? 0.f : vs / l;
-      const int64_t token = seq.q0 + ti;
-      const int head = w.r.h * a.group + gi;
+      const int64_t token = it.q0 + ti;
+      const int head = it.h * a.group + gi;
       const int prow = (kTiles == 2 ? x * kM : 0) + row;
       const int64_t at_part = p.parts.row(blockIdx.x, part, prow);
       if (valid && (kTiles == 2 || x == 0)) {
@@ -429,27 +528,6 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
         if (valid) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * inv);
-        if (fix) {
-          // values that are not finite, of the keys that not all rows see
-          const int from = max(least_of(w), w.r.unit0 * kN);
-          const int to = min(lim, (w.r.unit0 + w.count) * kN);
-#pragma unroll 1
-          for (int key = from; key < to; ++key) {
-            const int64_t page = checked_page(
-                a.seqs.table[int64_t(w.r.s) * a.seqs.width + key / a.cache.page_size],
-                a.cache.pages, a.err);
-            if (page == a.cache.pages) continue;
-            const int64_t off = page * a.cache.vs[0] + key % a.cache.page_size * a.cache.vs[1] +
-                                w.r.h * a.cache.vs[2] + i;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float v = kE4m3
-                                  ? e4m3_to_f32(static_cast<const uint8_t*>(a.cache.v)[off + j])
-                                  : __bfloat162float(static_cast<const __nv_bfloat16*>(a.cache.v)[off + j]);
-              if (!isfinite(v)) o[j] = __float_as_uint(__uint_as_float(o[j]) + v);
-            }
-          }
-        }
         if (whole) {
           uint4* dst = reinterpret_cast<uint4*>(a.out.data + token * a.out.ts + head * a.out.hs + i);
 #pragma unroll
@@ -470,7 +548,34 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
         }
         __syncwarp();
       }
-      if (kTiles == 1) asm volatile("bar.sync 1, 256;" ::: "memory");   // row_sum is free again
+      if (fix && valid) {
+        // values that are not finite, of the keys that not all rows see
+        const int from = max(it.least(), it.key0), to = min(lim, it.key0 + count * kN);
+#pragma unroll 1
+        for (int key = from; key < to; ++key) {
+          const int64_t page =
+              checked_page(a.seqs.table[int64_t(it.s) * a.seqs.width + key / a.cache.page_size],
+                           a.cache.pages, a.err);
+          if (page == a.cache.pages) continue;
+          const int64_t off = page * a.cache.vs[0] + key % a.cache.page_size * a.cache.vs[1] +
+                              it.h * a.cache.vs[2];
+#pragma unroll 1
+          for (int i = col0; i < col0 + kCols; ++i) {
+            const float v = kE4m3 ? e4m3_to_f32(static_cast<const uint8_t*>(a.cache.v)[off + i])
+                                  : __bfloat162float(static_cast<const __nv_bfloat16*>(a.cache.v)[off + i]);
+            if (isfinite(v)) continue;
+            if (whole) {
+              __nv_bfloat16* y = a.out.data + token * a.out.ts + head * a.out.hs + i;
+              *y = __float2bfloat16_rn(__bfloat162float(*y) + v);
+            } else {
+              p.parts.out[at_part * kDim + i] += v;
+            }
+          }
+        }
+      }
+      if (kTiles == 1) meet();                          // run_max and row_sum are free again
+      __syncwarp();
+      if (lane == 0) items.release(item);
     }
     if (threadIdx.x == 0) {
       note.x = flags;
@@ -483,186 +588,237 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
       if (lane == 0) {
         const uint32_t id_s = idesc<kE4m3>(kN, false);
         const uint32_t id_o = idesc<kE4m3>(kDim, true);
-        const uint32_t q_addr = smem_addr(q_sm), ring_addr = smem_addr(ring);
+        const uint32_t q_lo = desc_lo(smem_addr(q_sm), 0);
+        const uint32_t k_lo = desc_lo(smem_addr(ring), 0);
+        const uint32_t v_lo = desc_lo(smem_addr(ring), C::kVChunk);
         uint64_t* v_bar = kE4m3 ? full : checked;
-        Steps<kTiles> qk(range, p), pv(range, p);
-        int slot_q = 0, slot_v = 0;               // ring positions of the next K and V
-        int it = 0;                               // ring position in the order of the copies
+        Place qk, pv;                             // of the scores, of the products with V
+        int qk_x = 0, pv_x = 0;                   // and the tile (kTiles == 2)
+        qk.start(items);
+        pv.start(items);
+        Ring<C::kSlots> at, at_k, at_v;           // in the order of the copies; of the K and V in use
         bool ok = true;
-        for (int i = 0; ok && (qk.more() || pv.more()); ++i) {
+        for (int i = 0; ok && (qk.live || pv.live); ++i) {
+          const int x = i & 1;
+          const uint32_t t_s = tmem + C::kS + x * kN;
           if (i >= 2) {
-            // ---- O += P V
-            const int x = i & 1, u = (i - 2) >> 1;
-            ok = mbar_wait(&p_full[x], u & 1, abort_flag);
-            if (ok && pv.first() && pv.item > 0 && (kTiles == 2 || pv.b == 0))
-              ok = mbar_wait(&o_free[kTiles == 1 ? 0 : x], (pv.item - 1) & 1, abort_flag);
-            if (pv.x == 0) {
-              slot_v = it;
-              it += C::kPieces;
+            // ---- O += P V, two steps behind
+            ok = wait(&p_full[x], (i - 2) >> 1 & 1, abort_flag);
+            const bool fresh = pv.first();
+            if (ok && fresh && pv.item > 0)
+              ok = wait(&o_free[kTiles == 1 ? 0 : x], (pv.item - 1) & 1, abort_flag);
+            if (pv_x == 0) {
+              at_v = at;
+#pragma unroll
+              for (int h = 0; h < C::kPieces; ++h) at.next();
             }
             const uint32_t t_o = tmem + C::kO + (kTiles == 2 ? x * kDim : 0);
-            for (int h = 0; h < C::kPieces && ok; ++h) {
-              const int s = (slot_v + h) % C::kSlots;
-              ok = mbar_wait(&v_bar[s], ((slot_v + h) / C::kSlots) & 1, abort_flag);
+            Ring<C::kSlots> r = at_v;
+#pragma unroll
+            for (int h = 0; h < C::kPieces; ++h, r.next()) {
+              ok = ok && wait(&v_bar[r.slot], r.par, abort_flag);
               if (!ok) break;
               tc_fence_after_sync();
-              const uint32_t v = ring_addr + s * C::kSlotBytes;
-              const uint32_t t_p = tmem + C::kS + x * kN + h * (C::kVKeys / 2);
+              const uint32_t v = v_lo + r.slot * (C::kSlotBytes >> 4);
 #pragma unroll
               for (int kk = 0; kk < C::kVKeys / 16; ++kk)
-                umma_f16_tmem_a(t_o, t_p + kk * 8, umma_desc_mn_sw128(v + kk * 2048, C::kVChunk),
-                                id_o, !(pv.first() && (h | kk) == 0));
-              if (kTiles == 1 || x == 1) umma_commit(&empty[s]);
+                umma_ts(t_o, t_s + (h * C::kVKeys / 16 + kk) * 8, v + kk * (2048 >> 4), id_o,
+                        !fresh || (h | kk) != 0);
+              if (kTiles == 1 || x == 1) umma_commit(&empty[r.slot]);
             }
             if (!ok) break;
             umma_commit(&pv_done[x]);
-            pv.next(p);
-          }
-          if (qk.more()) {
-            // ---- S = Q K^T
-            const int x = i & 1;
-            if (qk.first() && qk.x == 0) ok = mbar_wait(q_full, qk.item & 1, abort_flag);
-            if (qk.x == 0) {
-              slot_q = it;
-              it += C::kPieces;
+            if (kTiles == 2 && pv_x == 0) {
+              pv_x = 1;
+            } else {
+              pv_x = 0;
+              const int was = pv.item;
+              if (pv.next(items)) items.release(was);
             }
-            for (int h = 0; h < C::kPieces && ok; ++h) {
-              const int s = (slot_q + h) % C::kSlots;
-              ok = mbar_wait(&full[s], ((slot_q + h) / C::kSlots) & 1, abort_flag);
+          }
+          if (qk.live) {
+            // ---- S = Q K^T
+            if (qk.first() && qk_x == 0) ok = wait(q_full, qk.item & 1, abort_flag);
+            if (qk_x == 0) {
+              at_k = at;
+#pragma unroll
+              for (int h = 0; h < C::kPieces; ++h) at.next();
+            }
+            Ring<C::kSlots> r = at_k;
+            const uint32_t q = q_lo + (kTiles == 2 ? x * (C::kQTile >> 4) : 0);
+#pragma unroll
+            for (int h = 0; h < C::kPieces; ++h, r.next()) {
+              ok = ok && wait(&full[r.slot], r.par, abort_flag);
               if (!ok) break;
               tc_fence_after_sync();
-              const uint32_t k = ring_addr + s * C::kSlotBytes;
-              const uint32_t q = q_addr + (kTiles == 2 ? x * C::kQTile : 0) + h * C::kSlotBytes;
+              const uint32_t k = k_lo + r.slot * (C::kSlotBytes >> 4);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                umma_bf16(tmem + C::kS + x * kN, umma_desc_sw128(q + kk * 32),
-                          umma_desc_sw128(k + kk * 32), id_s, (h | kk) != 0);
-              if (kTiles == 1 || x == 1) umma_commit(&empty[s]);
+              for (int kk = 0; kk < C::kKChunks * 4; ++kk) {
+                const uint32_t off = ((kk >> 2) * C::kKChunk + (kk & 3) * 32) >> 4;
+                umma_ss(t_s, q + ((h * C::kKChunks * C::kKChunk) >> 4) + off, k + off, id_s,
+                        (h | kk) != 0);
+              }
+              if (kTiles == 1 || x == 1) umma_commit(&empty[r.slot]);
             }
             if (!ok) break;
             umma_commit(&s_full[x]);
-            if (qk.last() && qk.x == kTiles - 1) umma_commit(q_empty);
-            qk.next(p);
+            if (qk.last() && qk_x == kTiles - 1) umma_commit(q_empty);
+            if (kTiles == 2 && qk_x == 0) {
+              qk_x = 1;
+            } else {
+              qk_x = 0;
+              qk.next(items);
+            }
           }
         }
         // nothing may be in flight when TMEM is released
         umma_commit(mma_done);
         volatile int no_abort = 0;
-        if (!mbar_wait(mma_done, 0, &no_abort)) atomicOr(a.err, NVFP4_ATTENTION_TIMEOUT);
+        if (!wait(mma_done, 0, &no_abort)) atomicOr(a.err, NVFP4_ATTENTION_TIMEOUT);
       }
       __syncwarp();
     } else if (warp == 8 && !kE4m3) {
       // ------------------------------------------------------ K, V copies
-      Steps<1> kc(range, p), vc(range, p);        // block by block for either kTiles
-      int it = 0;
+      // The warp looks up a block's pages together, one block ahead (lane i:
+      // the copy of rows i << box_shift on); lane 0 alone issues, since a
+      // copy's operands are warp-uniform registers (copies from several lanes
+      // took some 250 cycles each), and its steps are kept few: one warp's
+      // dependent instructions are what the copies would otherwise wait for.
+      Place kc, vc;
+      kc.start(items);
+      vc.start(items);
+      __syncwarp();
+      Ring<C::kSlots> at;
       bool ok = true;
-      // A block's pages: lane i holds that of rows i * box_rows on, read one
-      // block ahead of its use and kept for the V of the same keys.
-      struct Pages {
-        int key, entry, page, in_page;
-      };
-      const int k_boxes = kN / p.box_rows;
-      const int v_rows = min(p.box_rows, C::kVKeys), v_boxes = C::kVKeys / v_rows;
-      auto look_up = [&](const Steps<1>& st) {
-        Pages g{-1, 0, -1, 0};
-        if (!st.more()) return g;
-        const int key = (st.w.r.unit0 + st.b) * kN + lane * p.box_rows;
-        if (lane < k_boxes && key < st.w.seq.kv_len) {
-          g.key = key;
-          g.entry = a.seqs.table[int64_t(st.w.r.s) * a.seqs.width + key / a.cache.page_size];
+      int turns = 0;                              // slots filled, up to kSlots
+      const int shift = p.box_shift, k_boxes = kN >> shift;
+      constexpr int kVShift = C::kVKeys == 128 ? 7 : 6;
+      const int v_shift = min(shift, kVShift), v_boxes = 1 << (kVShift - v_shift);
+      const int v_chunks = v_boxes == 1 ? C::kVChunks : 1;          // of one copy
+      constexpr int kAhead = kTiles == 1 ? 2 : 1;
+      constexpr int kHeld = 4;
+      int2(*pages)[8] = reinterpret_cast<int2(*)[8]>(fixed + C::kRowOff);   // [kHeld]
+      auto look_up = [&](const Place& at, int& key) {
+        key = at.it.key0 + at.b * kN + (lane << shift);
+        if (!at.live || lane >= k_boxes || key >= at.it.kv_len) {
+          key = -1;
+          return 0;
         }
-        return g;
+        return a.seqs.table[int64_t(at.it.s) * a.seqs.width + key / a.cache.page_size];
       };
       auto next_slot = [&](uint32_t bytes) {
-        const int s = it % C::kSlots;
-        if (it >= C::kSlots)
-          ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], ((it / C::kSlots) & 1) ^ 1, abort_flag));
-        if (ok && lane == 0) mbar_arrive_expect_tx(&full[s], bytes);
-        return s;
+        if (turns == C::kSlots)
+          ok = wait(&empty[at.slot], at.par ^ 1, abort_flag);
+        else
+          ++turns;
+        if (ok) mbar_arrive_expect_tx(&full[at.slot], bytes);
       };
-      // One lane issues: a copy's operands are warp-uniform registers, and
-      // copies from several lanes took some 250 cycles each.
-      auto copy_k = [&](const Walk& w, const Pages& g) {
-        const int n = __popc(__ballot_sync(0xffffffffu, g.page >= 0));
-        for (int h = 0; h < C::kPieces; ++h, ++it) {
-          const int s = next_slot(n * p.box_rows * 128);
-          if (!ok) return;
-          for (int i = 0; i < k_boxes; ++i) {
-            const int page = __shfl_sync(0xffffffffu, g.page, i);
-            const int in_page = __shfl_sync(0xffffffffu, g.in_page, i);
-            if (lane == 0 && page >= 0)
-              tma_load_page(ring + s * C::kSlotBytes + i * p.box_rows * 128, &tm_k, &full[s], h,
-                            in_page, w.r.h, page);
-          }
-        }
-      };
-      auto copy_v = [&](const Walk& w, const Pages& g) {
-        const int v_chunks = v_boxes == 1 ? C::kPieces : 1;         // of one copy
-        for (int h = 0; h < C::kPieces; ++h, ++it) {
-          int n = 0;
-          for (int i = 0; i < v_boxes; ++i)
-            n += __shfl_sync(0xffffffffu, g.page, (h * C::kVKeys + i * v_rows) / p.box_rows) >= 0;
-          const int s = next_slot(n * C::kPieces * v_rows * 128);
-          if (!ok) return;
-          for (int i = 0; i < v_boxes; ++i) {
-            const int row = h * C::kVKeys + i * v_rows;             // of the block
-            const int from = row / p.box_rows;
-            const int page = __shfl_sync(0xffffffffu, g.page, from);
-            const int in_page = __shfl_sync(0xffffffffu, g.in_page, from) + row - from * p.box_rows;
-            if (lane == 0 && page >= 0)
-              for (int ch = 0; ch < C::kPieces; ch += v_chunks)
-                tma_load_page(ring + s * C::kSlotBytes + ch * C::kVChunk + i * v_rows * 128, &tm_v,
-                              &full[s], ch, in_page, w.r.h, page);
-          }
-        }
-      };
-      // in the order of the products: with one tile V0 after K1, with two after K0
-      constexpr int kAhead = kTiles == 1 ? 2 : 1;
-      Pages ahead = look_up(kc), held[kAhead];
-      for (int i = 0; ok && (kc.more() || vc.more()); ++i) {
-        Pages now = ahead;
-        if (now.key >= 0) {
-          now.page = static_cast<int>(checked_page(now.entry, a.cache.pages, a.err));
-          now.in_page = now.key % a.cache.page_size;
-        }
-        const Walk kw = kc.w;
-        const bool k_left = kc.more();
+      int key, entry = look_up(kc, key);
+      for (int i = 0; ok && (kc.live || vc.live); ++i) {
+        // the pages of block i, for its K now and its V kAhead turns on
+        const bool k_left = kc.live;
         if (k_left) {
-          kc.next(p);
-          ahead = look_up(kc);
+          if (lane < 8) {
+            int2 g = make_int2(-1, 0);
+            if (key >= 0) {
+              g.x = static_cast<int>(checked_page(entry, a.cache.pages, a.err));
+              g.y = key % a.cache.page_size;
+            }
+            pages[i % kHeld][lane] = g;
+          }
+          __syncwarp();
         }
+        const int head = kc.it.h;
+        if (k_left) {
+          kc.next(items);
+          __syncwarp();
+          entry = look_up(kc, key);
+        }
+        if (lane == 0) {
+          if (i >= kAhead) {
+            const int2* g = pages[(i - kAhead) % kHeld];
+#pragma unroll 1
+            for (int h = 0; h < C::kPieces; ++h) {
+              // copies of this slot: those that begin before the length
+              int n = 0;
+#pragma unroll 1
+              for (int j = 0; j < v_boxes; ++j)
+                n += g[(h * C::kVKeys + (j << v_shift)) >> shift].x >= 0;
+              next_slot(n * C::kVChunks << (v_shift + 7));
+              if (!ok) break;
+              uint8_t* slot = ring + at.slot * C::kSlotBytes;
+#pragma unroll 1
+              for (int j = 0; j < v_boxes; ++j) {
+                const int row = h * C::kVKeys + (j << v_shift);
+                const int2 e = g[row >> shift];
+                if (e.x < 0) break;
+#pragma unroll 1
+                for (int ch = 0; ch < C::kVChunks; ch += v_chunks)
+                  tma_load_page(slot + ch * C::kVChunk + (j << (v_shift + 7)), &tm_v,
+                                &full[at.slot], ch, e.y + (row & ((1 << shift) - 1)), vc.it.h,
+                                e.x);
+              }
+              at.next();
+            }
+          }
+          if (ok && k_left) {
+            const int2* g = pages[i % kHeld];
+            int n = 0;
+#pragma unroll 1
+            while (n < k_boxes && g[n].x >= 0) ++n;
+#pragma unroll 1
+            for (int h = 0; h < C::kPieces; ++h) {
+              next_slot(n * C::kKChunks << (shift + 7));
+              if (!ok) break;
+              uint8_t* slot = ring + at.slot * C::kSlotBytes;
+#pragma unroll 1
+              for (int j = 0; j < n; ++j)
+#pragma unroll 1
+                for (int ch = 0; ch < C::kKChunks; ++ch)
+                  tma_load_page(slot + ch * C::kKChunk + (j << (shift + 7)), &tm_k,
+                                &full[at.slot], h * C::kKChunks + ch, g[j].y, head, g[j].x);
+              at.next();
+            }
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
         if (i >= kAhead) {
-          copy_v(vc.w, held[0]);
-          vc.next(p);
+          const int was = vc.item;
+          const bool moved = vc.next(items);
+          __syncwarp();
+          if (moved && lane == 0) items.release(was);
         }
-        if (ok && k_left) copy_k(kw, now);
-        if (kAhead == 2) held[0] = held[kAhead - 1];
-        held[kAhead - 1] = now;
       }
-      for (int i = max(0, it - C::kSlots); i < it; ++i) {
-        volatile int no_abort = 0;
-        if (!mbar_wait(&full[i % C::kSlots], (i / C::kSlots) & 1, &no_abort))
-          atomicOr(a.err, NVFP4_ATTENTION_TIMEOUT);
-      }
+      // every copy has landed before the block may end: walk back over them
+      if (lane == 0)
+        for (int i = 0; i < turns; ++i) {
+          if (at.slot == 0) at.slot = C::kSlots, at.par ^= 1u;
+          --at.slot;
+          volatile int no_abort = 0;
+          if (!wait(&full[at.slot], at.par, &no_abort)) atomicOr(a.err, NVFP4_ATTENTION_TIMEOUT);
+        }
+      __syncwarp();
     } else if (warp == 10 && !kE4m3) {
       // ---------------------------------------------- V rows not all rows see
-      Steps<1> kc(range, p), vc(range, p);
-      int it = 0;
+      Place kc, vc;
+      kc.start(items);
+      vc.start(items);
+      __syncwarp();
+      Ring<C::kSlots> at;
       constexpr int kAhead = kTiles == 1 ? 2 : 1;
-      for (int i = 0; kc.more() || vc.more(); ++i) {
+      for (int i = 0; kc.live || vc.live; ++i) {
         if (i >= kAhead) {
-          const Walk& w = vc.w;
-          const int seen = tile_keys(w.seq, w.r.tile, p.plan);
-          const int least = least_of(w);
-          for (int h = 0; h < C::kPieces; ++h, ++it) {
-            const int key0 = (w.r.unit0 + vc.b) * kN + h * C::kVKeys;
-            const int s = it % C::kSlots;
-            mbar_wait(&full[s], (it / C::kSlots) & 1, abort_flag);
+          const int seen = vc.it.seen(p.plan), least = vc.it.least();
+#pragma unroll 1
+          for (int h = 0; h < C::kPieces; ++h, at.next()) {
+            const int key0 = vc.it.key0 + vc.b * kN + h * C::kVKeys;
+            const int s = at.slot;
+            wait(&full[s], at.par, abort_flag);
             __syncwarp();
             if (key0 + C::kVKeys > least) {
               // 16-byte pieces of the rows from `lo` on: the first `look` of them
               // are looked at, the others zeroed
-              constexpr int kPer = C::kPieces * 8;
+              constexpr int kPer = C::kVChunks * 8;
               const int lo = max(0, least - key0);
               const int look = (min(max(seen - key0, lo), C::kVKeys) - lo) * kPer;
               uint8_t* slot = ring + s * C::kSlotBytes;
@@ -671,7 +827,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
                                                 (lo + j / kPer) * 128 + (j & 7) * 16);
               };
               bool bad = false;
-#pragma unroll 4
+#pragma unroll 2
               for (int j = lane; j < look; j += 32) {
                 uint4 v = *at(j);
                 if (non_finite<kE4m3>(v.x) || non_finite<kE4m3>(v.y) || non_finite<kE4m3>(v.z) ||
@@ -682,7 +838,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
                   *at(j) = v;
                 }
               }
-#pragma unroll 4
+#pragma unroll 2
               for (int j = look + lane; j < (C::kVKeys - lo) * kPer; j += 32)
                 *at(j) = make_uint4(0, 0, 0, 0);
               if (bad) dirty[vc.item % kDirty] = vc.item + 1;
@@ -691,40 +847,46 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
             }
             if (lane == 0) mbar_arrive(&checked[s]);
           }
-          vc.next(p);
+          const int was = vc.item;
+          const bool moved = vc.next(items);
+          __syncwarp();
+          if (moved && lane == 0) items.release(was);
         }
-        if (kc.more()) {
+        if (kc.live) {
           // nothing to check in K, but a phase of `checked` goes with every
           // turn of the slot, and follows the turn's copy
-          for (int h = 0; h < C::kPieces; ++h, ++it) {
-            const int s = it % C::kSlots;
-            mbar_wait(&full[s], (it / C::kSlots) & 1, abort_flag);
+#pragma unroll 1
+          for (int h = 0; h < C::kPieces; ++h, at.next()) {
+            wait(&full[at.slot], at.par, abort_flag);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&checked[s]);
+            if (lane == 0) mbar_arrive(&checked[at.slot]);
           }
-          kc.next(p);
+          kc.next(items);
+          __syncwarp();
         }
       }
     } else if (!kE4m3) {
-      // --------------------------------------------------------- Q copies
+      // ------------------------------------------- the schedule, and Q copies
       if (lane == 0) {
         int item = 0;
         const int rows = p.tile_tokens * a.group;
-        for (Walk w(range, a.seqs, p.plan, a.err); w.more();
-             w.next(a.seqs, a.cache.heads, p.plan, a.err), ++item) {
-          if (item > 0 && !mbar_wait(q_empty, (item - 1) & 1, abort_flag)) break;
+        Walk w(range, a.seqs, p.plan, a.err);
+        while (publish(w, item)) {
+          if (item > 0 && !wait(q_empty, (item - 1) & 1, abort_flag)) break;
           mbar_arrive_expect_tx(q_full, kTiles * (kDim / 64) * rows * 128);
           const int t0 = w.seq.q0 + w.r.tile * p.plan.tile_tokens;
-#pragma unroll
+#pragma unroll 1
           for (int x = 0; x < kTiles; ++x)
-#pragma unroll
+#pragma unroll 1
             for (int ch = 0; ch < kDim / 64; ++ch)
               tma_load_3d(q_sm + x * C::kQTile + ch * kM * 128, &tm_q, q_full, ch * 64,
                           w.r.h * a.group, t0 + x * p.tile_tokens);
+          w.next(a.seqs, a.cache.heads, p.plan, a.err);
+          ++item;
         }
         if (item > 0) {
           volatile int no_abort = 0;
-          if (!mbar_wait(q_full, (item - 1) & 1, &no_abort)) atomicOr(a.err, NVFP4_ATTENTION_TIMEOUT);
+          if (!wait(q_full, (item - 1) & 1, &no_abort)) atomicOr(a.err, NVFP4_ATTENTION_TIMEOUT);
         }
       }
       __syncwarp();
@@ -732,11 +894,19 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
       // ---------------------------------- Q rows scaled to f16 (warps 8, 10, 11)
       const int part = warp == 8 ? 0 : warp - 9;
       constexpr int kWords = kDim / 64;             // 32-bit words per lane
-      int item = 0;
-      for (Walk w(range, a.seqs, p.plan, a.err); w.more();
-           w.next(a.seqs, a.cache.heads, p.plan, a.err), ++item) {
+      Walk w(range, a.seqs, p.plan, a.err);         // warp 11: the schedule
+      if (warp == 11 && lane == 0) publish(w, 0);
+      __syncwarp();
+      Item it;
+      for (int item = 0; items.get(item, it); ++item) {
+        __syncwarp();
+        if (warp == 11) {
+          w.next(a.seqs, a.cache.heads, p.plan, a.err);
+          if (lane == 0) publish(w, item + 1);
+          __syncwarp();
+        }
         if (item > 0) {
-          mbar_wait(q_empty, (item - 1) & 1, abort_flag);
+          wait(q_empty, (item - 1) & 1, abort_flag);
           __syncwarp();
         }
         constexpr int kAtOnce = 4;
@@ -746,10 +916,10 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
           for (int i = 0; i < kAtOnce; ++i) {
             const int r = r0 + i, x = r / kM, rr = r % kM;
             const int tok = rr / a.group, gi = rr - tok * a.group;
-            const int ti = w.r.tile * p.plan.tile_tokens + x * p.tile_tokens + tok;
-            const bool valid = tok < p.tile_tokens && ti < w.seq.q_len;
+            const int ti = it.tok0 + x * p.tile_tokens + tok;
+            const bool valid = tok < p.tile_tokens && ti < it.q_len;
             const uint32_t* src = reinterpret_cast<const uint32_t*>(
-                a.q.data + int64_t(w.seq.q0 + ti) * a.q.ts + int64_t(w.r.h * a.group + gi) * a.q.hs);
+                a.q.data + int64_t(it.q0 + ti) * a.q.ts + int64_t(it.h * a.group + gi) * a.q.hs);
 #pragma unroll
             for (int k = 0; k < kWords; ++k) v[i][k] = valid ? src[k * 32 + lane] : 0u;
           }
@@ -779,7 +949,10 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(q_full);
+        if (lane == 0) {
+          mbar_arrive(q_full);
+          if (warp != 11) items.release(item);
+        }
       }
     }
   } else {
@@ -787,34 +960,47 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
     if constexpr (kE4m3) {
       regs_dec<96>();
       const int tid = threadIdx.x - 384;            // 0..127
-      constexpr int kPasses = 4;                    // 16 codes a thread each
+      constexpr int kPasses = C::kSlotBytes / 4096; // 16 codes a thread each
       int64_t* row_at = reinterpret_cast<int64_t*>(fixed + C::kRowOff);   // [2][128], then V's
-      Steps<1> kc(range, p), vc(range, p);
-      int it = 0;
+      Place kc, vc;
+      kc.start(items);
+      vc.start(items);
+      __syncwarp();
+      Ring<C::kSlots> ring_at;
+      int turns = 0;
+      uint32_t widen_par = 0;
+      auto meet = [&]() {                             // the four warps
+        __syncwarp();
+        if (lane == 0) mbar_arrive(widen);
+        wait(widen, widen_par, abort_flag);
+        __syncwarp();
+        widen_par ^= 1u;
+      };
       constexpr int kAhead = kTiles == 1 ? 2 : 1;
-      auto fill = [&](auto values, const Steps<1>& st, const int64_t* rows, const uint8_t* base) {
+      auto fill = [&](auto values, const Place& st, const int64_t* rows, const uint8_t* base) {
         constexpr bool kV = decltype(values)::value;
-        constexpr int kPerRow = kV ? kDim / 16 : 4;          // threads of a row
+        constexpr int kPerRow = kV ? kDim / 16 : C::kKChunks * 4;   // threads of a row
         constexpr int kRowsAtOnce = 128 / kPerRow;
         const int my_row = tid / kPerRow, my_col = (tid % kPerRow) * 16;
-        const Walk& w = st.w;
-        const int seen = tile_keys(w.seq, w.r.tile, p.plan);
-        const int least = least_of(w);
-        for (int h = 0; h < C::kPieces; ++h, ++it) {
-          const int s = it % C::kSlots;
+        const int seen = st.it.seen(p.plan), least = st.it.least();
+#pragma unroll 1
+        for (int h = 0; h < C::kPieces; ++h, ring_at.next()) {
+          const int s = ring_at.slot;
           uint4 v[kPasses];
 #pragma unroll
           for (int i = 0; i < kPasses; ++i) {
             const int64_t at = rows[(kV ? h * C::kVKeys : 0) + i * kRowsAtOnce + my_row];
             v[i] = make_uint4(0, 0, 0, 0);
             if (at >= 0)                                      // else: a row past the length
-              v[i] = *reinterpret_cast<const uint4*>(base + at + (kV ? 0 : h * 64) + my_col);
+              v[i] = *reinterpret_cast<const uint4*>(base + at + (kV ? 0 : h * C::kKChunks * 64) + my_col);
           }
-          if (it >= C::kSlots) {
-            mbar_wait(&empty[s], ((it / C::kSlots) & 1) ^ 1, abort_flag);
+          if (turns == C::kSlots) {
+            wait(&empty[s], ring_at.par ^ 1, abort_flag);
             __syncwarp();
+          } else {
+            ++turns;
           }
-          const int key0 = (w.r.unit0 + st.b) * kN + (kV ? h * C::kVKeys : 0);
+          const int key0 = st.it.key0 + st.b * kN + (kV ? h * C::kVKeys : 0);
           const bool check = kV && key0 + C::kVKeys > least;
           bool bad = false;
 #pragma unroll
@@ -838,7 +1024,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
               }
             }
             // 16 codes: two 16-byte pieces of the 128-byte row
-            uint8_t* row = ring + s * C::kSlotBytes + (kV ? (my_col >> 6) * C::kVChunk : 0) + r * 128;
+            uint8_t* row = ring + s * C::kSlotBytes + (my_col >> 6) * (kV ? C::kVChunk : C::kKChunk) + r * 128;
             const int c16 = (my_col & 63) >> 3;
             *reinterpret_cast<uint4*>(row + ((c16 ^ (r & 7)) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
             *reinterpret_cast<uint4*>(row + (((c16 + 1) ^ (r & 7)) << 4)) =
@@ -851,31 +1037,34 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
         }
       };
       // row offsets of a block, by one thread per row
-      auto lookup = [&](const Steps<1>& st, const int64_t (&strides)[3], int64_t* rows) {
-        const Walk& w = st.w;
-        const int key = (w.r.unit0 + st.b) * kN + tid;
+      auto lookup = [&](const Place& st, const int64_t (&strides)[3], int64_t* rows) {
+        const int key = st.it.key0 + st.b * kN + tid;
         int64_t at = -1;
-        if (key < w.seq.kv_len) {
-          const int64_t page = checked_page(
-              a.seqs.table[int64_t(w.r.s) * a.seqs.width + key / a.cache.page_size], a.cache.pages,
-              a.err);
+        if (key < st.it.kv_len) {
+          const int64_t page =
+              checked_page(a.seqs.table[int64_t(st.it.s) * a.seqs.width + key / a.cache.page_size],
+                           a.cache.pages, a.err);
           if (page != a.cache.pages)
-            at = page * strides[0] + key % a.cache.page_size * strides[1] + w.r.h * strides[2];
+            at = page * strides[0] + key % a.cache.page_size * strides[1] + st.it.h * strides[2];
         }
-        asm volatile("bar.sync 2, 128;" ::: "memory");    // the rows before are read
+        meet();                                       // the rows before are read
         rows[tid] = at;
-        asm volatile("bar.sync 2, 128;" ::: "memory");
+        meet();
       };
-      for (int i = 0; kc.more() || vc.more(); ++i) {
+      for (int i = 0; kc.live || vc.live; ++i) {
         if (i >= kAhead) {
           lookup(vc, a.cache.vs, row_at + kN);
           fill(std::true_type{}, vc, row_at + kN, static_cast<const uint8_t*>(a.cache.v));
-          vc.next(p);
+          const int was = vc.item;
+          const bool moved = vc.next(items);
+          __syncwarp();
+          if (moved && lane == 0) items.release(was);
         }
-        if (kc.more()) {
+        if (kc.live) {
           lookup(kc, a.cache.ks, row_at);
           fill(std::false_type{}, kc, row_at, static_cast<const uint8_t*>(a.cache.k));
-          kc.next(p);
+          kc.next(items);
+          __syncwarp();
         }
       }
     }
@@ -907,14 +1096,15 @@ int run(const Attend& a, const Device& d, cudaStream_t stream) {
   }
   if (const int st = allow_smem(kernel, C::kSmem, d, ready)) return st;
   TcParams p{a, {}, Parts(a.workspace, d.num_sms, kM, kTiles, kDim), kM / a.group, 0};
-  p.plan = Plan{kTiles * p.tile_tokens, kN, 1};
-  p.box_rows = 16;
-  while (p.box_rows < kN && a.cache.page_size % (2 * p.box_rows) == 0) p.box_rows *= 2;
+  p.plan = Plan{kTiles * p.tile_tokens, kBlockShift, 1};
+  p.box_shift = 4;
+  while (p.box_shift < 7 && a.cache.page_size % (2 << p.box_shift) == 0) ++p.box_shift;
+  const int box = 1 << p.box_shift;
   CUtensorMap tm_q{}, tm_k{}, tm_v{};
   if (!kE4m3 && (!query_map(&tm_q, a, p.tile_tokens) ||
-                 !page_map(&tm_k, a.cache, false, 64, p.box_rows, 1) ||
-                 !page_map(&tm_v, a.cache, true, 64, std::min(p.box_rows, C::kVKeys),
-                           p.box_rows >= C::kVKeys ? C::kPieces : 1)))
+                 !page_map(&tm_k, a.cache, false, 64, box, 1) ||
+                 !page_map(&tm_v, a.cache, true, 64, std::min(box, C::kVKeys),
+                           box >= C::kVKeys ? C::kVChunks : 1)))
     return NVFP4_ERR_LAUNCH;
   if (const int st = launch(kernel, dim3(d.num_sms), dim3(C::kThreads), C::kSmem, stream, tm_q,
                             tm_k, tm_v, p))

@@ -32,7 +32,8 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kConsumers = kWarps * 32;
 constexpr int kThreads = kConsumers + 32;
-constexpr int kUnit = 16;                     // keys of one warp in a block
+constexpr int kUnitShift = 4;
+constexpr int kUnit = 1 << kUnitShift;        // keys of one warp in a block
 constexpr int kSlotKeys = 64;
 constexpr int kPPitch = 128 * 2 + 16;         // bytes of a row of weights
 
@@ -183,8 +184,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<kDim, kE4m3, kR>::kCtas)
   }
   griddep_wait();
   griddep_launch_dependents();
-  const Range range = find_range(p.seqs, p.cache.heads, plan, static_cast<int>(blockIdx.x),
-                                 static_cast<int>(gridDim.x), range_sm, p.err);
+  const Range range = find_range(p.seqs, p.cache.heads, plan, blockIdx.x,
+                                 gridDim.x, range_sm, p.err);
   Walk w(range, p.seqs, plan, p.err);
 
   if (warp == kWarps) {
@@ -215,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<kDim, kE4m3, kR>::kCtas)
           const int slot = it % C::kSlots;
           if (it >= C::kSlots)
             ok = __all_sync(0xffffffffu,
-                            mbar_wait(&empty[slot], ((it / C::kSlots) & 1) ^ 1, abort_flag));
+                            wait(&empty[slot], ((it / C::kSlots) & 1) ^ 1, abort_flag));
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(&full[slot], units * kUnit * C::kRowBytes);
           // one lane issues: a copy's operands are warp-uniform registers, and
@@ -233,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<kDim, kE4m3, kR>::kCtas)
     // every copy has landed before the block may end
     for (int i = max(0, it - C::kSlots); i < it; ++i) {
       volatile int no_abort = 0;
-      if (!mbar_wait(&full[i % C::kSlots], (i / C::kSlots) & 1, &no_abort))
+      if (!wait(&full[i % C::kSlots], (i / C::kSlots) & 1, &no_abort))
         atomicOr(p.err, NVFP4_ATTENTION_TIMEOUT);
     }
   } else {
@@ -345,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<kDim, kE4m3, kR>::kCtas)
             for (int i = 0; i < 4; ++i) s[rt][j][i] = 0.f;
         if (warp < n) {
           const int si = it + (warp >> 2);
-          mbar_wait(&full[si % C::kSlots], (si / C::kSlots) & 1, abort_flag);
+          wait(&full[si % C::kSlots], (si / C::kSlots) & 1, abort_flag);
           __syncwarp();
           const uint32_t base = ring + (si % C::kSlots) * C::kSlotBytes +
                                 (warp & 3) * C::kUnitBytes;
@@ -475,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<kDim, kE4m3, kR>::kCtas)
         // ---- P V for this warp's columns
         for (int half = 0; half < slots; ++half) {
           const int si = it + slots + half;
-          mbar_wait(&full[si % C::kSlots], (si / C::kSlots) & 1, abort_flag);
+          wait(&full[si % C::kSlots], (si / C::kSlots) & 1, abort_flag);
           __syncwarp();
           const uint32_t base = ring + (si % C::kSlots) * C::kSlotBytes;
 #pragma unroll
@@ -674,7 +675,7 @@ int run(const Attend& p, const Device& d, cudaStream_t stream) {
   if (!page_map(&tm_k, p.cache, false, inner, kUnit, C::kChunks) ||
       !page_map(&tm_v, p.cache, true, inner, kUnit, C::kChunks))
     return NVFP4_ERR_LAUNCH;
-  const Plan plan{std::max(1, C::kRows / p.group), kUnit, 4};
+  const Plan plan{std::max(1, C::kRows / p.group), kUnitShift, 4};
   const int ctas = d.num_sms * C::kCtas;
   const Parts parts(p.workspace, ctas, C::kRows, 1, kDim);
   if (const int st = launch(kernel, dim3(ctas), dim3(kThreads), C::kSmem, stream, tm_k, tm_v, p,

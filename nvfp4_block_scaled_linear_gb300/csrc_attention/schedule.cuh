@@ -18,7 +18,7 @@ constexpr int kMaxBatches = 256;            // of 32 sequences
 
 struct Plan {
   int tile_tokens;                          // tokens of one tile
-  int unit;                                 // keys of one unit
+  int unit_shift;                           // log2 of the keys of one unit
   int min_units;                            // least units worth a CTA of its own
 };
 
@@ -33,7 +33,7 @@ __device__ __forceinline__ int tile_keys(const SeqInfo& s, int tile, const Plan&
 }
 
 __device__ __forceinline__ int tile_units(const SeqInfo& s, int tile, const Plan& p) {
-  return max(1, (tile_keys(s, tile, p) + p.unit - 1) / p.unit);
+  return max(1, (tile_keys(s, tile, p) + (1 << p.unit_shift) - 1) >> p.unit_shift);
 }
 
 // Units of one head of each lane's sequence, all lanes of the warp together.
@@ -47,7 +47,9 @@ __device__ __forceinline__ int64_t seq_units(const SeqInfo& s, const Plan& p) {
     const SeqInfo o{__shfl_sync(0xffffffffu, s.q0, src), __shfl_sync(0xffffffffu, s.q_len, src),
                     __shfl_sync(0xffffffffu, s.kv_len, src)};
     int64_t sum = 0;
-    for (int i = lane; i < tiles_of(o, p); i += 32) sum += tile_units(o, i, p);
+    const int tiles = tiles_of(o, p);
+#pragma unroll 1
+    for (int i = lane; i < tiles; i += 32) sum += tile_units(o, i, p);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     if (lane == src) u = sum;
@@ -77,7 +79,7 @@ struct RangeSmem {
 };
 
 // The range of CTA `cta` of `ctas`, found by all threads of the block.
-__device__ inline Range find_range(const Seqs& q, int heads, const Plan& p, int cta, int ctas,
+__device__ inline Range find_range(const Seqs& q, int heads, const Plan& p, uint32_t cta, uint32_t ctas,
                                    RangeSmem* sm, unsigned int* err) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int warps = blockDim.x >> 5, batches = (q.count + 31) / 32;
@@ -85,6 +87,7 @@ __device__ inline Range find_range(const Seqs& q, int heads, const Plan& p, int 
     const int s = b * 32 + lane;
     return s < q.count ? load_seq(q, s, err) : SeqInfo{0, 0, 0};
   };
+#pragma unroll 1
   for (int b = warp; b < batches; b += warps) {
     const int64_t sum = warp_inclusive(seq_units(lane_seq(b), p));
     if (lane == 31) sm->batch[b] = sum * heads;
@@ -92,17 +95,23 @@ __device__ inline Range find_range(const Seqs& q, int heads, const Plan& p, int 
   __syncthreads();
   if (warp == 0) {
     int64_t total = 0;
+#pragma unroll 1
     for (int b = lane; b < batches; b += 32) total += sm->batch[b];
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
     // the units in equal shares, over no more CTAs than min_units leaves work for
-    const int64_t used = min(int64_t(ctas), max(int64_t(1), total / p.min_units));
-    const int64_t begin = cta < used ? total * cta / used : total;
-    const int64_t end = cta < used ? total * (cta + 1) / used : total;
+    const uint32_t used = total >= int64_t(ctas) * p.min_units
+                              ? ctas
+                              : max(1u, static_cast<uint32_t>(total) / p.min_units);
+    const int64_t share = total >> 32 ? total / used : static_cast<uint32_t>(total) / used;
+    const int64_t extra = total - share * used;         // of them take one more
+    const int64_t begin = share * cta + min(int64_t(cta), extra);
+    const int64_t end = begin + (cta < used ? share + (cta < extra) : 0);
     Range r{end - begin, 0, 0, 0, 0};
     if (r.left > 0) {
       int64_t at = begin;
       int b = 0;
+#pragma unroll 1
       while (at >= sm->batch[b]) at -= sm->batch[b++];
       const SeqInfo mine = lane_seq(b);
       const int64_t one = seq_units(mine, p);
@@ -114,10 +123,12 @@ __device__ inline Range find_range(const Seqs& q, int heads, const Plan& p, int 
                       __shfl_sync(0xffffffffu, mine.q_len, src),
                       __shfl_sync(0xffffffffu, mine.kv_len, src)};
       r.s = b * 32 + src;
-      r.h = static_cast<int>(at / per_head);
-      at -= r.h * per_head;
+#pragma unroll 1
+      for (; at >= per_head; at -= per_head) ++r.h;
+      const int tiles = tiles_of(o, p);
+#pragma unroll 1
       for (int t0 = 0;; t0 += 32) {
-        const int u = t0 + lane < tiles_of(o, p) ? tile_units(o, t0 + lane, p) : 0;
+        const int u = t0 + lane < tiles ? tile_units(o, t0 + lane, p) : 0;
         const int64_t sum = warp_inclusive(u);
         const unsigned past = __ballot_sync(0xffffffffu, sum > at);
         if (past) {
