@@ -23,12 +23,11 @@
 // tile, and beside them the shared-memory traffic of their operands (Q and K
 // each read per product, V once, plus the copies that bring K and V).
 //
-// Warps: 0-3 and 4-7 softmax and output; 8 K/V copies; 9 MMA; 10 the check of
-// V rows that not every row of the tile sees (or that lie past the length:
-// zeroed, as 0 times what a page happens to hold need not be 0); 11 Q copies.
-// Over an e4m3 cache warps 12-15 widen K and V to f16 (exact) on their way to
-// shared memory and do warp 10's work as they go, and warps 8, 10 and 11 bring
-// Q, scaled per row by a power of two (attend_warp.cu says why), in f16.
+// Warps: 0-3 and 4-7 softmax and output; 8 and 10 the copies of K and of V; 9
+// MMA; 11 the schedule and the copies of Q.  Over an e4m3 cache warps 12-15
+// widen K and V to f16 (exact) on their way to shared memory, and warps 8, 10
+// and 11 bring Q, scaled per row by a power of two (attend_warp.cu says why),
+// in f16.
 //
 // A V value that is not finite and that only some rows of the tile see would
 // reach the others as 0 * NaN: it is replaced by zero before the product and
@@ -65,18 +64,21 @@ struct Cfg {
   static constexpr int kQTile = kM * kDim * 2;
   static constexpr int kQBytes = kTiles * kQTile;
   static constexpr int kMaxSlots = 8;
-  static constexpr int kBars = 3 * kMaxSlots + 21 + 2 * kItems;
+  static constexpr int kBars = 2 * kMaxSlots + 23 + 2 * kItems;
   static constexpr int kBarOff = 0;
-  static constexpr int kItemOff = (kBarOff + kBars * 8 + 8 + kDirty * 4 + 15) / 16 * 16;  // descriptors
+  static constexpr int kItemOff = (kBarOff + kBars * 8 + 16 + kDirty * 4 + 15) / 16 * 16;  // descriptors
   static constexpr int kMaxOff = kItemOff + kItems * 32;                                   // running maxima
   static constexpr int kSumOff = kMaxOff + (kTiles == 1 ? kM * 4 : 0);        // row sums
   static constexpr int kFacOff = kSumOff + (kTiles == 1 ? kM * 4 : 0);    // Q row factors
   static constexpr int kRowOff = kFacOff + (kE4m3 ? kQFactors * kTiles * kM * 4 : 0);
-  static constexpr int kFixed = kRowOff + (kE4m3 ? 2 * kN * 8 : 4 * 8 * 8);
+  static constexpr int kFixed = kRowOff + (kE4m3 ? 2 * kN * 8 : 0);
   static constexpr int kBudget = 227 * 1024 - 1024 - kFixed - kQBytes;
   static constexpr int kSlots = std::min(kMaxSlots, kBudget / kSlotBytes);
   static constexpr int kSmem = kQBytes + kSlots * kSlotBytes + kFixed + 1024;
-  static_assert(kSlots >= 2 * kPieces, "K and V of one block have to fit");
+  // K and V have rings of their own, since different warps fill them.  K slots
+  // come free, and are filled again, while V is in use, and V's while K is.
+  static constexpr int kKSlots = kSlots / 2, kVSlots = kSlots - kKSlots;
+  static_assert(kKSlots >= kPieces, "K and V of one block have to fit");
   static_assert(kSlots * kSlotBytes >= static_cast<int>(sizeof(RangeSmem)), "scratch of the start");
   // TMEM columns: the accumulators, then the two score buffers
   static constexpr uint32_t kO = 0;
@@ -185,13 +187,14 @@ __device__ __forceinline__ uint32_t finite_mask(uint32_t w) {
   return ((w & e) == e ? 0u : 0xFFFFu) | ((w & (e << 16)) == (e << 16) ? 0u : 0xFFFF0000u);
 }
 
-// A position in the ring of slots, and the parity of its turn.
-template <int kSlots>
+// A position in a ring of slots, of which the first is `kFirst`, and the parity
+// of its turn.
+template <int kFirst, int kSlots>
 struct Ring {
-  int slot = 0;
+  int slot = kFirst;
   uint32_t par = 0;
   __device__ void next() {
-    if (++slot == kSlots) slot = 0, par ^= 1u;
+    if (++slot == kFirst + kSlots) slot = kFirst, par ^= 1u;
   }
 };
 
@@ -256,6 +259,11 @@ struct Place {
   }
 };
 
+template <class C>
+using KRing = Ring<0, C::kKSlots>;
+template <class C>
+using VRing = Ring<C::kKSlots, C::kVSlots>;
+
 template <int kDim, bool kE4m3, int kTiles>
 __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
     attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -268,8 +276,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
   uint8_t* fixed = ring + C::kSlots * C::kSlotBytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(fixed + C::kBarOff);
   uint64_t* empty = full + C::kMaxSlots;
-  uint64_t* checked = empty + C::kMaxSlots;       // slot looked over by warp 10 (bf16)
-  uint64_t* s_full = checked + C::kMaxSlots;      // [2] scores in buffer x
+  uint64_t* s_full = empty + C::kMaxSlots;        // [2] scores in buffer x
   uint64_t* p_full = s_full + 2;                  // [2] weights in buffer x
   uint64_t* pv_done = p_full + 2;                 // [2] product with buffer x's weights
   uint64_t* o_free = pv_done + 2;                 // [2] accumulator read out
@@ -279,11 +286,13 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
   uint64_t* mma_done = q_empty + 1;               // every product issued has completed
   uint64_t* pair = mma_done + 1;                  // both softmax groups (kTiles == 1)
   uint64_t* widen = pair + 1;                     // the widening warps (e4m3)
-  const Items items{reinterpret_cast<Item*>(fixed + C::kItemOff), widen + 1, widen + 1 + kItems,
+  uint64_t* v_known = widen + 1;                  // [2] v_slot[x] is that of buffer x's block
+  const Items items{reinterpret_cast<Item*>(fixed + C::kItemOff), v_known + 2, v_known + 2 + kItems,
                     reinterpret_cast<volatile int*>(full + C::kBars)};
   volatile int* abort_flag = reinterpret_cast<volatile int*>(full + C::kBars);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(full + C::kBars) + 1;
-  volatile int* dirty = reinterpret_cast<volatile int*>(full + C::kBars) + 2;  // item ordinal + 1
+  volatile int* v_slot = reinterpret_cast<volatile int*>(full + C::kBars) + 2; // [2] slot, parity << 8
+  volatile int* dirty = v_slot + 2;               // [kDirty] item ordinal + 1
   float* run_max = reinterpret_cast<float*>(fixed + C::kMaxOff);
   float* row_sum = reinterpret_cast<float*>(fixed + C::kSumOff);
   float* q_factor = reinterpret_cast<float*>(fixed + C::kFacOff);
@@ -294,12 +303,12 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(&full[i], kE4m3 ? 4 : 1);
       mbar_init(&empty[i], 1);
-      mbar_init(&checked[i], 1);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&s_full[x], 1);
       mbar_init(&p_full[x], 4);
       mbar_init(&pv_done[x], 1);
+      mbar_init(&v_known[x], 1);
       mbar_init(&o_free[x], kTiles == 1 ? 8 : 4);
       for (int i = 0; i < 4; ++i) mbar_init(&m_ready[x * 4 + i], 1);
     }
@@ -349,6 +358,120 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
     items.ring[i % kItems] = it;
     mbar_arrive(&items.full[i % kItems]);
     return w.more();
+  };
+
+  // The V rows of block b that not all rows of the tile see, a quarter of each
+  // slot by each warp of the group that gives the block's weights: rows that
+  // none sees become zero (0 times what a page happens to hold past the length
+  // need not be 0), and values that are not finite do; whether there were any.
+  auto check_v = [&](const Item& it, int b, int at, int quad) {
+    constexpr int kPer = C::kVChunks * 8;                   // 16-byte pieces of a row
+    constexpr int kRows = C::kVKeys / 4;
+    const int least = it.least(), seen = it.seen(p.plan);
+    VRing<C> r;
+    r.slot = at & 255, r.par = at >> 8;
+    bool bad = false;
+#pragma unroll 1
+    for (int h = 0; h < C::kPieces; ++h, r.next()) {
+      wait(&full[r.slot], r.par, abort_flag);
+      __syncwarp();
+      const int row0 = quad * kRows;
+      const int key0 = it.key0 + b * kN + h * C::kVKeys + row0;
+#pragma unroll 1
+      for (int j = lane + max(0, least - key0) * kPer; j < kRows * kPer; j += 32) {
+        uint4* at16 = reinterpret_cast<uint4*>(ring + r.slot * C::kSlotBytes +
+                                               (j % kPer >> 3) * C::kVChunk +
+                                               (row0 + j / kPer) * 128 + (j & 7) * 16);
+        if (key0 + j / kPer >= seen) {
+          *at16 = make_uint4(0, 0, 0, 0);
+          continue;
+        }
+        uint4 v = *at16;
+        if (!(non_finite<kE4m3>(v.x) || non_finite<kE4m3>(v.y) || non_finite<kE4m3>(v.z) ||
+              non_finite<kE4m3>(v.w)))
+          continue;
+        bad = true;
+        v.x &= finite_mask<kE4m3>(v.x), v.y &= finite_mask<kE4m3>(v.y);
+        v.z &= finite_mask<kE4m3>(v.z), v.w &= finite_mask<kE4m3>(v.w);
+        *at16 = v;
+      }
+    }
+    fence_proxy_async_smem();
+    return bad;
+  };
+
+  // One warp for the copies of K, one for those of V.  Each lane keeps the
+  // operands of one copy of a block (piece, rows, chunks), its page read one
+  // block ahead, so that a slot costs a wait and an issue: one warp's dependent
+  // instructions are what the copies would otherwise wait for.
+  auto copy_pages = [&](auto values) {
+    constexpr bool kV = decltype(values)::value;
+    constexpr int kRows = kV ? C::kVKeys : kN;              // of a slot
+    constexpr int kChunks = kV ? C::kVChunks : C::kKChunks; // of a slot
+    constexpr int kRowShift = kRows == 128 ? 7 : 6;
+    const CUtensorMap* map = kV ? &tm_v : &tm_k;
+    const int shift = min(p.box_shift, kRowShift);          // log2 of the rows of a copy
+    const int boxes = kRows >> shift;
+    const int at_once = kV && boxes == 1 ? kChunks : 1;     // chunks of a copy
+    // lane: copy (box, chunk) of each slot; of V also the slot, whose keys differ
+    const int per_slot = boxes * (kChunks / at_once);
+    const int piece = kV ? lane / per_slot : 0;
+    const int box = lane % per_slot / (kChunks / at_once);
+    const int chunk = lane % (kChunks / at_once) * at_once;
+    const bool has_copy = lane < (kV ? C::kPieces : 1) * per_slot;
+    const int row = (kV ? piece * kRows : 0) + (box << shift);
+    const uint32_t dst = chunk * (kRows * 128) + (box << (shift + 7));
+    const uint32_t bytes = at_once << (shift + 7);
+    Place at;
+    at.start(items);
+    __syncwarp();
+    std::conditional_t<kV, VRing<C>, KRing<C>> r;
+    constexpr int kTurns = kV ? C::kVSlots : C::kKSlots;
+    int turns = 0;                                          // slots filled, up to kTurns
+    bool ok = true;
+    int key = 0, entry = 0;
+    auto look_up = [&]() {
+      key = at.it.key0 + at.b * kN + row;
+      if (at.live && has_copy && key < at.it.kv_len)
+        entry = a.seqs.table[int64_t(at.it.s) * a.seqs.width + key / a.cache.page_size];
+      else
+        key = -1;
+    };
+    look_up();
+    while (ok && at.live) {
+      int page = -1, in_page = 0;
+      if (key >= 0) {
+        page = static_cast<int>(checked_page(entry, a.cache.pages, a.err));
+        in_page = key % a.cache.page_size;
+      }
+      const int head = at.it.h, was = at.item;
+      const bool moved = at.next(items);
+      __syncwarp();
+      if (moved && lane == 0) items.release(was);
+      look_up();
+      for (int h = 0; h < C::kPieces; ++h, r.next()) {
+        const bool mine = page >= 0 && (!kV || piece == h);
+        const int n = __popc(__ballot_sync(0xffffffffu, mine));
+        if (turns == kTurns)
+          ok = __all_sync(0xffffffffu, wait(&empty[r.slot], r.par ^ 1, abort_flag));
+        else
+          ++turns;
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&full[r.slot], n * bytes);
+        __syncwarp();
+        if (mine)
+          tma_load_page(ring + r.slot * C::kSlotBytes + dst, map, &full[r.slot],
+                        (kV ? 0 : h * kChunks) + chunk, in_page, head, page);
+      }
+    }
+    // every copy has landed before the block may end
+    const int first = kV ? C::kKSlots : 0;
+    for (int s = first; s < first + turns; ++s) {
+      volatile int no_abort = 0;
+      if (!wait(&full[s], s < r.slot ? r.par : r.par ^ 1, &no_abort))
+        atomicOr(a.err, NVFP4_ATTENTION_TIMEOUT);
+    }
+    __syncwarp();
   };
 
   if (warp < 8) {
@@ -470,6 +593,11 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
         sum[0] = add2(sum[0], sum[1]);
         l += sum[0].x + sum[0].y;
         tmem_st_wait();
+        if (!kE4m3 && (kTiles == 1 || x == 0) && it.key0 + (b + 1) * kN > it.least()) {
+          wait(&v_known[x], uses & 1, abort_flag);
+          __syncwarp();
+          if (check_v(it, b, v_slot[x], quad)) dirty[item % kDirty] = item + 1;
+        }
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[x]);
@@ -591,32 +719,36 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
         const uint32_t q_lo = desc_lo(smem_addr(q_sm), 0);
         const uint32_t k_lo = desc_lo(smem_addr(ring), 0);
         const uint32_t v_lo = desc_lo(smem_addr(ring), C::kVChunk);
-        uint64_t* v_bar = kE4m3 ? full : checked;
         Place qk, pv;                             // of the scores, of the products with V
         int qk_x = 0, pv_x = 0;                   // and the tile (kTiles == 2)
         qk.start(items);
         pv.start(items);
-        Ring<C::kSlots> at, at_k, at_v;           // in the order of the copies; of the K and V in use
+        KRing<C> k_next, at_k;                    // of the next block; of the one in use
+        VRing<C> v_next, at_v;
         bool ok = true;
         for (int i = 0; ok && (qk.live || pv.live); ++i) {
           const int x = i & 1;
           const uint32_t t_s = tmem + C::kS + x * kN;
           if (i >= 2) {
             // ---- O += P V, two steps behind
+            if (pv_x == 0) {
+              at_v = v_next;
+#pragma unroll
+              for (int h = 0; h < C::kPieces; ++h) v_next.next();
+              if (!kE4m3) {
+                v_slot[x] = at_v.slot | static_cast<int>(at_v.par) << 8;
+                mbar_arrive(&v_known[x]);
+              }
+            }
             ok = wait(&p_full[x], (i - 2) >> 1 & 1, abort_flag);
             const bool fresh = pv.first();
             if (ok && fresh && pv.item > 0)
               ok = wait(&o_free[kTiles == 1 ? 0 : x], (pv.item - 1) & 1, abort_flag);
-            if (pv_x == 0) {
-              at_v = at;
-#pragma unroll
-              for (int h = 0; h < C::kPieces; ++h) at.next();
-            }
             const uint32_t t_o = tmem + C::kO + (kTiles == 2 ? x * kDim : 0);
-            Ring<C::kSlots> r = at_v;
+            VRing<C> r = at_v;
 #pragma unroll
             for (int h = 0; h < C::kPieces; ++h, r.next()) {
-              ok = ok && wait(&v_bar[r.slot], r.par, abort_flag);
+              ok = ok && wait(&full[r.slot], r.par, abort_flag);
               if (!ok) break;
               tc_fence_after_sync();
               const uint32_t v = v_lo + r.slot * (C::kSlotBytes >> 4);
@@ -640,11 +772,11 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
             // ---- S = Q K^T
             if (qk.first() && qk_x == 0) ok = wait(q_full, qk.item & 1, abort_flag);
             if (qk_x == 0) {
-              at_k = at;
+              at_k = k_next;
 #pragma unroll
-              for (int h = 0; h < C::kPieces; ++h) at.next();
+              for (int h = 0; h < C::kPieces; ++h) k_next.next();
             }
-            Ring<C::kSlots> r = at_k;
+            KRing<C> r = at_k;
             const uint32_t q = q_lo + (kTiles == 2 ? x * (C::kQTile >> 4) : 0);
 #pragma unroll
             for (int h = 0; h < C::kPieces; ++h, r.next()) {
@@ -678,193 +810,9 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
       }
       __syncwarp();
     } else if (warp == 8 && !kE4m3) {
-      // ------------------------------------------------------ K, V copies
-      // The warp looks up a block's pages together, one block ahead (lane i:
-      // the copy of rows i << box_shift on); lane 0 alone issues, since a
-      // copy's operands are warp-uniform registers (copies from several lanes
-      // took some 250 cycles each), and its steps are kept few: one warp's
-      // dependent instructions are what the copies would otherwise wait for.
-      Place kc, vc;
-      kc.start(items);
-      vc.start(items);
-      __syncwarp();
-      Ring<C::kSlots> at;
-      bool ok = true;
-      int turns = 0;                              // slots filled, up to kSlots
-      const int shift = p.box_shift, k_boxes = kN >> shift;
-      constexpr int kVShift = C::kVKeys == 128 ? 7 : 6;
-      const int v_shift = min(shift, kVShift), v_boxes = 1 << (kVShift - v_shift);
-      const int v_chunks = v_boxes == 1 ? C::kVChunks : 1;          // of one copy
-      constexpr int kAhead = kTiles == 1 ? 2 : 1;
-      constexpr int kHeld = 4;
-      int2(*pages)[8] = reinterpret_cast<int2(*)[8]>(fixed + C::kRowOff);   // [kHeld]
-      auto look_up = [&](const Place& at, int& key) {
-        key = at.it.key0 + at.b * kN + (lane << shift);
-        if (!at.live || lane >= k_boxes || key >= at.it.kv_len) {
-          key = -1;
-          return 0;
-        }
-        return a.seqs.table[int64_t(at.it.s) * a.seqs.width + key / a.cache.page_size];
-      };
-      auto next_slot = [&](uint32_t bytes) {
-        if (turns == C::kSlots)
-          ok = wait(&empty[at.slot], at.par ^ 1, abort_flag);
-        else
-          ++turns;
-        if (ok) mbar_arrive_expect_tx(&full[at.slot], bytes);
-      };
-      int key, entry = look_up(kc, key);
-      for (int i = 0; ok && (kc.live || vc.live); ++i) {
-        // the pages of block i, for its K now and its V kAhead turns on
-        const bool k_left = kc.live;
-        if (k_left) {
-          if (lane < 8) {
-            int2 g = make_int2(-1, 0);
-            if (key >= 0) {
-              g.x = static_cast<int>(checked_page(entry, a.cache.pages, a.err));
-              g.y = key % a.cache.page_size;
-            }
-            pages[i % kHeld][lane] = g;
-          }
-          __syncwarp();
-        }
-        const int head = kc.it.h;
-        if (k_left) {
-          kc.next(items);
-          __syncwarp();
-          entry = look_up(kc, key);
-        }
-        if (lane == 0) {
-          if (i >= kAhead) {
-            const int2* g = pages[(i - kAhead) % kHeld];
-#pragma unroll 1
-            for (int h = 0; h < C::kPieces; ++h) {
-              // copies of this slot: those that begin before the length
-              int n = 0;
-#pragma unroll 1
-              for (int j = 0; j < v_boxes; ++j)
-                n += g[(h * C::kVKeys + (j << v_shift)) >> shift].x >= 0;
-              next_slot(n * C::kVChunks << (v_shift + 7));
-              if (!ok) break;
-              uint8_t* slot = ring + at.slot * C::kSlotBytes;
-#pragma unroll 1
-              for (int j = 0; j < v_boxes; ++j) {
-                const int row = h * C::kVKeys + (j << v_shift);
-                const int2 e = g[row >> shift];
-                if (e.x < 0) break;
-#pragma unroll 1
-                for (int ch = 0; ch < C::kVChunks; ch += v_chunks)
-                  tma_load_page(slot + ch * C::kVChunk + (j << (v_shift + 7)), &tm_v,
-                                &full[at.slot], ch, e.y + (row & ((1 << shift) - 1)), vc.it.h,
-                                e.x);
-              }
-              at.next();
-            }
-          }
-          if (ok && k_left) {
-            const int2* g = pages[i % kHeld];
-            int n = 0;
-#pragma unroll 1
-            while (n < k_boxes && g[n].x >= 0) ++n;
-#pragma unroll 1
-            for (int h = 0; h < C::kPieces; ++h) {
-              next_slot(n * C::kKChunks << (shift + 7));
-              if (!ok) break;
-              uint8_t* slot = ring + at.slot * C::kSlotBytes;
-#pragma unroll 1
-              for (int j = 0; j < n; ++j)
-#pragma unroll 1
-                for (int ch = 0; ch < C::kKChunks; ++ch)
-                  tma_load_page(slot + ch * C::kKChunk + (j << (shift + 7)), &tm_k,
-                                &full[at.slot], h * C::kKChunks + ch, g[j].y, head, g[j].x);
-              at.next();
-            }
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (i >= kAhead) {
-          const int was = vc.item;
-          const bool moved = vc.next(items);
-          __syncwarp();
-          if (moved && lane == 0) items.release(was);
-        }
-      }
-      // every copy has landed before the block may end: walk back over them
-      if (lane == 0)
-        for (int i = 0; i < turns; ++i) {
-          if (at.slot == 0) at.slot = C::kSlots, at.par ^= 1u;
-          --at.slot;
-          volatile int no_abort = 0;
-          if (!wait(&full[at.slot], at.par, &no_abort)) atomicOr(a.err, NVFP4_ATTENTION_TIMEOUT);
-        }
-      __syncwarp();
+      copy_pages(std::false_type{});
     } else if (warp == 10 && !kE4m3) {
-      // ---------------------------------------------- V rows not all rows see
-      Place kc, vc;
-      kc.start(items);
-      vc.start(items);
-      __syncwarp();
-      Ring<C::kSlots> at;
-      constexpr int kAhead = kTiles == 1 ? 2 : 1;
-      for (int i = 0; kc.live || vc.live; ++i) {
-        if (i >= kAhead) {
-          const int seen = vc.it.seen(p.plan), least = vc.it.least();
-#pragma unroll 1
-          for (int h = 0; h < C::kPieces; ++h, at.next()) {
-            const int key0 = vc.it.key0 + vc.b * kN + h * C::kVKeys;
-            const int s = at.slot;
-            wait(&full[s], at.par, abort_flag);
-            __syncwarp();
-            if (key0 + C::kVKeys > least) {
-              // 16-byte pieces of the rows from `lo` on: the first `look` of them
-              // are looked at, the others zeroed
-              constexpr int kPer = C::kVChunks * 8;
-              const int lo = max(0, least - key0);
-              const int look = (min(max(seen - key0, lo), C::kVKeys) - lo) * kPer;
-              uint8_t* slot = ring + s * C::kSlotBytes;
-              auto at = [&](int j) {
-                return reinterpret_cast<uint4*>(slot + (j % kPer >> 3) * C::kVChunk +
-                                                (lo + j / kPer) * 128 + (j & 7) * 16);
-              };
-              bool bad = false;
-#pragma unroll 2
-              for (int j = lane; j < look; j += 32) {
-                uint4 v = *at(j);
-                if (non_finite<kE4m3>(v.x) || non_finite<kE4m3>(v.y) || non_finite<kE4m3>(v.z) ||
-                    non_finite<kE4m3>(v.w)) {
-                  bad = true;
-                  v.x &= finite_mask<kE4m3>(v.x), v.y &= finite_mask<kE4m3>(v.y);
-                  v.z &= finite_mask<kE4m3>(v.z), v.w &= finite_mask<kE4m3>(v.w);
-                  *at(j) = v;
-                }
-              }
-#pragma unroll 2
-              for (int j = look + lane; j < (C::kVKeys - lo) * kPer; j += 32)
-                *at(j) = make_uint4(0, 0, 0, 0);
-              if (bad) dirty[vc.item % kDirty] = vc.item + 1;
-              fence_proxy_async_smem();
-              __syncwarp();
-            }
-            if (lane == 0) mbar_arrive(&checked[s]);
-          }
-          const int was = vc.item;
-          const bool moved = vc.next(items);
-          __syncwarp();
-          if (moved && lane == 0) items.release(was);
-        }
-        if (kc.live) {
-          // nothing to check in K, but a phase of `checked` goes with every
-          // turn of the slot, and follows the turn's copy
-#pragma unroll 1
-          for (int h = 0; h < C::kPieces; ++h, at.next()) {
-            wait(&full[at.slot], at.par, abort_flag);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&checked[at.slot]);
-          }
-          kc.next(items);
-          __syncwarp();
-        }
-      }
+      copy_pages(std::true_type{});
     } else if (!kE4m3) {
       // ------------------------------------------- the schedule, and Q copies
       if (lane == 0) {
@@ -966,8 +914,9 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
       kc.start(items);
       vc.start(items);
       __syncwarp();
-      Ring<C::kSlots> ring_at;
-      int turns = 0;
+      KRing<C> k_at;
+      VRing<C> v_at;
+      int k_turns = 0, v_turns = 0;                   // slots filled, up to the ring's
       uint32_t widen_par = 0;
       auto meet = [&]() {                             // the four warps
         __syncwarp();
@@ -977,7 +926,8 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
         widen_par ^= 1u;
       };
       constexpr int kAhead = kTiles == 1 ? 2 : 1;
-      auto fill = [&](auto values, const Place& st, const int64_t* rows, const uint8_t* base) {
+      auto fill = [&](auto values, auto& ring_at, int& turns, const Place& st, const int64_t* rows,
+                      const uint8_t* base) {
         constexpr bool kV = decltype(values)::value;
         constexpr int kPerRow = kV ? kDim / 16 : C::kKChunks * 4;   // threads of a row
         constexpr int kRowsAtOnce = 128 / kPerRow;
@@ -994,7 +944,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
             if (at >= 0)                                      // else: a row past the length
               v[i] = *reinterpret_cast<const uint4*>(base + at + (kV ? 0 : h * C::kKChunks * 64) + my_col);
           }
-          if (turns == C::kSlots) {
+          if (turns == (kV ? C::kVSlots : C::kKSlots)) {
             wait(&empty[s], ring_at.par ^ 1, abort_flag);
             __syncwarp();
           } else {
@@ -1054,7 +1004,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
       for (int i = 0; kc.live || vc.live; ++i) {
         if (i >= kAhead) {
           lookup(vc, a.cache.vs, row_at + kN);
-          fill(std::true_type{}, vc, row_at + kN, static_cast<const uint8_t*>(a.cache.v));
+          fill(std::true_type{}, v_at, v_turns, vc, row_at + kN, static_cast<const uint8_t*>(a.cache.v));
           const int was = vc.item;
           const bool moved = vc.next(items);
           __syncwarp();
@@ -1062,7 +1012,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
         }
         if (kc.live) {
           lookup(kc, a.cache.ks, row_at);
-          fill(std::false_type{}, kc, row_at, static_cast<const uint8_t*>(a.cache.k));
+          fill(std::false_type{}, k_at, k_turns, kc, row_at, static_cast<const uint8_t*>(a.cache.k));
           kc.next(items);
           __syncwarp();
         }
