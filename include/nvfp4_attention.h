@@ -132,7 +132,7 @@ int nvfp4_qk_norm_rope(const nvfp4_heads* q, const nvfp4_heads* k, const nvfp4_h
  *   q, out       bf16 [tokens, q_heads, head_dim] heads; q_heads a multiple
  *                of cache->kv_heads, at most 128 times it.
  *   lse          fp32 [tokens, q_heads], or NULL.
- *   workspace    16-byte aligned device memory of at least
+ *   workspace    32-byte aligned device memory of at least
  *                nvfp4_paged_attention_workspace() bytes; its contents need
  *                no set-up and mean nothing between calls, but calls that
  *                may overlap on the GPU need one each.

@@ -227,7 +227,7 @@ int nvfp4_paged_attention(const nvfp4_heads* q, int64_t tokens, int32_t q_heads,
   if (const int st = check_heads(q, tokens, q_heads)) return st;
   if (const int st = check_heads(out, tokens, q_heads)) return st;
   if (!workspace) return NVFP4_ERR_INVALID;
-  if (misaligned(workspace)) return NVFP4_ERR_MISALIGNED;
+  if (reinterpret_cast<uintptr_t>(workspace) & 31u) return NVFP4_ERR_MISALIGNED;
   Device d;
   if (const int st = device(&d)) return st;
   if (workspace_bytes < attend_workspace(cache->head_dim, d)) return NVFP4_ERR_TOO_LARGE;

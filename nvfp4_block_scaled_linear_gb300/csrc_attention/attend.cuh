@@ -13,6 +13,7 @@ namespace attn {
 // `abort_flag` set and false returned.  Little code, since it is inlined in
 // every role of kernels that have to stay within the instruction cache.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
   const uint32_t t0 = static_cast<uint32_t>(clock());
 #pragma unroll 1
   while (!mbar_try_wait(bar, parity)) {
@@ -34,15 +35,25 @@ bool page_map(CUtensorMap* map, const Cache& c, bool values, int inner, int rows
 // elements by one group of heads by `tokens` tokens.
 bool query_map(CUtensorMap* map, const Attend& a, int tokens);
 
+// kCluster = 2: into both CTAs of the pair, each told on its own barrier.
+template <int kCluster = 1>
 __device__ __forceinline__ void tma_load_page(void* dst, const CUtensorMap* map, uint64_t* bar,
                                               int32_t chunk, int32_t slot, int32_t head,
                                               int32_t page) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_addr(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(0), "r"(slot), "r"(chunk),
-      "r"(head), "r"(page)
-      : "memory");
+  if (kCluster == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(0), "r"(slot), "r"(chunk),
+        "r"(head), "r"(page)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".multicast::cluster [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(0), "r"(slot), "r"(chunk),
+        "r"(head), "r"(page), "h"(static_cast<uint16_t>((1 << kCluster) - 1))
+        : "memory");
 }
 
 // rows: query rows of one key/value head in the longest sequence, at most 64.

@@ -15,6 +15,11 @@
 // kTiles = 2 (head_dim 64, 128): the buffers hold two tiles on the same
 // block, which halves the copies per product.
 //
+// kCluster = 2 (head_dim 256, more than one tile of rows): two CTAs take two
+// adjacent tiles of an item through the same blocks, each copying half of every
+// slot into both.  One tile alone wants 64 bytes a clock from L2 on every SM
+// to keep the tensor core busy, about what the L2 gives all SMs together.
+//
 // The accumulator is rescaled only when a row's maximum has grown by more
 // than 2^8 since the last time (weights stay below 2^8, and the sums are
 // fp32), which after the first blocks is rare.
@@ -49,7 +54,7 @@ constexpr int kItems = 4;                     // item descriptors in flight
 constexpr int kQFactors = 4;                  // items whose row factors are held
 constexpr int kDirty = 8;                     // items whose `dirty` note is held: more than the ring's
 
-template <int kDim, bool kE4m3, int kTiles>
+template <int kDim, bool kE4m3, int kTiles, int kCluster>
 struct Cfg {
   static constexpr int kThreads = kE4m3 ? 512 : 384;
   // A slot holds up to 32 KB: 128 of head_dim of all keys of a K block, or all
@@ -64,7 +69,7 @@ struct Cfg {
   static constexpr int kQTile = kM * kDim * 2;
   static constexpr int kQBytes = kTiles * kQTile;
   static constexpr int kMaxSlots = 8;
-  static constexpr int kBars = 2 * kMaxSlots + 23 + 2 * kItems;
+  static constexpr int kBars = 2 * kMaxSlots + 25 + 2 * kItems;
   static constexpr int kBarOff = 0;
   static constexpr int kItemOff = (kBarOff + kBars * 8 + 16 + kDirty * 4 + 15) / 16 * 16;  // descriptors
   static constexpr int kMaxOff = kItemOff + kItems * 32;                                   // running maxima
@@ -84,6 +89,7 @@ struct Cfg {
   static constexpr uint32_t kO = 0;
   static constexpr uint32_t kS = kTiles * kDim;
   static_assert(kS + 2 * kN <= 512, "TMEM");
+  static_assert(kCluster == 1 || (!kE4m3 && kTiles == 1), "pairs of CTAs");
 };
 
 // Shared-memory matrix descriptors, 128-byte swizzled rows, 8-row groups 1024
@@ -92,7 +98,7 @@ struct Cfg {
 // of the next 64 columns.  Advancing along k adds to the low word.
 constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
-  return (addr >> 4) | (lbo >> 4) << 16;
+  return (addr >> 4 & 0x3FFFu) | (lbo >> 4) << 16;   // (the CTA's number is above)
 }
 __device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t id,
                                         uint32_t accumulate) {
@@ -147,6 +153,28 @@ __device__ __forceinline__ void tmem_st_16cols(uint32_t taddr, const uint32_t (&
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+
+// umma_commit on the barrier at this place in every CTA of the cluster.
+template <int kCluster>
+__device__ __forceinline__ void commit_empty(uint64_t* bar) {
+  if (kCluster == 1) {
+    umma_commit(bar);
+  } else {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;" ::"r"(smem_addr(bar)),
+        "h"(static_cast<uint16_t>((1 << kCluster) - 1))
+        : "memory");
+  }
+}
+
+// One 32-byte store (a whole sector): the rows of a warp's lanes lie far apart,
+// and two 16-byte halves would be two transactions.
+__device__ __forceinline__ void st_global_32(void* at, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 template <int kRegs>
@@ -264,12 +292,12 @@ using KRing = Ring<0, C::kKSlots>;
 template <class C>
 using VRing = Ring<C::kKSlots, C::kVSlots>;
 
-template <int kDim, bool kE4m3, int kTiles>
-__global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
+template <int kDim, bool kE4m3, int kTiles, int kCluster>
+__global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 1)
     attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
                      const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const TcParams p) {
-  using C = Cfg<kDim, kE4m3, kTiles>;
+  using C = Cfg<kDim, kE4m3, kTiles, kCluster>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* q_sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   uint8_t* ring = q_sm + C::kQBytes;
@@ -277,8 +305,8 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(fixed + C::kBarOff);
   uint64_t* empty = full + C::kMaxSlots;
   uint64_t* s_full = empty + C::kMaxSlots;        // [2] scores in buffer x
-  uint64_t* p_full = s_full + 2;                  // [2] weights in buffer x
-  uint64_t* pv_done = p_full + 2;                 // [2] product with buffer x's weights
+  uint64_t* p_full = s_full + 2;                  // [2][2] weights in buffer x, by halves of the keys
+  uint64_t* pv_done = p_full + 4;                 // [2] product with buffer x's weights
   uint64_t* o_free = pv_done + 2;                 // [2] accumulator read out
   uint64_t* m_ready = o_free + 2;                 // [2][4] running maximum handed on, per warp
   uint64_t* q_full = m_ready + 8;
@@ -302,11 +330,12 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(&full[i], kE4m3 ? 4 : 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], kCluster);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&s_full[x], 1);
-      mbar_init(&p_full[x], 4);
+      mbar_init(&p_full[2 * x], 4);
+      mbar_init(&p_full[2 * x + 1], 4);
       mbar_init(&pv_done[x], 1);
       mbar_init(&v_known[x], 1);
       mbar_init(&o_free[x], kTiles == 1 ? 8 : 4);
@@ -337,13 +366,17 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
   }
   griddep_wait();
   griddep_launch_dependents();
+  // the CTA's (or the pair's) number, and its tile of the item
+  const uint32_t unit = blockIdx.x / kCluster;
+  const int rank = kCluster == 2 ? static_cast<int>(cluster_ctarank()) : 0;
   // the range, in scratch that the ring's first copies will overwrite
   const Range range =
-      find_range(a.seqs, a.cache.heads, p.plan, blockIdx.x,
-                 gridDim.x, reinterpret_cast<RangeSmem*>(ring), a.err);
+      find_range(a.seqs, a.cache.heads, p.plan, unit, gridDim.x / kCluster,
+                 reinterpret_cast<RangeSmem*>(ring), a.err);
   fence_proxy_async_smem();
   tc_fence_before_sync();
   __syncthreads();
+  if (kCluster == 2) cluster_sync();               // the other CTA's barriers are set up
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
 
@@ -412,7 +445,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
     const CUtensorMap* map = kV ? &tm_v : &tm_k;
     const int shift = min(p.box_shift, kRowShift);          // log2 of the rows of a copy
     const int boxes = kRows >> shift;
-    const int at_once = kV && boxes == 1 ? kChunks : 1;     // chunks of a copy
+    const int at_once = kV && boxes == 1 ? kChunks / kCluster : 1;   // chunks of a copy
     // lane: copy (box, chunk) of each slot; of V also the slot, whose keys differ
     const int per_slot = boxes * (kChunks / at_once);
     const int piece = kV ? lane / per_slot : 0;
@@ -450,8 +483,9 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
       if (moved && lane == 0) items.release(was);
       look_up();
       for (int h = 0; h < C::kPieces; ++h, r.next()) {
-        const bool mine = page >= 0 && (!kV || piece == h);
-        const int n = __popc(__ballot_sync(0xffffffffu, mine));
+        const bool some = page >= 0 && (!kV || piece == h);
+        const bool mine = some && (kCluster == 1 || chunk / at_once % 2 == rank);
+        const int n = __popc(__ballot_sync(0xffffffffu, some));
         if (turns == kTurns)
           ok = __all_sync(0xffffffffu, wait(&empty[r.slot], r.par ^ 1, abort_flag));
         else
@@ -460,8 +494,8 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
         if (lane == 0) mbar_arrive_expect_tx(&full[r.slot], n * bytes);
         __syncwarp();
         if (mine)
-          tma_load_page(ring + r.slot * C::kSlotBytes + dst, map, &full[r.slot],
-                        (kV ? 0 : h * kChunks) + chunk, in_page, head, page);
+          tma_load_page<kCluster>(ring + r.slot * C::kSlotBytes + dst, map, &full[r.slot],
+                                  (kV ? 0 : h * kChunks) + chunk, in_page, head, page);
       }
     }
     // every copy has landed before the block may end
@@ -498,7 +532,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
     Item it;
     for (int item = 0; items.get(item, it); ++item) {
       __syncwarp();
-      const int ti = it.tok0 + (kTiles == 2 ? x * p.tile_tokens : 0) + tok;
+      const int ti = it.tok0 + (kTiles == 2 ? x : rank) * p.tile_tokens + tok;
       const bool valid = tok < p.tile_tokens && ti < it.q_len;
       const int lim = valid ? max(0, it.kv_len - it.q_len + ti + 1) : 0;
       const int count = it.count();
@@ -507,6 +541,12 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
       float m = -INFINITY, l = 0.f;                   // of the blocks that this thread saw
       for (int b = 0; b < count; ++b, ++step) {
         if (kTiles == 1 && (step & 1) != x) continue;
+        float prev = m;                               // the maximum before this block
+        if (kTiles == 1 && b > 0) {
+          wait(&m_ready[(x ^ 1) * 4 + quad], ((step - 1) >> 1) & 1, abort_flag);
+          __syncwarp();
+          prev = run_max[row];
+        }
         wait(&s_full[x], uses & 1, abort_flag);
         __syncwarp();
         tc_fence_after_sync();
@@ -536,12 +576,6 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
         // ---- the maximum the weights are taken against
         float now = top;
         if (b > 0) {
-          float prev = m;
-          if (kTiles == 1) {
-            wait(&m_ready[(x ^ 1) * 4 + quad], ((step - 1) >> 1) & 1, abort_flag);
-            __syncwarp();
-            prev = run_max[row];
-          }
           now = fmaxf(prev, top);
           if (__any_sync(0xffffffffu, now - prev > kSlack)) {
             // the accumulator, complete up to the block before
@@ -574,7 +608,12 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
         const float base = now == -INFINITY ? 0.f : now;
         if (m != now) l *= m == -INFINITY ? 0.f : ex2(m - base);
         m = now;
-        // ---- the weights
+        if (!kE4m3 && (kTiles == 1 || x == 0) && it.key0 + (b + 1) * kN > it.least()) {
+          wait(&v_known[x], uses & 1, abort_flag);
+          __syncwarp();
+          if (check_v(it, b, v_slot[x], quad)) dirty[item % kDirty] = item + 1;
+        }
+        // ---- the weights, handed over by halves
         const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -589,18 +628,15 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
             w16[j] = kE4m3 ? f32x2_to_f16x2(e.x, e.y) : f32x2_to_bf16x2(e.x, e.y);
           }
           tmem_st_16cols(t_s + i * 16, w16);
+          if (i & 1) {
+            tmem_st_wait();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[2 * x + (i >> 1)]);
+          }
         }
         sum[0] = add2(sum[0], sum[1]);
         l += sum[0].x + sum[0].y;
-        tmem_st_wait();
-        if (!kE4m3 && (kTiles == 1 || x == 0) && it.key0 + (b + 1) * kN > it.least()) {
-          wait(&v_known[x], uses & 1, abort_flag);
-          __syncwarp();
-          if (check_v(it, b, v_slot[x], quad)) dirty[item % kDirty] = item + 1;
-        }
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[x]);
         ++uses;
       }
       // ---- the row's sum, and the result
@@ -632,8 +668,8 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
       const float inv = l == 0.f ? 0.f : vs / l;
       const int64_t token = it.q0 + ti;
       const int head = it.h * a.group + gi;
-      const int prow = (kTiles == 2 ? x * kM : 0) + row;
-      const int64_t at_part = p.parts.row(blockIdx.x, part, prow);
+      const int prow = (kTiles == 2 ? x : rank) * kM + row;
+      const int64_t at_part = p.parts.row(unit, part, prow);
       if (valid && (kTiles == 2 || x == 0)) {
         const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
         if (whole && a.lse) a.lse[token * a.q_heads + head] = lse2 * 0.693147180559945f;
@@ -657,23 +693,31 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * inv);
         if (whole) {
-          uint4* dst = reinterpret_cast<uint4*>(a.out.data + token * a.out.ts + head * a.out.hs + i);
+          __nv_bfloat16* dst = a.out.data + token * a.out.ts + head * a.out.hs + i;
+          if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t y[4];
+            for (int j = 0; j < 32; j += 16) {
+              uint32_t y[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              y[k] = f32x2_to_bf16x2(__uint_as_float(o[8 * j + 2 * k]),
-                                     __uint_as_float(o[8 * j + 2 * k + 1]));
-            dst[j] = make_uint4(y[0], y[1], y[2], y[3]);
+              for (int k = 0; k < 8; ++k)
+                y[k] = f32x2_to_bf16x2(__uint_as_float(o[j + 2 * k]), __uint_as_float(o[j + 2 * k + 1]));
+              st_global_32(dst + j, y);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8)
+              *reinterpret_cast<uint4*>(dst + j) =
+                  make_uint4(f32x2_to_bf16x2(__uint_as_float(o[j]), __uint_as_float(o[j + 1])),
+                             f32x2_to_bf16x2(__uint_as_float(o[j + 2]), __uint_as_float(o[j + 3])),
+                             f32x2_to_bf16x2(__uint_as_float(o[j + 4]), __uint_as_float(o[j + 5])),
+                             f32x2_to_bf16x2(__uint_as_float(o[j + 6]), __uint_as_float(o[j + 7])));
           }
         } else {
-          uint4* dst = reinterpret_cast<uint4*>(p.parts.out + at_part * kDim + i);
+          float* dst = p.parts.out + at_part * kDim + i;
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          for (int j = 0; j < 32; j += 8) st_global_32(dst + j, &o[j]);
         }
-        }
+  }
         __syncwarp();
       }
       if (fix && valid) {
@@ -705,105 +749,129 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
       __syncwarp();
       if (lane == 0) items.release(item);
     }
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0 && rank == 0) {
       note.x = flags;
-      p.parts.note[blockIdx.x] = note;
+      p.parts.note[unit] = note;
     }
   } else if (warp < 12) {
     if constexpr (kE4m3) regs_dec<72>(); else regs_dec<80>();
     if (warp == 9) {
       // ------------------------------------------------------------- MMA
-      if (lane == 0) {
-        const uint32_t id_s = idesc<kE4m3>(kN, false);
-        const uint32_t id_o = idesc<kE4m3>(kDim, true);
-        const uint32_t q_lo = desc_lo(smem_addr(q_sm), 0);
-        const uint32_t k_lo = desc_lo(smem_addr(ring), 0);
-        const uint32_t v_lo = desc_lo(smem_addr(ring), C::kVChunk);
-        Place qk, pv;                             // of the scores, of the products with V
-        int qk_x = 0, pv_x = 0;                   // and the tile (kTiles == 2)
-        qk.start(items);
-        pv.start(items);
-        KRing<C> k_next, at_k;                    // of the next block; of the one in use
-        VRing<C> v_next, at_v;
-        bool ok = true;
-        for (int i = 0; ok && (qk.live || pv.live); ++i) {
-          const int x = i & 1;
-          const uint32_t t_s = tmem + C::kS + x * kN;
-          if (i >= 2) {
-            // ---- O += P V, two steps behind
-            if (pv_x == 0) {
-              at_v = v_next;
+      // The warp keeps together and one lane issues, so that the operands stay in
+      // uniform registers; the MMA loops are short, to stay in the nearest
+      // instruction cache.
+      const uint32_t id_s = idesc<kE4m3>(kN, false);
+      const uint32_t id_o = idesc<kE4m3>(kDim, true);
+      const uint32_t q_lo = desc_lo(smem_addr(q_sm), 0);
+      const uint32_t k_lo = desc_lo(smem_addr(ring), 0);
+      const uint32_t v_lo = desc_lo(smem_addr(ring), C::kVChunk);
+      const bool lead = lane == 0;
+      Place qk, pv;                             // of the scores, of the products with V
+      int qk_x = 0, pv_x = 0;                   // and the tile (kTiles == 2)
+      qk.start(items);
+      pv.start(items);
+      KRing<C> k_next, at_k;                    // of the next block; of the one in use
+      VRing<C> v_next, at_v;
+      bool ok = true;
+      auto ready = [&](uint64_t* bar, uint32_t parity) {
+        ok = ok && __all_sync(0xffffffffu, wait(bar, parity, abort_flag));
+      };
+      for (int i = 0; ok && (qk.live || pv.live); ++i) {
+        const int x = i & 1;
+        const uint32_t t_s = tmem + C::kS + x * kN;
+        if (i >= 2) {
+          // ---- O += P V, two steps behind
+          if (pv_x == 0) {
+            at_v = v_next;
 #pragma unroll
-              for (int h = 0; h < C::kPieces; ++h) v_next.next();
-              if (!kE4m3) {
-                v_slot[x] = at_v.slot | static_cast<int>(at_v.par) << 8;
-                mbar_arrive(&v_known[x]);
-              }
-            }
-            ok = wait(&p_full[x], (i - 2) >> 1 & 1, abort_flag);
-            const bool fresh = pv.first();
-            if (ok && fresh && pv.item > 0)
-              ok = wait(&o_free[kTiles == 1 ? 0 : x], (pv.item - 1) & 1, abort_flag);
-            const uint32_t t_o = tmem + C::kO + (kTiles == 2 ? x * kDim : 0);
-            VRing<C> r = at_v;
-#pragma unroll
-            for (int h = 0; h < C::kPieces; ++h, r.next()) {
-              ok = ok && wait(&full[r.slot], r.par, abort_flag);
-              if (!ok) break;
-              tc_fence_after_sync();
-              const uint32_t v = v_lo + r.slot * (C::kSlotBytes >> 4);
-#pragma unroll
-              for (int kk = 0; kk < C::kVKeys / 16; ++kk)
-                umma_ts(t_o, t_s + (h * C::kVKeys / 16 + kk) * 8, v + kk * (2048 >> 4), id_o,
-                        !fresh || (h | kk) != 0);
-              if (kTiles == 1 || x == 1) umma_commit(&empty[r.slot]);
-            }
-            if (!ok) break;
-            umma_commit(&pv_done[x]);
-            if (kTiles == 2 && pv_x == 0) {
-              pv_x = 1;
-            } else {
-              pv_x = 0;
-              const int was = pv.item;
-              if (pv.next(items)) items.release(was);
+            for (int h = 0; h < C::kPieces; ++h) v_next.next();
+            if (!kE4m3 && lead) {
+              v_slot[x] = at_v.slot | static_cast<int>(at_v.par) << 8;
+              mbar_arrive(&v_known[x]);
             }
           }
-          if (qk.live) {
-            // ---- S = Q K^T
-            if (qk.first() && qk_x == 0) ok = wait(q_full, qk.item & 1, abort_flag);
-            if (qk_x == 0) {
-              at_k = k_next;
-#pragma unroll
-              for (int h = 0; h < C::kPieces; ++h) k_next.next();
-            }
-            KRing<C> r = at_k;
-            const uint32_t q = q_lo + (kTiles == 2 ? x * (C::kQTile >> 4) : 0);
-#pragma unroll
-            for (int h = 0; h < C::kPieces; ++h, r.next()) {
-              ok = ok && wait(&full[r.slot], r.par, abort_flag);
-              if (!ok) break;
-              tc_fence_after_sync();
-              const uint32_t k = k_lo + r.slot * (C::kSlotBytes >> 4);
-#pragma unroll
-              for (int kk = 0; kk < C::kKChunks * 4; ++kk) {
-                const uint32_t off = ((kk >> 2) * C::kKChunk + (kk & 3) * 32) >> 4;
-                umma_ss(t_s, q + ((h * C::kKChunks * C::kKChunk) >> 4) + off, k + off, id_s,
-                        (h | kk) != 0);
-              }
-              if (kTiles == 1 || x == 1) umma_commit(&empty[r.slot]);
-            }
+          const bool fresh = pv.first();
+          if (fresh && pv.item > 0) ready(&o_free[kTiles == 1 ? 0 : x], (pv.item - 1) & 1);
+          const uint32_t t_o = tmem + C::kO + (kTiles == 2 ? x * kDim : 0);
+          VRing<C> r = at_v;
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {               // of the keys
+            if (pv_x == 0 && (half == 0 || C::kPieces == 2) ) ready(&full[r.slot], r.par);
+            ready(&p_full[2 * x + half], (i - 2) >> 1 & 1);
             if (!ok) break;
-            umma_commit(&s_full[x]);
-            if (qk.last() && qk_x == kTiles - 1) umma_commit(q_empty);
-            if (kTiles == 2 && qk_x == 0) {
-              qk_x = 1;
-            } else {
-              qk_x = 0;
-              qk.next(items);
+            tc_fence_after_sync();
+            if (lead) {
+              uint32_t v = v_lo + r.slot * (C::kSlotBytes >> 4) +
+                           (C::kPieces == 2 ? 0 : half * (kN / 32) * (2048 >> 4));
+              uint32_t t_p = t_s + half * (kN / 4);
+              uint32_t acc = !fresh || half != 0;
+#pragma unroll 1
+              for (int kk = 0; kk < kN / 32; ++kk, v += 2048 >> 4, t_p += 8, acc = 1)
+                umma_ts(t_o, t_p, v, id_o, acc);
+              if ((kTiles == 1 || x == 1) && (half == 1 || C::kPieces == 2)) commit_empty<kCluster>(&empty[r.slot]);
+              if (half == 1) umma_commit(&pv_done[x]);
             }
+            __syncwarp();
+            if (C::kPieces == 2) r.next();
+          }
+          if (!ok) break;
+          if (kTiles == 2 && pv_x == 0) {
+            pv_x = 1;
+          } else {
+            pv_x = 0;
+            const int was = pv.item;
+            if (pv.next(items) && lead) items.release(was);
+            __syncwarp();
           }
         }
-        // nothing may be in flight when TMEM is released
+        if (qk.live) {
+          // ---- S = Q K^T
+          if (qk.first() && qk_x == 0) ready(q_full, qk.item & 1);
+          if (qk_x == 0) {
+            at_k = k_next;
+#pragma unroll
+            for (int h = 0; h < C::kPieces; ++h) k_next.next();
+          }
+          KRing<C> r = at_k;
+          const uint32_t q = q_lo + (kTiles == 2 ? x * (C::kQTile >> 4) : 0);
+          const bool last = qk.last() && qk_x == kTiles - 1;
+#pragma unroll 1
+          for (int h = 0; h < C::kPieces; ++h, r.next()) {
+            if (qk_x == 0) ready(&full[r.slot], r.par);
+            if (!ok) break;
+            tc_fence_after_sync();
+            if (lead) {
+              uint32_t k = k_lo + r.slot * (C::kSlotBytes >> 4);
+              uint32_t qh = q + h * ((C::kKChunks * C::kKChunk) >> 4);
+              uint32_t acc = h != 0;
+#pragma unroll 1
+              for (int ch = 0; ch < C::kKChunks; ++ch) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk, acc = 1)
+                  umma_ss(t_s, qh + kk * (32 >> 4), k + kk * (32 >> 4), id_s, acc);
+                qh += C::kKChunk >> 4;
+                k += C::kKChunk >> 4;
+              }
+              if (kTiles == 1 || x == 1) commit_empty<kCluster>(&empty[r.slot]);
+              if (h == C::kPieces - 1) {
+                umma_commit(&s_full[x]);
+                if (last) umma_commit(q_empty);
+              }
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          if (kTiles == 2 && qk_x == 0) {
+            qk_x = 1;
+          } else {
+            qk_x = 0;
+            qk.next(items);
+            __syncwarp();
+          }
+        }
+      }
+      // nothing may be in flight when TMEM is released
+      if (lead) {
         umma_commit(mma_done);
         volatile int no_abort = 0;
         if (!wait(mma_done, 0, &no_abort)) atomicOr(a.err, NVFP4_ATTENTION_TIMEOUT);
@@ -822,7 +890,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
         while (publish(w, item)) {
           if (item > 0 && !wait(q_empty, (item - 1) & 1, abort_flag)) break;
           mbar_arrive_expect_tx(q_full, kTiles * (kDim / 64) * rows * 128);
-          const int t0 = w.seq.q0 + w.r.tile * p.plan.tile_tokens;
+          const int t0 = w.seq.q0 + w.r.tile * p.plan.tile_tokens + rank * p.tile_tokens;
 #pragma unroll 1
           for (int x = 0; x < kTiles; ++x)
 #pragma unroll 1
@@ -1022,16 +1090,17 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
   if (*abort_flag && threadIdx.x == 0) atomicOr(a.err, NVFP4_ATTENTION_TIMEOUT);
   tc_fence_before_sync();
   __syncthreads();
+  if (kCluster == 2) cluster_sync();               // nothing of the other CTA's is on its way here
   if (warp == 9) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, 512);
   }
 }
 
-template <int kDim, bool kE4m3, int kTiles>
+template <int kDim, bool kE4m3, int kTiles, int kCluster>
 int run(const Attend& a, const Device& d, cudaStream_t stream) {
-  using C = Cfg<kDim, kE4m3, kTiles>;
-  auto* kernel = attend_tc_kernel<kDim, kE4m3, kTiles>;
+  using C = Cfg<kDim, kE4m3, kTiles, kCluster>;
+  auto* kernel = attend_tc_kernel<kDim, kE4m3, kTiles, kCluster>;
   static std::atomic<bool> ready[kMaxDevices];
   if (!ready[d.id].load(std::memory_order_acquire)) {
     // the warpgroups' shares (setmaxnreg) have to come out of what the block
@@ -1045,8 +1114,9 @@ int run(const Attend& a, const Device& d, cudaStream_t stream) {
     if (attr.numRegs * C::kThreads < need) return NVFP4_ERR_LAUNCH;
   }
   if (const int st = allow_smem(kernel, C::kSmem, d, ready)) return st;
-  TcParams p{a, {}, Parts(a.workspace, d.num_sms, kM, kTiles, kDim), kM / a.group, 0};
-  p.plan = Plan{kTiles * p.tile_tokens, kBlockShift, 1};
+  const int units = d.num_sms / kCluster;
+  TcParams p{a, {}, Parts(a.workspace, units, kM, kTiles * kCluster, kDim), kM / a.group, 0};
+  p.plan = Plan{kTiles * kCluster * p.tile_tokens, kBlockShift, 1};
   p.box_shift = 4;
   while (p.box_shift < 7 && a.cache.page_size % (2 << p.box_shift) == 0) ++p.box_shift;
   const int box = 1 << p.box_shift;
@@ -1054,26 +1124,30 @@ int run(const Attend& a, const Device& d, cudaStream_t stream) {
   if (!kE4m3 && (!query_map(&tm_q, a, p.tile_tokens) ||
                  !page_map(&tm_k, a.cache, false, 64, box, 1) ||
                  !page_map(&tm_v, a.cache, true, 64, std::min(box, C::kVKeys),
-                           box >= C::kVKeys ? C::kVChunks : 1)))
+                           box >= C::kVKeys ? C::kVChunks / kCluster : 1)))
     return NVFP4_ERR_LAUNCH;
-  if (const int st = launch(kernel, dim3(d.num_sms), dim3(C::kThreads), C::kSmem, stream, tm_q,
-                            tm_k, tm_v, p))
+  if (const int st = launch_clusters(kCluster, kernel, dim3(units * kCluster), dim3(C::kThreads),
+                                     C::kSmem, stream, tm_q, tm_k, tm_v, p))
     return st;
-  return run_join(a, p.parts, p.plan, d.num_sms, stream);
+  return run_join(a, p.parts, p.plan, units, stream);
 }
 
+// One tile of rows; more: two tiles in a CTA, or in a pair of CTAs where one
+// accumulator leaves no room for another (over an e4m3 cache, whose rows are
+// half as long in L2, each CTA works alone).
 template <int kDim, bool kE4m3>
 int run_tiles(bool two, const Attend& a, const Device& d, cudaStream_t stream) {
-  if constexpr (kDim < 256) {
-    if (two) return run<kDim, kE4m3, 2>(a, d, stream);
+  if (two) {
+    if constexpr (kDim < 256) return run<kDim, kE4m3, 2, 1>(a, d, stream);
+    if constexpr (kDim == 256 && !kE4m3) return run<kDim, kE4m3, 1, 2>(a, d, stream);
   }
-  return run<kDim, kE4m3, 1>(a, d, stream);
+  return run<kDim, kE4m3, 1, 1>(a, d, stream);
 }
 
 }  // namespace
 
 int64_t attend_tc_workspace(int head_dim, const Device& d) {
-  return Parts::bytes(d.num_sms, head_dim == 256 ? kM : 2 * kM, head_dim);
+  return Parts::bytes(d.num_sms, 2 * kM, head_dim);
 }
 
 int run_attend_tc(int64_t rows, const Attend& a, const Device& d, cudaStream_t stream) {

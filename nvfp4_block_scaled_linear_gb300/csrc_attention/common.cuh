@@ -88,26 +88,37 @@ struct Device {
 // The current device's set-up (NVFP4_ERR_DEVICE where it is not sm_103).
 int device(Device* out);
 
-// Launch with programmatic stream serialization: every kernel here calls
-// griddep_wait() before its first access to memory.
+// Launch, in clusters of `cluster` CTAs, with programmatic stream
+// serialization: every kernel here calls griddep_wait() before its first access
+// to memory.
 template <typename... P, typename... A>
-int launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-           const A&... args) {
+int launch_clusters(int cluster, void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
+                    cudaStream_t stream, const A&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   if (cudaLaunchKernelEx(&cfg, kernel, P(args)...) != cudaSuccess) {
     cudaGetLastError();
     return NVFP4_ERR_LAUNCH;
   }
   return NVFP4_OK;
+}
+
+template <typename... P, typename... A>
+int launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+           const A&... args) {
+  return launch_clusters(1, kernel, grid, block, smem, stream, args...);
 }
 
 // Let `kernel` use `bytes` of dynamic shared memory, once per device.

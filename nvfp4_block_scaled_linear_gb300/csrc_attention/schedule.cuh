@@ -193,7 +193,7 @@ struct Walk {
 enum : int { kPart0 = 1, kPart0Ends = 2, kPart1 = 4 };
 
 // The workspace: one note per CTA, then the parts' rows: log2 of the sum and
-// the normalised output, fp32.
+// the normalised output, fp32 (32-byte aligned where the workspace is).
 struct Parts {
   int4* note;             // {flags, s, h, tile} of part 1's item
   float* lse2;            // [ctas][2][rows]
@@ -203,8 +203,8 @@ struct Parts {
 
   Parts(void* base, int ctas, int tile_rows_, int tiles, int dim_)
       : note(static_cast<int4*>(base)),
-        lse2(reinterpret_cast<float*>(note + ctas)),
-        out(lse2 + int64_t(ctas) * 2 * tile_rows_ * tiles),
+        lse2(reinterpret_cast<float*>(note + (ctas + 1) / 2 * 2)),
+        out(lse2 + (int64_t(ctas) * 2 * tile_rows_ * tiles + 7) / 8 * 8),
         tile_rows(tile_rows_),
         rows(tile_rows_ * tiles),
         dim(dim_) {}
@@ -212,7 +212,7 @@ struct Parts {
     return (int64_t(cta) * 2 + part) * rows + r;
   }
   static int64_t bytes(int ctas, int rows, int dim) {
-    return int64_t(ctas) * (16 + 2 * int64_t(rows) * (dim + 1) * 4);
+    return int64_t(ctas) * (16 + 2 * int64_t(rows) * (dim + 1) * 4) + 64;
   }
 };
 
