@@ -69,14 +69,13 @@ struct Cfg {
   static constexpr int kQTile = kM * kDim * 2;
   static constexpr int kQBytes = kTiles * kQTile;
   static constexpr int kMaxSlots = 8;
-  static constexpr int kBars = 2 * kMaxSlots + 25 + 2 * kItems;
+  static constexpr int kBars = 2 * kMaxSlots + 24 + 2 * kItems;
   static constexpr int kBarOff = 0;
   static constexpr int kItemOff = (kBarOff + kBars * 8 + 16 + kDirty * 4 + 15) / 16 * 16;  // descriptors
   static constexpr int kMaxOff = kItemOff + kItems * 32;                                   // running maxima
   static constexpr int kSumOff = kMaxOff + (kTiles == 1 ? kM * 4 : 0);        // row sums
   static constexpr int kFacOff = kSumOff + (kTiles == 1 ? kM * 4 : 0);    // Q row factors
-  static constexpr int kRowOff = kFacOff + (kE4m3 ? kQFactors * kTiles * kM * 4 : 0);
-  static constexpr int kFixed = kRowOff + (kE4m3 ? 2 * kN * 8 : 0);
+  static constexpr int kFixed = kFacOff + (kE4m3 ? kQFactors * kTiles * kM * 4 : 0);
   static constexpr int kBudget = 227 * 1024 - 1024 - kFixed - kQBytes;
   static constexpr int kSlots = std::min(kMaxSlots, kBudget / kSlotBytes);
   static constexpr int kSmem = kQBytes + kSlots * kSlotBytes + kFixed + 1024;
@@ -313,8 +312,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
   uint64_t* q_empty = q_full + 1;
   uint64_t* mma_done = q_empty + 1;               // every product issued has completed
   uint64_t* pair = mma_done + 1;                  // both softmax groups (kTiles == 1)
-  uint64_t* widen = pair + 1;                     // the widening warps (e4m3)
-  uint64_t* v_known = widen + 1;                  // [2] v_slot[x] is that of buffer x's block
+  uint64_t* v_known = pair + 1;                  // [2] v_slot[x] is that of buffer x's block
   const Items items{reinterpret_cast<Item*>(fixed + C::kItemOff), v_known + 2, v_known + 2 + kItems,
                     reinterpret_cast<volatile int*>(full + C::kBars)};
   volatile int* abort_flag = reinterpret_cast<volatile int*>(full + C::kBars);
@@ -329,7 +327,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
-      mbar_init(&full[i], kE4m3 ? 4 : 1);
+      mbar_init(&full[i], kE4m3 ? 2 : 1);
       mbar_init(&empty[i], kCluster);
     }
     for (int x = 0; x < 2; ++x) {
@@ -345,7 +343,6 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
     mbar_init(q_empty, 1);
     mbar_init(mma_done, 1);
     mbar_init(pair, 8);
-    mbar_init(widen, 4);
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&items.full[i], 1);
       // softmax warps, MMA, and the copying and checking (or Q and widening) warps
@@ -393,14 +390,38 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
     return w.more();
   };
 
-  // The V rows of block b that not all rows of the tile see, a quarter of each
-  // slot by each warp of the group that gives the block's weights: rows that
-  // none sees become zero (0 times what a page happens to hold past the length
-  // need not be 0), and values that are not finite do; whether there were any.
-  auto check_v = [&](const Item& it, int b, int at, int quad) {
+  // Of a V slot whose first key is key0, rows row0 to row0 + rows - 1, as far as
+  // not all rows of the tile see them: rows that none sees become zero (0 times
+  // what a page happens to hold past the length need not be 0), and values that
+  // are not finite do; whether there were any.  By one warp.
+  auto check_rows = [&](const Item& it, int key0, int slot, int row0, int rows) {
     constexpr int kPer = C::kVChunks * 8;                   // 16-byte pieces of a row
-    constexpr int kRows = C::kVKeys / 4;
     const int least = it.least(), seen = it.seen(p.plan);
+    const int from = max(row0, least - key0);
+    bool bad = false;
+#pragma unroll 1
+    for (int j = from * kPer + lane; j < (row0 + rows) * kPer; j += 32) {
+      uint4* at = reinterpret_cast<uint4*>(ring + slot * C::kSlotBytes +
+                                           (j % kPer >> 3) * C::kVChunk + j / kPer * 128 +
+                                           (j & 7) * 16);
+      if (key0 + j / kPer >= seen) {
+        *at = make_uint4(0, 0, 0, 0);
+        continue;
+      }
+      uint4 v = *at;
+      if (!(non_finite<kE4m3>(v.x) || non_finite<kE4m3>(v.y) || non_finite<kE4m3>(v.z) ||
+            non_finite<kE4m3>(v.w)))
+        continue;
+      bad = true;
+      v.x &= finite_mask<kE4m3>(v.x), v.y &= finite_mask<kE4m3>(v.y);
+      v.z &= finite_mask<kE4m3>(v.z), v.w &= finite_mask<kE4m3>(v.w);
+      *at = v;
+    }
+    return bad;
+  };
+  // All of block b, a quarter by each warp of the group that gives its weights.
+  auto check_v = [&](const Item& it, int b, int at, int quad) {
+    constexpr int kRows = C::kVKeys / 4;
     VRing<C> r;
     r.slot = at & 255, r.par = at >> 8;
     bool bad = false;
@@ -408,26 +429,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
     for (int h = 0; h < C::kPieces; ++h, r.next()) {
       wait(&full[r.slot], r.par, abort_flag);
       __syncwarp();
-      const int row0 = quad * kRows;
-      const int key0 = it.key0 + b * kN + h * C::kVKeys + row0;
-#pragma unroll 1
-      for (int j = lane + max(0, least - key0) * kPer; j < kRows * kPer; j += 32) {
-        uint4* at16 = reinterpret_cast<uint4*>(ring + r.slot * C::kSlotBytes +
-                                               (j % kPer >> 3) * C::kVChunk +
-                                               (row0 + j / kPer) * 128 + (j & 7) * 16);
-        if (key0 + j / kPer >= seen) {
-          *at16 = make_uint4(0, 0, 0, 0);
-          continue;
-        }
-        uint4 v = *at16;
-        if (!(non_finite<kE4m3>(v.x) || non_finite<kE4m3>(v.y) || non_finite<kE4m3>(v.z) ||
-              non_finite<kE4m3>(v.w)))
-          continue;
-        bad = true;
-        v.x &= finite_mask<kE4m3>(v.x), v.y &= finite_mask<kE4m3>(v.y);
-        v.z &= finite_mask<kE4m3>(v.z), v.w &= finite_mask<kE4m3>(v.w);
-        *at16 = v;
-      }
+      bad |= check_rows(it, it.key0 + b * kN + h * C::kVKeys, r.slot, quad * kRows, kRows);
     }
     fence_proxy_async_smem();
     return bad;
@@ -506,6 +508,129 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
         atomicOr(a.err, NVFP4_ATTENTION_TIMEOUT);
     }
     __syncwarp();
+  };
+
+  // Two warps widen K, two V: 16 codes (one load) become 32 bytes of the slot,
+  // and the load of the unit after next takes the register over at once, so
+  // that the loads of a whole unit (8 per thread) are always on their way.
+  auto widen_pages = [&](auto values) {
+    constexpr bool kV = decltype(values)::value;
+    constexpr int kRows = kV ? C::kVKeys : kN;                   // of a slot
+    constexpr int kChunkBytes = kV ? C::kVChunk : C::kKChunk;
+    constexpr int kPerRow = kV ? kDim / 16 : C::kKChunks * 4;    // threads of a row
+    constexpr int kRowsAtOnce = 64 / kPerRow;
+    constexpr int kPasses = 8;                                   // of a unit
+    constexpr int kUnitRows = kPasses * kRowsAtOnce;
+    constexpr int kHalves = kRows / kUnitRows;                   // units of a slot
+    constexpr int kUnits = C::kPieces * kHalves;                 // of a block
+    constexpr int kGroups = kUnitRows / 16, kOfGroup = kPasses / kGroups;
+    const int tid = threadIdx.x & 63;
+    const int my_row = tid / kPerRow, my_col = tid % kPerRow * 16;
+    const int64_t slot_stride = kV ? a.cache.vs[1] : a.cache.ks[1];
+    const uint8_t* base = static_cast<const uint8_t*>(kV ? a.cache.v : a.cache.k) +
+                          my_row * slot_stride + my_col;
+    const int64_t step = kRowsAtOnce * slot_stride;              // of a pass
+    // where a pass's 32 bytes go in the slot: the rows' swizzle repeats every 8
+    const int c16 = (my_col & 63) >> 3;
+    uint32_t put[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int rr = i * kRowsAtOnce + my_row;
+        put[i][k] = (my_col >> 6) * kChunkBytes + rr * 128 + (((c16 + k) ^ (rr & 7)) << 4);
+      }
+    Place at;
+    at.start(items);
+    __syncwarp();
+    // lane i: where the block's rows 16 i on are (pages hold whole sixteens), or
+    // -1 past the length; read one block ahead
+    int64_t group = -1;
+    auto look_up = [&]() {
+      const int key = at.it.key0 + at.b * kN + (lane & 7) * 16;
+      group = -1;
+      if (at.live && key < at.it.kv_len) {
+        const int64_t page = checked_page(
+            a.seqs.table[int64_t(at.it.s) * a.seqs.width + key / a.cache.page_size], a.cache.pages,
+            a.err);
+        const int64_t* st = kV ? a.cache.vs : a.cache.ks;
+        if (page != a.cache.pages)
+          group = page * st[0] + key % a.cache.page_size * st[1] + at.it.h * st[2];
+      }
+    };
+    uint4 v[kPasses];
+    // pass i (in order) of unit u of the block that `where` describes
+    const uint8_t* from = nullptr;
+    auto load = [&](int64_t where, int u, int i) {
+      if (i % kOfGroup == 0) {
+        const int64_t off =
+            __shfl_sync(0xffffffffu, where, (kV ? u : u % kHalves) * kGroups + i / kOfGroup);
+        from = off < 0 ? nullptr : base + off + (kV ? 0 : u / kHalves * C::kKChunks * 64);
+      } else if (from) {
+        from += step;
+      }
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (from) v[i] = *reinterpret_cast<const uint4*>(from);
+    };
+    look_up();
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) load(group, 0, i);
+    std::conditional_t<kV, VRing<C>, KRing<C>> r;
+    int turns = 0;                                               // slots filled, up to the ring's
+    while (at.live) {
+      const Item it = at.it;
+      const int key0 = it.key0 + at.b * kN, was = at.item;
+      const int64_t here = group;
+      const bool moved = at.next(items);
+      __syncwarp();
+      look_up();
+#pragma unroll 1
+      for (int u = 0; u < kUnits; ++u) {
+        if (u % kHalves == 0) {
+          if (turns == (kV ? C::kVSlots : C::kKSlots)) {
+            wait(&empty[r.slot], r.par ^ 1, abort_flag);
+            __syncwarp();
+          } else {
+            ++turns;
+          }
+        }
+        const int64_t where = u + 1 < kUnits ? here : group;
+        const int next_u = u + 1 < kUnits ? u + 1 : 0;
+        uint8_t* slot = ring + r.slot * C::kSlotBytes + (u % kHalves) * kUnitRows * 128;
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+          uint32_t f[8];
+          const uint32_t cw[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            f[2 * k] = e4m3x2_to_f16x2(cw[k] & 0xFFFFu);
+            f[2 * k + 1] = e4m3x2_to_f16x2(cw[k] >> 16);
+          }
+          load(where, next_u, i);
+          uint8_t* at_row = slot + (i >> 1) * (2 * kRowsAtOnce * 128);
+          *reinterpret_cast<uint4*>(at_row + put[i & 1][0]) = make_uint4(f[0], f[1], f[2], f[3]);
+          *reinterpret_cast<uint4*>(at_row + put[i & 1][1]) = make_uint4(f[4], f[5], f[6], f[7]);
+        }
+        if (u % kHalves == kHalves - 1) {
+          // the passes' rows of a V slot lie with both warps: each looks over the
+          // rows that it wrote
+          const int first = key0 + u / kHalves * kRows;
+          if (kV && first + kRows > it.least()) {
+            __syncwarp();
+            bool bad = false;
+#pragma unroll 1
+            for (int q = 0; q < kRows; q += kRowsAtOnce)
+              bad |= check_rows(it, first, r.slot, q + (warp & 1) * (kRowsAtOnce / 2), kRowsAtOnce / 2);
+            if (bad) dirty[was % kDirty] = was + 1;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[r.slot]);
+          r.next();
+        }
+      }
+      if (moved && lane == 0) items.release(was);
+    }
   };
 
   if (warp < 8) {
@@ -909,7 +1034,9 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
     } else {
       // ---------------------------------- Q rows scaled to f16 (warps 8, 10, 11)
       const int part = warp == 8 ? 0 : warp - 9;
-      constexpr int kWords = kDim / 64;             // 32-bit words per lane
+      constexpr int kLanes = kDim / 8;              // of a row, 8 elements each
+      constexpr int kRowsAtOnce = 32 / kLanes, kPasses = 4;
+      const int ql = lane % kLanes;
       Walk w(range, a.seqs, p.plan, a.err);         // warp 11: the schedule
       if (warp == 11 && lane == 0) publish(w, 0);
       __syncwarp();
@@ -925,42 +1052,52 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
           wait(q_empty, (item - 1) & 1, abort_flag);
           __syncwarp();
         }
-        constexpr int kAtOnce = 4;
-        for (int r0 = part * kAtOnce; r0 < kTiles * kM; r0 += 3 * kAtOnce) {
-          uint32_t v[kAtOnce][kWords];
+        // rows that hold no token are left as they are: their weights are 0
+        const int tokens = min(kTiles * p.tile_tokens, it.q_len - it.tok0);
+        const int rows = kTiles == 1 || tokens <= p.tile_tokens
+                             ? tokens * a.group
+                             : kM + (tokens - p.tile_tokens) * a.group;
+#pragma unroll 1
+        for (int r0 = part * kPasses * kRowsAtOnce; r0 < rows; r0 += 3 * kPasses * kRowsAtOnce) {
+          uint4 v[kPasses];
 #pragma unroll
-          for (int i = 0; i < kAtOnce; ++i) {
-            const int r = r0 + i, x = r / kM, rr = r % kM;
+          for (int i = 0; i < kPasses; ++i) {
+            const int r = r0 + i * kRowsAtOnce + lane / kLanes;
+            const int x = r / kM, rr = r % kM;
             const int tok = rr / a.group, gi = rr - tok * a.group;
             const int ti = it.tok0 + x * p.tile_tokens + tok;
-            const bool valid = tok < p.tile_tokens && ti < it.q_len;
-            const uint32_t* src = reinterpret_cast<const uint32_t*>(
-                a.q.data + int64_t(it.q0 + ti) * a.q.ts + int64_t(it.h * a.group + gi) * a.q.hs);
-#pragma unroll
-            for (int k = 0; k < kWords; ++k) v[i][k] = valid ? src[k * 32 + lane] : 0u;
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (tok < p.tile_tokens && ti < it.q_len)
+              v[i] = *reinterpret_cast<const uint4*>(a.q.data + int64_t(it.q0 + ti) * a.q.ts +
+                                                     int64_t(it.h * a.group + gi) * a.q.hs + ql * 8);
           }
 #pragma unroll
-          for (int i = 0; i < kAtOnce; ++i) {
-            const int r = r0 + i, x = r / kM, rr = r % kM;
+          for (int i = 0; i < kPasses; ++i) {
+            const int r = r0 + i * kRowsAtOnce + lane / kLanes;
+            const int x = r / kM, rr = r % kM;
+            const uint32_t in[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
             float top = 0.f;
 #pragma unroll
-            for (int k = 0; k < kWords; ++k)
-              top = fmaxf(top, fmaxf(fabsf(bf16_lo(v[i][k])), fabsf(bf16_hi(v[i][k]))));
+            for (int k = 0; k < 4; ++k)
+              top = fmaxf(top, fmaxf(fabsf(bf16_lo(in[k])), fabsf(bf16_hi(in[k]))));
 #pragma unroll
-            for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            for (int d = kLanes / 2; d > 0; d >>= 1)
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
             int e = 141 - static_cast<int>(__float_as_uint(top) >> 23);
             e = top == 0.f || top > 3.4e38f ? 0 : min(e, 100);
             const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-            if (lane == 0)
+            if (r < kTiles * kM) {
+            if (ql == 0)
               q_factor[(item % kQFactors) * kTiles * kM + r] =
                   __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+            uint32_t f[4];
 #pragma unroll
-            for (int k = 0; k < kWords; ++k) {
-              // elements 64 k + 2 lane and the next: chunk k, byte 4 lane of the row
-              const uint32_t f = f32x2_to_f16x2(bf16_lo(v[i][k]) * up, bf16_hi(v[i][k]) * up);
-              *reinterpret_cast<uint32_t*>(q_sm + x * C::kQTile + k * kM * 128 + rr * 128 +
-                                           (((lane >> 2) ^ (rr & 7)) << 4) + (lane & 3) * 4) = f;
+            for (int k = 0; k < 4; ++k) f[k] = f32x2_to_f16x2(bf16_lo(in[k]) * up, bf16_hi(in[k]) * up);
+            // elements 8 ql on: 64-column chunk ql / 8, 16-byte piece ql % 8 of the row
+            *reinterpret_cast<uint4*>(q_sm + x * C::kQTile + (ql >> 3) * kM * 128 + rr * 128 +
+                                      (((ql & 7) ^ (rr & 7)) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
             }
+            __syncwarp();
           }
         }
         fence_proxy_async_smem();
@@ -975,116 +1112,10 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
     // ------------------------------------------ K, V codes widened to f16
     if constexpr (kE4m3) {
       regs_dec<96>();
-      const int tid = threadIdx.x - 384;            // 0..127
-      constexpr int kPasses = C::kSlotBytes / 4096; // 16 codes a thread each
-      int64_t* row_at = reinterpret_cast<int64_t*>(fixed + C::kRowOff);   // [2][128], then V's
-      Place kc, vc;
-      kc.start(items);
-      vc.start(items);
-      __syncwarp();
-      KRing<C> k_at;
-      VRing<C> v_at;
-      int k_turns = 0, v_turns = 0;                   // slots filled, up to the ring's
-      uint32_t widen_par = 0;
-      auto meet = [&]() {                             // the four warps
-        __syncwarp();
-        if (lane == 0) mbar_arrive(widen);
-        wait(widen, widen_par, abort_flag);
-        __syncwarp();
-        widen_par ^= 1u;
-      };
-      constexpr int kAhead = kTiles == 1 ? 2 : 1;
-      auto fill = [&](auto values, auto& ring_at, int& turns, const Place& st, const int64_t* rows,
-                      const uint8_t* base) {
-        constexpr bool kV = decltype(values)::value;
-        constexpr int kPerRow = kV ? kDim / 16 : C::kKChunks * 4;   // threads of a row
-        constexpr int kRowsAtOnce = 128 / kPerRow;
-        const int my_row = tid / kPerRow, my_col = (tid % kPerRow) * 16;
-        const int seen = st.it.seen(p.plan), least = st.it.least();
-#pragma unroll 1
-        for (int h = 0; h < C::kPieces; ++h, ring_at.next()) {
-          const int s = ring_at.slot;
-          uint4 v[kPasses];
-#pragma unroll
-          for (int i = 0; i < kPasses; ++i) {
-            const int64_t at = rows[(kV ? h * C::kVKeys : 0) + i * kRowsAtOnce + my_row];
-            v[i] = make_uint4(0, 0, 0, 0);
-            if (at >= 0)                                      // else: a row past the length
-              v[i] = *reinterpret_cast<const uint4*>(base + at + (kV ? 0 : h * C::kKChunks * 64) + my_col);
-          }
-          if (turns == (kV ? C::kVSlots : C::kKSlots)) {
-            wait(&empty[s], ring_at.par ^ 1, abort_flag);
-            __syncwarp();
-          } else {
-            ++turns;
-          }
-          const int key0 = st.it.key0 + st.b * kN + (kV ? h * C::kVKeys : 0);
-          const bool check = kV && key0 + C::kVKeys > least;
-          bool bad = false;
-#pragma unroll
-          for (int i = 0; i < kPasses; ++i) {
-            const int r = i * kRowsAtOnce + my_row;
-            const uint32_t cw[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-            uint32_t f[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              f[2 * k] = e4m3x2_to_f16x2(cw[k] & 0xFFFFu);
-              f[2 * k + 1] = e4m3x2_to_f16x2(cw[k] >> 16);
-            }
-            if (check) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                if (key0 + r >= seen) f[k] = 0;
-                if (key0 + r >= least && non_finite<true>(f[k])) {
-                  bad = true;
-                  f[k] &= finite_mask<true>(f[k]);
-                }
-              }
-            }
-            // 16 codes: two 16-byte pieces of the 128-byte row
-            uint8_t* row = ring + s * C::kSlotBytes + (my_col >> 6) * (kV ? C::kVChunk : C::kKChunk) + r * 128;
-            const int c16 = (my_col & 63) >> 3;
-            *reinterpret_cast<uint4*>(row + ((c16 ^ (r & 7)) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
-            *reinterpret_cast<uint4*>(row + (((c16 + 1) ^ (r & 7)) << 4)) =
-                make_uint4(f[4], f[5], f[6], f[7]);
-          }
-          if (bad) dirty[st.item % kDirty] = st.item + 1;
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&full[s]);
-        }
-      };
-      // row offsets of a block, by one thread per row
-      auto lookup = [&](const Place& st, const int64_t (&strides)[3], int64_t* rows) {
-        const int key = st.it.key0 + st.b * kN + tid;
-        int64_t at = -1;
-        if (key < st.it.kv_len) {
-          const int64_t page =
-              checked_page(a.seqs.table[int64_t(st.it.s) * a.seqs.width + key / a.cache.page_size],
-                           a.cache.pages, a.err);
-          if (page != a.cache.pages)
-            at = page * strides[0] + key % a.cache.page_size * strides[1] + st.it.h * strides[2];
-        }
-        meet();                                       // the rows before are read
-        rows[tid] = at;
-        meet();
-      };
-      for (int i = 0; kc.live || vc.live; ++i) {
-        if (i >= kAhead) {
-          lookup(vc, a.cache.vs, row_at + kN);
-          fill(std::true_type{}, v_at, v_turns, vc, row_at + kN, static_cast<const uint8_t*>(a.cache.v));
-          const int was = vc.item;
-          const bool moved = vc.next(items);
-          __syncwarp();
-          if (moved && lane == 0) items.release(was);
-        }
-        if (kc.live) {
-          lookup(kc, a.cache.ks, row_at);
-          fill(std::false_type{}, k_at, k_turns, kc, row_at, static_cast<const uint8_t*>(a.cache.k));
-          kc.next(items);
-          __syncwarp();
-        }
-      }
+      if (warp < 14)
+        widen_pages(std::false_type{});
+      else
+        widen_pages(std::true_type{});
     }
   }
   if (*abort_flag && threadIdx.x == 0) atomicOr(a.err, NVFP4_ATTENTION_TIMEOUT);
