@@ -73,7 +73,9 @@ typedef struct nvfp4_kv_cache {
   int32_t head_dim;
 } nvfp4_kv_cache;
 
-/* The most sequences of one attention call. */
+/* The most sequences of one attention call.  (Its work, counted in 16 keys for
+ * each few tokens and each key/value head of the longest sequence that the
+ * block table has room for, has to stay below 2^32 as well: NVFP4_ERR_SHAPE.) */
 #define NVFP4_ATTENTION_MAX_SEQUENCES 8192
 
 /* A batch of sequences over a cache.  Sequence s holds its first kv_lens[s]

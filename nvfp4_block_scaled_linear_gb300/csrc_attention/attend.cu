@@ -108,6 +108,11 @@ int64_t attend_workspace(int head_dim, const Device& d) {
   return std::max(attend_warp_workspace(head_dim, d), attend_tc_workspace(head_dim, d));
 }
 
+bool countable(const Seqs& s, int heads, const Plan& p) {
+  const double items = double(heads) * (double(s.tokens) / p.tile_tokens + s.count);
+  return items * (double(s.max_kv >> p.unit_shift) + 1) < 4294967296.0;
+}
+
 int run_attend(const Attend& p, const Device& d, cudaStream_t stream) {
   const int64_t rows = int64_t(std::max(1, p.max_q_len)) * p.group;
   return rows <= 64 ? run_attend_warp(static_cast<int>(rows), p, d, stream)

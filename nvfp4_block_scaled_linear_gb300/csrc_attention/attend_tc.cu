@@ -1148,6 +1148,7 @@ int run(const Attend& a, const Device& d, cudaStream_t stream) {
   const int units = d.num_sms / kCluster;
   TcParams p{a, {}, Parts(a.workspace, units, kM, kTiles * kCluster, kDim), kM / a.group, 0};
   p.plan = Plan{kTiles * kCluster * p.tile_tokens, kBlockShift, 1};
+  if (!countable(a.seqs, a.cache.heads, p.plan)) return NVFP4_ERR_SHAPE;
   p.box_shift = 4;
   while (p.box_shift < 7 && a.cache.page_size % (2 << p.box_shift) == 0) ++p.box_shift;
   const int box = 1 << p.box_shift;

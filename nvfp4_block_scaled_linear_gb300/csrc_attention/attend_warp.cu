@@ -221,6 +221,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<kDim, kE4m3, kR>::kCtas)
           if (lane == 0) mbar_arrive_expect_tx(&full[slot], units * kUnit * C::kRowBytes);
           // one lane issues: a copy's operands are warp-uniform registers, and
           // copies from several lanes took some 250 cycles each
+#pragma unroll 1
           for (int lu = 0; lu < units; ++lu) {
             const int pg = __shfl_sync(0xffffffffu, page, half * 4 + lu);
             const int ip = __shfl_sync(0xffffffffu, in_page, half * 4 + lu);
@@ -411,6 +412,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<kDim, kE4m3, kR>::kCtas)
         }
         __syncwarp();
         if (lane == 0)
+#pragma unroll 1
           for (int i = 0; i < slots; ++i) mbar_arrive(&empty[(it + i) % C::kSlots]);
         // ---- scale, mask, and the rows' maxima over this warp's keys
         const int kb = key0 + warp * kUnit + 2 * t;      // keys kb, kb + 1, kb + 8, kb + 9
@@ -474,13 +476,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<kDim, kE4m3, kR>::kCtas)
         }
         consumer_sync();
         // ---- P V for this warp's columns
+#pragma unroll 1
         for (int half = 0; half < slots; ++half) {
           const int si = it + slots + half;
           wait(&full[si % C::kSlots], (si / C::kSlots) & 1, abort_flag);
           __syncwarp();
           const uint32_t base = ring + (si % C::kSlots) * C::kSlotBytes;
-#pragma unroll
-          for (int lu = 0; lu < 4; ++lu) {
+#pragma unroll 1
+          for (int lu = 0; lu < 4; ++lu) {              // (not unrolled: code size)
             const int u = half * 4 + lu;
             if (u >= n) break;
             uint32_t b[kNt][2];
@@ -676,6 +679,7 @@ int run(const Attend& p, const Device& d, cudaStream_t stream) {
       !page_map(&tm_v, p.cache, true, inner, kUnit, C::kChunks))
     return NVFP4_ERR_LAUNCH;
   const Plan plan{std::max(1, C::kRows / p.group), kUnitShift, 4};
+  if (!countable(p.seqs, p.cache.heads, plan)) return NVFP4_ERR_SHAPE;
   const int ctas = d.num_sms * C::kCtas;
   const Parts parts(p.workspace, ctas, C::kRows, 1, kDim);
   if (const int st = launch(kernel, dim3(ctas), dim3(kThreads), C::kSmem, stream, tm_k, tm_v, p,

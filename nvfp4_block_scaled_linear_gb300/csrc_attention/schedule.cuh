@@ -26,6 +26,9 @@ __device__ __forceinline__ int tiles_of(const SeqInfo& s, const Plan& p) {
   return (s.q_len + p.tile_tokens - 1) / p.tile_tokens;
 }
 
+// Whether the units of any batch of these sizes can be counted in 32 bits.
+bool countable(const Seqs& s, int heads, const Plan& p);
+
 // Keys that the last token of a tile sees.
 __device__ __forceinline__ int tile_keys(const SeqInfo& s, int tile, const Plan& p) {
   const int last = min(s.q_len, (tile + 1) * p.tile_tokens);
@@ -36,32 +39,12 @@ __device__ __forceinline__ int tile_units(const SeqInfo& s, int tile, const Plan
   return max(1, (tile_keys(s, tile, p) + (1 << p.unit_shift) - 1) >> p.unit_shift);
 }
 
-// Units of one head of each lane's sequence, all lanes of the warp together.
-__device__ __forceinline__ int64_t seq_units(const SeqInfo& s, const Plan& p) {
-  const int lane = threadIdx.x & 31, n = tiles_of(s, p);
-  int64_t u = n == 1 ? tile_units(s, 0, p) : 0;
-  unsigned many = __ballot_sync(0xffffffffu, n > 1);
-  while (many) {
-    const int src = __ffs(many) - 1;
-    many &= many - 1;
-    const SeqInfo o{__shfl_sync(0xffffffffu, s.q0, src), __shfl_sync(0xffffffffu, s.q_len, src),
-                    __shfl_sync(0xffffffffu, s.kv_len, src)};
-    int64_t sum = 0;
-    const int tiles = tiles_of(o, p);
-#pragma unroll 1
-    for (int i = lane; i < tiles; i += 32) sum += tile_units(o, i, p);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    if (lane == src) u = sum;
-  }
-  return u;
-}
-
-__device__ __forceinline__ int64_t warp_inclusive(int64_t v) {
+// Sum of the lanes before and with this one.
+__device__ __forceinline__ uint32_t warp_inclusive(uint32_t v) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int64_t o = __shfl_up_sync(0xffffffffu, v, d);
+    const uint32_t o = __shfl_up_sync(0xffffffffu, v, d);
     if (lane >= d) v += o;
   }
   return v;
@@ -69,80 +52,108 @@ __device__ __forceinline__ int64_t warp_inclusive(int64_t v) {
 
 // Where a CTA's range begins, and how many units it holds.
 struct Range {
-  int64_t left;
+  uint32_t left;
   int s, h, tile, unit0;
 };
 
 struct RangeSmem {
-  int64_t batch[kMaxBatches];
+  uint32_t batch[kMaxBatches];              // units of 32 sequences
   Range range;
 };
 
-// The range of CTA `cta` of `ctas`, found by all threads of the block.
-__device__ inline Range find_range(const Seqs& q, int heads, const Plan& p, uint32_t cta, uint32_t ctas,
-                                   RangeSmem* sm, unsigned int* err) {
+// The range of CTA `cta` of `ctas`, found by all threads of the block: each
+// warp sums up batches of 32 sequences, and the warp whose batch holds the
+// range's first unit finds its place in it.  Everything is in two passes over
+// the same code, since what runs once per launch costs as much in instruction
+// fetches as in instructions.
+__device__ inline Range find_range(const Seqs& q, int heads, const Plan& p, uint32_t cta,
+                                   uint32_t ctas, RangeSmem* sm, unsigned int* err) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int warps = blockDim.x >> 5, batches = (q.count + 31) / 32;
-  auto lane_seq = [&](int b) {
-    const int s = b * 32 + lane;
-    return s < q.count ? load_seq(q, s, err) : SeqInfo{0, 0, 0};
-  };
+  uint32_t begin = 0;
 #pragma unroll 1
-  for (int b = warp; b < batches; b += warps) {
-    const int64_t sum = warp_inclusive(seq_units(lane_seq(b), p));
-    if (lane == 31) sm->batch[b] = sum * heads;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    int64_t total = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    uint32_t before = 0;                    // units of the batches before b
 #pragma unroll 1
-    for (int b = lane; b < batches; b += 32) total += sm->batch[b];
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
-    // the units in equal shares, over no more CTAs than min_units leaves work for
-    const uint32_t used = total >= int64_t(ctas) * p.min_units
-                              ? ctas
-                              : max(1u, static_cast<uint32_t>(total) / p.min_units);
-    const int64_t share = total >> 32 ? total / used : static_cast<uint32_t>(total) / used;
-    const int64_t extra = total - share * used;         // of them take one more
-    const int64_t begin = share * cta + min(int64_t(cta), extra);
-    const int64_t end = begin + (cta < used ? share + (cta < extra) : 0);
-    Range r{end - begin, 0, 0, 0, 0};
-    if (r.left > 0) {
-      int64_t at = begin;
-      int b = 0;
+    for (int b = 0; b < batches; ++b) {
+      if (pass == 1) {
+        const uint32_t here = sm->batch[b];
+        if (begin - before >= here) {       // (also where `begin` lies in an earlier one)
+          before += here;
+          continue;
+        }
+      }
+      if (pass == 0 ? b % warps != warp : warp != 0) {
+        if (pass == 1) break;
+        continue;
+      }
+      const int s = b * 32 + lane;
+      const SeqInfo mine = s < q.count ? load_seq(q, s, err) : SeqInfo{0, 0, 0};
+      // units of one head of each lane's sequence
+      const int tiles = tiles_of(mine, p);
+      uint32_t one = tiles == 1 ? tile_units(mine, 0, p) : 0;
+      unsigned many = __ballot_sync(0xffffffffu, tiles > 1);
 #pragma unroll 1
-      while (at >= sm->batch[b]) at -= sm->batch[b++];
-      const SeqInfo mine = lane_seq(b);
-      const int64_t one = seq_units(mine, p);
-      const int64_t upto = warp_inclusive(one) * heads;
+      while (many) {
+        const int src = __ffs(many) - 1;
+        many &= many - 1;
+        const SeqInfo o{0, __shfl_sync(0xffffffffu, mine.q_len, src),
+                        __shfl_sync(0xffffffffu, mine.kv_len, src)};
+        const int n = __shfl_sync(0xffffffffu, tiles, src);
+        uint32_t sum = 0;
+#pragma unroll 1
+        for (int i = lane; i < n; i += 32) sum += tile_units(o, i, p);
+        sum = __reduce_add_sync(0xffffffffu, sum);
+        if (lane == src) one = sum;
+      }
+      const uint32_t upto = warp_inclusive(one) * heads;
+      if (pass == 0) {
+        if (lane == 31) sm->batch[b] = upto;
+        continue;
+      }
+      // the sequence, the head and the tile that hold the first unit
+      uint32_t at = begin - before;
       const int src = __ffs(__ballot_sync(0xffffffffu, upto > at)) - 1;
       at -= __shfl_sync(0xffffffffu, upto - one * heads, src);
-      const int64_t per_head = __shfl_sync(0xffffffffu, one, src);
-      const SeqInfo o{__shfl_sync(0xffffffffu, mine.q0, src),
-                      __shfl_sync(0xffffffffu, mine.q_len, src),
+      const uint32_t per_head = __shfl_sync(0xffffffffu, one, src);
+      const SeqInfo o{0, __shfl_sync(0xffffffffu, mine.q_len, src),
                       __shfl_sync(0xffffffffu, mine.kv_len, src)};
-      r.s = b * 32 + src;
+      const int n = __shfl_sync(0xffffffffu, tiles, src);
+      const uint32_t h = at / per_head;
+      at -= h * per_head;
+      int t0 = 0;
+      uint32_t u, sum;
+      unsigned past;
 #pragma unroll 1
-      for (; at >= per_head; at -= per_head) ++r.h;
-      const int tiles = tiles_of(o, p);
-#pragma unroll 1
-      for (int t0 = 0;; t0 += 32) {
-        const int u = t0 + lane < tiles ? tile_units(o, t0 + lane, p) : 0;
-        const int64_t sum = warp_inclusive(u);
-        const unsigned past = __ballot_sync(0xffffffffu, sum > at);
-        if (past) {
-          const int i = __ffs(past) - 1;
-          r.tile = t0 + i;
-          r.unit0 = static_cast<int>(at - __shfl_sync(0xffffffffu, sum - u, i));
-          break;
-        }
+      for (;; t0 += 32) {
+        u = t0 + lane < n ? tile_units(o, t0 + lane, p) : 0;
+        sum = warp_inclusive(u);
+        past = __ballot_sync(0xffffffffu, sum > at);
+        if (past || t0 >= n) break;
         at -= __shfl_sync(0xffffffffu, sum, 31);
       }
+      const int i = past ? __ffs(past) - 1 : 0;
+      if (lane == i) {
+        sm->range.s = b * 32 + src;
+        sm->range.h = static_cast<int>(h);
+        sm->range.tile = t0 + i;
+        sm->range.unit0 = static_cast<int>(at - (sum - u));
+      }
+      break;
     }
-    if (lane == 0) sm->range = r;
+    __syncthreads();
+    if (pass == 0) {
+      uint32_t total = 0;
+#pragma unroll 1
+      for (int b = 0; b < batches; ++b) total += sm->batch[b];
+      // the units in equal shares, over no more CTAs than min_units leaves work for
+      const uint32_t used = min(ctas, max(1u, total / p.min_units));
+      const uint32_t share = total / used, extra = total - share * used;
+      begin = share * cta + min(cta, extra);
+      if (threadIdx.x == 0) sm->range.left = cta < used ? share + (cta < extra) : 0;
+      if (cta >= used) begin = total;                  // in no batch
+    }
   }
-  __syncthreads();
   return sm->range;
 }
 
@@ -164,12 +175,12 @@ struct Walk {
   __device__ bool ends() const { return r.unit0 + count == units; }
   __device__ void item(const Plan& p) {
     units = tile_units(seq, r.tile, p);
-    count = static_cast<int>(min(int64_t(units - r.unit0), r.left));
+    count = static_cast<int>(min(static_cast<uint32_t>(units - r.unit0), r.left));
   }
   __device__ void next(const Seqs& q, int heads, const Plan& p, unsigned int* err) {
     r.left -= count;
     r.unit0 = 0;
-    if (r.left <= 0) return;
+    if (r.left == 0) return;
     if (++r.tile == tiles_of(seq, p)) {
       r.tile = 0;
       if (++r.h == heads) {
