@@ -5,9 +5,9 @@
 //   (a, b) = (y[i], y[i + rot/2]) -> (a cos - b sin, b cos + a sin), i < rot/2
 //
 // Bound by bytes: every head is read once and written once.  A lane holds 8
-// consecutive elements (one 16-byte access), so a head takes dim/8 lanes and
-// the sum of squares that many lanes' shuffles; the rotation's partner sits
-// rot/16 lanes away and arrives by one shuffle per element.  A warp takes
+// elements: in the rotated dimensions 4 and the 4 they are paired with, so that
+// the rotation needs no other lane, beyond them 8 consecutive ones; a head takes
+// dim/8 lanes, and the sum of squares that many lanes' shuffles.  A warp takes
 // kSteps rows of heads of one token, all loaded before the first is used, so
 // that the row of the cosine table and the two weight rows are read once for
 // them and enough bytes are in flight to reach the memory's rate.
@@ -20,16 +20,14 @@ namespace {
 constexpr int kSteps = 4;
 constexpr int kThreads = 128;
 
-__device__ __forceinline__ void unpack8(const uint4 w, float (&f)[8]) {
-  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = bf16_lo(v[i]);
-    f[2 * i + 1] = bf16_hi(v[i]);
-  }
+__device__ __forceinline__ void unpack4(const uint2 w, float* f) {
+  f[0] = bf16_lo(w.x), f[1] = bf16_hi(w.x), f[2] = bf16_lo(w.y), f[3] = bf16_hi(w.y);
+}
+__device__ __forceinline__ uint2 pack4(const float* f) {
+  return make_uint2(f32x2_to_bf16x2(f[0], f[1]), f32x2_to_bf16x2(f[2], f[3]));
 }
 
-// dim: the head's width; a warp's step covers 256 / dim heads.
+// kDim: the head's width; a warp's step covers 256 / kDim heads.
 template <int kDim>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRope p, int warps_per_token,
                                                              int heads) {
@@ -41,49 +39,43 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRope p, i
   const int64_t t = w / warps_per_token;
   if (t >= p.tokens) return;
   const int h0 = static_cast<int>(w - t * warps_per_token) * (kSteps * kPerStep) + lane / kLanes;
+  // this lane's two fours of elements
+  const bool turns = li * 8 < p.rot;
+  const int at0 = turns ? li * 4 : li * 8, at1 = turns ? p.rot / 2 + li * 4 : li * 8 + 4;
 
-  uint4 x[kSteps];
+  uint2 x[kSteps][2];
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
     const int h = h0 + s * kPerStep;
-    x[s] = make_uint4(0, 0, 0, 0);
+    x[s][0] = x[s][1] = make_uint2(0, 0);
     if (h < heads) {
       const Heads& src = h < p.q_heads ? p.q : h < p.q_heads + p.kv_heads ? p.k : p.v;
       const int hh = h < p.q_heads ? h
                      : h < p.q_heads + p.kv_heads ? h - p.q_heads
                                                   : h - p.q_heads - p.kv_heads;
-      x[s] = *reinterpret_cast<const uint4*>(src.data + t * src.ts + hh * src.hs + li * 8);
+      const __nv_bfloat16* row = src.data + t * src.ts + hh * src.hs;
+      x[s][0] = *reinterpret_cast<const uint2*>(row + at0);
+      x[s][1] = *reinterpret_cast<const uint2*>(row + at1);
     }
   }
-  const uint4 qw = *reinterpret_cast<const uint4*>(p.q_weight + li * 8);
-  const uint4 kw = *reinterpret_cast<const uint4*>(p.k_weight + li * 8);
-  // cosines and signed sines of this lane's elements: identity outside the
-  // rotated dimensions
-  const int half = p.rot / 16;                        // lanes holding the first of each pair
-  float cs[8], sn[8];
+  uint2 qw[2], kw[2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) cs[i] = 1.f, sn[i] = 0.f;
-  int partner = lane;
-  if (li < 2 * half) {
+  for (int i = 0; i < 2; ++i) {
+    qw[i] = *reinterpret_cast<const uint2*>(p.q_weight + (i ? at1 : at0));
+    kw[i] = *reinterpret_cast<const uint2*>(p.k_weight + (i ? at1 : at0));
+  }
+  float4 cs = make_float4(1.f, 1.f, 1.f, 1.f), sn = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (turns) {
     const int64_t pos = p.positions[t];
-    partner = li < half ? lane + half : lane - half;
     if (pos >= 0 && pos < p.max_position) {
-      const float* row = p.cos_sin + pos * p.rot + (li < half ? li : li - half) * 8;
-#pragma unroll
-      for (int i = 0; i < 8; i += 4) {
-        const float4 c = *reinterpret_cast<const float4*>(row + i);
-        const float4 s = *reinterpret_cast<const float4*>(row + p.rot / 2 + i);
-        cs[i] = c.x, cs[i + 1] = c.y, cs[i + 2] = c.z, cs[i + 3] = c.w;
-        sn[i] = s.x, sn[i + 1] = s.y, sn[i + 2] = s.z, sn[i + 3] = s.w;
-      }
-      if (li < half) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sn[i] = -sn[i];
-      }
+      const float* row = p.cos_sin + pos * p.rot + at0;
+      cs = *reinterpret_cast<const float4*>(row);
+      sn = *reinterpret_cast<const float4*>(row + p.rot / 2);
     } else {
       atomicOr(p.err, NVFP4_ATTENTION_BAD_INDEX);
     }
   }
+  const float c4[4] = {cs.x, cs.y, cs.z, cs.w}, s4[4] = {sn.x, sn.y, sn.z, sn.w};
   int64_t page = -1;
   int in_page = 0;
   if (p.store) {
@@ -101,36 +93,41 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRope p, i
     const int h = h0 + s * kPerStep;
     const bool is_q = h < p.q_heads, is_v = h >= p.q_heads + p.kv_heads;
     float y[8];
-    unpack8(x[s], y);
+    unpack4(x[s][0], y);
+    unpack4(x[s][1], y + 4);
     float sq = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) sq = fmaf(y[i], y[i], sq);
 #pragma unroll
     for (int m = kLanes / 2; m > 0; m >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, m);
-    const float r = rsqrtf(sq * (1.f / kDim) + p.eps);
-    float wt[8];
-    unpack8(is_q ? qw : kw, wt);
-    float n[8];
+    if (!is_v) {
+      const float r = rsqrtf(sq * (1.f / kDim) + p.eps);
+      float wt[8];
+      unpack4(is_q ? qw[0] : kw[0], wt);
+      unpack4(is_q ? qw[1] : kw[1], wt + 4);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) n[i] = y[i] * r * wt[i];
+      for (int i = 0; i < 8; ++i) y[i] = y[i] * r * wt[i];
+      if (turns) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float other = __shfl_sync(0xffffffffu, n[i], partner);
-      const float turned = partner == lane ? n[i] : fmaf(other, sn[i], n[i] * cs[i]);
-      if (!is_v) y[i] = turned;
+        for (int i = 0; i < 4; ++i) {
+          const float a = y[i], b = y[i + 4];
+          y[i] = a * c4[i] - b * s4[i];
+          y[i + 4] = b * c4[i] + a * s4[i];
+        }
+      }
     }
     if (h >= heads) continue;
     const int hh = is_q ? h : is_v ? h - p.q_heads - p.kv_heads : h - p.q_heads;
     if (is_q || !p.store) {
       const Heads& dst = is_q ? p.q_out : p.k_out;
-      *reinterpret_cast<uint4*>(dst.data + t * dst.ts + hh * dst.hs + li * 8) =
-          make_uint4(f32x2_to_bf16x2(y[0], y[1]), f32x2_to_bf16x2(y[2], y[3]),
-                     f32x2_to_bf16x2(y[4], y[5]), f32x2_to_bf16x2(y[6], y[7]));
+      __nv_bfloat16* row = dst.data + t * dst.ts + hh * dst.hs;
+      *reinterpret_cast<uint2*>(row + at0) = pack4(y);
+      *reinterpret_cast<uint2*>(row + at1) = pack4(y + 4);
       continue;
     }
     if (page < 0) continue;
     const int64_t* st = is_v ? p.cache.vs : p.cache.ks;
-    const int64_t off = page * st[0] + in_page * st[1] + hh * st[2] + li * 8;
+    const int64_t off = page * st[0] + in_page * st[1] + hh * st[2];
     void* base = is_v ? p.cache.v : p.cache.k;
     if (p.cache.e4m3) {
       const float* scales = is_v ? p.cache.v_scale : p.cache.k_scale;
@@ -140,12 +137,13 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRope p, i
       for (int i = 0; i < 4; ++i)
         c[i] = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * i] / scale, y[2 * i + 1] / scale),
                                         __NV_SATFINITE, __NV_E4M3);
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(base) + off) =
-          make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+      uint8_t* row = static_cast<uint8_t*>(base) + off;
+      *reinterpret_cast<uint32_t*>(row + at0) = c[0] | c[1] << 16;
+      *reinterpret_cast<uint32_t*>(row + at1) = c[2] | c[3] << 16;
     } else {
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + off) =
-          make_uint4(f32x2_to_bf16x2(y[0], y[1]), f32x2_to_bf16x2(y[2], y[3]),
-                     f32x2_to_bf16x2(y[4], y[5]), f32x2_to_bf16x2(y[6], y[7]));
+      __nv_bfloat16* row = static_cast<__nv_bfloat16*>(base) + off;
+      *reinterpret_cast<uint2*>(row + at0) = pack4(y);
+      *reinterpret_cast<uint2*>(row + at1) = pack4(y + 4);
     }
   }
 }
