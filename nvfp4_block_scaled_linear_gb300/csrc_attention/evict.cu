@@ -13,7 +13,7 @@
 // of the slice, in order, behind those of the runs and slices before it.
 //
 // What bounds it: the copy moves every kept row once in and once out; the
-// choice is latency (two cluster barriers a pass), so it is spread over as many
+// choice is latency (a cluster barrier a pass), so it is spread over as many
 // CTAs as the slices keep busy.
 #include <algorithm>
 
@@ -43,7 +43,7 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
 
 __global__ void __launch_bounds__(kThreads) choose_kernel(const Evict p, int slice_room) {
   extern __shared__ uint32_t keys[];          // the slice, up to slice_room of it
-  __shared__ uint32_t count[256];             // this slice's
+  __shared__ uint32_t counts[4][256];         // this slice's, pass by pass
   __shared__ uint32_t total[256];             // the cluster's
   __shared__ uint32_t warp_sum[kWarps];
   __shared__ uint32_t mine[2];                // larger than the bar, equal to it
@@ -65,7 +65,6 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const Evict p, int sli
   const int old = n - newest;                 // candidates
   const float* mass = p.mass + row * p.room;
   int32_t* index = p.index + row * p.keep;
-  float* new_mass = p.new_mass + row * p.keep;
   // the slice, in runs of `run` candidates per thread (odd: no bank conflicts)
   const int share = static_cast<int>((old + ctas - 1) / ctas);
   const int run = ((share + kThreads - 1) / kThreads) | 1;
@@ -75,23 +74,33 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const Evict p, int sli
   const bool held = len <= slice_room;
   if (rank == 0 && tid == 0 && row % p.from.heads == 0) p.new_lens[s] = m;
   if (choose && held)
+#pragma unroll 8
     for (int j = tid; j < len; j += kThreads) keys[j] = ordered(mass[j0 + j]);
   if (tid == 0) sh_prefix = 0, sh_left = m - newest;
   auto key_at = [&](int j) { return held ? keys[j] : ordered(mass[j0 + j]); };
+  for (int i = tid; i < 4 * 256; i += kThreads) counts[i >> 8][i & 255] = 0;
   if (choose) {
     // ---- the last kept candidate's bits, and how many of its equals are kept
 #pragma unroll 1
     for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) count[tid] = 0;
       __syncthreads();
+      uint32_t* count = counts[shift >> 3];
       const uint32_t prefix = sh_prefix, mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
       for (int j = tid; j < (len + 31) / 32 * 32; j += kThreads) {
         const uint32_t u = j < len ? key_at(j) : 0u;
-        const bool in = j < len && (u & mask) == prefix;
-        // equal values (and equal high bytes) are common: one add for a warp's
-        const uint32_t bin = in ? (u >> shift) & 255 : 256;
-        const unsigned same = __match_any_sync(0xffffffffu, bin);
-        if (in && lane == __ffs(same) - 1) atomicAdd(&count[bin], __popc(same));
+        const uint32_t bin = (u >> shift) & 255;
+        unsigned left = __ballot_sync(0xffffffffu, j < len && (u & mask) == prefix);
+        // equal values (and equal high bytes) are common: the bins of the first
+        // lanes with one add for all that share them, the rest one by one
+#pragma unroll
+        for (int round = 0; round < 3 && left; ++round) {
+          const int lead = __ffs(left) - 1;
+          const unsigned same =
+              left & __ballot_sync(0xffffffffu, bin == __shfl_sync(0xffffffffu, bin, lead));
+          if (lane == lead) atomicAdd(&count[bin], __popc(same));
+          left &= ~same;
+        }
+        if (left >> lane & 1) atomicAdd(&count[bin], 1u);
       }
       cluster_sync();
       if (tid < 256) {
@@ -100,7 +109,7 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const Evict p, int sli
         for (uint32_t r = 0; r < ctas; ++r) sum += ld_cluster_u32(map_to_rank(at, r));
         total[tid] = sum;
       }
-      cluster_sync();                         // the counts may be cleared again
+      __syncthreads();
       if (warp == 0) {
         // from the top: the bin in which the running count reaches `left`
         const uint32_t left = sh_left;
@@ -125,8 +134,8 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const Evict p, int sli
           above += __shfl_sync(0xffffffffu, x, 31);
         }
       }
-      __syncthreads();
     }
+    __syncthreads();
     // ---- each thread's run: how many are larger, how many equal
     const uint32_t bar = sh_prefix, equals = sh_left;
     const int from = min(len, tid * run), to = min(len, from + run);
@@ -172,51 +181,62 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const Evict p, int sli
       const uint32_t u = key_at(j);
       const bool take = u > bar || (u == bar && eq < equals);
       eq += u == bar;
-      if (take) {
-        index[at] = j0 + j;
-        new_mass[at] = mass[j0 + j];
-        ++at;
-      }
+      if (take) index[at++] = j0 + j;
     }
     cluster_sync();                           // no CTA ends while its counts are read
   }
   for (int i = rank * kThreads + tid; i < p.keep - (m - newest); i += ctas * kThreads) {
     const int at = m - newest + i;
     index[at] = at < m ? old + i : -1;
-    new_mass[at] = at < m ? mass[old + i] : 0.f;
   }
 }
 
-// One warp copies the key and value rows of one kept place.
-__global__ void __launch_bounds__(256) move_kernel(const Evict p) {
+// A block moves the rows of kPlaces kept places of one sequence and head: a
+// thread per place hands on its mass and finds where its rows come from and go
+// to, then all threads copy 16 bytes at a time, several on their way each.
+constexpr int kPlaces = 64;
+constexpr int kMoveThreads = 256;
+
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(const Evict p) {
+  __shared__ int64_t from[2][kPlaces], to[2][kPlaces];     // bytes; from < 0: nothing
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t(blockIdx.x) * 256 + threadIdx.x) >> 5;
-  const int64_t row = w / p.keep;
-  const int r = static_cast<int>(w - row * p.keep);
-  const int s = static_cast<int>(row / p.from.heads), h = static_cast<int>(row % p.from.heads);
-  if (s >= p.count) return;
-  const int j = p.index[row * p.keep + r];
-  if (j < 0) return;
-  const int64_t from = checked_page(p.table[int64_t(s) * p.width + j / p.from.page_size],
-                                    p.from.pages, p.err);
-  const int64_t to = checked_page(p.to_table[int64_t(s) * p.to_width + r / p.to.page_size],
-                                  p.to.pages, p.err);
-  if (from == p.from.pages || to == p.to.pages) return;
+  const int row = blockIdx.x, tid = threadIdx.x;
+  const int s = row / p.from.heads, h = row - s * p.from.heads;
   const int size = p.from.e4m3 ? 1 : 2;
-  const int bytes = p.from.dim * size;
-  const int jf = j % p.from.page_size, rt = r % p.to.page_size;
-  for (int i = lane * 16; i < 2 * bytes; i += 512) {
-    const bool v = i >= bytes;
-    const int b = v ? i - bytes : i;
-    const int64_t* fs = v ? p.from.vs : p.from.ks;
-    const int64_t* ts = v ? p.to.vs : p.to.ks;
-    const uint8_t* src = static_cast<const uint8_t*>(v ? p.from.v : p.from.k) +
-                         (from * fs[0] + jf * fs[1] + h * fs[2]) * size + b;
-    uint8_t* dst = static_cast<uint8_t*>(v ? p.to.v : p.to.k) +
-                   (to * ts[0] + rt * ts[1] + h * ts[2]) * size + b;
-    *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
+  if (tid < kPlaces) {
+    const int r = blockIdx.y * kPlaces + tid;
+    const int j = r < p.keep ? p.index[int64_t(row) * p.keep + r] : -1;
+    if (r < p.keep)
+      p.new_mass[int64_t(row) * p.keep + r] = j >= 0 ? p.mass[row * p.room + j] : 0.f;
+    from[0][tid] = -1;
+    if (j >= 0) {
+      const int jp = j / p.from.page_size, rp = r / p.to.page_size;
+      const int64_t a = checked_page(p.table[int64_t(s) * p.width + jp], p.from.pages, p.err);
+      const int64_t b = checked_page(p.to_table[int64_t(s) * p.to_width + rp], p.to.pages, p.err);
+      if (a != p.from.pages && b != p.to.pages) {
+        const int jf = j - jp * p.from.page_size, rt = r - rp * p.to.page_size;
+        from[0][tid] = (a * p.from.ks[0] + jf * p.from.ks[1] + h * p.from.ks[2]) * size;
+        from[1][tid] = (a * p.from.vs[0] + jf * p.from.vs[1] + h * p.from.vs[2]) * size;
+        to[0][tid] = (b * p.to.ks[0] + rt * p.to.ks[1] + h * p.to.ks[2]) * size;
+        to[1][tid] = (b * p.to.vs[0] + rt * p.to.vs[1] + h * p.to.vs[2]) * size;
+      }
+    }
+  }
+  __syncthreads();
+  // 16-byte pieces of a row: a power of two, 4 to 32
+  const int shift = 31 - __clz(p.from.dim * size >> 4);
+  const int piece = tid & ((1 << shift) - 1), first = tid >> shift, step = kMoveThreads >> shift;
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    const uint8_t* src = static_cast<const uint8_t*>(v ? p.from.v : p.from.k) + piece * 16;
+    uint8_t* dst = static_cast<uint8_t*>(v ? p.to.v : p.to.k) + piece * 16;
+#pragma unroll 4
+    for (int i = first; i < kPlaces; i += step) {
+      if (from[0][i] < 0) continue;
+      *reinterpret_cast<uint4*>(dst + to[v][i]) =
+          __ldcs(reinterpret_cast<const uint4*>(src + from[v][i]));
+    }
   }
 }
 
@@ -224,11 +244,11 @@ __global__ void __launch_bounds__(256) move_kernel(const Evict p) {
 
 int run_evict(const Evict& p, const Device& d, cudaStream_t stream) {
   const int64_t rows = int64_t(p.count) * p.from.heads;
-  const int64_t blocks = (rows * p.keep + 7) / 8;
+  const int64_t blocks = (int64_t(p.keep) + kPlaces - 1) / kPlaces;
   // CTAs of a cluster: while there are SMs for them and candidates for each
   int ctas = 1;
   while (ctas < kMaxCluster && rows * ctas < d.num_sms && p.room > int64_t(ctas) * kMinSlice) ctas *= 2;
-  if (rows * ctas > INT32_MAX || blocks > INT32_MAX) return NVFP4_ERR_SHAPE;
+  if (rows * ctas > INT32_MAX || blocks > 65535) return NVFP4_ERR_SHAPE;
   // the longest slice there can be, as far as it is held
   const int64_t slice = ((p.room + ctas - 1) / ctas + kThreads) / kThreads * kThreads + kThreads;
   const int held = static_cast<int>(std::min<int64_t>(slice, kSmemKeys));
@@ -237,7 +257,8 @@ int run_evict(const Evict& p, const Device& d, cudaStream_t stream) {
   if (const int st = launch_clusters(ctas, choose_kernel, dim3(static_cast<unsigned>(rows * ctas)),
                                      dim3(kThreads), held * 4, stream, p, held))
     return st;
-  return launch(move_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, p);
+  return launch(move_kernel, dim3(static_cast<unsigned>(rows), static_cast<unsigned>(blocks)),
+                dim3(kMoveThreads), 0, stream, p);
 }
 
 }  // namespace attn

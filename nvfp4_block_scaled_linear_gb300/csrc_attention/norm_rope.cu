@@ -18,7 +18,7 @@ namespace attn {
 namespace {
 
 constexpr int kSteps = 4;
-constexpr int kThreads = 128;
+constexpr int kMaxThreads = 256;
 
 __device__ __forceinline__ void unpack4(const uint2 w, float* f) {
   f[0] = bf16_lo(w.x), f[1] = bf16_hi(w.x), f[2] = bf16_lo(w.y), f[3] = bf16_hi(w.y);
@@ -27,42 +27,55 @@ __device__ __forceinline__ uint2 pack4(const float* f) {
   return make_uint2(f32x2_to_bf16x2(f[0], f[1]), f32x2_to_bf16x2(f[2], f[3]));
 }
 
-// kDim: the head's width; a warp's step covers 256 / kDim heads.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// kDim: the head's width; a warp's step covers 256 / kDim heads.  A warp's heads
+// are all query, all key or all value heads.
 template <int kDim>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRope p, int warps_per_token,
-                                                             int heads) {
+__global__ void __launch_bounds__(kMaxThreads) norm_rope_kernel(const NormRope p, int q_warps,
+                                                                int k_warps) {
   constexpr int kLanes = kDim / 8, kPerStep = 32 / kLanes;
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, li = lane % kLanes;
-  const int64_t w = (int64_t(blockIdx.x) * kThreads + threadIdx.x) >> 5;
-  const int64_t t = w / warps_per_token;
-  if (t >= p.tokens) return;
-  const int h0 = static_cast<int>(w - t * warps_per_token) * (kSteps * kPerStep) + lane / kLanes;
+  const int64_t t = blockIdx.x;
+  const int w = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const int kind = w < q_warps ? 0 : w < q_warps + k_warps ? 1 : 2;      // query, key, value
+  const int h0 = (w - (kind > 0 ? q_warps : 0) - (kind > 1 ? k_warps : 0)) * (kSteps * kPerStep) +
+                 lane / kLanes;
+  const int heads = kind == 0 ? p.q_heads : p.kv_heads;
+  const Heads src = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
   // this lane's two fours of elements
-  const bool turns = li * 8 < p.rot;
+  const bool turns = kind < 2 && li * 8 < p.rot;
   const int at0 = turns ? li * 4 : li * 8, at1 = turns ? p.rot / 2 + li * 4 : li * 8 + 4;
+  if (kind == 2 && !p.store) return;
 
   uint2 x[kSteps][2];
+  const __nv_bfloat16* in = src.data + t * src.ts + h0 * src.hs;
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
-    const int h = h0 + s * kPerStep;
     x[s][0] = x[s][1] = make_uint2(0, 0);
-    if (h < heads) {
-      const Heads& src = h < p.q_heads ? p.q : h < p.q_heads + p.kv_heads ? p.k : p.v;
-      const int hh = h < p.q_heads ? h
-                     : h < p.q_heads + p.kv_heads ? h - p.q_heads
-                                                  : h - p.q_heads - p.kv_heads;
-      const __nv_bfloat16* row = src.data + t * src.ts + hh * src.hs;
-      x[s][0] = *reinterpret_cast<const uint2*>(row + at0);
-      x[s][1] = *reinterpret_cast<const uint2*>(row + at1);
+    if (h0 + s * kPerStep < heads) {
+      x[s][0] = *reinterpret_cast<const uint2*>(in + at0);
+      x[s][1] = *reinterpret_cast<const uint2*>(in + at1);
+      in += kPerStep * src.hs;
     }
   }
-  uint2 qw[2], kw[2];
+  float2 wt[4];
+  if (kind < 2) {
+    const __nv_bfloat16* weight = kind == 0 ? p.q_weight : p.k_weight;
+    float f[8];
+    unpack4(*reinterpret_cast<const uint2*>(weight + at0), f);
+    unpack4(*reinterpret_cast<const uint2*>(weight + at1), f + 4);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    qw[i] = *reinterpret_cast<const uint2*>(p.q_weight + (i ? at1 : at0));
-    kw[i] = *reinterpret_cast<const uint2*>(p.k_weight + (i ? at1 : at0));
+    for (int i = 0; i < 4; ++i) wt[i] = make_float2(f[2 * i], f[2 * i + 1]);
   }
   float4 cs = make_float4(1.f, 1.f, 1.f, 1.f), sn = make_float4(0.f, 0.f, 0.f, 0.f);
   if (turns) {
@@ -75,73 +88,80 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRope p, i
       atomicOr(p.err, NVFP4_ATTENTION_BAD_INDEX);
     }
   }
-  const float c4[4] = {cs.x, cs.y, cs.z, cs.w}, s4[4] = {sn.x, sn.y, sn.z, sn.w};
-  int64_t page = -1;
-  int in_page = 0;
-  if (p.store) {
+  // where the first of the warp's rows goes, and the step to the next
+  const bool to_cache = kind > 0 && p.store;
+  const bool narrow = to_cache && p.cache.e4m3;
+  int64_t off, next;
+  void* out;
+  bool stored = true;
+  if (to_cache) {
     const int64_t slot = p.slots[t];
-    if (slot >= 0 && slot < p.cache.pages * p.cache.page_size) {
-      page = slot / p.cache.page_size;
-      in_page = static_cast<int>(slot - page * p.cache.page_size);
-    } else if (slot != -1) {
-      atomicOr(p.err, NVFP4_ATTENTION_BAD_INDEX);
-    }
+    stored = slot >= 0 && slot < p.cache.pages * p.cache.page_size;
+    if (!stored && slot != -1) atomicOr(p.err, NVFP4_ATTENTION_BAD_INDEX);
+    const int64_t page = slot >> 31 ? slot / p.cache.page_size
+                                    : static_cast<uint32_t>(slot) / static_cast<uint32_t>(p.cache.page_size);
+    const int64_t in_page = slot - page * p.cache.page_size;
+    off = kind == 2 ? page * p.cache.vs[0] + in_page * p.cache.vs[1] + h0 * p.cache.vs[2]
+                    : page * p.cache.ks[0] + in_page * p.cache.ks[1] + h0 * p.cache.ks[2];
+    next = kPerStep * (kind == 2 ? p.cache.vs[2] : p.cache.ks[2]);
+    out = kind == 2 ? p.cache.v : p.cache.k;
+  } else {
+    const Heads dst = kind == 0 ? p.q_out : p.k_out;
+    off = t * dst.ts + h0 * dst.hs;
+    next = kPerStep * dst.hs;
+    out = dst.data;
   }
 
 #pragma unroll
-  for (int s = 0; s < kSteps; ++s) {
+  for (int s = 0; s < kSteps; ++s, off += next) {
     const int h = h0 + s * kPerStep;
-    const bool is_q = h < p.q_heads, is_v = h >= p.q_heads + p.kv_heads;
     float y[8];
     unpack4(x[s][0], y);
     unpack4(x[s][1], y + 4);
-    float sq = 0.f;
+    if (kind < 2) {
+      float2 sq = mul2(make_float2(y[0], y[1]), make_float2(y[0], y[1]));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sq = fmaf(y[i], y[i], sq);
+      for (int i = 2; i < 8; i += 2) {
+        sq.x = fmaf(y[i], y[i], sq.x);
+        sq.y = fmaf(y[i + 1], y[i + 1], sq.y);
+      }
+      float sum = sq.x + sq.y;
 #pragma unroll
-    for (int m = kLanes / 2; m > 0; m >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, m);
-    if (!is_v) {
-      const float r = rsqrtf(sq * (1.f / kDim) + p.eps);
-      float wt[8];
-      unpack4(is_q ? qw[0] : kw[0], wt);
-      unpack4(is_q ? qw[1] : kw[1], wt + 4);
+      for (int m = kLanes / 2; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+      const float r = rsqrtf(sum * (1.f / kDim) + p.eps);
+      float2 z[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = y[i] * r * wt[i];
+      for (int i = 0; i < 4; ++i)
+        z[i] = mul2(mul2(make_float2(y[2 * i], y[2 * i + 1]), make_float2(r, r)), wt[i]);
+      // (lanes that do not turn: cosine 1, sine 0)
       if (turns) {
+        const float c4[4] = {cs.x, cs.y, cs.z, cs.w}, s4[4] = {sn.x, sn.y, sn.z, sn.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float a = y[i], b = y[i + 4];
+          const float a = i & 1 ? z[i >> 1].y : z[i >> 1].x;
+          const float b = i & 1 ? z[2 + (i >> 1)].y : z[2 + (i >> 1)].x;
           y[i] = a * c4[i] - b * s4[i];
           y[i + 4] = b * c4[i] + a * s4[i];
         }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[2 * i] = z[i].x, y[2 * i + 1] = z[i].y;
       }
     }
-    if (h >= heads) continue;
-    const int hh = is_q ? h : is_v ? h - p.q_heads - p.kv_heads : h - p.q_heads;
-    if (is_q || !p.store) {
-      const Heads& dst = is_q ? p.q_out : p.k_out;
-      __nv_bfloat16* row = dst.data + t * dst.ts + hh * dst.hs;
-      *reinterpret_cast<uint2*>(row + at0) = pack4(y);
-      *reinterpret_cast<uint2*>(row + at1) = pack4(y + 4);
-      continue;
-    }
-    if (page < 0) continue;
-    const int64_t* st = is_v ? p.cache.vs : p.cache.ks;
-    const int64_t off = page * st[0] + in_page * st[1] + hh * st[2];
-    void* base = is_v ? p.cache.v : p.cache.k;
-    if (p.cache.e4m3) {
-      const float* scales = is_v ? p.cache.v_scale : p.cache.k_scale;
-      const float scale = scales ? scales[hh] : 1.f;
+    if (h >= heads || !stored) continue;
+    if (narrow) {
+      const float* scales = kind == 2 ? p.cache.v_scale : p.cache.k_scale;
+      const float scale = scales ? scales[h] : 1.f;
       uint32_t c[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         c[i] = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * i] / scale, y[2 * i + 1] / scale),
                                         __NV_SATFINITE, __NV_E4M3);
-      uint8_t* row = static_cast<uint8_t*>(base) + off;
+      uint8_t* row = static_cast<uint8_t*>(out) + off;
       *reinterpret_cast<uint32_t*>(row + at0) = c[0] | c[1] << 16;
       *reinterpret_cast<uint32_t*>(row + at1) = c[2] | c[3] << 16;
     } else {
-      __nv_bfloat16* row = static_cast<__nv_bfloat16*>(base) + off;
+      __nv_bfloat16* row = static_cast<__nv_bfloat16*>(out) + off;
       *reinterpret_cast<uint2*>(row + at0) = pack4(y);
       *reinterpret_cast<uint2*>(row + at1) = pack4(y + 4);
     }
@@ -151,16 +171,18 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRope p, i
 }  // namespace
 
 int run_norm_rope(const NormRope& p, const Device&, cudaStream_t stream) {
-  const int heads = p.q_heads + p.kv_heads * (p.store ? 2 : 1);
   const int per_warp = kSteps * (256 / p.dim);
-  const int wpt = (heads + per_warp - 1) / per_warp;
-  const int64_t blocks = (p.tokens * wpt * 32 + kThreads - 1) / kThreads;
-  if (blocks > INT32_MAX) return NVFP4_ERR_SHAPE;
+  const int q_warps = (p.q_heads + per_warp - 1) / per_warp;
+  const int k_warps = (p.kv_heads + per_warp - 1) / per_warp;
+  // a block per token, or several where it has more heads than one holds
+  const int warps = q_warps + k_warps * (p.store ? 2 : 1);
+  const int blocks = (warps * 32 + kMaxThreads - 1) / kMaxThreads;
+  const int threads = (warps + blocks - 1) / blocks * 32;
   auto* kernel = p.dim == 256   ? norm_rope_kernel<256>
                  : p.dim == 128 ? norm_rope_kernel<128>
                                 : norm_rope_kernel<64>;
-  return launch(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, p, wpt,
-                heads);
+  return launch(kernel, dim3(static_cast<unsigned>(p.tokens), blocks), dim3(threads), 0, stream, p,
+                q_warps, k_warps);
 }
 
 }  // namespace attn
