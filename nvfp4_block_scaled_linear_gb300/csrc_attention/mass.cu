@@ -1,67 +1,263 @@
 // mass.cu -- the attention weight that each cached key receives from the new
-// tokens, one warp per sequence, key/value head and key.
+// tokens:  out[j] = mass[j] + sum over rows r that see j of 2^(c_r q_r . k_j - L_r)
+// with c_r the scores' scale times log2 e and L_r = lse_r log2 e.
+//
+// The keys stay and the queries pass by: a warp keeps 16 (or 32) keys' rows in
+// registers as the warp MMA's A operand, loaded once and straight from the
+// pages (a lane's 16-byte pieces are its operands when the k index inside an MMA
+// is permuted alike for the queries), and the query rows come through shared
+// memory, 32 at a time for the block's 8 warps.  Every row of scores is then a
+// column of the accumulator, so a key's sum stays with one lane group from the
+// first row to the last: no atomics, one order.
+//
+// A single token's call reads the keys once and is bound by that; a chunk of
+// them is bound by the products, 2 * head_dim flops a pair, and beside them the
+// shared-memory reads of the query operand, which 32 keys a warp halve.
+//
+// Over an e4m3 cache the codes are widened to f16 (exact) as they are loaded,
+// and each query row is scaled by a power of two (attend_warp.cu says why).
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
 #include "common.cuh"
 
 namespace nvfp4 {
 namespace attn {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStageRows = 32;                // query rows in shared memory at a time
 
-template <int kDim>
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
+  uint32_t d;
+  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}"
+      : "=r"(d)
+      : "r"(v));
+  return d;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// kTiles: 16-key MMA tiles of a warp.
+template <int kDim, bool kE4m3, int kTiles>
 __global__ void __launch_bounds__(kThreads) mass_kernel(const Mass p) {
-  constexpr int kPer = kDim / 32;
+  constexpr int kPitch = kDim * 2 + 16;                    // bytes of a query row
+  constexpr int kSteps = kDim / 16;
+  constexpr int kBlockKeys = kWarps * 16 * kTiles;
+  __shared__ __align__(16) uint8_t q_sm[2][kStageRows * kPitch];
+  __shared__ float2 row_sm[2][kStageRows];                 // (c, L) of a row
   griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t(blockIdx.x) * kThreads + threadIdx.x) >> 5;
-  const int64_t sh = w / p.room;
-  const int j = static_cast<int>(w - sh * p.room);
-  const int s = static_cast<int>(sh / p.cache.heads), kvh = static_cast<int>(sh % p.cache.heads);
-  if (s >= p.seqs.count) return;
+  griddep_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int s = blockIdx.z, kvh = blockIdx.y;
   const SeqInfo si = load_seq(p.seqs, s, p.err);
-  float sum = 0.f;
-  int64_t page = p.cache.pages;
-  if (j < si.kv_len)
-    page = checked_page(p.seqs.table[int64_t(s) * p.seqs.width + j / p.cache.page_size],
-                        p.cache.pages, p.err);
-  if (page != p.cache.pages) {
-    const float ks = (p.cache.k_scale ? p.cache.k_scale[kvh] : 1.f) * p.scale;
-    const int64_t ko = page * p.cache.ks[0] + (j % p.cache.page_size) * p.cache.ks[1] +
-                       kvh * p.cache.ks[2] + lane;
-    float k[kPer];
+  const int key0 = blockIdx.x * kBlockKeys;
+  const int64_t out0 = (int64_t(s) * p.cache.heads + kvh) * p.room;
+  const int my_key = key0 + warp * 16 * kTiles;
+  const int before = si.kv_len - si.q_len;                 // keys before the first new token
+  // the rows of this head's group, token by token; those that see key0 on
+  const int rows = si.q_len * p.group;
+  const int row0 = max(0, key0 - before) * p.group / kStageRows * kStageRows;
+  const bool any = key0 < si.kv_len && row0 < rows;
+
+  // ---- the keys: A operands, steps in an order of k that fits 16-byte pieces
+  uint32_t a[kTiles][kSteps][4];
+  if (any) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      k[i] = ks * (p.cache.e4m3
-                       ? e4m3_to_f32(static_cast<const uint8_t*>(p.cache.k)[ko + i * 32])
-                       : __bfloat162float(static_cast<const __nv_bfloat16*>(p.cache.k)[ko + i * 32]));
-    // the first new token that sees key j
-    for (int i = max(0, j - (si.kv_len - si.q_len)); i < si.q_len; ++i) {
-      const int64_t t = si.q0 + i;
-      for (int g = 0; g < p.group; ++g) {
-        const int h = kvh * p.group + g;
-        float x = 0.f;
+    for (int m = 0; m < kTiles; ++m)
 #pragma unroll
-        for (int e = 0; e < kPer; ++e)
-          x = fmaf(k[e], __bfloat162float(p.q.data[t * p.q.ts + h * p.q.hs + e * 32 + lane]), x);
+      for (int half = 0; half < 2; ++half) {
+        const int key = my_key + m * 16 + half * 8 + g;
+        int64_t page = p.cache.pages;
+        int in_page = 0;
+        if (key < si.kv_len) {
+          const int n = key / p.cache.page_size;
+          page = checked_page(p.seqs.table[int64_t(s) * p.seqs.width + n], p.cache.pages, p.err);
+          in_page = key - n * p.cache.page_size;
+        }
+        const bool valid = page != p.cache.pages;
+        const int64_t off = valid ? page * p.cache.ks[0] + in_page * p.cache.ks[1] + kvh * p.cache.ks[2] : 0;
+        constexpr int kPieces = kDim * (kE4m3 ? 1 : 2) / 64;     // 16-byte pieces of a lane
+        const uint8_t* row = static_cast<const uint8_t*>(p.cache.k) + off * (kE4m3 ? 1 : 2) + t * 16;
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-        sum += expf(x - p.lse[t * p.q_heads + h]);
+        for (int i = 0; i < kPieces; ++i) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (valid) v = *reinterpret_cast<const uint4*>(row + i * 64);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          if (kE4m3) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              a[m][(4 * i + j) % kSteps][half] = e4m3x2_to_f16x2(w[j] & 0xFFFFu);
+              a[m][(4 * i + j) % kSteps][2 + half] = e4m3x2_to_f16x2(w[j] >> 16);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              a[m][(2 * i + j) % kSteps][half] = w[2 * j];
+              a[m][(2 * i + j) % kSteps][2 + half] = w[2 * j + 1];
+            }
+          }
+        }
+      }
+  }
+
+  // ---- the rows: 8 threads to each, one stage ahead in registers
+  const float c0 = p.scale * 1.44269504088896f *
+                   (kE4m3 && p.cache.k_scale ? p.cache.k_scale[kvh] : 1.f);
+  constexpr int kVec = kDim / 64;                          // 16-byte pieces of a thread
+  const int my_row = tid >> 3, my_piece = tid & 7;
+  uint4 next[kVec];
+  float next_lse = 0.f;
+  auto fetch = [&](int r) {
+    const int tok = r / p.group, gi = r - tok * p.group;
+    const bool valid = r < rows;
+    const int64_t token = si.q0 + tok;
+    const int head = kvh * p.group + gi;
+    const __nv_bfloat16* src = p.q.data + token * p.q.ts + head * p.q.hs + my_piece * 8;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i)
+      next[i] = valid ? *reinterpret_cast<const uint4*>(src + i * 64) : make_uint4(0, 0, 0, 0);
+    next_lse = valid ? p.lse[token * p.q_heads + head] : 0.f;
+  };
+  auto put = [&](int b) {
+    float c = c0;
+    if (kE4m3) {
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        const uint32_t w[4] = {next[i].x, next[i].y, next[i].z, next[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[j])), fabsf(bf16_hi(w[j]))));
+      }
+#pragma unroll
+      for (int d = 4; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      int e = 141 - static_cast<int>(__float_as_uint(top) >> 23);
+      e = top == 0.f || top > 3.4e38f ? 0 : min(e, 100);
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+      c *= __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        uint32_t w[4] = {next[i].x, next[i].y, next[i].z, next[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = f32x2_to_f16x2(bf16_lo(w[j]) * up, bf16_hi(w[j]) * up);
+        next[i] = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
+#pragma unroll
+    for (int i = 0; i < kVec; ++i)
+      *reinterpret_cast<uint4*>(&q_sm[b][my_row * kPitch + (i * 8 + my_piece) * 16]) = next[i];
+    if (my_piece == 0) row_sm[b][my_row] = make_float2(c, next_lse * 1.44269504088896f);
+  };
+
+  float sum[kTiles][2];
+#pragma unroll
+  for (int m = 0; m < kTiles; ++m) sum[m][0] = sum[m][1] = 0.f;
+  if (any) {
+    fetch(row0 + my_row);
+    put(0);
+    __syncthreads();
+    int b = 0;
+    for (int r0 = row0; r0 < rows; r0 += kStageRows, b ^= 1) {
+      const bool more = r0 + kStageRows < rows;
+      if (more) fetch(r0 + kStageRows + my_row);
+      // rows that see this warp's last key, and so all of them, need no mask
+      const bool mask = r0 + kStageRows > rows ||
+                        r0 < max(0, my_key + 16 * kTiles - 1 - before) * p.group;
+#pragma unroll 1
+      for (int n = 0; n < kStageRows / 8; ++n) {
+        if (r0 + n * 8 >= rows) break;
+        float d[kTiles][4];
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d[m][i] = 0.f;
+        const uint8_t* qr = &q_sm[b][(n * 8 + g) * kPitch];
+#pragma unroll
+        for (int i = 0; i < kSteps; i += kE4m3 ? 4 : 2) {
+          // the pieces of this lane, in the order of the keys'
+          uint32_t w[8];
+          const uint4 lo = *reinterpret_cast<const uint4*>(qr + (kE4m3 ? (i / 4 * 4 + t) * 32 : (i / 2 * 4 + t) * 16));
+          w[0] = lo.x, w[1] = lo.y, w[2] = lo.z, w[3] = lo.w;
+          if (kE4m3) {
+            const uint4 hi = *reinterpret_cast<const uint4*>(qr + (i / 4 * 4 + t) * 32 + 16);
+            w[4] = hi.x, w[5] = hi.y, w[6] = hi.z, w[7] = hi.w;
+          }
+#pragma unroll
+          for (int j = 0; j < (kE4m3 ? 4 : 2); ++j)
+#pragma unroll
+            for (int m = 0; m < kTiles; ++m) {
+              const uint32_t(&am)[4] = a[m][(i + j) % kSteps];
+              if (kE4m3)
+                mma_f16_16816(d[m], am[0], am[1], am[2], am[3], w[2 * j], w[2 * j + 1]);
+              else
+                mma_bf16_16816(d[m], am[0], am[1], am[2], am[3], w[2 * j], w[2 * j + 1]);
+            }
+        }
+        // columns 2t, 2t + 1 of this tile: rows of queries
+        const float4 cl = *reinterpret_cast<const float4*>(&row_sm[b][n * 8 + 2 * t]);
+        const int r = r0 + n * 8 + 2 * t;
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            float e0 = ex2(fmaf(d[m][2 * half], cl.x, -cl.y));
+            float e1 = ex2(fmaf(d[m][2 * half + 1], cl.z, -cl.w));
+            if (mask) {
+              const int least = max(0, my_key + m * 16 + half * 8 + g - before) * p.group;
+              if (r < least || r >= rows) e0 = 0.f;
+              if (r + 1 < least || r + 1 >= rows) e1 = 0.f;
+            }
+            sum[m][half] += e0 + e1;
+          }
+      }
+      if (more) put(b ^ 1);
+      __syncthreads();
+    }
   }
-  if (lane == 0)
-    p.out[w] = j < si.kv_len ? (p.mass ? p.mass[w] : 0.f) + sum : 0.f;
+#pragma unroll
+  for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      float x = sum[m][half];
+      x += __shfl_xor_sync(0xffffffffu, x, 1);
+      x += __shfl_xor_sync(0xffffffffu, x, 2);
+      const int key = my_key + m * 16 + half * 8 + g;
+      if (t == 0 && key < p.room)
+        p.out[out0 + key] = key < si.kv_len ? (p.mass ? p.mass[out0 + key] : 0.f) + x : 0.f;
+    }
+}
+
+template <int kDim, bool kE4m3>
+int run(const Mass& p, cudaStream_t stream) {
+  // 32 keys a warp where the products count (more than a few tiles of 8 rows)
+  const bool two = int64_t(p.max_q_len) * p.group > 32;
+  const int keys = kWarps * 16 * (two ? 2 : 1);
+  const int64_t blocks = (p.room + keys - 1) / keys;
+  if (blocks > INT32_MAX || p.cache.heads > 65535 || p.seqs.count > 65535) return NVFP4_ERR_SHAPE;
+  return launch(two ? mass_kernel<kDim, kE4m3, 2> : mass_kernel<kDim, kE4m3, 1>,
+                dim3(static_cast<unsigned>(blocks), p.cache.heads, p.seqs.count), dim3(kThreads), 0,
+                stream, p);
 }
 
 }  // namespace
 
 int run_mass(const Mass& p, const Device&, cudaStream_t stream) {
-  const int64_t blocks = (p.room * p.seqs.count * p.cache.heads * 32 + kThreads - 1) / kThreads;
-  if (blocks > INT32_MAX) return NVFP4_ERR_SHAPE;
-  auto* kernel = p.cache.dim == 256   ? mass_kernel<256>
-                 : p.cache.dim == 128 ? mass_kernel<128>
-                                      : mass_kernel<64>;
-  return launch(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, p);
+  const bool f8 = p.cache.e4m3;
+  switch (p.cache.dim) {
+    case 64:
+      return f8 ? run<64, true>(p, stream) : run<64, false>(p, stream);
+    case 128:
+      return f8 ? run<128, true>(p, stream) : run<128, false>(p, stream);
+    default:
+      return f8 ? run<256, true>(p, stream) : run<256, false>(p, stream);
+  }
 }
 
 }  // namespace attn

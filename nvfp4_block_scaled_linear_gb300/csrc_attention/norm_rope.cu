@@ -17,8 +17,8 @@ namespace nvfp4 {
 namespace attn {
 namespace {
 
-constexpr int kSteps = 4;
-constexpr int kMaxThreads = 256;
+constexpr int kSteps = 2;
+constexpr int kMaxThreads = 128;
 
 __device__ __forceinline__ void unpack4(const uint2 w, float* f) {
   f[0] = bf16_lo(w.x), f[1] = bf16_hi(w.x), f[2] = bf16_lo(w.y), f[3] = bf16_hi(w.y);
