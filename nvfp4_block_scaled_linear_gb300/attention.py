@@ -18,11 +18,12 @@ kernels, on the current CUDA stream unless one is given.
 import ctypes
 import os
 import re
+import struct
 
 import torch
 
 from . import _lib
-from ._lib import OK, Nvfp4Error, _on_device
+from ._lib import OK, Nvfp4Error
 
 ATTENTION_HEADER = os.path.join(os.path.dirname(_lib.HEADER), "nvfp4_attention.h")
 
@@ -30,24 +31,11 @@ CACHE_BF16, CACHE_E4M3 = 0, 1
 ATTENTION_TIMEOUT, ATTENTION_BAD_INDEX = 1, 2
 
 
-class _Heads(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
-                ("head_stride", ctypes.c_int64)]
-
-
-class _Cache(ctypes.Structure):
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
-                ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3),
-                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
-                ("type", ctypes.c_int32), ("page_size", ctypes.c_int32),
-                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
-
-
-class _Seqs(ctypes.Structure):
-    _fields_ = [("block_table", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p),
-                ("q_starts", ctypes.c_void_p), ("count", ctypes.c_int32),
-                ("table_width", ctypes.c_int32), ("max_q_len", ctypes.c_int32)]
-
+# The C structures, packed into bytes (which a pointer argument takes as they
+# are: a ctypes.Structure costs several times as much to fill).
+_pack_heads = struct.Struct("@Pqq").pack                   # nvfp4_heads
+_pack_cache = struct.Struct("@PPqqqqqqqPPiiii").pack       # nvfp4_kv_cache
+_pack_seqs = struct.Struct("@PPPiii4x").pack               # nvfp4_sequences
 
 _ready = None
 
@@ -123,13 +111,11 @@ class KVCache:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.num_pages, self.page_size, self.kv_heads, self.head_dim = k.shape
         self.device = k.device
-        self._c = _Cache(
-            k.data_ptr(), v.data_ptr(), self.num_pages, (ctypes.c_int64 * 3)(*k.stride()[:3]),
-            (ctypes.c_int64 * 3)(*v.stride()[:3]),
-            k_scale.data_ptr() if k_scale is not None else None,
-            v_scale.data_ptr() if v_scale is not None else None,
+        self._c = _pack_cache(
+            k.data_ptr(), v.data_ptr(), self.num_pages, *k.stride()[:3], *v.stride()[:3],
+            0 if k_scale is None else k_scale.data_ptr(),
+            0 if v_scale is None else v_scale.data_ptr(),
             CACHE_E4M3 if e4m3 else CACHE_BF16, self.page_size, self.kv_heads, self.head_dim)
-        self._ref = ctypes.addressof(self._c)
 
 
 def new_kv_cache(num_pages, page_size, kv_heads, head_dim, dtype=torch.bfloat16, k_scale=None,
@@ -152,9 +138,9 @@ def _heads(t, name, tokens, heads, dim, device):
         raise ValueError("%s must have shape %s on %s, got %s on %s"
                          % (name, (tokens, heads, dim), device, tuple(t.shape), t.device))
     a, b, c = t.stride()
-    if c != 1 and dim > 1:
+    if c != 1:
         raise ValueError("the last dimension of %s must be dense" % name)
-    return _Heads(t.data_ptr(), a, b)
+    return _pack_heads(t.data_ptr(), a, b)
 
 
 def _flat(t, name, dtype, shape, device):
@@ -166,10 +152,21 @@ def _flat(t, name, dtype, shape, device):
     return t.data_ptr()
 
 
-def _stream(stream, device):
+def _call(function, device, stream, *args):
+    """One library call on `stream` (the device's current one by default)."""
+    index = device.index
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    return stream.cuda_stream
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    f = getattr(_ready or _library(), function)
+    if index == torch._C._cuda_getDevice():
+        st = f(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            st = f(*args, stream)
+    if st != OK:
+        raise Nvfp4Error(st, function)
 
 
 def _norm_rope(q, k, v, q_weight, k_weight, cos_sin, positions, eps, q_out, k_out, cache, slots,
@@ -185,21 +182,16 @@ def _norm_rope(q, k, v, q_weight, k_weight, cos_sin, positions, eps, q_out, k_ou
     rows = 0 if cos_sin is None else cos_sin.shape[0]
     qh, kh = _heads(q, "q", tokens, hq, dim, dev), _heads(k, "k", tokens, hk, dim, dev)
     qo = _heads(q_out, "q_out", tokens, hq, dim, dev)
-    ko = None if k_out is None else ctypes.byref(_heads(k_out, "k_out", tokens, hk, dim, dev))
-    vh = None if v is None else ctypes.byref(_heads(v, "v", tokens, hk, dim, dev))
-    with _on_device(dev):
-        st = _library().nvfp4_qk_norm_rope(
-            ctypes.byref(qh), ctypes.byref(kh), vh, tokens, hq, hk, dim,
-            _flat(q_weight, "q_weight", torch.bfloat16, (dim,), dev),
-            _flat(k_weight, "k_weight", torch.bfloat16, (dim,), dev), eps,
-            None if cos_sin is None else _flat(cos_sin, "cos_sin", torch.float32, (rows, rot), dev),
-            rows, rot,
-            None if positions is None else _flat(positions, "positions", torch.int64, (tokens,), dev),
-            ctypes.byref(qo), ko, None if cache is None else cache._ref,
-            None if slots is None else _flat(slots, "slots", torch.int64, (tokens,), dev),
-            _stream(stream, dev))
-    if st != OK:
-        raise Nvfp4Error(st, "nvfp4_qk_norm_rope")
+    ko = None if k_out is None else _heads(k_out, "k_out", tokens, hk, dim, dev)
+    vh = None if v is None else _heads(v, "v", tokens, hk, dim, dev)
+    _call("nvfp4_qk_norm_rope", dev, stream, qh, kh, vh, tokens, hq, hk, dim,
+          _flat(q_weight, "q_weight", torch.bfloat16, (dim,), dev),
+          _flat(k_weight, "k_weight", torch.bfloat16, (dim,), dev), eps,
+          None if cos_sin is None else _flat(cos_sin, "cos_sin", torch.float32, (rows, rot), dev),
+          rows, rot,
+          None if positions is None else _flat(positions, "positions", torch.int64, (tokens,), dev),
+          qo, ko, None if cache is None else cache._c,
+          None if slots is None else _flat(slots, "slots", torch.int64, (tokens,), dev))
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps=1e-6, q_out=None, k_out=None,
@@ -231,22 +223,36 @@ def qk_norm_rope_store(q, k, v, q_weight, k_weight, cos_sin, positions, cache, s
 def _seqs(cache, block_table, kv_lens, q_starts, max_q_len):
     dev = cache.device
     n, width = block_table.shape
-    return _Seqs(_flat(block_table, "block_table", torch.int32, (n, width), dev),
-                 _flat(kv_lens, "kv_lens", torch.int32, (n,), dev),
-                 None if q_starts is None else _flat(q_starts, "q_starts", torch.int32, (n + 1,), dev),
-                 n, width, max_q_len)
+    return _pack_seqs(
+        _flat(block_table, "block_table", torch.int32, (n, width), dev),
+        _flat(kv_lens, "kv_lens", torch.int32, (n,), dev),
+        0 if q_starts is None else _flat(q_starts, "q_starts", torch.int32, (n + 1,), dev),
+        n, width, max_q_len)
 
 
 _workspace_bytes = {}
+_workspaces = {}
 
 
 def attention_workspace(cache):
     """A workspace for ``paged_attention`` calls that run one after another."""
     key = (cache.device.index, cache.head_dim)
     if key not in _workspace_bytes:
-        with _on_device(cache.device):
+        with torch.cuda.device(cache.device):
             _workspace_bytes[key] = _library().nvfp4_paged_attention_workspace(cache.head_dim)
     return torch.empty(_workspace_bytes[key], dtype=torch.uint8, device=cache.device)
+
+
+def _stream_workspace(cache, stream):
+    """The workspace of the calls on one stream, which run one after another;
+    a call that is being captured into a graph gets one of its own."""
+    if torch.cuda.is_current_stream_capturing():
+        return attention_workspace(cache)
+    key = (cache.device.index, cache.head_dim, stream)
+    w = _workspaces.get(key)
+    if w is None:
+        w = _workspaces[key] = attention_workspace(cache)
+    return w
 
 
 def paged_attention(q, cache, block_table, kv_lens, q_starts, max_q_len, scale=None, out=None,
@@ -268,22 +274,16 @@ def paged_attention(q, cache, block_table, kv_lens, q_starts, max_q_len, scale=N
     if out is None:
         out = torch.empty((tokens, hq, dim), dtype=torch.bfloat16, device=dev)
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
+        stream = torch._C._cuda_getCurrentRawStream(dev.index)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
     if workspace is None:
-        # from the caching allocator, for the stream that will use it
-        with torch.cuda.stream(stream):
-            workspace = attention_workspace(cache)
-    seqs = _seqs(cache, block_table, kv_lens, q_starts, max_q_len)
-    qh, oh = _heads(q, "q", tokens, hq, dim, dev), _heads(out, "out", tokens, hq, dim, dev)
-    with _on_device(dev):
-        st = _library().nvfp4_paged_attention(
-            ctypes.byref(qh), tokens, hq, cache._ref, ctypes.byref(seqs),
-            dim ** -0.5 if scale is None else scale, ctypes.byref(oh),
-            None if lse is None else _flat(lse, "lse", torch.float32, (tokens, hq), dev),
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-            stream.cuda_stream)
-    if st != OK:
-        raise Nvfp4Error(st, "nvfp4_paged_attention")
+        workspace = _stream_workspace(cache, stream)
+    _call("nvfp4_paged_attention", dev, stream, _heads(q, "q", tokens, hq, dim, dev), tokens, hq,
+          cache._c, _seqs(cache, block_table, kv_lens, q_starts, max_q_len),
+          dim ** -0.5 if scale is None else scale, _heads(out, "out", tokens, hq, dim, dev),
+          None if lse is None else _flat(lse, "lse", torch.float32, (tokens, hq), dev),
+          workspace.data_ptr(), workspace.nbytes)
     return out
 
 
@@ -301,24 +301,19 @@ def attention_mass(q, cache, block_table, kv_lens, q_starts, max_q_len, lse, mas
         raise ValueError("the cache holds %d heads of %d on %s, q has %d of %d on %s"
                          % (cache.kv_heads, cache.head_dim, cache.device, hq, dim, dev))
     seqs = _seqs(cache, block_table, kv_lens, q_starts, max_q_len)
+    n, width = block_table.shape
     if out is None:
-        shape = ((seqs.count, cache.kv_heads, seqs.table_width * cache.page_size)
-                 if mass is None else mass.shape)
+        shape = (n, cache.kv_heads, width * cache.page_size) if mass is None else mass.shape
         out = torch.empty(shape, dtype=torch.float32, device=dev)
     if out.dim() != 3:
         raise ValueError("out must be [sequences, kv_heads, room], got %s" % (tuple(out.shape),))
     room = out.shape[2]
-    shape = (seqs.count, cache.kv_heads, room)
-    qh = _heads(q, "q", tokens, hq, dim, dev)
-    with _on_device(dev):
-        st = _library().nvfp4_attention_mass(
-            ctypes.byref(qh), tokens, hq, cache._ref, ctypes.byref(seqs),
-            dim ** -0.5 if scale is None else scale,
-            _flat(lse, "lse", torch.float32, (tokens, hq), dev),
-            None if mass is None else _flat(mass, "mass", torch.float32, shape, dev),
-            _flat(out, "out", torch.float32, shape, dev), room, _stream(stream, dev))
-    if st != OK:
-        raise Nvfp4Error(st, "nvfp4_attention_mass")
+    shape = (n, cache.kv_heads, room)
+    _call("nvfp4_attention_mass", dev, stream, _heads(q, "q", tokens, hq, dim, dev), tokens, hq,
+          cache._c, seqs, dim ** -0.5 if scale is None else scale,
+          _flat(lse, "lse", torch.float32, (tokens, hq), dev),
+          None if mass is None else _flat(mass, "mass", torch.float32, shape, dev),
+          _flat(out, "out", torch.float32, shape, dev), room)
     return out
 
 
@@ -334,7 +329,7 @@ def evict(cache, block_table, kv_lens, mass, keep, recent, to, to_table, index=N
     seqs = _seqs(cache, block_table, kv_lens, None, 0)
     if mass.dim() != 3:
         raise ValueError("mass must be [sequences, kv_heads, room], got %s" % (tuple(mass.shape),))
-    n, hk, room = seqs.count, cache.kv_heads, mass.shape[2]
+    n, hk, room = block_table.shape[0], cache.kv_heads, mass.shape[2]
     if index is None:
         index = torch.empty((n, hk, keep), dtype=torch.int32, device=dev)
     if new_mass is None:
@@ -343,14 +338,10 @@ def evict(cache, block_table, kv_lens, mass, keep, recent, to, to_table, index=N
         new_lens = torch.empty(n, dtype=torch.int32, device=dev)
     if to.device != dev or to_table.dim() != 2:
         raise ValueError("to must live on %s and to_table be 2-D" % dev)
-    with _on_device(dev):
-        st = _library().nvfp4_cache_evict(
-            cache._ref, ctypes.byref(seqs),
-            _flat(mass, "mass", torch.float32, (n, hk, room), dev), room, keep, recent, to._ref,
-            _flat(to_table, "to_table", torch.int32, (n, to_table.shape[1]), dev),
-            to_table.shape[1], _flat(index, "index", torch.int32, (n, hk, keep), dev),
-            _flat(new_mass, "new_mass", torch.float32, (n, hk, keep), dev),
-            _flat(new_lens, "new_lens", torch.int32, (n,), dev), _stream(stream, dev))
-    if st != OK:
-        raise Nvfp4Error(st, "nvfp4_cache_evict")
+    _call("nvfp4_cache_evict", dev, stream, cache._c, seqs,
+          _flat(mass, "mass", torch.float32, (n, hk, room), dev), room, keep, recent, to._c,
+          _flat(to_table, "to_table", torch.int32, (n, to_table.shape[1]), dev), to_table.shape[1],
+          _flat(index, "index", torch.int32, (n, hk, keep), dev),
+          _flat(new_mass, "new_mass", torch.float32, (n, hk, keep), dev),
+          _flat(new_lens, "new_lens", torch.int32, (n,), dev))
     return new_lens, index, new_mass

@@ -33,20 +33,36 @@ def test_exports_and_constants(lib):
         assert getattr(att, "ATTENTION_" + name) == value
 
 
+class _Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("type", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class _Seqs(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("q_starts", ctypes.c_void_p),
+                ("count", ctypes.c_int32), ("table_width", ctypes.c_int32), ("max_q_len", ctypes.c_int32)]
+
+
 def heads(data=A, ts=1024, hs=256):
-    return att._Heads(data, ts, hs)
+    return _Heads(data, ts, hs)
 
 
 def cache(**kw):
-    c = att._Cache(A, A, 8, (ctypes.c_int64 * 3)(16384, 256, 4096), (ctypes.c_int64 * 3)(16384, 256, 4096),
-                   None, None, 0, 16, 4, 256)
+    c = _Cache(A, A, 8, (ctypes.c_int64 * 3)(16384, 256, 4096), (ctypes.c_int64 * 3)(16384, 256, 4096), None, None, 0, 16,
+               4, 256)
     for k, v in kw.items():
         setattr(c, k, v)
     return c
 
 
 def seqs(**kw):
-    s = att._Seqs(A, A, A, 2, 4, 1)
+    s = _Seqs(A, A, A, 2, 4, 1)
     for k, v in kw.items():
         setattr(s, k, v)
     return s
@@ -54,6 +70,14 @@ def seqs(**kw):
 
 def ref(x):
     return None if x is None else ctypes.byref(x)
+
+
+def test_packed_structures_have_the_c_layout():
+    assert len(att._pack_heads(A, 8, 16)) == ctypes.sizeof(_Heads)
+    assert att._pack_heads(A, 8, 16) == bytes(_Heads(A, 8, 16))
+    a = att._pack_cache(1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15)
+    assert a == bytes(_Cache(1, 2, 3, (ctypes.c_int64 * 3)(4, 5, 6), (ctypes.c_int64 * 3)(7, 8, 9), 10, 11, 12, 13, 14, 15))
+    assert att._pack_seqs(1, 2, 3, 4, 5, 6) == bytes(_Seqs(1, 2, 3, 4, 5, 6))
 
 
 BAD_CACHES = [(None, INVALID), (cache(k=None), INVALID), (cache(type=2), INVALID), (cache(num_pages=0), INVALID),
