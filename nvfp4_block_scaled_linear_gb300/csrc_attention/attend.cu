@@ -110,7 +110,7 @@ int64_t attend_workspace(int head_dim, const Device& d) {
 
 bool countable(const Seqs& s, int heads, const Plan& p) {
   const double items = double(heads) * (double(s.tokens) / p.tile_tokens + s.count);
-  return items * (double(s.max_kv >> p.unit_shift) + 1) < 4294967296.0;
+  return items * (double(s.max_kv >> p.unit_shift) + 1 + p.extra) < 4294967296.0;
 }
 
 int run_attend(const Attend& p, const Device& d, cudaStream_t stream) {

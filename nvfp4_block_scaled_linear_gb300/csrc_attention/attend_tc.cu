@@ -49,6 +49,7 @@ namespace {
 constexpr int kM = 128;                       // rows of a tile
 constexpr int kBlockShift = 7;
 constexpr int kN = 1 << kBlockShift;          // keys of a block (one unit)
+constexpr int kExtra = 2;                     // blocks that an item's beginning costs
 constexpr float kSlack = 8.f;                 // growth of log2 of a weight before rescaling
 constexpr int kItems = 4;                     // item descriptors in flight
 constexpr int kQFactors = 4;                  // items whose row factors are held
@@ -194,12 +195,12 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
-  uint32_t d;
-  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}"
-      : "=r"(d)
+// Four e4m3 codes as two f16x2: exact.
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t v, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
       : "r"(v));
-  return d;
 }
 
 // Whether any of a word's two 16-bit values is not finite.
@@ -384,7 +385,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
     Item it{};
     if (w.more())
       it = Item{w.r.s, w.r.h, w.seq.q0, w.seq.q_len, w.seq.kv_len, w.r.tile * p.plan.tile_tokens,
-                w.r.unit0 * kN, w.count | (w.begins() ? kBegins : 0) | (w.ends() ? kEnds : 0)};
+                w.unit0 * kN, w.count | (w.begins() ? kBegins : 0) | (w.ends() ? kEnds : 0)};
     items.ring[i % kItems] = it;
     mbar_arrive(&items.full[i % kItems]);
     return w.more();
@@ -543,12 +544,13 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
     Place at;
     at.start(items);
     __syncwarp();
-    // lane i: where the block's rows 16 i on are (pages hold whole sixteens), or
-    // -1 past the length; read one block ahead
-    int64_t group = -1;
+    // lane i: where the block's rows 16 i on are (pages hold whole sixteens), read
+    // one block ahead; past the length the cache's first rows, whose scores are
+    // masked and whose values become zero
+    int64_t group = 0;
     auto look_up = [&]() {
       const int key = at.it.key0 + at.b * kN + (lane & 7) * 16;
-      group = -1;
+      group = 0;
       if (at.live && key < at.it.kv_len) {
         const int64_t page = checked_page(
             a.seqs.table[int64_t(at.it.s) * a.seqs.width + key / a.cache.page_size], a.cache.pages,
@@ -563,14 +565,12 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
     const uint8_t* from = nullptr;
     auto load = [&](int64_t where, int u, int i) {
       if (i % kOfGroup == 0) {
-        const int64_t off =
-            __shfl_sync(0xffffffffu, where, (kV ? u : u % kHalves) * kGroups + i / kOfGroup);
-        from = off < 0 ? nullptr : base + off + (kV ? 0 : u / kHalves * C::kKChunks * 64);
-      } else if (from) {
+        from = base + (kV ? 0 : u / kHalves * C::kKChunks * 64) +
+               __shfl_sync(0xffffffffu, where, (kV ? u : u % kHalves) * kGroups + i / kOfGroup);
+      } else {
         from += step;
       }
-      v[i] = make_uint4(0, 0, 0, 0);
-      if (from) v[i] = *reinterpret_cast<const uint4*>(from);
+      v[i] = *reinterpret_cast<const uint4*>(from);
     };
     look_up();
 #pragma unroll
@@ -602,10 +602,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
           uint32_t f[8];
           const uint32_t cw[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            f[2 * k] = e4m3x2_to_f16x2(cw[k] & 0xFFFFu);
-            f[2 * k + 1] = e4m3x2_to_f16x2(cw[k] >> 16);
-          }
+          for (int k = 0; k < 4; ++k) e4m3x4_to_f16x4(cw[k], f[2 * k], f[2 * k + 1]);
           load(where, next_u, i);
           uint8_t* at_row = slot + (i >> 1) * (2 * kRowsAtOnce * 128);
           *reinterpret_cast<uint4*>(at_row + put[i & 1][0]) = make_uint4(f[0], f[1], f[2], f[3]);
@@ -1011,7 +1008,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
       if (lane == 0) {
         int item = 0;
         const int rows = p.tile_tokens * a.group;
-        Walk w(range, a.seqs, p.plan, a.err);
+        Walk w(range, a.seqs, a.cache.heads, p.plan, a.err);
         while (publish(w, item)) {
           if (item > 0 && !wait(q_empty, (item - 1) & 1, abort_flag)) break;
           mbar_arrive_expect_tx(q_full, kTiles * (kDim / 64) * rows * 128);
@@ -1035,9 +1032,9 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
       // ---------------------------------- Q rows scaled to f16 (warps 8, 10, 11)
       const int part = warp == 8 ? 0 : warp - 9;
       constexpr int kLanes = kDim / 8;              // of a row, 8 elements each
-      constexpr int kRowsAtOnce = 32 / kLanes, kPasses = 4;
+      constexpr int kRowsAtOnce = 32 / kLanes, kPasses = kDim == 256 ? 8 : 4;
       const int ql = lane % kLanes;
-      Walk w(range, a.seqs, p.plan, a.err);         // warp 11: the schedule
+      Walk w(range, a.seqs, a.cache.heads, p.plan, a.err);         // warp 11: the schedule
       if (warp == 11 && lane == 0) publish(w, 0);
       __syncwarp();
       Item it;
@@ -1147,7 +1144,7 @@ int run(const Attend& a, const Device& d, cudaStream_t stream) {
   if (const int st = allow_smem(kernel, C::kSmem, d, ready)) return st;
   const int units = d.num_sms / kCluster;
   TcParams p{a, {}, Parts(a.workspace, units, kM, kTiles * kCluster, kDim), kM / a.group, 0};
-  p.plan = Plan{kTiles * kCluster * p.tile_tokens, kBlockShift, 1};
+  p.plan = Plan{kTiles * kCluster * p.tile_tokens, kBlockShift, 1, kExtra};
   if (!countable(a.seqs, a.cache.heads, p.plan)) return NVFP4_ERR_SHAPE;
   p.box_shift = 4;
   while (p.box_shift < 7 && a.cache.page_size % (2 << p.box_shift) == 0) ++p.box_shift;
@@ -1161,7 +1158,7 @@ int run(const Attend& a, const Device& d, cudaStream_t stream) {
   if (const int st = launch_clusters(kCluster, kernel, dim3(units * kCluster), dim3(C::kThreads),
                                      C::kSmem, stream, tm_q, tm_k, tm_v, p))
     return st;
-  return run_join(a, p.parts, p.plan, units, stream);
+  return run_join(a, p.parts, p.plan, units, d.id, stream);
 }
 
 // One tile of rows; more: two tiles in a CTA, or in a pair of CTAs where one

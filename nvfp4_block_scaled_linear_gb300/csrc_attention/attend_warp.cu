@@ -35,6 +35,7 @@ constexpr int kThreads = kConsumers + 32;
 constexpr int kUnitShift = 4;
 constexpr int kUnit = 1 << kUnitShift;        // keys of one warp in a block
 constexpr int kSlotKeys = 64;
+constexpr int kExtra = 8;                     // units that an item's beginning costs
 constexpr int kPPitch = 128 * 2 + 16;         // bytes of a row of weights
 
 template <int kDim, bool kE4m3, int kR>
@@ -186,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<kDim, kE4m3, kR>::kCtas)
   griddep_launch_dependents();
   const Range range = find_range(p.seqs, p.cache.heads, plan, blockIdx.x,
                                  gridDim.x, range_sm, p.err);
-  Walk w(range, p.seqs, plan, p.err);
+  Walk w(range, p.seqs, p.cache.heads, plan, p.err);
 
   if (warp == kWarps) {
     // ------------------------------------------------------------ producer
@@ -196,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<kDim, kE4m3, kR>::kCtas)
       for (int u0 = 0; u0 < w.count && ok; u0 += kWarps) {
         const int n = min(kWarps, w.count - u0);  // units of this block
         const int u = lane & 7;
-        const int key = (w.r.unit0 + u0 + u) * kUnit;
+        const int key = (w.unit0 + u0 + u) * kUnit;
         int page = 0, in_page = 0;
         if (u < n) {
           // the last unit of a sequence may start past its length when it
@@ -336,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<kDim, kE4m3, kR>::kCtas)
       for (int u0 = 0; u0 < w.count; u0 += kWarps) {
         const int n = min(kWarps, w.count - u0);
         const int slots = (n + 3) / 4;
-        const int key0 = (w.r.unit0 + u0) * kUnit;
+        const int key0 = (w.unit0 + u0) * kUnit;
         // ---- scores of this warp's 16 keys
         float s[kR][2][4];
 #pragma unroll
@@ -678,14 +679,14 @@ int run(const Attend& p, const Device& d, cudaStream_t stream) {
   if (!page_map(&tm_k, p.cache, false, inner, kUnit, C::kChunks) ||
       !page_map(&tm_v, p.cache, true, inner, kUnit, C::kChunks))
     return NVFP4_ERR_LAUNCH;
-  const Plan plan{std::max(1, C::kRows / p.group), kUnitShift, 4};
+  const Plan plan{std::max(1, C::kRows / p.group), kUnitShift, 4, kExtra};
   if (!countable(p.seqs, p.cache.heads, plan)) return NVFP4_ERR_SHAPE;
   const int ctas = d.num_sms * C::kCtas;
   const Parts parts(p.workspace, ctas, C::kRows, 1, kDim);
   if (const int st = launch(kernel, dim3(ctas), dim3(kThreads), C::kSmem, stream, tm_k, tm_v, p,
                             plan, parts))
     return st;
-  return run_join(p, parts, plan, ctas, stream);
+  return run_join(p, parts, plan, ctas, d.id, stream);
 }
 
 template <int kDim, bool kE4m3>

@@ -96,11 +96,23 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Attend p, const Pa
 
 }  // namespace
 
-int run_join(const Attend& p, const Parts& parts, const Plan& plan, int ctas,
+int run_join(const Attend& p, const Parts& parts, const Plan& plan, int ctas, int device,
              cudaStream_t stream) {
   auto* kernel = p.cache.dim == 256   ? join_kernel<256>
                  : p.cache.dim == 128 ? join_kernel<128>
                                       : join_kernel<64>;
+  // The attention kernels leave the SMs with all memory given to shared memory;
+  // blocks that ask for another split could only start when those have ended.
+  static std::atomic<bool> ready[3][kMaxDevices];
+  std::atomic<bool>& set = ready[p.cache.dim / 128][device];
+  if (!set.load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared) != cudaSuccess) {
+      cudaGetLastError();
+      return NVFP4_ERR_LAUNCH;
+    }
+    set.store(true, std::memory_order_release);
+  }
   return launch(kernel, dim3(ctas, parts.rows), dim3(kThreads), 0, stream, p,
                 parts, plan, ctas);
 }

@@ -5,9 +5,11 @@
 // that its last token sees, one at least.  Items are ordered by sequence,
 // head and tile, and the units of all items, end to end, are cut into equal
 // ranges, one per CTA: long sequences are split over many CTAs, short ones
-// share one, and causal tiles of different length balance.  A range that
-// begins or ends inside an item leaves a partial result for the join kernel.
-// The lengths live on the device, so each CTA finds its own range.
+// share one, and causal tiles of different length balance.  An item counts
+// `extra` units more than it has, ahead of its first, for what it costs to
+// begin and to end one.  A range that begins or ends inside an item leaves a
+// partial result for the join kernel.  The lengths live on the device, so each
+// CTA finds its own range.
 #pragma once
 #include "common.cuh"
 
@@ -20,6 +22,7 @@ struct Plan {
   int tile_tokens;                          // tokens of one tile
   int unit_shift;                           // log2 of the keys of one unit
   int min_units;                            // least units worth a CTA of its own
+  int extra;                                // units that beginning an item costs
 };
 
 __device__ __forceinline__ int tiles_of(const SeqInfo& s, const Plan& p) {
@@ -35,6 +38,7 @@ __device__ __forceinline__ int tile_keys(const SeqInfo& s, int tile, const Plan&
   return max(0, s.kv_len - s.q_len + last);
 }
 
+// Units of an item; with `extra`, what it counts.
 __device__ __forceinline__ int tile_units(const SeqInfo& s, int tile, const Plan& p) {
   return max(1, (tile_keys(s, tile, p) + (1 << p.unit_shift) - 1) >> p.unit_shift);
 }
@@ -52,8 +56,8 @@ __device__ __forceinline__ uint32_t warp_inclusive(uint32_t v) {
 
 // Where a CTA's range begins, and how many units it holds.
 struct Range {
-  uint32_t left;
-  int s, h, tile, unit0;
+  uint32_t left;           // counted units
+  int s, h, tile, at;      // `at`: counted units of the item before the range
 };
 
 struct RangeSmem {
@@ -71,6 +75,7 @@ __device__ inline Range find_range(const Seqs& q, int heads, const Plan& p, uint
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int warps = blockDim.x >> 5, batches = (q.count + 31) / 32;
   uint32_t begin = 0;
+  SeqInfo mine{0, 0, 0};
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     uint32_t before = 0;                    // units of the batches before b
@@ -88,10 +93,11 @@ __device__ inline Range find_range(const Seqs& q, int heads, const Plan& p, uint
         continue;
       }
       const int s = b * 32 + lane;
-      const SeqInfo mine = s < q.count ? load_seq(q, s, err) : SeqInfo{0, 0, 0};
+      if (pass == 0 || batches > 1)
+        mine = s < q.count ? load_seq(q, s, err) : SeqInfo{0, 0, 0};
       // units of one head of each lane's sequence
       const int tiles = tiles_of(mine, p);
-      uint32_t one = tiles == 1 ? tile_units(mine, 0, p) : 0;
+      uint32_t one = tiles == 1 ? tile_units(mine, 0, p) + p.extra : 0;
       unsigned many = __ballot_sync(0xffffffffu, tiles > 1);
 #pragma unroll 1
       while (many) {
@@ -102,7 +108,7 @@ __device__ inline Range find_range(const Seqs& q, int heads, const Plan& p, uint
         const int n = __shfl_sync(0xffffffffu, tiles, src);
         uint32_t sum = 0;
 #pragma unroll 1
-        for (int i = lane; i < n; i += 32) sum += tile_units(o, i, p);
+        for (int i = lane; i < n; i += 32) sum += tile_units(o, i, p) + p.extra;
         sum = __reduce_add_sync(0xffffffffu, sum);
         if (lane == src) one = sum;
       }
@@ -126,7 +132,7 @@ __device__ inline Range find_range(const Seqs& q, int heads, const Plan& p, uint
       unsigned past;
 #pragma unroll 1
       for (;; t0 += 32) {
-        u = t0 + lane < n ? tile_units(o, t0 + lane, p) : 0;
+        u = t0 + lane < n ? tile_units(o, t0 + lane, p) + p.extra : 0;
         sum = warp_inclusive(u);
         past = __ballot_sync(0xffffffffu, sum > at);
         if (past || t0 >= n) break;
@@ -137,7 +143,7 @@ __device__ inline Range find_range(const Seqs& q, int heads, const Plan& p, uint
         sm->range.s = b * 32 + src;
         sm->range.h = static_cast<int>(h);
         sm->range.tile = t0 + i;
-        sm->range.unit0 = static_cast<int>(at - (sum - u));
+        sm->range.at = static_cast<int>(at - (sum - u));
       }
       break;
     }
@@ -162,25 +168,43 @@ struct Walk {
   Range r;
   SeqInfo seq;
   int units;          // of the item
-  int count;          // of them in this range, from r.unit0
+  int unit0, count;   // the range's part of them
 
-  __device__ Walk(const Range& range, const Seqs& q, const Plan& p, unsigned int* err) : r(range) {
+  __device__ Walk(const Range& range, const Seqs& q, int heads, const Plan& p, unsigned int* err)
+      : r(range) {
     if (r.left > 0) {
       seq = load_seq(q, r.s, err);
-      item(p);
+      settle(q, heads, p, err);
     }
   }
   __device__ bool more() const { return r.left > 0; }
-  __device__ bool begins() const { return r.unit0 == 0; }
-  __device__ bool ends() const { return r.unit0 + count == units; }
-  __device__ void item(const Plan& p) {
-    units = tile_units(seq, r.tile, p);
-    count = static_cast<int>(min(static_cast<uint32_t>(units - r.unit0), r.left));
-  }
+  __device__ bool begins() const { return unit0 == 0; }
+  __device__ bool ends() const { return unit0 + count == units; }
   __device__ void next(const Seqs& q, int heads, const Plan& p, unsigned int* err) {
-    r.left -= count;
-    r.unit0 = 0;
-    if (r.left == 0) return;
+    step(q, heads, p, err);
+    settle(q, heads, p, err);
+  }
+
+ private:
+  // On to the first item of which the range holds more than the `extra`.
+  __device__ void settle(const Seqs& q, int heads, const Plan& p, unsigned int* err) {
+    while (r.left > 0) {
+      units = tile_units(seq, r.tile, p);
+      const int end = static_cast<int>(min(static_cast<uint32_t>(units + p.extra - r.at), r.left)) + r.at;
+      unit0 = max(0, r.at - p.extra);
+      count = max(0, end - p.extra) - unit0;
+      if (count > 0) return;
+      step(q, heads, p, err);
+    }
+  }
+  __device__ void step(const Seqs& q, int heads, const Plan& p, unsigned int* err) {
+    const uint32_t here = units + p.extra - r.at;
+    r.at = 0;
+    if (here >= r.left) {
+      r.left = 0;
+      return;
+    }
+    r.left -= here;
     if (++r.tile == tiles_of(seq, p)) {
       r.tile = 0;
       if (++r.h == heads) {
@@ -194,7 +218,6 @@ struct Walk {
         } while (seq.q_len == 0);
       }
     }
-    item(p);
   }
 };
 
@@ -227,7 +250,8 @@ struct Parts {
   }
 };
 
-int run_join(const Attend& p, const Parts& parts, const Plan& plan, int ctas, cudaStream_t stream);
+int run_join(const Attend& p, const Parts& parts, const Plan& plan, int ctas, int device,
+             cudaStream_t stream);
 
 }  // namespace attn
 }  // namespace nvfp4
