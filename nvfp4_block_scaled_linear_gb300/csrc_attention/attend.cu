@@ -92,15 +92,15 @@ bool page_map(CUtensorMap* map, const Cache& c, bool values, int inner, int rows
   return encode(map, key);
 }
 
-bool query_map(CUtensorMap* map, const Attend& a, int tokens) {
+bool query_map(CUtensorMap* map, const Heads& q, int dim, int heads, int tokens, int group, int box) {
   MapKey key;
   std::memset(&key, 0, sizeof(key));
-  key.base = a.q.data;
+  key.base = q.data;
   key.rank = 3;
   key.bytes = 2;
-  key.dims[0] = a.cache.dim, key.dims[1] = a.q_heads, key.dims[2] = a.seqs.tokens;
-  key.strides[0] = a.q.hs * 2, key.strides[1] = a.q.ts * 2;
-  key.box[0] = 64, key.box[1] = a.group, key.box[2] = tokens;
+  key.dims[0] = dim, key.dims[1] = heads, key.dims[2] = tokens;
+  key.strides[0] = q.hs * 2, key.strides[1] = q.ts * 2;
+  key.box[0] = 64, key.box[1] = group, key.box[2] = box;
   return encode(map, key);
 }
 
@@ -115,7 +115,14 @@ bool countable(const Seqs& s, int heads, const Plan& p) {
 
 int run_attend(const Attend& p, const Device& d, cudaStream_t stream) {
   const int64_t rows = int64_t(std::max(1, p.max_q_len)) * p.group;
-  return rows <= 64 ? run_attend_warp(static_cast<int>(rows), p, d, stream)
+  // The warp MMA costs some 34 cycles for each 16 x 8 x 16 on an SM quarter, so
+  // its time grows with every 16 rows where that of the tcgen05 kernel stands
+  // still: 7 tokens x 6 heads (42 rows) over 32771 keys of 256, bf16: 67.6 us
+  // against 52.7; 5 tokens (30 rows): 39.1 against 52.0.  Over e4m3 pages, which
+  // the tcgen05 kernel has to widen in shared memory, 42 rows take 78.3 against
+  // 76.6 and 60 rows 81.9 against 79.6 (head_dim 128: 79.1 against 82.5).
+  const int few = p.cache.e4m3 ? 64 : 32;
+  return rows <= few ? run_attend_warp(static_cast<int>(rows), p, d, stream)
                     : run_attend_tc(rows, p, d, stream);
 }
 

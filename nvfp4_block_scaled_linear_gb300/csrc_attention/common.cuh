@@ -177,6 +177,7 @@ struct Mass {
   unsigned int* err;
 };
 int run_mass(const Mass& p, const Device& d, cudaStream_t stream);
+int run_mass_tc(const Mass& p, const Device& d, cudaStream_t stream);
 
 struct Evict {
   Cache from, to;

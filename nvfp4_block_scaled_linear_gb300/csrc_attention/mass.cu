@@ -2,7 +2,7 @@
 // tokens:  out[j] = mass[j] + sum over rows r that see j of 2^(c_r q_r . k_j - L_r)
 // with c_r the scores' scale times log2 e and L_r = lse_r log2 e.
 //
-// The keys stay and the queries pass by: a warp keeps 16 (or 32) keys' rows in
+// The keys stay and the queries pass by: a warp keeps 16 keys' rows in
 // registers as the warp MMA's A operand, loaded once and straight from the
 // pages (a lane's 16-byte pieces are its operands when the k index inside an MMA
 // is permuted alike for the queries), and the query rows come through shared
@@ -10,9 +10,8 @@
 // column of the accumulator, so a key's sum stays with one lane group from the
 // first row to the last: no atomics, one order.
 //
-// A single token's call reads the keys once and is bound by that; a chunk of
-// them is bound by the products, 2 * head_dim flops a pair, and beside them the
-// shared-memory reads of the query operand, which 32 keys a warp halve.
+// For few rows (64 at most; mass_tc.cu takes more): a single token's call reads
+// the keys once and is bound by that.
 //
 // Over an e4m3 cache the codes are widened to f16 (exact) as they are loaded,
 // and each query row is scaled by a power of two (attend_warp.cu says why).
@@ -44,11 +43,11 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// kTiles: 16-key MMA tiles of a warp.
-template <int kDim, bool kE4m3, int kTiles>
+template <int kDim, bool kE4m3>
 __global__ void __launch_bounds__(kThreads) mass_kernel(const Mass p) {
   constexpr int kPitch = kDim * 2 + 16;                    // bytes of a query row
   constexpr int kSteps = kDim / 16;
+  constexpr int kTiles = 1;                                // 16-key tiles of a warp
   constexpr int kBlockKeys = kWarps * 16 * kTiles;
   __shared__ __align__(16) uint8_t q_sm[2][kStageRows * kPitch];
   __shared__ float2 row_sm[2][kStageRows];                 // (c, L) of a row
@@ -236,19 +235,18 @@ __global__ void __launch_bounds__(kThreads) mass_kernel(const Mass p) {
 
 template <int kDim, bool kE4m3>
 int run(const Mass& p, cudaStream_t stream) {
-  // 32 keys a warp where the products count (more than a few tiles of 8 rows)
-  const bool two = int64_t(p.max_q_len) * p.group > 32;
-  const int keys = kWarps * 16 * (two ? 2 : 1);
+  constexpr int keys = kWarps * 16;
   const int64_t blocks = (p.room + keys - 1) / keys;
   if (blocks > INT32_MAX || p.cache.heads > 65535 || p.seqs.count > 65535) return NVFP4_ERR_SHAPE;
-  return launch(two ? mass_kernel<kDim, kE4m3, 2> : mass_kernel<kDim, kE4m3, 1>,
+  return launch(mass_kernel<kDim, kE4m3>,
                 dim3(static_cast<unsigned>(blocks), p.cache.heads, p.seqs.count), dim3(kThreads), 0,
                 stream, p);
 }
 
 }  // namespace
 
-int run_mass(const Mass& p, const Device&, cudaStream_t stream) {
+int run_mass(const Mass& p, const Device& d, cudaStream_t stream) {
+  if (int64_t(p.max_q_len) * p.group > 64) return run_mass_tc(p, d, stream);
   const bool f8 = p.cache.e4m3;
   switch (p.cache.dim) {
     case 64:
