@@ -486,17 +486,23 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
     Place at;
     at.start(items);
     __syncwarp();
-    // lane i: where the block's rows 16 i on are (pages hold whole sixteens), read
-    // one block ahead; past the length the cache's first rows, whose scores are
-    // masked and whose values become zero
+    // lane i: where the block's rows 16 i on are (pages hold whole sixteens); past
+    // the length the cache's first rows, whose scores are masked and whose values
+    // become zero.  The table entry is asked for a block ahead, and used only
+    // before the block's last unit.
     int64_t group = 0;
+    int key = -1, entry = 0;
+    auto ask = [&]() {
+      key = at.it.key0 + at.b * kN + (lane & 7) * 16;
+      if (at.live && key < at.it.kv_len)
+        entry = a.seqs.table[int64_t(at.it.s) * a.seqs.width + key / a.cache.page_size];
+      else
+        key = -1;
+    };
     auto look_up = [&]() {
-      const int key = at.it.key0 + at.b * kN + (lane & 7) * 16;
       group = 0;
-      if (at.live && key < at.it.kv_len) {
-        const int64_t page = checked_page(
-            a.seqs.table[int64_t(at.it.s) * a.seqs.width + key / a.cache.page_size], a.cache.pages,
-            a.err);
+      if (key >= 0) {
+        const int64_t page = checked_page(entry, a.cache.pages, a.err);
         const int64_t* st = kV ? a.cache.vs : a.cache.ks;
         if (page != a.cache.pages)
           group = page * st[0] + key % a.cache.page_size * st[1] + at.it.h * st[2];
@@ -514,6 +520,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
       }
       v[i] = *reinterpret_cast<const uint4*>(from);
     };
+    ask();
     look_up();
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) load(group, 0, i);
@@ -525,7 +532,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
       const int64_t here = group;
       const bool moved = at.next(items);
       __syncwarp();
-      look_up();
+      ask();
 #pragma unroll 1
       for (int u = 0; u < kUnits; ++u) {
         if (u % kHalves == 0) {
@@ -536,6 +543,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
             ++turns;
           }
         }
+        if (u == kUnits - 1) look_up();
         const int64_t where = u + 1 < kUnits ? here : group;
         const int next_u = u + 1 < kUnits ? u + 1 : 0;
         uint8_t* slot = ring + r.slot * C::kSlotBytes + (u % kHalves) * kUnitRows * 128;
@@ -821,9 +829,8 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
     if constexpr (kE4m3) regs_dec<72>(); else regs_dec<80>();
     if (warp == 9) {
       // ------------------------------------------------------------- MMA
-      // The warp keeps together and one lane issues, so that the operands stay in
-      // uniform registers; the MMA loops are short, to stay in the nearest
-      // instruction cache.
+      // The warp keeps together and one lane issues; the MMA loops are unrolled
+      // (rolled, an issue took over 100 cycles, more than the product).
       const uint32_t id_s = idesc<kE4m3>(kN, false);
       const uint32_t id_o = idesc<kE4m3>(kDim, true);
       const uint32_t q_lo = desc_lo(smem_addr(q_sm), 0);
@@ -865,13 +872,13 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
             if (!ok) break;
             tc_fence_after_sync();
             if (lead) {
-              uint32_t v = v_lo + r.slot * (C::kSlotBytes >> 4) +
+              const uint32_t v = v_lo + r.slot * (C::kSlotBytes >> 4) +
                            (C::kPieces == 2 ? 0 : half * (kN / 32) * (2048 >> 4));
-              uint32_t t_p = t_s + half * (kN / 4);
-              uint32_t acc = !fresh || half != 0;
-#pragma unroll 1
-              for (int kk = 0; kk < kN / 32; ++kk, v += 2048 >> 4, t_p += 8, acc = 1)
-                umma_ts(t_o, t_p, v, id_o, acc);
+              const uint32_t t_p = t_s + half * (kN / 4);
+              const uint32_t acc = !fresh || half != 0;
+#pragma unroll
+              for (int kk = 0; kk < kN / 32; ++kk)
+                umma_ts(t_o, t_p + kk * 8, v + kk * (2048 >> 4), id_o, kk == 0 ? acc : 1u);
               if ((kTiles == 1 || x == 1) && (half == 1 || C::kPieces == 2)) commit_empty<kCluster>(&empty[r.slot]);
               if (half == 1) umma_commit(&pv_done[x]);
             }
@@ -905,16 +912,13 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
             if (!ok) break;
             tc_fence_after_sync();
             if (lead) {
-              uint32_t k = k_lo + r.slot * (C::kSlotBytes >> 4);
-              uint32_t qh = q + h * ((C::kKChunks * C::kKChunk) >> 4);
-              uint32_t acc = h != 0;
-#pragma unroll 1
-              for (int ch = 0; ch < C::kKChunks; ++ch) {
+              const uint32_t k = k_lo + r.slot * (C::kSlotBytes >> 4);
+              const uint32_t qh = q + h * ((C::kKChunks * C::kKChunk) >> 4);
+              const uint32_t acc = h != 0;
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk, acc = 1)
-                  umma_ss(t_s, qh + kk * (32 >> 4), k + kk * (32 >> 4), id_s, acc);
-                qh += C::kKChunk >> 4;
-                k += C::kKChunk >> 4;
+              for (int kk = 0; kk < C::kKChunks * 4; ++kk) {
+                const uint32_t off = ((kk >> 2) * C::kKChunk + (kk & 3) * 32) >> 4;
+                umma_ss(t_s, qh + off, k + off, id_s, kk == 0 ? acc : 1u);
               }
               if (kTiles == 1 || x == 1) commit_empty<kCluster>(&empty[r.slot]);
               if (h == C::kPieces - 1) {

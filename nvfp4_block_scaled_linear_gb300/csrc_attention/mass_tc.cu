@@ -282,14 +282,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after_sync();
           if (lane == 0) {
-            uint32_t k = k_lo + ((x * C::kTileBytes + h * C::kSlotBytes) >> 4);
-            uint32_t q = q_lo + at * (C::kSlotBytes >> 4);
-            uint32_t acc = h != 0;
-#pragma unroll 1
-            for (int ch = 0; ch < C::kSlotChunks; ++ch, k += C::kChunk >> 4, q += C::kChunk >> 4) {
+            const uint32_t k = k_lo + ((x * C::kTileBytes + h * C::kSlotBytes) >> 4);
+            const uint32_t q = q_lo + at * (C::kSlotBytes >> 4);
+            const uint32_t t_s = tmem + (2 * x + b) * kN, acc = h != 0;
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk, acc = 1)
-                umma_ss(tmem + (2 * x + b) * kN, k + kk * 2, q + kk * 2, id, acc);
+            for (int kk = 0; kk < C::kSlotChunks * 4; ++kk) {
+              const uint32_t off = ((kk >> 2) * C::kChunk + (kk & 3) * 32) >> 4;
+              umma_ss(t_s, k + off, q + off, id, kk == 0 ? acc : 1u);
             }
             if (x == 1) umma_commit(&empty[at]);
             if (h == C::kPieces - 1) umma_commit(&s_full[2 * x + b]);
