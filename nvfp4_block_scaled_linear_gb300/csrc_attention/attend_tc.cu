@@ -5,7 +5,7 @@
 // the 128 lanes of TMEM; a block is 128 keys.  S = Q K^T lands in one of two
 // 128-column buffers, a thread per row turns it into weights P in place (16
 // bits, over the first half of the same columns), and O += P V takes P from
-// TMEM.  The one issuing thread keeps two blocks of scores ahead of the
+// TMEM.  Scores run two blocks ahead of the
 // weights:   S0 S1 | PV0 S2 | PV1 S3 | ...
 // so that the softmax of one block overlaps the products of the others.
 //
@@ -29,10 +29,10 @@
 // each read per product, V once, plus the copies that bring K and V).
 //
 // Warps: 0-3 and 4-7 softmax and output; 8 and 10 the copies of K and of V; 9
-// MMA; 11 the schedule and the copies of Q.  Over an e4m3 cache warps 12-15
-// widen K and V to f16 (exact) on their way to shared memory, and warps 8, 10
-// and 11 bring Q, scaled per row by a power of two (attend_warp.cu says why),
-// in f16.
+// the MMAs of P V, 12 those of Q K^T; 11 the schedule and the copies of Q.  Over
+// an e4m3 cache warps 12-15 widen K and V to f16 (exact) on their way to shared
+// memory, warp 10 issues Q K^T, and warps 8 and 11 bring Q, scaled per row by a
+// power of two (attend_warp.cu says why), in f16.
 //
 // A V value that is not finite and that only some rows of the tile see would
 // reach the others as 0 * NaN: it is replaced by zero before the product and
@@ -51,13 +51,20 @@ constexpr int kBlockShift = 7;
 constexpr int kN = 1 << kBlockShift;          // keys of a block (one unit)
 constexpr int kExtra = 2;                     // blocks that an item's beginning costs
 constexpr float kSlack = 8.f;                 // growth of log2 of a weight before rescaling
+// Registers of a thread in the softmax warps, in warps 8 to 11, and in 12 to 15:
+// in all what 512 threads of 128 registers are launched with.
+template <bool kE4m3>
+constexpr int kSoftmaxRegs = kE4m3 ? 168 : 192;
+template <bool kE4m3>
+constexpr int kHelperRegs = kE4m3 ? 72 : 64;
+constexpr int kWidenRegs = 96, kScoreRegs = 64;
 constexpr int kItems = 4;                     // item descriptors in flight
 constexpr int kQFactors = 4;                  // items whose row factors are held
 constexpr int kDirty = 8;                     // items whose `dirty` note is held: more than the ring's
 
 template <int kDim, bool kE4m3, int kTiles, int kCluster>
 struct Cfg {
-  static constexpr int kThreads = kE4m3 ? 512 : 384;
+  static constexpr int kThreads = 512;
   // A slot holds up to 32 KB: 128 of head_dim of all keys of a K block, or all
   // of head_dim of some keys of a V block, in chunks of 64 columns.
   static constexpr int kSlotBytes = std::min(kDim * kN * 2, 32 * 1024);
@@ -282,14 +289,14 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
       mbar_init(&o_free[x], kTiles == 1 ? 8 : 4);
       for (int i = 0; i < 4; ++i) mbar_init(&m_ready[x * 4 + i], 1);
     }
-    mbar_init(q_full, kE4m3 ? 3 : 1);
+    mbar_init(q_full, kE4m3 ? 2 : 1);
     mbar_init(q_empty, 1);
-    mbar_init(mma_done, 1);
+    mbar_init(mma_done, 2);
     mbar_init(pair, 8);
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&items.full[i], 1);
-      // softmax warps, MMA, and the copying and checking (or Q and widening) warps
-      mbar_init(&items.empty[i], 8 + 1 + (kE4m3 ? 2 + 4 : 2));
+      // softmax, MMA, and the copying (or Q and widening) warps
+      mbar_init(&items.empty[i], 8 + 2 + (kE4m3 ? 1 + 4 : 2));
     }
     *abort_flag = 0;
     for (int i = 0; i < kDirty; ++i) dirty[i] = 0;
@@ -580,9 +587,78 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
     }
   };
 
+  const bool lead = lane == 0;
+  constexpr int kScoreWarp = kE4m3 ? 10 : 12;
+  // Nothing may be in flight when TMEM is released.
+  auto drain = [&]() {
+    if (lead) {
+      umma_commit(mma_done);
+      volatile int no_abort = 0;
+      if (!wait(mma_done, 0, &no_abort)) atomicOr(a.err, NVFP4_ATTENTION_TIMEOUT);
+    }
+    __syncwarp();
+  };
+  // MMA: S = Q K^T.  A warp of its own: an issue waits for the pipe, so that what
+  // one warp spends between its products the other's have to fill.
+  auto score_mma = [&]() {
+    const uint32_t id_s = idesc<kE4m3>(kN, false);
+    const uint32_t q_lo = desc_lo(smem_addr(q_sm), 0);
+    const uint32_t k_lo = desc_lo(smem_addr(ring), 0);
+    Place qk;
+    int x = 0;                                  // the score buffer (and tile)
+    qk.start(items);
+    KRing<C> next, at;                          // of the next block; of the one in use
+    bool ok = true;
+    auto ready = [&](uint64_t* bar, uint32_t parity) {
+      ok = ok && __all_sync(0xffffffffu, wait(bar, parity, abort_flag));
+    };
+    for (int i = 0; ok && qk.live; ++i, x ^= 1) {
+      const uint32_t t_s = tmem + C::kS + x * kN;
+      if (kTiles == 1 || x == 0) {
+        if (qk.first()) ready(q_full, qk.item & 1);
+        at = next;
+#pragma unroll
+        for (int h = 0; h < C::kPieces; ++h) next.next();
+      }
+      // the weights that the buffer held have been used
+      if (i >= 2) ready(&pv_done[x], (i >> 1 & 1) ^ 1);
+      KRing<C> r = at;
+      const uint32_t q = q_lo + (kTiles == 2 ? x * (C::kQTile >> 4) : 0);
+      const bool last = qk.last() && (kTiles == 1 || x == 1);
+#pragma unroll 1
+      for (int h = 0; h < C::kPieces; ++h, r.next()) {
+        if (kTiles == 1 || x == 0) ready(&full[r.slot], r.par);
+        if (!ok) break;
+        tc_fence_after_sync();
+        if (lead) {
+          const uint32_t k = k_lo + r.slot * (C::kSlotBytes >> 4);
+          const uint32_t qh = q + h * ((C::kKChunks * C::kKChunk) >> 4);
+          const uint32_t acc = h != 0;
+#pragma unroll
+          for (int kk = 0; kk < C::kKChunks * 4; ++kk) {
+            const uint32_t off = ((kk >> 2) * C::kKChunk + (kk & 3) * 32) >> 4;
+            umma_ss(t_s, qh + off, k + off, id_s, kk == 0 ? acc : 1u);
+          }
+          if (kTiles == 1 || x == 1) commit_empty<kCluster>(&empty[r.slot]);
+          if (h == C::kPieces - 1) {
+            umma_commit(&s_full[x]);
+            if (last) umma_commit(q_empty);
+          }
+        }
+        __syncwarp();
+      }
+      if (ok && (kTiles == 1 || x == 1)) {
+        const int was = qk.item;
+        if (qk.next(items) && lead) items.release(was);
+        __syncwarp();
+      }
+    }
+    drain();
+  };
+
   if (warp < 8) {
     // ------------------------------------------------------ softmax, output
-    if constexpr (kE4m3) regs_inc<168>(); else regs_inc<208>();
+    regs_inc<kSoftmaxRegs<kE4m3>>();
     const int x = warp >> 2, quad = warp & 3;
     const int row = quad * 32 + lane;                 // of the tile
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
@@ -826,125 +902,64 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
       p.parts.note[unit] = note;
     }
   } else if (warp < 12) {
-    if constexpr (kE4m3) regs_dec<72>(); else regs_dec<80>();
+    regs_dec<kHelperRegs<kE4m3>>();
     if (warp == 9) {
-      // ------------------------------------------------------------- MMA
-      // The warp keeps together and one lane issues; the MMA loops are unrolled
-      // (rolled, an issue took over 100 cycles, more than the product).
-      const uint32_t id_s = idesc<kE4m3>(kN, false);
+      // ------------------------------------------------ MMA: O += P V
       const uint32_t id_o = idesc<kE4m3>(kDim, true);
-      const uint32_t q_lo = desc_lo(smem_addr(q_sm), 0);
-      const uint32_t k_lo = desc_lo(smem_addr(ring), 0);
       const uint32_t v_lo = desc_lo(smem_addr(ring), C::kVChunk);
-      const bool lead = lane == 0;
-      Place qk, pv;                             // of the scores, of the products with V
-      int qk_x = 0, pv_x = 0;                   // and the tile (kTiles == 2)
-      qk.start(items);
+      Place pv;
+      int x = 0;                                // the score buffer (and tile)
       pv.start(items);
-      KRing<C> k_next, at_k;                    // of the next block; of the one in use
-      VRing<C> v_next, at_v;
+      VRing<C> next, at;                        // of the next block; of the one in use
       bool ok = true;
       auto ready = [&](uint64_t* bar, uint32_t parity) {
         ok = ok && __all_sync(0xffffffffu, wait(bar, parity, abort_flag));
       };
-      for (int i = 0; ok && (qk.live || pv.live); ++i) {
-        const int x = i & 1;
+      for (int i = 0; ok && pv.live; ++i, x ^= 1) {
         const uint32_t t_s = tmem + C::kS + x * kN;
-        if (i >= 2) {
-          // ---- O += P V, two steps behind
-          if (pv_x == 0) {
-            at_v = v_next;
+        const uint32_t t_o = tmem + C::kO + (kTiles == 2 ? x * kDim : 0);
+        const bool fresh = pv.first();
+        if (kTiles == 1 || x == 0) {
+          at = next;
 #pragma unroll
-            for (int h = 0; h < C::kPieces; ++h) v_next.next();
-            if (!kE4m3 && lead) {
-              v_slot[x] = at_v.slot | static_cast<int>(at_v.par) << 8;
-              mbar_arrive(&v_known[x]);
-            }
-          }
-          const bool fresh = pv.first();
-          if (fresh && pv.item > 0) ready(&o_free[kTiles == 1 ? 0 : x], (pv.item - 1) & 1);
-          const uint32_t t_o = tmem + C::kO + (kTiles == 2 ? x * kDim : 0);
-          VRing<C> r = at_v;
-#pragma unroll 1
-          for (int half = 0; half < 2; ++half) {               // of the keys
-            if (pv_x == 0 && (half == 0 || C::kPieces == 2) ) ready(&full[r.slot], r.par);
-            ready(&p_full[2 * x + half], (i - 2) >> 1 & 1);
-            if (!ok) break;
-            tc_fence_after_sync();
-            if (lead) {
-              const uint32_t v = v_lo + r.slot * (C::kSlotBytes >> 4) +
-                           (C::kPieces == 2 ? 0 : half * (kN / 32) * (2048 >> 4));
-              const uint32_t t_p = t_s + half * (kN / 4);
-              const uint32_t acc = !fresh || half != 0;
-#pragma unroll
-              for (int kk = 0; kk < kN / 32; ++kk)
-                umma_ts(t_o, t_p + kk * 8, v + kk * (2048 >> 4), id_o, kk == 0 ? acc : 1u);
-              if ((kTiles == 1 || x == 1) && (half == 1 || C::kPieces == 2)) commit_empty<kCluster>(&empty[r.slot]);
-              if (half == 1) umma_commit(&pv_done[x]);
-            }
-            __syncwarp();
-            if (C::kPieces == 2) r.next();
-          }
-          if (!ok) break;
-          if (kTiles == 2 && pv_x == 0) {
-            pv_x = 1;
-          } else {
-            pv_x = 0;
-            const int was = pv.item;
-            if (pv.next(items) && lead) items.release(was);
-            __syncwarp();
+          for (int h = 0; h < C::kPieces; ++h) next.next();
+          if (!kE4m3 && lead) {
+            v_slot[x] = at.slot | static_cast<int>(at.par) << 8;
+            mbar_arrive(&v_known[x]);
           }
         }
-        if (qk.live) {
-          // ---- S = Q K^T
-          if (qk.first() && qk_x == 0) ready(q_full, qk.item & 1);
-          if (qk_x == 0) {
-            at_k = k_next;
-#pragma unroll
-            for (int h = 0; h < C::kPieces; ++h) k_next.next();
-          }
-          KRing<C> r = at_k;
-          const uint32_t q = q_lo + (kTiles == 2 ? x * (C::kQTile >> 4) : 0);
-          const bool last = qk.last() && qk_x == kTiles - 1;
+        if (fresh && pv.item > 0) ready(&o_free[kTiles == 1 ? 0 : x], (pv.item - 1) & 1);
+        VRing<C> r = at;
 #pragma unroll 1
-          for (int h = 0; h < C::kPieces; ++h, r.next()) {
-            if (qk_x == 0) ready(&full[r.slot], r.par);
-            if (!ok) break;
-            tc_fence_after_sync();
-            if (lead) {
-              const uint32_t k = k_lo + r.slot * (C::kSlotBytes >> 4);
-              const uint32_t qh = q + h * ((C::kKChunks * C::kKChunk) >> 4);
-              const uint32_t acc = h != 0;
-#pragma unroll
-              for (int kk = 0; kk < C::kKChunks * 4; ++kk) {
-                const uint32_t off = ((kk >> 2) * C::kKChunk + (kk & 3) * 32) >> 4;
-                umma_ss(t_s, qh + off, k + off, id_s, kk == 0 ? acc : 1u);
-              }
-              if (kTiles == 1 || x == 1) commit_empty<kCluster>(&empty[r.slot]);
-              if (h == C::kPieces - 1) {
-                umma_commit(&s_full[x]);
-                if (last) umma_commit(q_empty);
-              }
-            }
-            __syncwarp();
-          }
+        for (int half = 0; half < 2; ++half) {                 // of the keys
+          if ((kTiles == 1 || x == 0) && (half == 0 || C::kPieces == 2)) ready(&full[r.slot], r.par);
+          ready(&p_full[2 * x + half], i >> 1 & 1);
           if (!ok) break;
-          if (kTiles == 2 && qk_x == 0) {
-            qk_x = 1;
-          } else {
-            qk_x = 0;
-            qk.next(items);
-            __syncwarp();
+          tc_fence_after_sync();
+          if (lead) {
+            const uint32_t v = v_lo + r.slot * (C::kSlotBytes >> 4) +
+                               (C::kPieces == 2 ? 0 : half * (kN / 32) * (2048 >> 4));
+            const uint32_t t_p = t_s + half * (kN / 4);
+            const uint32_t acc = !fresh || half != 0;
+#pragma unroll
+            for (int kk = 0; kk < kN / 32; ++kk)
+              umma_ts(t_o, t_p + kk * 8, v + kk * (2048 >> 4), id_o, kk == 0 ? acc : 1u);
+            if ((kTiles == 1 || x == 1) && (half == 1 || C::kPieces == 2))
+              commit_empty<kCluster>(&empty[r.slot]);
+            if (half == 1) umma_commit(&pv_done[x]);
           }
+          __syncwarp();
+          if (C::kPieces == 2) r.next();
+        }
+        if (ok && (kTiles == 1 || x == 1)) {
+          const int was = pv.item;
+          if (pv.next(items) && lead) items.release(was);
+          __syncwarp();
         }
       }
-      // nothing may be in flight when TMEM is released
-      if (lead) {
-        umma_commit(mma_done);
-        volatile int no_abort = 0;
-        if (!wait(mma_done, 0, &no_abort)) atomicOr(a.err, NVFP4_ATTENTION_TIMEOUT);
-      }
-      __syncwarp();
+      drain();
+    } else if (kE4m3 && warp == kScoreWarp) {
+      score_mma();
     } else if (warp == 8 && !kE4m3) {
       copy_pages(std::false_type{});
     } else if (warp == 10 && !kE4m3) {
@@ -975,8 +990,8 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
       }
       __syncwarp();
     } else {
-      // ---------------------------------- Q rows scaled to f16 (warps 8, 10, 11)
-      const int part = warp == 8 ? 0 : warp - 9;
+      // -------------------------------------- Q rows scaled to f16 (warps 8, 11)
+      const int part = warp == 8 ? 0 : 1;
       constexpr int kLanes = kDim / 8;              // of a row, 8 elements each
       constexpr int kRowsAtOnce = 32 / kLanes, kPasses = kDim == 256 ? 8 : 4;
       const int ql = lane % kLanes;
@@ -1001,7 +1016,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
                              ? tokens * a.group
                              : kM + (tokens - p.tile_tokens) * a.group;
 #pragma unroll 1
-        for (int r0 = part * kPasses * kRowsAtOnce; r0 < rows; r0 += 3 * kPasses * kRowsAtOnce) {
+        for (int r0 = part * kPasses * kRowsAtOnce; r0 < rows; r0 += 2 * kPasses * kRowsAtOnce) {
           uint4 v[kPasses];
 #pragma unroll
           for (int i = 0; i < kPasses; ++i) {
@@ -1053,8 +1068,11 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
     }
   } else {
     // ------------------------------------------ K, V codes widened to f16
-    if constexpr (kE4m3) {
-      regs_dec<96>();
+    if constexpr (!kE4m3) {
+      regs_dec<kScoreRegs>();
+      if (warp == kScoreWarp) score_mma();
+    } else {
+      regs_dec<kWidenRegs>();
       if (warp < 14)
         widen_pages(std::false_type{});
       else
@@ -1084,7 +1102,8 @@ int run(const Attend& a, const Device& d, cudaStream_t stream) {
       cudaGetLastError();
       return NVFP4_ERR_LAUNCH;
     }
-    constexpr int need = kE4m3 ? 256 * 168 + 128 * 72 + 128 * 96 : 256 * 208 + 128 * 80;
+    constexpr int need = 256 * kSoftmaxRegs<kE4m3> + 128 * kHelperRegs<kE4m3> +
+                         128 * (kE4m3 ? kWidenRegs : kScoreRegs);
     if (attr.numRegs * C::kThreads < need) return NVFP4_ERR_LAUNCH;
   }
   if (const int st = allow_smem(kernel, C::kSmem, d, ready)) return st;
