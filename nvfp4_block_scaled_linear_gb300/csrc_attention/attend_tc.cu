@@ -54,10 +54,10 @@ constexpr float kSlack = 8.f;                 // growth of log2 of a weight befo
 // Registers of a thread in the softmax warps, in warps 8 to 11, and in 12 to 15:
 // in all what 512 threads of 128 registers are launched with.
 template <bool kE4m3>
-constexpr int kSoftmaxRegs = kE4m3 ? 168 : 192;
+constexpr int kSoftmaxRegs = kE4m3 ? 176 : 192;
 template <bool kE4m3>
 constexpr int kHelperRegs = kE4m3 ? 72 : 64;
-constexpr int kWidenRegs = 96, kScoreRegs = 64;
+constexpr int kWidenRegs = 88, kScoreRegs = 64;
 constexpr int kItems = 4;                     // item descriptors in flight
 constexpr int kQFactors = 4;                  // items whose row factors are held
 constexpr int kDirty = 8;                     // items whose `dirty` note is held: more than the ring's
@@ -577,7 +577,8 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
               bad |= check_rows(it, first, r.slot, q + (warp & 1) * (kRowsAtOnce / 2), kRowsAtOnce / 2);
             if (bad) dirty[was % kDirty] = was + 1;
           }
-          fence_proxy_async_smem();
+          // (the proxy fence is the MMA warp's: here it would wait for the loads
+          // that are on their way)
           __syncwarp();
           if (lane == 0) mbar_arrive(&full[r.slot]);
           r.next();
@@ -627,7 +628,10 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
       const bool last = qk.last() && (kTiles == 1 || x == 1);
 #pragma unroll 1
       for (int h = 0; h < C::kPieces; ++h, r.next()) {
-        if (kTiles == 1 || x == 0) ready(&full[r.slot], r.par);
+        if (kTiles == 1 || x == 0) {
+          ready(&full[r.slot], r.par);
+          if (kE4m3) fence_proxy_async_smem();
+        }
         if (!ok) break;
         tc_fence_after_sync();
         if (lead) {
@@ -932,7 +936,10 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
         VRing<C> r = at;
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {                 // of the keys
-          if ((kTiles == 1 || x == 0) && (half == 0 || C::kPieces == 2)) ready(&full[r.slot], r.par);
+          if ((kTiles == 1 || x == 0) && (half == 0 || C::kPieces == 2)) {
+            ready(&full[r.slot], r.par);
+            if (kE4m3) fence_proxy_async_smem();
+          }
           ready(&p_full[2 * x + half], i >> 1 & 1);
           if (!ok) break;
           tc_fence_after_sync();

@@ -13,7 +13,7 @@
 // the exponentials, 256 for a thread in the same time, run beside them.
 //
 // Warps: 0-3 and 4-7 sum up (tile 0, tile 1); 8 copies K once and then the
-// queries; 9 MMA; 10 the rows' log-sums.  An e4m3 K becomes bf16 (exact) on its
+// queries; 9 and 11 MMA (tile 0, tile 1); 10 the rows' log-sums.  An e4m3 K becomes bf16 (exact) on its
 // way to shared memory, by warps 0-7.
 #include <algorithm>
 
@@ -89,11 +89,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kSlots; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
+    for (int i = 0; i < C::kSlots; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 2);
     for (int i = 0; i < 4; ++i) mbar_init(&s_full[i], 1), mbar_init(&s_free[i], 4);
     for (int i = 0; i < kLogs; ++i) mbar_init(&log_full[i], 1), mbar_init(&log_free[i], 8);
     mbar_init(k_full, kE4m3 ? 8 : 1);
-    mbar_init(mma_done, 1);
+    mbar_init(mma_done, 2);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -258,10 +258,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 9) {
-    // ---------------------------------------------------------------- MMA
+  } else if (warp == 9 || warp == 11) {
+    // ------------------------------- MMA, a warp for each tile: an issue waits for
+    // the pipe, so that what one warp spends between its products the other fills
     constexpr uint32_t id = umma_idesc_bf16(kM, kN);
-    const uint32_t k_lo = desc_lo(smem_addr(k_sm), 0), q_lo = desc_lo(smem_addr(ring), 0);
+    const int x = warp == 11;
+    const uint32_t k_lo = desc_lo(smem_addr(k_sm), 0) + x * (C::kTileBytes >> 4);
+    const uint32_t q_lo = desc_lo(smem_addr(ring), 0);
     bool ok = true;
     auto ready = [&](uint64_t* bar, uint32_t parity) {
       ok = ok && __all_sync(0xffffffffu, wait(bar, parity, abort_flag));
@@ -271,32 +274,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t par = 0;
     for (int i = 0; i < n && ok; ++i) {
       const int b = i & 1;
+      if (i >= 2) ready(&s_free[2 * x + b], (i >> 1 & 1) ^ 1);
 #pragma unroll 1
-      for (int x = 0; x < 2; ++x) {
-        if (i >= 2) ready(&s_free[2 * x + b], (i >> 1 & 1) ^ 1);
-        int at = slot;
-        uint32_t at_par = par;
-#pragma unroll 1
-        for (int h = 0; h < C::kPieces; ++h) {
-          if (x == 0) ready(&full[at], at_par);
-          if (!ok) break;
-          tc_fence_after_sync();
-          if (lane == 0) {
-            const uint32_t k = k_lo + ((x * C::kTileBytes + h * C::kSlotBytes) >> 4);
-            const uint32_t q = q_lo + at * (C::kSlotBytes >> 4);
-            const uint32_t t_s = tmem + (2 * x + b) * kN, acc = h != 0;
+      for (int h = 0; h < C::kPieces; ++h) {
+        ready(&full[slot], par);
+        if (!ok) break;
+        tc_fence_after_sync();
+        if (lane == 0) {
+          const uint32_t k = k_lo + h * (C::kSlotBytes >> 4);
+          const uint32_t q = q_lo + slot * (C::kSlotBytes >> 4);
+          const uint32_t t_s = tmem + (2 * x + b) * kN, acc = h != 0;
 #pragma unroll
-            for (int kk = 0; kk < C::kSlotChunks * 4; ++kk) {
-              const uint32_t off = ((kk >> 2) * C::kChunk + (kk & 3) * 32) >> 4;
-              umma_ss(t_s, k + off, q + off, id, kk == 0 ? acc : 1u);
-            }
-            if (x == 1) umma_commit(&empty[at]);
-            if (h == C::kPieces - 1) umma_commit(&s_full[2 * x + b]);
+          for (int kk = 0; kk < C::kSlotChunks * 4; ++kk) {
+            const uint32_t off = ((kk >> 2) * C::kChunk + (kk & 3) * 32) >> 4;
+            umma_ss(t_s, k + off, q + off, id, kk == 0 ? acc : 1u);
           }
-          __syncwarp();
-          if (++at == C::kSlots) at = 0, at_par ^= 1u;
+          umma_commit(&empty[slot]);
+          if (h == C::kPieces - 1) umma_commit(&s_full[2 * x + b]);
         }
-        if (x == 1) slot = at, par = at_par;
+        __syncwarp();
+        if (++slot == C::kSlots) slot = 0, par ^= 1u;
       }
     }
     if (lane == 0) {
