@@ -114,7 +114,7 @@ __device__ __forceinline__ void tma_load_page(void* dst, const CUtensorMap* map,
         : "memory");
 }
 
-// rows: query rows of one key/value head in the longest sequence, at most 64.
+// rows: query rows of one key/value head in the longest sequence, at most 32.
 int run_attend_warp(int rows, const Attend& p, const Device& d, cudaStream_t stream);
 int64_t attend_warp_workspace(int head_dim, const Device& d);
 

@@ -30,9 +30,9 @@
 //
 // Warps: 0-3 and 4-7 softmax and output; 8 and 10 the copies of K and of V; 9
 // the MMAs of P V, 12 those of Q K^T; 11 the schedule and the copies of Q.  Over
-// an e4m3 cache warps 12-15 widen K and V to f16 (exact) on their way to shared
-// memory, warp 10 issues Q K^T, and warps 8 and 11 bring Q, scaled per row by a
-// power of two (attend_warp.cu says why), in f16.
+// an e4m3 cache warps 8 and 11 copy the codes of K and of V, warps 12-15 widen
+// them to f16 (exact), warp 10 issues Q K^T, and the softmax warps bring their
+// rows of Q, scaled by a power of two each (attend_warp.cu says why), in f16.
 //
 // A V value that is not finite and that only some rows of the tile see would
 // reach the others as 0 * NaN: it is replaced by zero before the product and
@@ -51,15 +51,11 @@ constexpr int kBlockShift = 7;
 constexpr int kN = 1 << kBlockShift;          // keys of a block (one unit)
 constexpr int kExtra = 2;                     // blocks that an item's beginning costs
 constexpr float kSlack = 8.f;                 // growth of log2 of a weight before rescaling
-// Registers of a thread in the softmax warps, in warps 8 to 11, and in 12 to 15:
-// in all what 512 threads of 128 registers are launched with.
-template <bool kE4m3>
-constexpr int kSoftmaxRegs = kE4m3 ? 176 : 192;
-template <bool kE4m3>
-constexpr int kHelperRegs = kE4m3 ? 72 : 64;
-constexpr int kWidenRegs = 88, kScoreRegs = 64;
+// Registers of a thread in the softmax warps and in the others: in all what 512
+// threads of 128 registers are launched with.
+constexpr int kSoftmaxRegs = 192, kHelperRegs = 64;
+constexpr int kRawBytes = 8 * 1024;           // of a unit of e4m3 codes
 constexpr int kItems = 4;                     // item descriptors in flight
-constexpr int kQFactors = 4;                  // items whose row factors are held
 constexpr int kDirty = 8;                     // items whose `dirty` note is held: more than the ring's
 
 template <int kDim, bool kE4m3, int kTiles, int kCluster>
@@ -77,16 +73,17 @@ struct Cfg {
   static constexpr int kQTile = kM * kDim * 2;
   static constexpr int kQBytes = kTiles * kQTile;
   static constexpr int kMaxSlots = 8;
-  static constexpr int kBars = 2 * kMaxSlots + 24 + 2 * kItems;
+  static constexpr int kBars = 2 * kMaxSlots + 32 + 2 * kItems;
   static constexpr int kBarOff = 0;
   static constexpr int kItemOff = (kBarOff + kBars * 8 + 16 + kDirty * 4 + 15) / 16 * 16;  // descriptors
   static constexpr int kMaxOff = kItemOff + kItems * 32;                                   // running maxima
   static constexpr int kSumOff = kMaxOff + (kTiles == 1 ? kM * 4 : 0);        // row sums
-  static constexpr int kFacOff = kSumOff + (kTiles == 1 ? kM * 4 : 0);    // Q row factors
-  static constexpr int kFixed = kFacOff + (kE4m3 ? kQFactors * kTiles * kM * 4 : 0);
-  static constexpr int kBudget = 227 * 1024 - 1024 - kFixed - kQBytes;
+  static constexpr int kFixed = kSumOff + (kTiles == 1 ? kM * 4 : 0);
+  // e4m3 codes on their way: two units of K, two of V
+  static constexpr int kRaw = kE4m3 ? 4 * kRawBytes : 0;
+  static constexpr int kBudget = 227 * 1024 - 1024 - kFixed - kQBytes - kRaw;
   static constexpr int kSlots = std::min(kMaxSlots, kBudget / kSlotBytes);
-  static constexpr int kSmem = kQBytes + kSlots * kSlotBytes + kFixed + 1024;
+  static constexpr int kSmem = kQBytes + kRaw + kSlots * kSlotBytes + kFixed + 1024;
   // K and V have rings of their own, since different warps fill them.  K slots
   // come free, and are filled again, while V is in use, and V's while K is.
   static constexpr int kKSlots = kSlots / 2, kVSlots = kSlots - kKSlots;
@@ -236,6 +233,22 @@ struct Place {
   }
 };
 
+// How the widening warps of K or V cut a block: units of 8 passes by 64 threads.
+template <class C, int kDim, bool kV>
+struct Units {
+  static constexpr int kSlotRows = kV ? C::kVKeys : kN;
+  static constexpr int kPerRow = kV ? kDim / 16 : C::kKChunks * 4;    // threads of a row
+  static constexpr int kRowsAtOnce = 64 / kPerRow;
+  static constexpr int kPasses = 8;
+  static constexpr int kRows = kPasses * kRowsAtOnce;
+  static constexpr int kRowShift = kRows == 128 ? 7 : kRows == 64 ? 6 : 5;
+  static constexpr int kHalves = kSlotRows / kRows;                   // units of a slot
+  static constexpr int kCount = C::kPieces * kHalves;                 // of a block
+  static constexpr int kWidth = kDim < 128 ? 64 : 128;                // bytes of a row's copy
+  static constexpr int kChunks = kV && kDim == 256 ? 2 : 1;           // copies of a row
+  static_assert(kRows * kPerRow * 16 == kRawBytes && (1 << kRowShift) == kRows, "a unit's bytes");
+};
+
 template <class C>
 using KRing = Ring<0, C::kKSlots>;
 template <class C>
@@ -249,7 +262,8 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
   using C = Cfg<kDim, kE4m3, kTiles, kCluster>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* q_sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-  uint8_t* ring = q_sm + C::kQBytes;
+  uint8_t* raw = q_sm + C::kQBytes;                // [K, V][2]
+  uint8_t* ring = raw + C::kRaw;
   uint8_t* fixed = ring + C::kSlots * C::kSlotBytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(fixed + C::kBarOff);
   uint64_t* empty = full + C::kMaxSlots;
@@ -262,7 +276,9 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
   uint64_t* q_empty = q_full + 1;
   uint64_t* mma_done = q_empty + 1;               // every product issued has completed
   uint64_t* pair = mma_done + 1;                  // both softmax groups (kTiles == 1)
-  uint64_t* v_known = pair + 1;                  // [2] v_slot[x] is that of buffer x's block
+  uint64_t* raw_full = pair + 1;                  // [K, V][2] (e4m3)
+  uint64_t* raw_free = raw_full + 4;
+  uint64_t* v_known = raw_free + 4;                  // [2] v_slot[x] is that of buffer x's block
   const Items items{reinterpret_cast<Item*>(fixed + C::kItemOff), v_known + 2, v_known + 2 + kItems,
                     reinterpret_cast<volatile int*>(full + C::kBars)};
   volatile int* abort_flag = reinterpret_cast<volatile int*>(full + C::kBars);
@@ -271,7 +287,6 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
   volatile int* dirty = v_slot + 2;               // [kDirty] item ordinal + 1
   float* run_max = reinterpret_cast<float*>(fixed + C::kMaxOff);
   float* row_sum = reinterpret_cast<float*>(fixed + C::kSumOff);
-  float* q_factor = reinterpret_cast<float*>(fixed + C::kFacOff);
   const Attend& a = p.a;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -289,23 +304,22 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
       mbar_init(&o_free[x], kTiles == 1 ? 8 : 4);
       for (int i = 0; i < 4; ++i) mbar_init(&m_ready[x * 4 + i], 1);
     }
-    mbar_init(q_full, kE4m3 ? 2 : 1);
+    mbar_init(q_full, kE4m3 ? 8 : 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_free[i], 2);
     mbar_init(q_empty, 1);
     mbar_init(mma_done, 2);
     mbar_init(pair, 8);
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&items.full[i], 1);
-      // softmax, MMA, and the copying (or Q and widening) warps
-      mbar_init(&items.empty[i], 8 + 2 + (kE4m3 ? 1 + 4 : 2));
+      // softmax, MMA, copying and widening warps
+      mbar_init(&items.empty[i], 8 + 2 + (kE4m3 ? 2 + 4 : 2));
     }
     *abort_flag = 0;
     for (int i = 0; i < kDirty; ++i) dirty[i] = 0;
     fence_mbar_init();
-    if (!kE4m3) {
-      prefetch_tensormap(&tm_q);
-      prefetch_tensormap(&tm_k);
-      prefetch_tensormap(&tm_v);
-    }
+    if (!kE4m3) prefetch_tensormap(&tm_q);
+    prefetch_tensormap(&tm_k);
+    prefetch_tensormap(&tm_v);
   }
   if (warp == 9) {
     tmem_alloc(tmem_slot, 512);
@@ -460,89 +474,104 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
     __syncwarp();
   };
 
-  // Two warps widen K, two V: 16 codes (one load) become 32 bytes of the slot,
-  // and the load of the unit after next takes the register over at once, so
-  // that the loads of a whole unit (8 per thread) are always on their way.
-  auto widen_pages = [&](auto values) {
+  // e4m3 codes of K or of V, unit by unit (a unit: 8 KB, what 64 threads widen in
+  // 8 passes), copied by one warp into two buffers.  Lane: copy (box, chunk).
+  // `moved(item)`: called when the item before `item` is done with.
+  auto copy_raw = [&](auto values, auto moved) {
     constexpr bool kV = decltype(values)::value;
-    constexpr int kRows = kV ? C::kVKeys : kN;                   // of a slot
-    constexpr int kChunkBytes = kV ? C::kVChunk : C::kKChunk;
-    constexpr int kPerRow = kV ? kDim / 16 : C::kKChunks * 4;    // threads of a row
-    constexpr int kRowsAtOnce = 64 / kPerRow;
-    constexpr int kPasses = 8;                                   // of a unit
-    constexpr int kUnitRows = kPasses * kRowsAtOnce;
-    constexpr int kHalves = kRows / kUnitRows;                   // units of a slot
-    constexpr int kUnits = C::kPieces * kHalves;                 // of a block
-    constexpr int kGroups = kUnitRows / 16, kOfGroup = kPasses / kGroups;
-    const int tid = threadIdx.x & 63;
-    const int my_row = tid / kPerRow, my_col = tid % kPerRow * 16;
-    const int64_t slot_stride = kV ? a.cache.vs[1] : a.cache.ks[1];
-    const uint8_t* base = static_cast<const uint8_t*>(kV ? a.cache.v : a.cache.k) +
-                          my_row * slot_stride + my_col;
-    const int64_t step = kRowsAtOnce * slot_stride;              // of a pass
-    // where a pass's 32 bytes go in the slot: the rows' swizzle repeats every 8
-    const int c16 = (my_col & 63) >> 3;
-    uint32_t put[2][2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int rr = i * kRowsAtOnce + my_row;
-        put[i][k] = (my_col >> 6) * kChunkBytes + rr * 128 + (((c16 + k) ^ (rr & 7)) << 4);
-      }
+    using U = Units<C, kDim, kV>;
+    const CUtensorMap* map = kV ? &tm_v : &tm_k;
+    const int shift = min(p.box_shift, U::kRowShift);
+    const int copies = (U::kRows >> shift) * U::kChunks;
+    const int box = lane / U::kChunks, chunk = lane % U::kChunks;
+    const uint32_t dst = chunk * U::kRows * U::kWidth + (box << shift) * U::kWidth;
+    uint64_t* bar = raw_full + (kV ? 2 : 0);
+    uint64_t* free = raw_free + (kV ? 2 : 0);
     Place at;
     at.start(items);
     __syncwarp();
-    // lane i: where the block's rows 16 i on are (pages hold whole sixteens); past
-    // the length the cache's first rows, whose scores are masked and whose values
-    // become zero.  The table entry is asked for a block ahead, and used only
-    // before the block's last unit.
-    int64_t group = 0;
-    int key = -1, entry = 0;
+    bool ok = true;
+    int count = 0, key = -1, entry = 0, u = 0;
     auto ask = [&]() {
-      key = at.it.key0 + at.b * kN + (lane & 7) * 16;
-      if (at.live && key < at.it.kv_len)
+      key = at.it.key0 + at.b * kN + (kV ? u : u % U::kHalves) * U::kRows + (box << shift);
+      if (at.live && lane < copies && key < at.it.kv_len)
         entry = a.seqs.table[int64_t(at.it.s) * a.seqs.width + key / a.cache.page_size];
       else
         key = -1;
     };
-    auto look_up = [&]() {
-      group = 0;
-      if (key >= 0) {
-        const int64_t page = checked_page(entry, a.cache.pages, a.err);
-        const int64_t* st = kV ? a.cache.vs : a.cache.ks;
-        if (page != a.cache.pages)
-          group = page * st[0] + key % a.cache.page_size * st[1] + at.it.h * st[2];
-      }
-    };
-    uint4 v[kPasses];
-    // pass i (in order) of unit u of the block that `where` describes
-    const uint8_t* from = nullptr;
-    auto load = [&](int64_t where, int u, int i) {
-      if (i % kOfGroup == 0) {
-        from = base + (kV ? 0 : u / kHalves * C::kKChunks * 64) +
-               __shfl_sync(0xffffffffu, where, (kV ? u : u % kHalves) * kGroups + i / kOfGroup);
-      } else {
-        from += step;
-      }
-      v[i] = *reinterpret_cast<const uint4*>(from);
-    };
     ask();
-    look_up();
+    while (ok && at.live) {
+      int page = -1, in_page = 0;
+      if (key >= 0) {
+        page = static_cast<int>(checked_page(entry, a.cache.pages, a.err));
+        in_page = key % a.cache.page_size;
+      }
+      const int head = at.it.h, piece = kV ? 0 : u / U::kHalves, b = count & 1, was = at.item;
+      bool next_item = false;
+      if (++u == U::kCount) {
+        u = 0;
+        next_item = at.next(items);
+        __syncwarp();
+      }
+      ask();
+      const int n = __popc(__ballot_sync(0xffffffffu, page >= 0));
+      if (count >= 2)
+        ok = __all_sync(0xffffffffu, wait(&free[b], (count >> 1 & 1) ^ 1, abort_flag));
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(&bar[b], n * (U::kWidth << shift));
+      __syncwarp();
+      if (page >= 0)
+        tma_load_page(raw + ((kV ? 2 : 0) + b) * kRawBytes + dst, map, &bar[b], piece + chunk,
+                      in_page, head, page);
+      ++count;
+      if (next_item) {
+        if (lane == 0) items.release(was);
+        moved(was + 1);
+      }
+    }
+    // every copy has landed before the block may end
+    for (int i = max(0, count - 2); i < count; ++i) {
+      volatile int no_abort = 0;
+      if (!wait(&bar[i & 1], i >> 1 & 1, &no_abort)) atomicOr(a.err, NVFP4_ATTENTION_TIMEOUT);
+    }
+    __syncwarp();
+  };
+
+  // Two warps widen K, two V: a thread's 16 codes become 32 bytes of the slot.
+  // (Codes loaded from the pages to registers held up every arrival and fence,
+  // which wait for the loads before them.)
+  auto widen_pages = [&](auto values) {
+    constexpr bool kV = decltype(values)::value;
+    using U = Units<C, kDim, kV>;
+    constexpr int kChunkBytes = kV ? C::kVChunk : C::kKChunk;
+    constexpr int kRowsAtOnce = U::kRowsAtOnce;
+    const int tid = threadIdx.x & 63;
+    const int my_row = tid / U::kPerRow, my_col = tid % U::kPerRow * 16;
+    // where a pass's 16 bytes come from in the unit, and its 32 bytes go in the
+    // slot: both swizzles repeat every 8 rows
+    const int c16 = (my_col & 63) >> 3;
+    uint32_t get[2], put[2][2];
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) load(group, 0, i);
+    for (int i = 0; i < 2; ++i) {
+      const int rr = i * kRowsAtOnce + my_row;
+      get[i] = U::kWidth == 128
+                   ? (my_col >> 7) * U::kRows * 128 + rr * 128 + (((my_col & 127) >> 4 ^ (rr & 7)) << 4)
+                   : rr * 64 + ((my_col >> 4 ^ (rr >> 1 & 3)) << 4);
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        put[i][k] = (my_col >> 6) * kChunkBytes + rr * 128 + (((c16 + k) ^ (rr & 7)) << 4);
+    }
+    Place at;
+    at.start(items);
+    __syncwarp();
     std::conditional_t<kV, VRing<C>, KRing<C>> r;
     int turns = 0;                                               // slots filled, up to the ring's
+    int count = 0;                                               // units widened
     while (at.live) {
-      const Item it = at.it;
-      const int key0 = it.key0 + at.b * kN, was = at.item;
-      const int64_t here = group;
-      const bool moved = at.next(items);
-      __syncwarp();
-      ask();
+      const int key0 = at.it.key0 + at.b * kN;
 #pragma unroll 1
-      for (int u = 0; u < kUnits; ++u) {
-        if (u % kHalves == 0) {
+      for (int u = 0; u < U::kCount; ++u, ++count) {
+        if (u % U::kHalves == 0) {
           if (turns == (kV ? C::kVSlots : C::kKSlots)) {
             wait(&empty[r.slot], r.par ^ 1, abort_flag);
             __syncwarp();
@@ -550,42 +579,102 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
             ++turns;
           }
         }
-        if (u == kUnits - 1) look_up();
-        const int64_t where = u + 1 < kUnits ? here : group;
-        const int next_u = u + 1 < kUnits ? u + 1 : 0;
-        uint8_t* slot = ring + r.slot * C::kSlotBytes + (u % kHalves) * kUnitRows * 128;
+        const int b = (kV ? 2 : 0) + (count & 1);
+        wait(&raw_full[b], count >> 1 & 1, abort_flag);
+        __syncwarp();
+        const uint8_t* unit = raw + b * kRawBytes;
+        uint8_t* slot = ring + r.slot * C::kSlotBytes + (u % U::kHalves) * U::kRows * 128;
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
+        for (int i = 0; i < U::kPasses; ++i) {
+          const uint4 v = *reinterpret_cast<const uint4*>(unit + (i >> 1) * (2 * kRowsAtOnce * U::kWidth) + get[i & 1]);
           uint32_t f[8];
-          const uint32_t cw[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) e4m3x4_to_f16x4(cw[k], f[2 * k], f[2 * k + 1]);
-          load(where, next_u, i);
+          e4m3x4_to_f16x4(v.x, f[0], f[1]);
+          e4m3x4_to_f16x4(v.y, f[2], f[3]);
+          e4m3x4_to_f16x4(v.z, f[4], f[5]);
+          e4m3x4_to_f16x4(v.w, f[6], f[7]);
           uint8_t* at_row = slot + (i >> 1) * (2 * kRowsAtOnce * 128);
           *reinterpret_cast<uint4*>(at_row + put[i & 1][0]) = make_uint4(f[0], f[1], f[2], f[3]);
           *reinterpret_cast<uint4*>(at_row + put[i & 1][1]) = make_uint4(f[4], f[5], f[6], f[7]);
         }
-        if (u % kHalves == kHalves - 1) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&raw_free[b]);
+        if (u % U::kHalves == U::kHalves - 1) {
           // the passes' rows of a V slot lie with both warps: each looks over the
           // rows that it wrote
-          const int first = key0 + u / kHalves * kRows;
-          if (kV && first + kRows > it.least()) {
-            __syncwarp();
+          const int first = key0 + u / U::kHalves * (U::kRows * U::kHalves);
+          if (kV && first + U::kRows * U::kHalves > at.it.least()) {
             bool bad = false;
 #pragma unroll 1
-            for (int q = 0; q < kRows; q += kRowsAtOnce)
-              bad |= check_rows(it, first, r.slot, q + (warp & 1) * (kRowsAtOnce / 2), kRowsAtOnce / 2);
-            if (bad) dirty[was % kDirty] = was + 1;
+            for (int q = 0; q < U::kRows * U::kHalves; q += kRowsAtOnce)
+              bad |= check_rows(at.it, first, r.slot, q + (warp & 1) * (kRowsAtOnce / 2), kRowsAtOnce / 2);
+            if (bad) dirty[at.item % kDirty] = at.item + 1;
           }
-          // (the proxy fence is the MMA warp's: here it would wait for the loads
-          // that are on their way)
+          fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&full[r.slot]);
           r.next();
         }
       }
+      const int was = at.item;
+      const bool moved = at.next(items);
+      __syncwarp();
       if (moved && lane == 0) items.release(was);
     }
+  };
+
+  // The 32 query rows of a softmax warp, scaled by a power of two each, in f16;
+  // what the scores of the lane's own row have to be multiplied by.  With one
+  // tile both groups read all rows and each stores every other one.
+  auto scale_rows = [&](const Item& it, int x, int quad) {
+    constexpr int kLanes = kDim / 8, kRowsAtOnce = 32 / kLanes;      // 8 elements a lane
+    constexpr int kBatch = 32 / kRowsAtOnce < 8 ? 32 / kRowsAtOnce : 8;
+    const int ql = lane % kLanes, tile = kTiles == 2 ? x : 0;
+    float factor = 1.f;
+#pragma unroll 1
+    for (int p0 = 0; p0 < 32 / kRowsAtOnce; p0 += kBatch) {
+      uint4 v[kBatch];
+      uint32_t held = 0;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int row = quad * 32 + (p0 + i) * kRowsAtOnce + lane / kLanes;
+        const int tok = row / a.group, gi = row - tok * a.group;
+        const int ti = it.tok0 + tile * p.tile_tokens + tok;
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (tok < p.tile_tokens && ti < it.q_len) {
+          held |= 1u << i;
+          v[i] = *reinterpret_cast<const uint4*>(a.q.data + int64_t(it.q0 + ti) * a.q.ts +
+                                                 int64_t(it.h * a.group + gi) * a.q.hs + ql * 8);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int r0 = (p0 + i) * kRowsAtOnce, rr = quad * 32 + r0 + lane / kLanes;
+        const uint32_t in[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        float top = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          top = fmaxf(top, fmaxf(fabsf(bf16_lo(in[k])), fabsf(bf16_hi(in[k]))));
+#pragma unroll
+        for (int d = kLanes / 2; d > 0; d >>= 1)
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        int e = 141 - static_cast<int>(__float_as_uint(top) >> 23);
+        e = top == 0.f || top > 3.4e38f ? 0 : min(e, 100);
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        const float own = __shfl_sync(0xffffffffu, down, (lane - r0) % kRowsAtOnce * kLanes & 31);
+        if (lane >= r0 && lane < r0 + kRowsAtOnce) factor = own;
+        if ((held >> i & 1) && (kTiles == 2 || (rr & 1) == x)) {
+          uint32_t f[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) f[k] = f32x2_to_f16x2(bf16_lo(in[k]) * up, bf16_hi(in[k]) * up);
+          // elements 8 ql on: 64-column chunk ql / 8, 16-byte piece ql % 8 of the row
+          *reinterpret_cast<uint4*>(q_sm + tile * C::kQTile + (ql >> 3) * kM * 128 + rr * 128 +
+                                    (((ql & 7) ^ (rr & 7)) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
+        }
+        __syncwarp();
+      }
+    }
+    return factor;
   };
 
   const bool lead = lane == 0;
@@ -628,10 +717,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
       const bool last = qk.last() && (kTiles == 1 || x == 1);
 #pragma unroll 1
       for (int h = 0; h < C::kPieces; ++h, r.next()) {
-        if (kTiles == 1 || x == 0) {
-          ready(&full[r.slot], r.par);
-          if (kE4m3) fence_proxy_async_smem();
-        }
+        if (kTiles == 1 || x == 0) ready(&full[r.slot], r.par);
         if (!ok) break;
         tc_fence_after_sync();
         if (lead) {
@@ -662,7 +748,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
 
   if (warp < 8) {
     // ------------------------------------------------------ softmax, output
-    regs_inc<kSoftmaxRegs<kE4m3>>();
+    regs_inc<kSoftmaxRegs>();
     const int x = warp >> 2, quad = warp & 3;
     const int row = quad * 32 + lane;                 // of the tile
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
@@ -689,7 +775,15 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
       const int lim = valid ? max(0, it.kv_len - it.q_len + ti + 1) : 0;
       const int count = it.count();
       float c = a.scale * 1.44269504088896f;
-      if (kE4m3 && a.cache.k_scale) c *= a.cache.k_scale[it.h];
+      if constexpr (kE4m3) {
+        if (a.cache.k_scale) c *= a.cache.k_scale[it.h];
+        if (item > 0) wait(q_empty, (item - 1) & 1, abort_flag);
+        __syncwarp();
+        c *= scale_rows(it, x, quad);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+      }
       float m = -INFINITY, l = 0.f;                   // of the blocks that this thread saw
       for (int b = 0; b < count; ++b, ++step) {
         if (kTiles == 1 && (step & 1) != x) continue;
@@ -702,8 +796,6 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
         wait(&s_full[x], uses & 1, abort_flag);
         __syncwarp();
         tc_fence_after_sync();
-        if (kE4m3 && (b == 0 || (kTiles == 1 && b == 1)))
-          c *= q_factor[(item % kQFactors) * kTiles * kM + (kTiles == 2 ? x * kM : 0) + row];
         uint32_t s[4][32];
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_ld_32cols(t_s + i * 32, s[i]);
@@ -906,7 +998,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
       p.parts.note[unit] = note;
     }
   } else if (warp < 12) {
-    regs_dec<kHelperRegs<kE4m3>>();
+    regs_dec<kHelperRegs>();
     if (warp == 9) {
       // ------------------------------------------------ MMA: O += P V
       const uint32_t id_o = idesc<kE4m3>(kDim, true);
@@ -936,10 +1028,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
         VRing<C> r = at;
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {                 // of the keys
-          if ((kTiles == 1 || x == 0) && (half == 0 || C::kPieces == 2)) {
-            ready(&full[r.slot], r.par);
-            if (kE4m3) fence_proxy_async_smem();
-          }
+          if ((kTiles == 1 || x == 0) && (half == 0 || C::kPieces == 2)) ready(&full[r.slot], r.par);
           ready(&p_full[2 * x + half], i >> 1 & 1);
           if (!ok) break;
           tc_fence_after_sync();
@@ -996,90 +1085,33 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
         }
       }
       __syncwarp();
-    } else {
-      // -------------------------------------- Q rows scaled to f16 (warps 8, 11)
-      const int part = warp == 8 ? 0 : 1;
-      constexpr int kLanes = kDim / 8;              // of a row, 8 elements each
-      constexpr int kRowsAtOnce = 32 / kLanes, kPasses = kDim == 256 ? 8 : 4;
-      const int ql = lane % kLanes;
-      Walk w(range, a.seqs, a.cache.heads, p.plan, a.err);         // warp 11: the schedule
-      if (warp == 11 && lane == 0) publish(w, 0);
-      __syncwarp();
-      Item it;
-      for (int item = 0; items.get(item, it); ++item) {
+    } else if (warp == 8) {
+      copy_raw(std::false_type{}, [](int) {});
+    } else if (warp == 11) {
+      // ------------------------------- the schedule, and the copies of V's codes
+      Walk w(range, a.seqs, a.cache.heads, p.plan, a.err);
+      auto ahead = [&](int item) {                  // item `item` to the other warps
+        if (lane == 0) publish(w, item);
+        if (w.more()) w.next(a.seqs, a.cache.heads, p.plan, a.err);
         __syncwarp();
-        if (warp == 11) {
-          w.next(a.seqs, a.cache.heads, p.plan, a.err);
-          if (lane == 0) publish(w, item + 1);
-          __syncwarp();
-        }
-        if (item > 0) {
-          wait(q_empty, (item - 1) & 1, abort_flag);
-          __syncwarp();
-        }
-        // rows that hold no token are left as they are: their weights are 0
-        const int tokens = min(kTiles * p.tile_tokens, it.q_len - it.tok0);
-        const int rows = kTiles == 1 || tokens <= p.tile_tokens
-                             ? tokens * a.group
-                             : kM + (tokens - p.tile_tokens) * a.group;
-#pragma unroll 1
-        for (int r0 = part * kPasses * kRowsAtOnce; r0 < rows; r0 += 2 * kPasses * kRowsAtOnce) {
-          uint4 v[kPasses];
-#pragma unroll
-          for (int i = 0; i < kPasses; ++i) {
-            const int r = r0 + i * kRowsAtOnce + lane / kLanes;
-            const int x = r / kM, rr = r % kM;
-            const int tok = rr / a.group, gi = rr - tok * a.group;
-            const int ti = it.tok0 + x * p.tile_tokens + tok;
-            v[i] = make_uint4(0, 0, 0, 0);
-            if (tok < p.tile_tokens && ti < it.q_len)
-              v[i] = *reinterpret_cast<const uint4*>(a.q.data + int64_t(it.q0 + ti) * a.q.ts +
-                                                     int64_t(it.h * a.group + gi) * a.q.hs + ql * 8);
-          }
-#pragma unroll
-          for (int i = 0; i < kPasses; ++i) {
-            const int r = r0 + i * kRowsAtOnce + lane / kLanes;
-            const int x = r / kM, rr = r % kM;
-            const uint32_t in[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-            float top = 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              top = fmaxf(top, fmaxf(fabsf(bf16_lo(in[k])), fabsf(bf16_hi(in[k]))));
-#pragma unroll
-            for (int d = kLanes / 2; d > 0; d >>= 1)
-              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            int e = 141 - static_cast<int>(__float_as_uint(top) >> 23);
-            e = top == 0.f || top > 3.4e38f ? 0 : min(e, 100);
-            const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-            if (r < kTiles * kM) {
-            if (ql == 0)
-              q_factor[(item % kQFactors) * kTiles * kM + r] =
-                  __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-            uint32_t f[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) f[k] = f32x2_to_f16x2(bf16_lo(in[k]) * up, bf16_hi(in[k]) * up);
-            // elements 8 ql on: 64-column chunk ql / 8, 16-byte piece ql % 8 of the row
-            *reinterpret_cast<uint4*>(q_sm + x * C::kQTile + (ql >> 3) * kM * 128 + rr * 128 +
-                                      (((ql & 7) ^ (rr & 7)) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
-            }
-            __syncwarp();
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(q_full);
-          if (warp != 11) items.release(item);
-        }
-      }
+      };
+      bool all = false;                             // the end has been published
+      auto more = [&](int item) {
+        if (all) return;
+        all = !w.more();
+        ahead(item);
+      };
+      more(0);
+      more(1);
+      copy_raw(std::true_type{}, [&](int item) { more(item + 1); });
     }
   } else {
     // ------------------------------------------ K, V codes widened to f16
     if constexpr (!kE4m3) {
-      regs_dec<kScoreRegs>();
+      regs_dec<kHelperRegs>();
       if (warp == kScoreWarp) score_mma();
     } else {
-      regs_dec<kWidenRegs>();
+      regs_dec<kHelperRegs>();
       if (warp < 14)
         widen_pages(std::false_type{});
       else
@@ -1109,8 +1141,7 @@ int run(const Attend& a, const Device& d, cudaStream_t stream) {
       cudaGetLastError();
       return NVFP4_ERR_LAUNCH;
     }
-    constexpr int need = 256 * kSoftmaxRegs<kE4m3> + 128 * kHelperRegs<kE4m3> +
-                         128 * (kE4m3 ? kWidenRegs : kScoreRegs);
+    constexpr int need = 256 * (kSoftmaxRegs + kHelperRegs);
     if (attr.numRegs * C::kThreads < need) return NVFP4_ERR_LAUNCH;
   }
   if (const int st = allow_smem(kernel, C::kSmem, d, ready)) return st;
@@ -1122,11 +1153,18 @@ int run(const Attend& a, const Device& d, cudaStream_t stream) {
   while (p.box_shift < 7 && a.cache.page_size % (2 << p.box_shift) == 0) ++p.box_shift;
   const int box = 1 << p.box_shift;
   CUtensorMap tm_q{}, tm_k{}, tm_v{};
-  if (!kE4m3 && (!query_map(&tm_q, a.q, a.cache.dim, a.q_heads, a.seqs.tokens, a.group, p.tile_tokens) ||
-                 !page_map(&tm_k, a.cache, false, 64, box, 1) ||
-                 !page_map(&tm_v, a.cache, true, 64, std::min(box, C::kVKeys),
-                           box >= C::kVKeys ? C::kVChunks / kCluster : 1)))
+  if (kE4m3) {
+    // rows of the units, 64 or 128 bytes of each (the readers undo the swizzle)
+    constexpr int width = kDim < 128 ? 64 : 128;
+    if (!page_map(&tm_k, a.cache, false, width, std::min(box, Units<C, kDim, false>::kRows), 1) ||
+        !page_map(&tm_v, a.cache, true, width, std::min(box, Units<C, kDim, true>::kRows), 1))
+      return NVFP4_ERR_LAUNCH;
+  } else if (!query_map(&tm_q, a.q, a.cache.dim, a.q_heads, a.seqs.tokens, a.group, p.tile_tokens) ||
+             !page_map(&tm_k, a.cache, false, 64, box, 1) ||
+             !page_map(&tm_v, a.cache, true, 64, std::min(box, C::kVKeys),
+                       box >= C::kVKeys ? C::kVChunks / kCluster : 1)) {
     return NVFP4_ERR_LAUNCH;
+  }
   if (const int st = launch_clusters(kCluster, kernel, dim3(units * kCluster), dim3(C::kThreads),
                                      C::kSmem, stream, tm_q, tm_k, tm_v, p))
     return st;

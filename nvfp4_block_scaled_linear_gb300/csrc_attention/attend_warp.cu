@@ -1,7 +1,7 @@
 // attend_warp.cu -- paged attention for few query rows (decode, verify).
 //
 // The rows of one key/value head (its group's query heads times a few tokens)
-// fill at most four 16-row tiles of the warp MMA, so the work is reading the
+// fill at most two 16-row tiles of the warp MMA, so the work is reading the
 // cache once: bound by bytes.  The design is about keeping the memory busy:
 // one CTA per SM (two where rows are short) takes an equal share of all keys
 // (schedule.cuh) and one producer warp keeps a ring of 64-key tiles in flight
@@ -691,15 +691,13 @@ int run(const Attend& p, const Device& d, cudaStream_t stream) {
 
 template <int kDim, bool kE4m3>
 int run_rows(int rows, const Attend& p, const Device& d, cudaStream_t stream) {
-  return rows <= 16   ? run<kDim, kE4m3, 1>(p, d, stream)
-         : rows <= 32 ? run<kDim, kE4m3, 2>(p, d, stream)
-                      : run<kDim, kE4m3, 4>(p, d, stream);
+  return rows <= 16 ? run<kDim, kE4m3, 1>(p, d, stream) : run<kDim, kE4m3, 2>(p, d, stream);
 }
 
 }  // namespace
 
 int64_t attend_warp_workspace(int head_dim, const Device& d) {
-  return std::max(Parts::bytes(2 * d.num_sms, 64, head_dim), Parts::bytes(d.num_sms, 64, head_dim));
+  return std::max(Parts::bytes(2 * d.num_sms, 16, head_dim), Parts::bytes(d.num_sms, 32, head_dim));
 }
 
 int run_attend_warp(int rows, const Attend& p, const Device& d, cudaStream_t stream) {
