@@ -49,7 +49,7 @@ namespace {
 constexpr int kM = 128;                       // rows of a tile
 constexpr int kBlockShift = 7;
 constexpr int kN = 1 << kBlockShift;          // keys of a block (one unit)
-constexpr int kExtra = 2;                     // blocks that an item's beginning costs
+constexpr int kExtra = 3;                     // blocks that an item's beginning costs
 constexpr float kSlack = 8.f;                 // growth of log2 of a weight before rescaling
 // Registers of a thread in the softmax warps and in the others: in all what 512
 // threads of 128 registers are launched with.
@@ -627,11 +627,14 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
   // tile both groups read all rows and each stores every other one.
   auto scale_rows = [&](const Item& it, int x, int quad) {
     constexpr int kLanes = kDim / 8, kRowsAtOnce = 32 / kLanes;      // 8 elements a lane
-    constexpr int kBatch = 32 / kRowsAtOnce < 8 ? 32 / kRowsAtOnce : 8;
+    constexpr int kBatch = 32 / kRowsAtOnce < 16 ? 32 / kRowsAtOnce : 16;
     const int ql = lane % kLanes, tile = kTiles == 2 ? x : 0;
     float factor = 1.f;
 #pragma unroll 1
     for (int p0 = 0; p0 < 32 / kRowsAtOnce; p0 += kBatch) {
+      // (rows that hold no token are left as they are: their weights are 0)
+      const int first = quad * 32 + p0 * kRowsAtOnce;
+      if (first >= min(p.tile_tokens, it.q_len - it.tok0 - tile * p.tile_tokens) * a.group) break;
       uint4 v[kBatch];
       uint32_t held = 0;
 #pragma unroll
