@@ -622,62 +622,43 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
     }
   };
 
-  // The 32 query rows of a softmax warp, scaled by a power of two each, in f16;
-  // what the scores of the lane's own row have to be multiplied by.  With one
-  // tile both groups read all rows and each stores every other one.
-  auto scale_rows = [&](const Item& it, int x, int quad) {
-    constexpr int kLanes = kDim / 8, kRowsAtOnce = 32 / kLanes;      // 8 elements a lane
-    constexpr int kBatch = 32 / kRowsAtOnce < 16 ? 32 / kRowsAtOnce : 16;
-    const int ql = lane % kLanes, tile = kTiles == 2 ? x : 0;
-    float factor = 1.f;
-#pragma unroll 1
-    for (int p0 = 0; p0 < 32 / kRowsAtOnce; p0 += kBatch) {
-      // (rows that hold no token are left as they are: their weights are 0)
-      const int first = quad * 32 + p0 * kRowsAtOnce;
-      if (first >= min(p.tile_tokens, it.q_len - it.tok0 - tile * p.tile_tokens) * a.group) break;
-      uint4 v[kBatch];
-      uint32_t held = 0;
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int row = quad * 32 + (p0 + i) * kRowsAtOnce + lane / kLanes;
-        const int tok = row / a.group, gi = row - tok * a.group;
-        const int ti = it.tok0 + tile * p.tile_tokens + tok;
-        v[i] = make_uint4(0, 0, 0, 0);
-        if (tok < p.tile_tokens && ti < it.q_len) {
-          held |= 1u << i;
-          v[i] = *reinterpret_cast<const uint4*>(a.q.data + int64_t(it.q0 + ti) * a.q.ts +
-                                                 int64_t(it.h * a.group + gi) * a.q.hs + ql * 8);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int r0 = (p0 + i) * kRowsAtOnce, rr = quad * 32 + r0 + lane / kLanes;
-        const uint32_t in[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-        float top = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          top = fmaxf(top, fmaxf(fabsf(bf16_lo(in[k])), fabsf(bf16_hi(in[k]))));
-#pragma unroll
-        for (int d = kLanes / 2; d > 0; d >>= 1)
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        int e = 141 - static_cast<int>(__float_as_uint(top) >> 23);
-        e = top == 0.f || top > 3.4e38f ? 0 : min(e, 100);
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        const float own = __shfl_sync(0xffffffffu, down, (lane - r0) % kRowsAtOnce * kLanes & 31);
-        if (lane >= r0 && lane < r0 + kRowsAtOnce) factor = own;
-        if ((held >> i & 1) && (kTiles == 2 || (rr & 1) == x)) {
-          uint32_t f[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) f[k] = f32x2_to_f16x2(bf16_lo(in[k]) * up, bf16_hi(in[k]) * up);
-          // elements 8 ql on: 64-column chunk ql / 8, 16-byte piece ql % 8 of the row
-          *reinterpret_cast<uint4*>(q_sm + tile * C::kQTile + (ql >> 3) * kM * 128 + rr * 128 +
-                                    (((ql & 7) ^ (rr & 7)) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
-        }
-        __syncwarp();
-      }
+  // A softmax thread's query row, scaled by a power of two, in f16; what the
+  // row's scores have to be multiplied by.  With one tile the thread of either
+  // group stores half of the columns.  (A lane per row keeps this to two short
+  // loops: unrolled over rows it was 28 KB of code that runs once, and fetching
+  // it took 10 us.)
+  auto scale_row = [&](const Item& it, int x, int row, bool valid) {
+    // a row that holds no token is left as it is: its weights are 0
+    if (!valid) return 1.f;
+    const int tok = row / a.group, gi = row - tok * a.group, tile = kTiles == 2 ? x : 0;
+    const int ti = it.tok0 + tile * p.tile_tokens + tok;
+    const uint4* src = reinterpret_cast<const uint4*>(
+        a.q.data + int64_t(it.q0 + ti) * a.q.ts + int64_t(it.h * a.group + gi) * a.q.hs);
+    uint32_t top2 = 0;                                  // magnitudes order as integers
+#pragma unroll 8
+    for (int k = 0; k < kDim / 8; ++k) {
+      const uint4 v = src[k];
+      top2 = max_u16x2(max_u16x2(top2, v.x & 0x7FFF7FFFu), v.y & 0x7FFF7FFFu);
+      top2 = max_u16x2(max_u16x2(top2, v.z & 0x7FFF7FFFu), v.w & 0x7FFF7FFFu);
     }
-    return factor;
+    const uint32_t top = max(top2 & 0xFFFFu, top2 >> 16);
+    const int e = top == 0 || top >= 0x7F80u ? 0 : min(141 - static_cast<int>(top >> 7), 100);
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    constexpr int kPieces = kDim / 8 / (kTiles == 1 ? 2 : 1);
+    const int k0 = kTiles == 1 ? x * kPieces : 0;
+    uint8_t* dst = q_sm + tile * C::kQTile + row * 128;
+#pragma unroll 2
+    for (int k = k0; k < k0 + kPieces; ++k) {
+      const uint4 v = src[k];
+      const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+      uint32_t f[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = f32x2_to_f16x2(bf16_lo(in[i]) * up, bf16_hi(in[i]) * up);
+      // elements 8 k on: 64-column chunk k / 8, 16-byte piece k % 8 of the row
+      *reinterpret_cast<uint4*>(dst + (k >> 3) * kM * 128 + (((k & 7) ^ (row & 7)) << 4)) =
+          make_uint4(f[0], f[1], f[2], f[3]);
+    }
+    return __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
   };
 
   const bool lead = lane == 0;
@@ -782,7 +763,8 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
         if (a.cache.k_scale) c *= a.cache.k_scale[it.h];
         if (item > 0) wait(q_empty, (item - 1) & 1, abort_flag);
         __syncwarp();
-        c *= scale_rows(it, x, quad);
+        c *= scale_row(it, x, row, valid);
+        __syncwarp();
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);
