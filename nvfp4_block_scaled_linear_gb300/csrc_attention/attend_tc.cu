@@ -49,7 +49,7 @@ namespace {
 constexpr int kM = 128;                       // rows of a tile
 constexpr int kBlockShift = 7;
 constexpr int kN = 1 << kBlockShift;          // keys of a block (one unit)
-constexpr int kExtra = 3;                     // blocks that an item's beginning costs
+constexpr int kExtra = 5;                     // blocks that an item's beginning costs
 constexpr float kSlack = 8.f;                 // growth of log2 of a weight before rescaling
 // Registers of a thread in the softmax warps and in the others: in all what 512
 // threads of 128 registers are launched with.

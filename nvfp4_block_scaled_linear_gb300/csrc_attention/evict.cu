@@ -86,14 +86,14 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const Evict p, int sli
       __syncthreads();
       uint32_t* count = counts[shift >> 3];
       const uint32_t prefix = sh_prefix, mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
+#pragma unroll 4
       for (int j = tid; j < (len + 31) / 32 * 32; j += kThreads) {
         const uint32_t u = j < len ? key_at(j) : 0u;
         const uint32_t bin = (u >> shift) & 255;
         unsigned left = __ballot_sync(0xffffffffu, j < len && (u & mask) == prefix);
-        // equal values (and equal high bytes) are common: the bins of the first
-        // lanes with one add for all that share them, the rest one by one
-#pragma unroll
-        for (int round = 0; round < 3 && left; ++round) {
+        // equal values (and equal high bytes) are common: the first lane's bin
+        // with one add for all that share it, the rest one by one
+        if (left) {
           const int lead = __ffs(left) - 1;
           const unsigned same =
               left & __ballot_sync(0xffffffffu, bin == __shfl_sync(0xffffffffu, bin, lead));
