@@ -4,8 +4,8 @@
 
 Output: nvfp4_block_scaled_linear_gb300/_build/libnvfp4_linear.so (ignored by
 git), from the linear layer's translation unit (csrc/) and the attention
-block's (csrc_attention/).  The CUDA runtime is linked as a shared library so that the process
-shares one runtime (current device, streams) with PyTorch.
+block's (csrc_attention/).  The CUDA runtime is linked as a shared library so
+that the process shares one runtime (current device, streams) with PyTorch.
 """
 import glob
 import os
