@@ -1,7 +1,5 @@
 // attend.cu -- the choice of the attention kernel, and the tensor maps.
 #include <algorithm>
-#include <cstring>
-#include <mutex>
 
 #include <cudaTypedefs.h>
 
@@ -11,67 +9,31 @@ namespace nvfp4 {
 namespace attn {
 namespace {
 
-// Encoding a tensor map costs microseconds of host time, so encoded maps are
-// kept in a small direct-mapped cache.  The key holds every encoding input,
-// so a hit is always valid.
-struct MapKey {
-  const void* base;
-  uint64_t dims[5], strides[4];
-  uint32_t box[5];
-  int32_t rank, bytes, zero; // bytes of an element
-};
-struct MapSlot {
-  MapKey key;
-  CUtensorMap map;
-};
-constexpr int kMapSlots = 256;
-MapSlot g_maps[kMapSlots];
-std::mutex g_map_mutex;
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+using Encode = PFN_cuTensorMapEncodeTiled_v12000;
 
-bool encode(CUtensorMap* map, const MapKey& key) {
-  uint64_t h = 0;
-  const unsigned char* bytes = reinterpret_cast<const unsigned char*>(&key);
-  for (size_t i = 0; i + 8 <= sizeof(key); i += 8) {
-    uint64_t w;
-    std::memcpy(&w, bytes + i, 8);
-    h = (h ^ w) * 0x9E3779B97F4A7C15ull;
-    h ^= h >> 29;
+Encode find_encode() {
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                       &q) != cudaSuccess ||
+      q != cudaDriverEntryPointSuccess) {
+    cudaGetLastError();
+    return nullptr;
   }
-  std::lock_guard<std::mutex> lock(g_map_mutex);
-  MapSlot& slot = g_maps[h % kMapSlots];
-  if (slot.key.rank == 0 || std::memcmp(&slot.key, &key, sizeof(key)) != 0) {
-    if (!g_encode) {
-      void* fn = nullptr;
-      cudaDriverEntryPointQueryResult q;
-      if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
-                                           &q) != cudaSuccess ||
-          q != cudaDriverEntryPointSuccess || !fn) {
-        cudaGetLastError();
-        return false;
-      }
-      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-    }
-    cuuint64_t dims[5], strides[4];
-    cuuint32_t box[5];
-    const cuuint32_t unit[5] = {1, 1, 1, 1, 1};
-    for (int i = 0; i < 5; ++i) dims[i] = key.dims[i], box[i] = key.box[i];
-    for (int i = 0; i < 4; ++i) strides[i] = key.strides[i];
-    CUtensorMap fresh;
-    if (g_encode(&fresh,
-                 key.bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                 key.rank, const_cast<void*>(key.base), dims, strides, box, unit,
-                 CU_TENSOR_MAP_INTERLEAVE_NONE,
-                 key.box[0] * key.bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
-                                               : CU_TENSOR_MAP_SWIZZLE_64B,
-                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return false;
-    slot.key = key;
-    slot.map = fresh;
-  }
-  *map = slot.map;
-  return true;
+  return reinterpret_cast<Encode>(fn);
+}
+
+// A map is encoded anew for each call: a few tenths of a microsecond.
+bool encode(CUtensorMap* map, int rank, int bytes, void* base, const cuuint64_t* dims,
+            const cuuint64_t* strides, const cuuint32_t* box) {
+  static const Encode fn = find_encode();
+  const cuuint32_t unit[5] = {1, 1, 1, 1, 1};
+  return fn && fn(map,
+                  bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                  rank, base, dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  box[0] * bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -79,29 +41,19 @@ bool encode(CUtensorMap* map, const MapKey& key) {
 bool page_map(CUtensorMap* map, const Cache& c, bool values, int inner, int rows, int chunks) {
   const int64_t* st = values ? c.vs : c.ks;
   const int size = c.e4m3 ? 1 : 2;
-  MapKey key;
-  std::memset(&key, 0, sizeof(key));
-  key.base = values ? c.v : c.k;
-  key.rank = 5;
-  key.bytes = size;
-  key.dims[0] = inner, key.dims[1] = c.page_size, key.dims[2] = c.dim / inner;
-  key.dims[3] = c.heads, key.dims[4] = c.pages;
-  key.strides[0] = st[1] * size, key.strides[1] = inner * size;
-  key.strides[2] = st[2] * size, key.strides[3] = st[0] * size;
-  key.box[0] = inner, key.box[1] = rows, key.box[2] = chunks, key.box[3] = 1, key.box[4] = 1;
-  return encode(map, key);
+  const cuuint64_t dims[5] = {cuuint64_t(inner), cuuint64_t(c.page_size), cuuint64_t(c.dim / inner),
+                              cuuint64_t(c.heads), cuuint64_t(c.pages)};
+  const cuuint64_t strides[4] = {cuuint64_t(st[1] * size), cuuint64_t(inner * size),
+                                 cuuint64_t(st[2] * size), cuuint64_t(st[0] * size)};
+  const cuuint32_t box[5] = {cuuint32_t(inner), cuuint32_t(rows), cuuint32_t(chunks), 1, 1};
+  return encode(map, 5, size, values ? c.v : c.k, dims, strides, box);
 }
 
 bool query_map(CUtensorMap* map, const Heads& q, int dim, int heads, int tokens, int group, int box) {
-  MapKey key;
-  std::memset(&key, 0, sizeof(key));
-  key.base = q.data;
-  key.rank = 3;
-  key.bytes = 2;
-  key.dims[0] = dim, key.dims[1] = heads, key.dims[2] = tokens;
-  key.strides[0] = q.hs * 2, key.strides[1] = q.ts * 2;
-  key.box[0] = 64, key.box[1] = group, key.box[2] = box;
-  return encode(map, key);
+  const cuuint64_t dims[3] = {cuuint64_t(dim), cuuint64_t(heads), cuuint64_t(tokens)};
+  const cuuint64_t strides[2] = {cuuint64_t(q.hs * 2), cuuint64_t(q.ts * 2)};
+  const cuuint32_t boxes[3] = {64, cuuint32_t(group), cuuint32_t(box)};
+  return encode(map, 3, 2, q.data, dims, strides, boxes);
 }
 
 int64_t attend_workspace(int head_dim, const Device& d) {
