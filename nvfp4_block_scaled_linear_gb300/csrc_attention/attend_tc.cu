@@ -244,6 +244,7 @@ struct Units {
   static constexpr int kRowShift = kRows == 128 ? 7 : kRows == 64 ? 6 : 5;
   static constexpr int kHalves = kSlotRows / kRows;                   // units of a slot
   static constexpr int kCount = C::kPieces * kHalves;                 // of a block
+  static constexpr int kKeyUnits = kN / kRows;                        // of different keys
   static constexpr int kWidth = kDim < 128 ? 64 : 128;                // bytes of a row's copy
   static constexpr int kChunks = kV && kDim == 256 ? 2 : 1;           // copies of a row
   static_assert(kRows * kPerRow * 16 == kRawBytes && (1 << kRowShift) == kRows, "a unit's bytes");
@@ -475,15 +476,21 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
   };
 
   // e4m3 codes of K or of V, unit by unit (a unit: 8 KB, what 64 threads widen in
-  // 8 passes), copied by one warp into two buffers.  Lane: copy (box, chunk).
+  // 8 passes), copied by one warp into two buffers.  Each lane keeps the operands
+  // of one copy of a block (unit, box, chunk), its page read one block ahead.
   // `moved(item)`: called when the item before `item` is done with.
   auto copy_raw = [&](auto values, auto moved) {
     constexpr bool kV = decltype(values)::value;
     using U = Units<C, kDim, kV>;
     const CUtensorMap* map = kV ? &tm_v : &tm_k;
     const int shift = min(p.box_shift, U::kRowShift);
-    const int copies = (U::kRows >> shift) * U::kChunks;
-    const int box = lane / U::kChunks, chunk = lane % U::kChunks;
+    // a row's chunks: in one copy, where that has all rows of the unit
+    const int chunks = (1 << shift) == U::kRows ? 1 : U::kChunks;
+    const int per_unit = (U::kRows >> shift) * chunks;
+    const int unit = lane / per_unit, box = lane % per_unit / chunks, chunk = lane % chunks;
+    const bool has_copy = unit < U::kKeyUnits;
+    const int row = unit * U::kRows + (box << shift);
+    const int bytes = (U::kWidth << shift) * (U::kChunks / chunks);
     const uint32_t dst = chunk * U::kRows * U::kWidth + (box << shift) * U::kWidth;
     uint64_t* bar = raw_full + (kV ? 2 : 0);
     uint64_t* free = raw_free + (kV ? 2 : 0);
@@ -491,40 +498,40 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
     at.start(items);
     __syncwarp();
     bool ok = true;
-    int count = 0, key = -1, entry = 0, u = 0;
-    auto ask = [&]() {
-      key = at.it.key0 + at.b * kN + (kV ? u : u % U::kHalves) * U::kRows + (box << shift);
-      if (at.live && lane < copies && key < at.it.kv_len)
+    int count = 0, key = -1, entry = 0;
+    auto look_up = [&]() {
+      key = at.it.key0 + at.b * kN + row;
+      if (at.live && has_copy && key < at.it.kv_len)
         entry = a.seqs.table[int64_t(at.it.s) * a.seqs.width + key / a.cache.page_size];
       else
         key = -1;
     };
-    ask();
+    look_up();
     while (ok && at.live) {
       int page = -1, in_page = 0;
       if (key >= 0) {
         page = static_cast<int>(checked_page(entry, a.cache.pages, a.err));
         in_page = key % a.cache.page_size;
       }
-      const int head = at.it.h, piece = kV ? 0 : u / U::kHalves, b = count & 1, was = at.item;
-      bool next_item = false;
-      if (++u == U::kCount) {
-        u = 0;
-        next_item = at.next(items);
-        __syncwarp();
-      }
-      ask();
-      const int n = __popc(__ballot_sync(0xffffffffu, page >= 0));
-      if (count >= 2)
-        ok = __all_sync(0xffffffffu, wait(&free[b], (count >> 1 & 1) ^ 1, abort_flag));
-      if (!ok) break;
-      if (lane == 0) mbar_arrive_expect_tx(&bar[b], n * (U::kWidth << shift));
+      const int head = at.it.h, was = at.item;
+      const bool next_item = at.next(items);
       __syncwarp();
-      if (page >= 0)
-        tma_load_page(raw + ((kV ? 2 : 0) + b) * kRawBytes + dst, map, &bar[b], piece + chunk,
-                      in_page, head, page);
-      ++count;
-      if (next_item) {
+      look_up();
+#pragma unroll 1
+      for (int u = 0; u < U::kCount; ++u, ++count) {
+        const int b = count & 1;
+        const bool mine = page >= 0 && unit == u % U::kKeyUnits;
+        const int n = __popc(__ballot_sync(0xffffffffu, mine));
+        if (count >= 2)
+          ok = __all_sync(0xffffffffu, wait(&free[b], (count >> 1 & 1) ^ 1, abort_flag));
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&bar[b], n * bytes);
+        __syncwarp();
+        if (mine)
+          tma_load_page(raw + ((kV ? 2 : 0) + b) * kRawBytes + dst, map, &bar[b],
+                        u / U::kKeyUnits + chunk, in_page, head, page);
+      }
+      if (ok && next_item) {
         if (lane == 0) items.release(was);
         moved(was + 1);
       }
@@ -545,15 +552,26 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
     using U = Units<C, kDim, kV>;
     constexpr int kChunkBytes = kV ? C::kVChunk : C::kKChunk;
     constexpr int kRowsAtOnce = U::kRowsAtOnce;
-    const int tid = threadIdx.x & 63;
-    const int my_row = tid / U::kPerRow, my_col = tid % U::kPerRow * 16;
+    // Four lanes take 64 codes of a row and the next four those of another row,
+    // whose number differs in bits 0 and 2: so that of eight lanes neither the
+    // loads nor the stores meet in a bank.  (All eight in one row: their stores
+    // meet, pass time 850 to 1080 clocks.)
+    const int tid = threadIdx.x & 63, odd = U::kPerRow >= 8 ? tid >> 2 & 1 : 0;
+    const int my_row = U::kPerRow == 16  ? (tid >> 5) * 2 + odd
+                       : U::kPerRow == 8 ? (tid >> 4 & 1) * 4 + (tid >> 5) * 2 + odd
+                                         : tid / U::kPerRow;
+    const int my_col = U::kPerRow == 16  ? ((tid >> 3 & 3) * 4 + (tid & 3)) * 16
+                       : U::kPerRow == 8 ? ((tid >> 3 & 1) * 4 + (tid & 3)) * 16
+                                         : tid % U::kPerRow * 16;
+    // consecutive rows of a slot that one of the two warps writes, and their distance
+    constexpr int kRun = U::kPerRow >= 8 ? 2 : kRowsAtOnce / 2;
     // where a pass's 16 bytes come from in the unit, and its 32 bytes go in the
     // slot: both swizzles repeat every 8 rows
     const int c16 = (my_col & 63) >> 3;
     uint32_t get[2], put[2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int rr = i * kRowsAtOnce + my_row;
+      const int rr = (i * kRowsAtOnce + my_row) ^ (odd << 2);
       get[i] = U::kWidth == 128
                    ? (my_col >> 7) * U::kRows * 128 + rr * 128 + (((my_col & 127) >> 4 ^ (rr & 7)) << 4)
                    : rr * 64 + ((my_col >> 4 ^ (rr >> 1 & 3)) << 4);
@@ -605,8 +623,8 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
           if (kV && first + U::kRows * U::kHalves > at.it.least()) {
             bool bad = false;
 #pragma unroll 1
-            for (int q = 0; q < U::kRows * U::kHalves; q += kRowsAtOnce)
-              bad |= check_rows(at.it, first, r.slot, q + (warp & 1) * (kRowsAtOnce / 2), kRowsAtOnce / 2);
+            for (int q = 0; q < U::kRows * U::kHalves; q += 2 * kRun)
+              bad |= check_rows(at.it, first, r.slot, q + (warp & 1) * kRun, kRun);
             if (bad) dirty[at.item % kDirty] = at.item + 1;
           }
           fence_proxy_async_smem();
@@ -1141,8 +1159,9 @@ int run(const Attend& a, const Device& d, cudaStream_t stream) {
   if (kE4m3) {
     // rows of the units, 64 or 128 bytes of each (the readers undo the swizzle)
     constexpr int width = kDim < 128 ? 64 : 128;
+    using UV = Units<C, kDim, true>;
     if (!page_map(&tm_k, a.cache, false, width, std::min(box, Units<C, kDim, false>::kRows), 1) ||
-        !page_map(&tm_v, a.cache, true, width, std::min(box, Units<C, kDim, true>::kRows), 1))
+        !page_map(&tm_v, a.cache, true, width, std::min(box, UV::kRows), box >= UV::kRows ? UV::kChunks : 1))
       return NVFP4_ERR_LAUNCH;
   } else if (!query_map(&tm_q, a.q, a.cache.dim, a.q_heads, a.seqs.tokens, a.group, p.tile_tokens) ||
              !page_map(&tm_k, a.cache, false, 64, box, 1) ||
