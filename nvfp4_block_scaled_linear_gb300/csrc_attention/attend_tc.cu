@@ -1184,7 +1184,7 @@ int run(const Attend& a, const Device& d, cudaStream_t stream) {
   if (const int st = launch_clusters(kCluster, kernel, dim3(units * kCluster), dim3(C::kThreads),
                                      C::kSmem, stream, tm_q, tm_k, tm_v, p))
     return st;
-  return run_join(a, p.parts, p.plan, units, d.id, stream);
+  return run_join(int64_t(a.max_q_len) * a.group > kM, a, p.parts, p.plan, units, d.id, stream);
 }
 
 // One tile of rows; more: two tiles in a CTA, or in a pair of CTAs where one

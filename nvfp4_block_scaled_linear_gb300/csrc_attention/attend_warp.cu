@@ -697,7 +697,7 @@ int run(const Attend& p, const Device& d, cudaStream_t stream) {
   if (const int st = launch(kernel, dim3(ctas), dim3(kThreads), C::kSmem, stream, tm_k, tm_v, p,
                             plan, parts))
     return st;
-  return run_join(p, parts, plan, ctas, d.id, stream);
+  return run_join(false, p, parts, plan, ctas, d.id, stream);
 }
 
 template <int kDim, bool kE4m3>

@@ -13,25 +13,24 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxParts = 512;
 
-template <int kDim>
+// kMany: many rows in few parts each, so the block's groups of threads take a
+// row each; else they share the parts of one.
+template <int kDim, bool kMany>
 __global__ void __launch_bounds__(kThreads) join_kernel(const Attend p, const Parts parts,
                                                         const Plan plan, int ctas) {
   constexpr int kCols = kDim / 4;                // threads of one part, 4 columns each
-  constexpr int kWays = kThreads / kCols;        // parts read at a time
+  constexpr int kWays = kThreads / kCols;        // parts (or rows) read at a time
   __shared__ float weight[kMaxParts];
   __shared__ float4 sum_sm[kWays][kCols];
   __shared__ float total_sm;
   griddep_wait();
   griddep_launch_dependents();
-  const int c = blockIdx.x, r = blockIdx.y, lane = threadIdx.x & 31;
+  const int way = threadIdx.x / kCols, col = threadIdx.x % kCols;
+  const int c = blockIdx.x, r = kMany ? blockIdx.y * kWays + way : blockIdx.y;
+  const int lane = threadIdx.x & 31;
   const int4 note = parts.note[c];
   if (!(note.x & kPart1)) return;
   const SeqInfo si = load_seq(p.seqs, note.y, p.err);
-  const int tile_tokens = parts.tile_rows / p.group;
-  const int sub = r / parts.tile_rows, rr = r - sub * parts.tile_rows;
-  const int tok = rr / p.group, g = rr - tok * p.group;
-  const int ti = note.w * plan.tile_tokens + sub * tile_tokens + tok;
-  if (tok >= tile_tokens || ti >= si.q_len) return;
   // the CTA in which the item ends
   int last = ctas;
   for (int i = c + 1; i < ctas; i += 32) {
@@ -44,6 +43,34 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Attend p, const Pa
   }
   const int n = last - c + 1;
   if (last == ctas || n > kMaxParts) return;
+  const int tile_tokens = parts.tile_rows / p.group;
+  const int sub = r / parts.tile_rows, rr = r - sub * parts.tile_rows;
+  const int tok = rr / p.group, g = rr - tok * p.group;
+  const int ti = note.w * plan.tile_tokens + sub * tile_tokens + tok;
+  if (tok >= tile_tokens || ti >= si.q_len) return;
+  const int64_t t = si.q0 + ti;
+  const int h = note.z * p.group + g;
+  if constexpr (kMany) {
+    float top = -INFINITY;
+    for (int i = 0; i < n; ++i) top = fmaxf(top, parts.lse2[parts.row(c + i, i == 0, r)]);
+    const float base = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int i = 0; i < n; ++i) {
+      const int64_t at = parts.row(c + i, i == 0, r);
+      const float4 x = *reinterpret_cast<const float4*>(parts.out + at * kDim + col * 4);
+      const float w = exp2f(parts.lse2[at] - base);
+      sum += w;
+      o.x = fmaf(w, x.x, o.x), o.y = fmaf(w, x.y, o.y);
+      o.z = fmaf(w, x.z, o.z), o.w = fmaf(w, x.w, o.w);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    if (p.lse && col == 0) p.lse[t * p.q_heads + h] = (base + log2f(sum)) * 0.693147180559945f;
+    *reinterpret_cast<uint2*>(p.out.data + t * p.out.ts + h * p.out.hs + col * 4) =
+        make_uint2(f32x2_to_bf16x2(o.x * inv, o.y * inv), f32x2_to_bf16x2(o.z * inv, o.w * inv));
+    return;
+  }
   if (threadIdx.x < 32) {
     float top = -INFINITY;
     for (int i = lane; i < n; i += 32) {
@@ -64,13 +91,10 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Attend p, const Pa
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     if (lane == 0) {
       total_sm = sum;
-      if (p.lse)
-        p.lse[int64_t(si.q0 + ti) * p.q_heads + note.z * p.group + g] =
-            (base + log2f(sum)) * 0.693147180559945f;
+      if (p.lse) p.lse[t * p.q_heads + h] = (base + log2f(sum)) * 0.693147180559945f;
     }
   }
   __syncthreads();
-  const int col = threadIdx.x % kCols, way = threadIdx.x / kCols;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
   for (int i = way; i < n; i += kWays) {
@@ -89,19 +113,18 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Attend p, const Pa
     o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
   }
   const float inv = total_sm == 0.f ? 0.f : 1.f / total_sm;
-  const int64_t t = si.q0 + ti;
-  const int h = note.z * p.group + g;
   *reinterpret_cast<uint2*>(p.out.data + t * p.out.ts + h * p.out.hs + col * 4) =
       make_uint2(f32x2_to_bf16x2(o.x * inv, o.y * inv), f32x2_to_bf16x2(o.z * inv, o.w * inv));
 }
 
 }  // namespace
 
-int run_join(const Attend& p, const Parts& parts, const Plan& plan, int ctas, int device,
-             cudaStream_t stream) {
-  auto* kernel = p.cache.dim == 256   ? join_kernel<256>
-                 : p.cache.dim == 128 ? join_kernel<128>
-                                      : join_kernel<64>;
+template <bool kMany>
+static int run(const Attend& p, const Parts& parts, const Plan& plan, int ctas, int device,
+               cudaStream_t stream) {
+  auto* kernel = p.cache.dim == 256   ? join_kernel<256, kMany>
+                 : p.cache.dim == 128 ? join_kernel<128, kMany>
+                                      : join_kernel<64, kMany>;
   // The attention kernels leave the SMs with all memory given to shared memory;
   // blocks that ask for another split could only start when those have ended.
   static std::atomic<bool> ready[3][kMaxDevices];
@@ -114,8 +137,15 @@ int run_join(const Attend& p, const Parts& parts, const Plan& plan, int ctas, in
     }
     set.store(true, std::memory_order_release);
   }
-  return launch(kernel, dim3(ctas, parts.rows), dim3(kThreads), 0, stream, p,
+  const int rows = kMany ? kThreads * 4 / p.cache.dim : 1;       // of a block
+  return launch(kernel, dim3(ctas, parts.rows / rows), dim3(kThreads), 0, stream, p,
                 parts, plan, ctas);
+}
+
+int run_join(bool many, const Attend& p, const Parts& parts, const Plan& plan, int ctas,
+             int device, cudaStream_t stream) {
+  return many ? run<true>(p, parts, plan, ctas, device, stream)
+              : run<false>(p, parts, plan, ctas, device, stream);
 }
 
 }  // namespace attn

@@ -250,8 +250,9 @@ struct Parts {
   }
 };
 
-int run_join(const Attend& p, const Parts& parts, const Plan& plan, int ctas, int device,
-             cudaStream_t stream);
+// `many`: items of several tiles, whose rows lie in few parts each.
+int run_join(bool many, const Attend& p, const Parts& parts, const Plan& plan, int ctas,
+             int device, cudaStream_t stream);
 
 }  // namespace attn
 }  // namespace nvfp4
