@@ -29,11 +29,11 @@
 // each read per product, V once, plus the copies that bring K and V).  Over e4m3
 // pages the widening comes on top of that traffic, and Q K^T waits for it.
 //
-// Measured with 24 query and 4 key/value heads of 256: a prompt of 8192 tokens
-// 637 us, 1294 TFLOP/s, 67% of the burst rate of a matrix product; 2048 tokens
-// over 8192 keys in e4m3 pages 526 us, 687 TFLOP/s (in bf16 pages 293, 1230); 7
-// tokens over 32771 keys in e4m3 pages 55 us.  32 heads of 128 over 8, three
-// ragged chunks of 1111 over up to 20011 keys: 562 us e4m3 (649 TFLOP/s), 437 us bf16.
+// Measured with the join, 24 query and 4 key/value heads of 256: a prompt of 8192
+// tokens 609 us, 1355 TFLOP/s, 70% of the burst rate of a matrix product; 2048
+// tokens over 8192 keys 266 us, 1356 TFLOP/s (in e4m3 pages 495, 729); 7 tokens
+// over 32771 keys in e4m3 pages 55 us.  32 heads of 128 over 8, three ragged
+// chunks of 1111 over up to 20011 keys: 363 us, 1005 TFLOP/s (e4m3 498, 732).
 //
 // The weights are rounded to the MMA's 16 bits before P V, and the row sums add
 // the unrounded ones in fp32 (attend_warp.cu).
@@ -59,9 +59,9 @@ namespace {
 constexpr int kM = 128;                       // rows of a tile
 constexpr int kBlockShift = 7;
 constexpr int kN = 1 << kBlockShift;          // keys of a block (one unit)
-// Blocks that an item's beginning costs.  A prompt of 8192 tokens measured 662 us
-// at 3, 639 at 5 and 648 at 8.
-constexpr int kExtra = 5;
+// Blocks that an item's beginning costs.  A prompt of 8192 tokens measured 640 us
+// at 3, 609 at 4, 612 at 5 and 618 at 6; chunks of 128 over bf16 363, 363, 372, 373.
+constexpr int kExtra = 4;
 constexpr float kSlack = 8.f;                 // growth of log2 of a weight before rescaling
 // Registers of a thread in the softmax warps and in the others: in all what 512
 // threads of 128 registers are launched with.

@@ -45,7 +45,8 @@ constexpr int kUnitShift = 4;
 constexpr int kUnit = 1 << kUnitShift;        // keys of one warp in a block
 constexpr int kSlotKeys = 64;
 // Units that an item's beginning costs.  The 32 sequences measured 83 us at 2, 81
-// at 4, 77.6 at 8 and 77.7 at 16; one token over 4099 keys 14 us at all of them.
+// at 4, 77.6 at 8 and 77.7 at 16; one token over 4099 keys 13.8, 15.5, 13.9 and
+// 13.5.
 constexpr int kExtra = 8;
 constexpr int kPPitch = 128 * 2 + 16;         // bytes of a row of weights
 

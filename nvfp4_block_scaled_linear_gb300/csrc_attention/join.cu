@@ -4,6 +4,8 @@
 // does not end, in one CTA's range.  A few KB per row: bound by the latency of
 // its four dependent loads (note, end, sums, outputs), so each is one round.
 // Behind one token over 4099 keys it ends some 3 us after the grid before it.
+// Behind many rows it is the number of blocks that counts: a block for each of
+// 152 x 128 rows of 256 took 33 us from a cold L2, 4 rows a block 14.
 #include "schedule.cuh"
 
 namespace nvfp4 {
