@@ -906,7 +906,14 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
         if (part) note = make_int4(0, it.s, it.h, it.tok0 / p.plan.tile_tokens);
       }
       if (kTiles == 1) {
-        // the last product with either buffer, whose weights both groups gave
+        // The last block's maximum, and the last product, whose weights both groups
+        // gave.  The group that did not give the last block's waits for its maximum
+        // first: only then is the product two blocks before known to have completed,
+        // and the parity of the last one's barrier that of no earlier phase.
+        if (((step - 1) & 1) != x) {
+          wait(&m_ready[(x ^ 1) * 4 + quad], ((step - 1) >> 1) & 1, abort_flag);
+          __syncwarp();
+        }
         wait(&pv_done[(step - 1) & 1], ((step - 1) >> 1) & 1, abort_flag);
         __syncwarp();
         const float now = run_max[row];               // of the last block
