@@ -128,8 +128,8 @@ int nvfp4_qk_norm_rope(const nvfp4_heads* q, const nvfp4_heads* k, const nvfp4_h
  * that sees no key gets 0 and -inf.  Rows of the cache at or past a
  * sequence's length are never used, whatever they hold.  Scores, maxima and
  * sums are fp32; the weights are rounded to the cache's operand type (bf16,
- * or f16 over an E4M3 cache) before they meet the values; out is rounded
- * once to bf16.
+ * or f16 over an E4M3 cache, in which weights down to 2^-36 of a row's largest
+ * count) before they meet the values; out is rounded once to bf16.
  *   scale        positive and finite.
  *   q, out       bf16 [tokens, q_heads, head_dim] heads; q_heads a multiple
  *                of cache->kv_heads, at most 128 times it.

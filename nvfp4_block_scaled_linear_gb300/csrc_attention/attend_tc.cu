@@ -22,7 +22,8 @@
 //
 // The accumulator is rescaled only when a row's maximum has grown by more
 // than 2^8 since the last time (weights stay below 2^8, and the sums are
-// fp32), which after the first blocks is rare.
+// fp32), which after the first blocks is rare; over e4m3 pages by more than 2^4.9,
+// which leaves f16 weights more of their range (kLift).
 //
 // What bounds it: the products, 4 * 128 * 128 * head_dim flops a block and
 // tile, and beside them the shared-memory traffic of their operands (Q and K
@@ -62,7 +63,16 @@ constexpr int kN = 1 << kBlockShift;          // keys of a block (one unit)
 // Blocks that an item's beginning costs.  A prompt of 8192 tokens measured 640 us
 // at 3, 609 at 4, 612 at 5 and 618 at 6; chunks of 128 over bf16 363, 363, 372, 373.
 constexpr int kExtra = 4;
-constexpr float kSlack = 8.f;                 // growth of log2 of a weight before rescaling
+// Growth of log2 of a weight before rescaling, and log2 of the weight of the
+// maximum that weights are taken against.  f16 ends just below 2^16 and has no
+// weight below 2^-25 (attend_warp.cu says what that cost): relative error 2^-9
+// down to 2^-27 of the largest, nothing lost above 2^-36.  (Slack 8 and lift 7
+// rescale less often, chunks of 128 497 us against 503, but 2^-27 would have an
+// error of 2^-5.)
+template <bool kE4m3>
+constexpr float kSlack = kE4m3 ? 4.9375f : 8.f;
+template <bool kE4m3>
+constexpr float kLift = kE4m3 ? 11.f : 0.f;
 // Registers of a thread in the softmax warps and in the others: in all what 512
 // threads of 128 registers are launched with.
 constexpr int kSoftmaxRegs = 192, kHelperRegs = 64;
@@ -836,7 +846,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
         float now = top;
         if (b > 0) {
           now = fmaxf(prev, top);
-          if (__any_sync(0xffffffffu, now - prev > kSlack)) {
+          if (__any_sync(0xffffffffu, now - prev > kSlack<kE4m3>)) {
             // the accumulator, complete up to the block before
             if (kTiles == 1)
               wait(&pv_done[x ^ 1], ((step - 1) >> 1) & 1, abort_flag);
@@ -873,7 +883,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
           if (check_v(it, b, v_slot[x], quad)) dirty[item % kDirty] = item + 1;
         }
         // ---- the weights, handed over by halves
-        const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
+        const float2 c2 = make_float2(c, c), b2 = make_float2(kLift<kE4m3> - base, kLift<kE4m3> - base);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -937,7 +947,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
       const int prow = (kTiles == 2 ? x : rank) * kM + row;
       const int64_t at_part = p.parts.row(unit, part, prow);
       if (valid && (kTiles == 2 || x == 0)) {
-        const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
+        const float lse2 = l == 0.f ? -INFINITY : m + (log2f(l) - kLift<kE4m3>);
         if (whole && a.lse) a.lse[token * a.q_heads + head] = lse2 * 0.693147180559945f;
         if (!whole) p.parts.lse2[at_part] = lse2;
       }

@@ -23,8 +23,12 @@
 // is permuted so that a lane's codes are 16 consecutive bytes.
 //
 // The weights are rounded to the MMA's 16 bits (bf16, f16 over e4m3 pages)
-// before P V, relative error 2^-9 or 2^-12, below that of the bf16 result; the
-// row sums add the unrounded weights in fp32.
+// before P V, relative error 2^-8 or 2^-11 at most, no more than that of the bf16
+// result; the row sums add the unrounded weights in fp32.  f16 has no weight below
+// 2^-25, so there the row's largest is 2^kLift and not 1: relative error 2^-11 down
+// to 2^-29 of the largest, nothing lost above 2^-40.  With the largest at 1 a tail of
+// n keys near 2^-26 was lost from P V and not from the sum, up to n 2^-25 of the
+// output.
 //
 // Measured with the join at 24 query and 4 key/value heads of 256: 32 ragged
 // sequences of one token (451 MB of cache) 77.5 us, 5.83 TB/s, 87% of the copy
@@ -49,6 +53,9 @@ constexpr int kSlotKeys = 64;
 // 13.5.
 constexpr int kExtra = 8;
 constexpr int kPPitch = 128 * 2 + 16;         // bytes of a row of weights
+// log2 of a row's largest weight (f16 ends at 2^16).
+template <bool kE4m3>
+constexpr float kLift = kE4m3 ? 15.f : 0.f;
 
 template <int kDim, bool kE4m3, int kR>
 struct Cfg {
@@ -463,6 +470,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<kDim, kE4m3, kR>::kCtas)
             const float top = fmaxf(m[rt][i], now);
             base[i] = top == -INFINITY ? 0.f : top;
             const float alpha = exp2f(m[rt][i] - base[i]);      // 0 from -inf
+            base[i] -= kLift<kE4m3>;
             m[rt][i] = top;
             l[rt][i] *= alpha;
 #pragma unroll
@@ -634,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<kDim, kE4m3, kR>::kCtas)
           if (r >= rows_used || tok0 + tok >= seq.q_len) continue;
           const int64_t token = seq.q0 + tok0 + tok;
           const int head = w.r.h * p.group + gi;
-          const float lse2 = sum == 0.f ? -INFINITY : m[rt][i] + log2f(sum);
+          const float lse2 = sum == 0.f ? -INFINITY : m[rt][i] + (log2f(sum) - kLift<kE4m3>);
           if (warp == 0 && t == 0) {
             if (whole && p.lse) p.lse[token * p.q_heads + head] = lse2 * 0.693147180559945f;
             if (!whole) parts.lse2[parts.row(blockIdx.x, part, r)] = lse2;
