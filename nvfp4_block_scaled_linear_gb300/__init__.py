@@ -15,7 +15,7 @@ from .inputs import WORKLOADS, LinearInputs, algorithmic_bytes, flops  # noqa: F
 # The attention block's names (of the module ``attention``).
 _ATTENTION = frozenset((
     "KVCache", "new_kv_cache", "qk_norm_rope", "qk_norm_rope_store", "attention_workspace",
-    "paged_attention", "attention_mass", "evict", "attention_error", "ATTENTION_TIMEOUT",
+    "release_workspaces", "paged_attention", "attention_mass", "evict", "attention_error", "ATTENTION_TIMEOUT",
     "ATTENTION_BAD_INDEX"))
 
 

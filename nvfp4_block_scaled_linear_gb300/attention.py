@@ -13,7 +13,9 @@ and, to bound a long context's cache,
     lens, index, mass = evict(cache, block_table, kv_lens, mass, keep, recent, to, to_table)
 
 Argument marshalling only, as in ``_lib``: every step runs in the library's
-kernels, on the current CUDA stream unless one is given.
+kernels, on the current CUDA stream unless one is given (a ``torch.cuda.Stream``
+or a raw handle).  What a call makes itself, results and workspaces, belongs to
+the stream that it runs on, as under ``torch.cuda.stream(stream)``.
 """
 import ctypes
 import os
@@ -152,6 +154,17 @@ def _flat(t, name, dtype, shape, device):
     return t.data_ptr()
 
 
+def _empty(shape, dtype, device, stream):
+    """A tensor that belongs to `stream` (the device's current one by default):
+    its memory is reused only in that stream's order."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _call(function, device, stream, *args):
     """One library call on `stream` (the device's current one by default)."""
     index = device.index
@@ -202,8 +215,8 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps=1e-6, q_out=N
     positions (int64 [T], rows of the float32 table cos_sin: cosines, then
     sines).  Without a table nothing is rotated.  Returns (q_out, k_out);
     they may be q and k themselves."""
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
+    q_out = _empty(q.shape, q.dtype, q.device, stream) if q_out is None else q_out
+    k_out = _empty(k.shape, k.dtype, k.device, stream) if k_out is None else k_out
     _norm_rope(q, k, None, q_weight, k_weight, cos_sin, positions, eps, q_out, k_out, None, None,
                stream)
     return q_out, k_out
@@ -214,7 +227,7 @@ def qk_norm_rope_store(q, k, v, q_weight, k_weight, cos_sin, positions, cache, s
     """As ``qk_norm_rope`` for q, with the key rows and the rows of v stored
     in the cache: token t's in slot slots[t] % page_size of page slots[t] //
     page_size (int64 [T]; -1 stores nothing).  Returns the queries."""
-    out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
+    out = _empty(q.shape, q.dtype, q.device, stream) if out is None else out
     _norm_rope(q, k, v, q_weight, k_weight, cos_sin, positions, eps, out, None, cache, slots,
                stream)
     return out
@@ -231,26 +244,42 @@ def _seqs(cache, block_table, kv_lens, q_starts, max_q_len):
 
 
 _workspace_bytes = {}
-_workspaces = {}
+_workspaces = {}                 # (device index, head_dim, raw current stream): workspace
+_MAX_WORKSPACES = 16
 
 
-def attention_workspace(cache):
+def attention_workspace(cache, stream=None):
     """A workspace for ``paged_attention`` calls that run one after another."""
     key = (cache.device.index, cache.head_dim)
     if key not in _workspace_bytes:
         with torch.cuda.device(cache.device):
             _workspace_bytes[key] = _library().nvfp4_paged_attention_workspace(cache.head_dim)
-    return torch.empty(_workspace_bytes[key], dtype=torch.uint8, device=cache.device)
+    return _empty(_workspace_bytes[key], torch.uint8, cache.device, stream)
 
 
-def _stream_workspace(cache, stream):
-    """The workspace of the calls on one stream, which run one after another;
-    a call that is being captured into a graph gets one of its own."""
-    if torch.cuda.is_current_stream_capturing():
+def release_workspaces():
+    """Give the workspaces kept for the streams of earlier calls back to
+    PyTorch's allocator."""
+    _workspaces.clear()
+
+
+def _call_workspace(cache, stream):
+    """The workspace of a call on `stream`.  One is kept for each stream that is
+    current when it is called on (asking the allocator for 80 MB costs some 8 us of
+    host time), for the last few of them; a call on another stream than the
+    current one, or that is being captured into a graph, gets one of its own."""
+    index = cache.device.index
+    current = torch._C._cuda_getCurrentRawStream(index)
+    if stream is not None and current != (stream if isinstance(stream, int) else stream.cuda_stream):
+        return attention_workspace(cache, stream)
+    # (the query is of the current device's stream)
+    if index != torch._C._cuda_getDevice() or torch.cuda.is_current_stream_capturing():
         return attention_workspace(cache)
-    key = (cache.device.index, cache.head_dim, stream)
+    key = (index, cache.head_dim, current)
     w = _workspaces.get(key)
     if w is None:
+        while len(_workspaces) >= _MAX_WORKSPACES:
+            _workspaces.pop(next(iter(_workspaces)), None)
         w = _workspaces[key] = attention_workspace(cache)
     return w
 
@@ -272,13 +301,9 @@ def paged_attention(q, cache, block_table, kv_lens, q_starts, max_q_len, scale=N
         raise ValueError("the cache holds %d heads of %d on %s, q has %d of %d on %s"
                          % (cache.kv_heads, cache.head_dim, cache.device, hq, dim, dev))
     if out is None:
-        out = torch.empty((tokens, hq, dim), dtype=torch.bfloat16, device=dev)
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev.index)
-    elif not isinstance(stream, int):
-        stream = stream.cuda_stream
+        out = _empty((tokens, hq, dim), torch.bfloat16, dev, stream)
     if workspace is None:
-        workspace = _stream_workspace(cache, stream)
+        workspace = _call_workspace(cache, stream)
     _call("nvfp4_paged_attention", dev, stream, _heads(q, "q", tokens, hq, dim, dev), tokens, hq,
           cache._c, _seqs(cache, block_table, kv_lens, q_starts, max_q_len),
           dim ** -0.5 if scale is None else scale, _heads(out, "out", tokens, hq, dim, dev),
@@ -304,7 +329,7 @@ def attention_mass(q, cache, block_table, kv_lens, q_starts, max_q_len, lse, mas
     n, width = block_table.shape
     if out is None:
         shape = (n, cache.kv_heads, width * cache.page_size) if mass is None else mass.shape
-        out = torch.empty(shape, dtype=torch.float32, device=dev)
+        out = _empty(shape, torch.float32, dev, stream)
     if out.dim() != 3:
         raise ValueError("out must be [sequences, kv_heads, room], got %s" % (tuple(out.shape),))
     room = out.shape[2]
@@ -331,11 +356,11 @@ def evict(cache, block_table, kv_lens, mass, keep, recent, to, to_table, index=N
         raise ValueError("mass must be [sequences, kv_heads, room], got %s" % (tuple(mass.shape),))
     n, hk, room = block_table.shape[0], cache.kv_heads, mass.shape[2]
     if index is None:
-        index = torch.empty((n, hk, keep), dtype=torch.int32, device=dev)
+        index = _empty((n, hk, keep), torch.int32, dev, stream)
     if new_mass is None:
-        new_mass = torch.empty((n, hk, keep), dtype=torch.float32, device=dev)
+        new_mass = _empty((n, hk, keep), torch.float32, dev, stream)
     if new_lens is None:
-        new_lens = torch.empty(n, dtype=torch.int32, device=dev)
+        new_lens = _empty(n, torch.int32, dev, stream)
     if to.device != dev or to_table.dim() != 2:
         raise ValueError("to must live on %s and to_table be 2-D" % dev)
     _call("nvfp4_cache_evict", dev, stream, cache._c, seqs,
