@@ -15,10 +15,9 @@
 // kTiles = 2 (head_dim 64, 128): the buffers hold two tiles on the same
 // block, which halves the copies per product.
 //
-// kCluster = 2 (head_dim 256, more than one tile of rows): two CTAs take two
-// adjacent tiles of an item through the same blocks, each copying half of every
-// slot into both.  One tile alone wants 64 bytes a clock from L2 on every SM
-// to keep the tensor core busy, about what the L2 gives all SMs together.
+// (CTAs of a cluster do not share copies: one tile of head_dim 256 alone wants 64
+// bytes a clock from L2 on every SM to keep the tensor core busy, about what the L2
+// gives all SMs together, so there the copies count.)
 //
 // The accumulator is rescaled only when a row's maximum has grown by more
 // than 2^8 since the last time (weights stay below 2^8, and the sums are
@@ -31,10 +30,10 @@
 // pages the widening comes on top of that traffic, and Q K^T waits for it.
 //
 // Measured with the join, 24 query and 4 key/value heads of 256: a prompt of 8192
-// tokens 609 us, 1355 TFLOP/s, 70% of the burst rate of a matrix product; 2048
-// tokens over 8192 keys 266 us, 1356 TFLOP/s (in e4m3 pages 495, 729); 7 tokens
+// tokens 646 us, 1276 TFLOP/s, 66% of the burst rate of a matrix product; 2048
+// tokens over 8192 keys 274 us, 1315 TFLOP/s (in e4m3 pages 511, 706); 7 tokens
 // over 32771 keys in e4m3 pages 55 us.  32 heads of 128 over 8, three ragged
-// chunks of 1111 over up to 20011 keys: 363 us, 1005 TFLOP/s (e4m3 498, 732).
+// chunks of 1111 over up to 20011 keys: 364 us, 1001 TFLOP/s (e4m3 499, 731).
 //
 // The weights are rounded to the MMA's 16 bits before P V, and the row sums add
 // the unrounded ones in fp32 (attend_warp.cu).
@@ -60,8 +59,8 @@ namespace {
 constexpr int kM = 128;                       // rows of a tile
 constexpr int kBlockShift = 7;
 constexpr int kN = 1 << kBlockShift;          // keys of a block (one unit)
-// Blocks that an item's beginning costs.  A prompt of 8192 tokens measured 640 us
-// at 3, 609 at 4, 612 at 5 and 618 at 6; chunks of 128 over bf16 363, 363, 372, 373.
+// Blocks that an item's beginning costs.  A prompt of 8192 tokens measured 667 us
+// at 3, 646 at 4, 649 at 5 and 6; chunks of 128 over bf16 364, 364, 373, 374.
 constexpr int kExtra = 4;
 // Growth of log2 of a weight before rescaling, and log2 of the weight of the
 // maximum that weights are taken against.  f16 ends just below 2^16 and has no
@@ -80,7 +79,7 @@ constexpr int kRawBytes = 8 * 1024;           // of a unit of e4m3 codes
 constexpr int kItems = 4;                     // item descriptors in flight
 constexpr int kDirty = 8;                     // items whose `dirty` note is held: more than the ring's
 
-template <int kDim, bool kE4m3, int kTiles, int kCluster>
+template <int kDim, bool kE4m3, int kTiles>
 struct Cfg {
   static constexpr int kThreads = 512;
   // A slot holds up to 32 KB: 128 of head_dim of all keys of a K block, or all
@@ -115,7 +114,6 @@ struct Cfg {
   static constexpr uint32_t kO = 0;
   static constexpr uint32_t kS = kTiles * kDim;
   static_assert(kS + 2 * kN <= 512, "TMEM");
-  static_assert(kCluster == 1 || (!kE4m3 && kTiles == 1), "pairs of CTAs");
 };
 
 template <bool kE4m3>
@@ -130,20 +128,6 @@ __device__ __forceinline__ void tmem_st_16cols(uint32_t taddr, const uint32_t (&
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
-}
-
-// umma_commit on the barrier at this place in every CTA of the cluster.
-template <int kCluster>
-__device__ __forceinline__ void commit_empty(uint64_t* bar) {
-  if (kCluster == 1) {
-    umma_commit(bar);
-  } else {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-        " [%0], %1;" ::"r"(smem_addr(bar)),
-        "h"(static_cast<uint16_t>((1 << kCluster) - 1))
-        : "memory");
-  }
 }
 
 // One 32-byte store (a whole sector): the rows of a warp's lanes lie far apart,
@@ -277,12 +261,12 @@ using KRing = Ring<0, C::kKSlots>;
 template <class C>
 using VRing = Ring<C::kKSlots, C::kVSlots>;
 
-template <int kDim, bool kE4m3, int kTiles, int kCluster>
-__global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 1)
+template <int kDim, bool kE4m3, int kTiles>
+__global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
     attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
                      const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const TcParams p) {
-  using C = Cfg<kDim, kE4m3, kTiles, kCluster>;
+  using C = Cfg<kDim, kE4m3, kTiles>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* q_sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   uint8_t* raw = q_sm + C::kQBytes;                // [K, V][2]
@@ -316,7 +300,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(&full[i], kE4m3 ? 2 : 1);
-      mbar_init(&empty[i], kCluster);
+      mbar_init(&empty[i], 1);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&s_full[x], 1);
@@ -350,17 +334,13 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
   }
   griddep_wait();
   griddep_launch_dependents();
-  // the CTA's (or the pair's) number, and its tile of the item
-  const uint32_t unit = blockIdx.x / kCluster;
-  const int rank = kCluster == 2 ? static_cast<int>(cluster_ctarank()) : 0;
   // the range, in scratch that the ring's first copies will overwrite
   const Range range =
-      find_range(a.seqs, a.cache.heads, p.plan, unit, gridDim.x / kCluster,
+      find_range(a.seqs, a.cache.heads, p.plan, blockIdx.x, gridDim.x,
                  reinterpret_cast<RangeSmem*>(ring), a.err);
   fence_proxy_async_smem();
   tc_fence_before_sync();
   __syncthreads();
-  if (kCluster == 2) cluster_sync();               // the other CTA's barriers are set up
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
 
@@ -434,7 +414,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
     const CUtensorMap* map = kV ? &tm_v : &tm_k;
     const int shift = min(p.box_shift, kRowShift);          // log2 of the rows of a copy
     const int boxes = kRows >> shift;
-    const int at_once = kV && boxes == 1 ? kChunks / kCluster : 1;   // chunks of a copy
+    const int at_once = kV && boxes == 1 ? kChunks : 1;     // chunks of a copy
     // lane: copy (box, chunk) of each slot; of V also the slot, whose keys differ
     const int per_slot = boxes * (kChunks / at_once);
     const int piece = kV ? lane / per_slot : 0;
@@ -472,9 +452,8 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
       if (moved && lane == 0) items.release(was);
       look_up();
       for (int h = 0; h < C::kPieces; ++h, r.next()) {
-        const bool some = page >= 0 && (!kV || piece == h);
-        const bool mine = some && (kCluster == 1 || chunk / at_once % 2 == rank);
-        const int n = __popc(__ballot_sync(0xffffffffu, some));
+        const bool mine = page >= 0 && (!kV || piece == h);
+        const int n = __popc(__ballot_sync(0xffffffffu, mine));
         if (turns == kTurns)
           ok = __all_sync(0xffffffffu, wait(&empty[r.slot], r.par ^ 1, abort_flag));
         else
@@ -483,8 +462,8 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
         if (lane == 0) mbar_arrive_expect_tx(&full[r.slot], n * bytes);
         __syncwarp();
         if (mine)
-          tma_load_page<kCluster>(ring + r.slot * C::kSlotBytes + dst, map, &full[r.slot],
-                                  (kV ? 0 : h * kChunks) + chunk, in_page, head, page);
+          tma_load_page(ring + r.slot * C::kSlotBytes + dst, map, &full[r.slot],
+                        (kV ? 0 : h * kChunks) + chunk, in_page, head, page);
       }
     }
     // every copy has landed before the block may end
@@ -753,7 +732,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
             const uint32_t off = ((kk >> 2) * C::kKChunk + (kk & 3) * 32) >> 4;
             umma_ss(t_s, qh + off, k + off, id_s, kk == 0 ? acc : 1u);
           }
-          if (kTiles == 1 || x == 1) commit_empty<kCluster>(&empty[r.slot]);
+          if (kTiles == 1 || x == 1) umma_commit(&empty[r.slot]);
           if (h == C::kPieces - 1) {
             umma_commit(&s_full[x]);
             if (last) umma_commit(q_empty);
@@ -794,7 +773,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
     Item it;
     for (int item = 0; items.get(item, it); ++item) {
       __syncwarp();
-      const int ti = it.tok0 + (kTiles == 2 ? x : rank) * p.tile_tokens + tok;
+      const int ti = it.tok0 + (kTiles == 2 ? x : 0) * p.tile_tokens + tok;
       const bool valid = tok < p.tile_tokens && ti < it.q_len;
       const int lim = valid ? max(0, it.kv_len - it.q_len + ti + 1) : 0;
       const int count = it.count();
@@ -944,8 +923,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
       const float inv = l == 0.f ? 0.f : vs / l;
       const int64_t token = it.q0 + ti;
       const int head = it.h * a.group + gi;
-      const int prow = (kTiles == 2 ? x : rank) * kM + row;
-      const int64_t at_part = p.parts.row(unit, part, prow);
+      const int64_t at_part = p.parts.row(blockIdx.x, part, (kTiles == 2 ? x * kM : 0) + row);
       if (valid && (kTiles == 2 || x == 0)) {
         const float lse2 = l == 0.f ? -INFINITY : m + (log2f(l) - kLift<kE4m3>);
         if (whole && a.lse) a.lse[token * a.q_heads + head] = lse2 * 0.693147180559945f;
@@ -1025,9 +1003,9 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
       __syncwarp();
       if (lane == 0) items.release(item);
     }
-    if (threadIdx.x == 0 && rank == 0) {
+    if (threadIdx.x == 0) {
       note.x = flags;
-      p.parts.note[unit] = note;
+      p.parts.note[blockIdx.x] = note;
     }
   } else if (warp < 12) {
     regs_dec<kHelperRegs>();
@@ -1073,7 +1051,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
             for (int kk = 0; kk < kN / 32; ++kk)
               umma_ts(t_o, t_p + kk * 8, v + kk * (2048 >> 4), id_o, kk == 0 ? acc : 1u);
             if ((kTiles == 1 || x == 1) && (half == 1 || C::kPieces == 2))
-              commit_empty<kCluster>(&empty[r.slot]);
+              umma_commit(&empty[r.slot]);
             if (half == 1) umma_commit(&pv_done[x]);
           }
           __syncwarp();
@@ -1101,7 +1079,7 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
         while (publish(w, item)) {
           if (item > 0 && !wait(q_empty, (item - 1) & 1, abort_flag)) break;
           mbar_arrive_expect_tx(q_full, kTiles * (kDim / 64) * rows * 128);
-          const int t0 = w.seq.q0 + w.r.tile * p.plan.tile_tokens + rank * p.tile_tokens;
+          const int t0 = w.seq.q0 + w.r.tile * p.plan.tile_tokens;
 #pragma unroll 1
           for (int x = 0; x < kTiles; ++x)
 #pragma unroll 1
@@ -1153,17 +1131,16 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles, kCluster>::kThreads, 
   if (*abort_flag && threadIdx.x == 0) atomicOr(a.err, NVFP4_ATTENTION_TIMEOUT);
   tc_fence_before_sync();
   __syncthreads();
-  if (kCluster == 2) cluster_sync();               // nothing of the other CTA's is on its way here
   if (warp == 9) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, 512);
   }
 }
 
-template <int kDim, bool kE4m3, int kTiles, int kCluster>
+template <int kDim, bool kE4m3, int kTiles>
 int run(const Attend& a, const Device& d, cudaStream_t stream) {
-  using C = Cfg<kDim, kE4m3, kTiles, kCluster>;
-  auto* kernel = attend_tc_kernel<kDim, kE4m3, kTiles, kCluster>;
+  using C = Cfg<kDim, kE4m3, kTiles>;
+  auto* kernel = attend_tc_kernel<kDim, kE4m3, kTiles>;
   static std::atomic<bool> ready[kMaxDevices];
   if (!ready[d.id].load(std::memory_order_acquire)) {
     // the warpgroups' shares (setmaxnreg) have to come out of what the block
@@ -1177,9 +1154,8 @@ int run(const Attend& a, const Device& d, cudaStream_t stream) {
     if (attr.numRegs * C::kThreads < need) return NVFP4_ERR_LAUNCH;
   }
   if (const int st = allow_smem(kernel, C::kSmem, d, ready)) return st;
-  const int units = d.num_sms / kCluster;
-  TcParams p{a, {}, Parts(a.workspace, units, kM, kTiles * kCluster, kDim), kM / a.group, 0};
-  p.plan = Plan{kTiles * kCluster * p.tile_tokens, kBlockShift, 1, kExtra};
+  TcParams p{a, {}, Parts(a.workspace, d.num_sms, kM, kTiles, kDim), kM / a.group, 0};
+  p.plan = Plan{kTiles * p.tile_tokens, kBlockShift, 1, kExtra};
   if (!countable(a.seqs, a.cache.heads, p.plan)) return NVFP4_ERR_SHAPE;
   p.box_shift = 4;
   while (p.box_shift < 7 && a.cache.page_size % (2 << p.box_shift) == 0) ++p.box_shift;
@@ -1195,25 +1171,22 @@ int run(const Attend& a, const Device& d, cudaStream_t stream) {
   } else if (!query_map(&tm_q, a.q, a.cache.dim, a.q_heads, a.seqs.tokens, a.group, p.tile_tokens) ||
              !page_map(&tm_k, a.cache, false, 64, box, 1) ||
              !page_map(&tm_v, a.cache, true, 64, std::min(box, C::kVKeys),
-                       box >= C::kVKeys ? C::kVChunks / kCluster : 1)) {
+                       box >= C::kVKeys ? C::kVChunks : 1)) {
     return NVFP4_ERR_LAUNCH;
   }
-  if (const int st = launch_clusters(kCluster, kernel, dim3(units * kCluster), dim3(C::kThreads),
-                                     C::kSmem, stream, tm_q, tm_k, tm_v, p))
+  if (const int st = launch(kernel, dim3(d.num_sms), dim3(C::kThreads), C::kSmem, stream, tm_q, tm_k,
+                            tm_v, p))
     return st;
-  return run_join(int64_t(a.max_q_len) * a.group > kM, a, p.parts, p.plan, units, d.id, stream);
+  return run_join(int64_t(a.max_q_len) * a.group > kM, a, p.parts, p.plan, d.num_sms, d.id, stream);
 }
 
-// One tile of rows; more: two tiles in a CTA, or in a pair of CTAs where one
-// accumulator leaves no room for another (over an e4m3 cache, whose rows are
-// half as long in L2, each CTA works alone).
+// One tile of rows; more: two tiles in a CTA, where TMEM has room for two
+// accumulators.
 template <int kDim, bool kE4m3>
 int run_tiles(bool two, const Attend& a, const Device& d, cudaStream_t stream) {
-  if (two) {
-    if constexpr (kDim < 256) return run<kDim, kE4m3, 2, 1>(a, d, stream);
-    if constexpr (kDim == 256 && !kE4m3) return run<kDim, kE4m3, 1, 2>(a, d, stream);
-  }
-  return run<kDim, kE4m3, 1, 1>(a, d, stream);
+  if constexpr (kDim < 256)
+    if (two) return run<kDim, kE4m3, 2>(a, d, stream);
+  return run<kDim, kE4m3, 1>(a, d, stream);
 }
 
 }  // namespace
