@@ -255,7 +255,9 @@ int run_mass(const Mass& p, const Device& d, cudaStream_t stream) {
   // 32771 keys of 256: bf16 30 rows 28.5 us here against 33.2, 48 rows 34.3
   // against 33.3, 60 rows 39.0 against 33.0; e4m3 96 rows 38.9 against 64.7, 192
   // rows 61.5 against 71.1, 252 rows 77.4 against 67.5.
-  if (int64_t(p.max_q_len) * p.group > (f8 ? 192 : 32)) return run_mass_tc(p, d, stream);
+  // (No tokens: no query tile to copy, and only what was received before to hand on.)
+  if (p.seqs.tokens > 0 && int64_t(p.max_q_len) * p.group > (f8 ? 192 : 32))
+    return run_mass_tc(p, d, stream);
   switch (p.cache.dim) {
     case 64:
       return f8 ? run<64, true>(p, stream) : run<64, false>(p, stream);
