@@ -170,8 +170,10 @@ int nvfp4_attention_mass(const nvfp4_heads* q, int64_t tokens, int32_t q_heads,
  *   its key and value rows are copied to slot r % page_size of page
  *   to_table[s][r / page_size] of `to`
  * and new_lens[s] = m.  `to` has the source's type, kv_heads and head_dim
- * (its own page size and strides; the scales are the caller's to share) and
- * its pages named in to_table are none of those the sequences still hold.
+ * (its own page size, strides and scales: an E4M3 row's codes are taken over
+ * where the head's scales are equal, else its values are rounded once to the
+ * new scale, saturating at 448) and its pages named in to_table are none of
+ * those the sequences still hold.
  *   mass         fp32 [count, kv_heads, room].
  *   seqs         block_table, kv_lens, count and table_width are read.
  *   to_table     int32 [count, to_width], to_width * to->page_size >= keep.

@@ -347,7 +347,8 @@ def evict(cache, block_table, kv_lens, mass, keep, recent, to, to_table, index=N
     """Cut every sequence to its newest min(recent, keep) keys and, head by
     head, the others with the most mass, ``keep`` in all at most, in their
     order; their rows move to the pages to_table (int32 [S, to_width]) of the
-    cache ``to``.  Returns (new_lens int32 [S], index int32 [S, Hk, keep]: the
+    cache ``to``, keeping their values (rounded once more where the caches' scales
+    differ).  Returns (new_lens int32 [S], index int32 [S, Hk, keep]: the
     kept keys' old places, new_mass float32 [S, Hk, keep]); past a sequence's
     new length index is -1 and new_mass 0."""
     dev = cache.device

@@ -195,9 +195,28 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const Evict p, int sli
   }
 }
 
+// Sixteen e4m3 codes of scale `from` as codes of scale `to`, one rounding each.
+__device__ __forceinline__ uint4 rescale(uint4 v, float from, float to) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t c[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      c[k] = __nv_cvt_float2_to_fp8x2(
+          make_float2(e4m3_to_f32(w[i] >> (16 * k) & 0xFFu) * from / to,
+                      e4m3_to_f32(w[i] >> (16 * k + 8) & 0xFFu) * from / to),
+          __NV_SATFINITE, __NV_E4M3);
+    w[i] = c[0] | c[1] << 16;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // A block moves the rows of kPlaces kept places of one sequence and head: a
 // thread per place hands on its mass and finds where its rows come from and go
-// to, then all threads copy 16 bytes at a time, several on their way each.
+// to, then all threads copy 16 bytes at a time, several on their way each.  Where
+// the two caches have different scales for the head, the codes are changed on the
+// way, so that a row keeps the values that it stands for.
 constexpr int kPlaces = 64;
 constexpr int kMoveThreads = 256;
 
@@ -235,6 +254,17 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const Evict p) {
   for (int v = 0; v < 2; ++v) {
     const uint8_t* src = static_cast<const uint8_t*>(v ? p.from.v : p.from.k) + piece * 16;
     uint8_t* dst = static_cast<uint8_t*>(v ? p.to.v : p.to.k) + piece * 16;
+    const float* from_scale = v ? p.from.v_scale : p.from.k_scale;
+    const float* to_scale = v ? p.to.v_scale : p.to.k_scale;
+    const float a = from_scale ? from_scale[h] : 1.f, b = to_scale ? to_scale[h] : 1.f;
+    if (a != b) {
+#pragma unroll 1
+      for (int i = first; i < kPlaces; i += step)
+        if (from[0][i] >= 0)
+          *reinterpret_cast<uint4*>(dst + to[v][i]) =
+              rescale(__ldcs(reinterpret_cast<const uint4*>(src + from[v][i])), a, b);
+      continue;
+    }
 #pragma unroll 4
     for (int i = first; i < kPlaces; i += step) {
       if (from[0][i] < 0) continue;

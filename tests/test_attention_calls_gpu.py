@@ -2,7 +2,8 @@
 import pytest
 import torch
 
-from test_attention_gpu import BF16, DEV, E4M3, Batch, att, no_device_error  # noqa: F401
+import _attention_ref as ref
+from test_attention_gpu import BF16, DEV, E4M3, Batch, att, no_device_error, to_dev  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -22,3 +23,41 @@ def test_mass_of_no_tokens(dtype, hint):
         got = att.attention_mass(q, *args, lse, start, out=out).cpu()
         want = torch.zeros_like(before) if start is None else before * held[:, None]
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("which", ["other", "none_to_some", "some_to_none", "equal"])
+@pytest.mark.parametrize("page,order", [(16, "heads"), (48, "tokens")])
+def test_evict_between_caches_of_different_scales(which, page, order):
+    """A row keeps the values it stands for: its codes are taken over where the
+    head's scales are equal, and rounded once to the new scale where not."""
+    g = torch.Generator().manual_seed(page)
+    n, hk, dim, keep = 300, 3, 128, 64
+    table, pages = ref.table_for([n], page, g)
+    k, v = (ref.pages(pages, page, hk, dim, E4M3, order, g, 40.0) for _ in range(2))
+    k.view(torch.uint8)[:, :, 0, 5] = 0x7F                       # NaN stays NaN
+    some = [(0.5 + torch.rand(hk, generator=g)) / 16 for _ in range(4)]
+    one = torch.ones(hk)
+    a, b = {"other": (some[:2], some[2:]), "none_to_some": ([None] * 2, some[2:]), "some_to_none": (some[:2], [None] * 2),
+            "equal": (some[:2], [x.clone() for x in some[:2]])}[which]
+    if which == "other":
+        b[0][1] = a[0][1]                                        # one head alike
+    width = -(-keep // page)
+    to = att.new_kv_cache(width, page, hk, dim, E4M3, *(x if x is None else x.to(DEV) for x in b))
+    cache = att.KVCache(to_dev(k), to_dev(v), *(x if x is None else x.to(DEV) for x in a))
+    mass = torch.rand(1, hk, n, generator=g)
+    to_table = torch.arange(width, dtype=torch.int32).view(1, width)
+    _, index, _ = att.evict(cache, table.to(DEV), torch.tensor([n], dtype=torch.int32, device=DEV), mass.to(DEV), keep, 7, to,
+                            to_table.to(DEV))
+    r = torch.arange(keep)
+    for src, dst, x, y in ((k, to.k, a[0], b[0]), (v, to.v, a[1], b[1])):
+        x, y = (one if s is None else s for s in (x, y))
+        got = dst.view(torch.uint8).cpu()
+        for h in range(hk):
+            at = index[0, h].cpu().long()
+            codes = src.view(torch.uint8)[table[0].long()[at // page], at % page, h]
+            want = codes
+            if x[h] != y[h]:
+                want = (codes.view(E4M3).float() * x[h] / y[h]).clamp(-448.0, 448.0).to(E4M3).view(torch.uint8)
+            here = got[to_table[0].long()[r // page], r % page, h]
+            nan = (want & 0x7F) == 0x7F
+            assert torch.equal(here[~nan], want[~nan]) and ((here[nan] & 0x7F) == 0x7F).all()
