@@ -199,6 +199,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j)
             if (k * 32 + j < lo || k * 32 + j >= hi) sc[k][j] = 0xFF800000u;     // weight 0
+      } else {
+        // rows that hold no token: 0 times a key that is not finite need not be 0
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (rows < (k + 1) * 32) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (k * 32 + j >= rows) sc[k][j] = 0xFF800000u;
+          }
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k)

@@ -61,3 +61,26 @@ def test_evict_between_caches_of_different_scales(which, page, order):
             here = got[to_table[0].long()[r // page], r % page, h]
             nan = (want & 0x7F) == 0x7F
             assert torch.equal(here[~nan], want[~nan]) and ((here[nan] & 0x7F) == 0x7F).all()
+
+
+@pytest.mark.parametrize("hq,hk,dim", [(24, 4, 256), (12, 4, 128), (7, 1, 64)])
+@pytest.mark.parametrize("hint", [1, 400])
+@pytest.mark.parametrize("q_len", [1, 150])
+def test_mass_of_a_key_whose_scores_are_minus_infinity(hq, hk, dim, hint, q_len):
+    """Groups of 3, 6 and 7 leave rows of a 128-row tile without a token: a key
+    with an infinite element, whose score is -inf for every query, receives
+    nothing from them either."""
+    n, room = 300, 320
+    b = Batch([n], [q_len], hq, hk, dim, seed=dim + q_len, width=20)
+    b.q[..., 3] = b.q[..., 3].abs() + 0.5
+    keys = [0, 17, 100]
+    at = torch.tensor(keys)
+    _, lse, _, _ = b.reference()
+    lse = lse.float()
+    want, tol = ref.mass(b.q, b.k, None, b.table, [n], [q_len], b.scale, lse, None, room)
+    want[..., keys] = tol[..., keys] = 0.0
+    b.cache.k[b.table[0].long()[at // 16].to(DEV), (at % 16).to(DEV), :, 3] = float("-inf")
+    args = b.args[:-1] + (hint,)
+    got = att.attention_mass(b.q.to(DEV), *args, lse.to(DEV), out=torch.empty(1, hk, room, device=DEV)).double().cpu()
+    assert not torch.isnan(got).any()
+    assert ((got - want).abs() <= tol).all()
