@@ -151,7 +151,8 @@ int64_t nvfp4_paged_attention_workspace(int32_t head_dim);
 /* out[s, h, j] = mass[s, h, j] + sum over the tokens t of sequence s that see
  * key j and the query heads g of group h of exp(scale * q[t, g] . k_j -
  * lse[t, g]), for j < kv_lens[s]; 0 for the other j < room.  lse is what
- * nvfp4_paged_attention wrote for the same q, cache and scale.  mass and out
+ * nvfp4_paged_attention wrote for the same q, cache and scale; where it is
+ * -inf the token's head adds nothing.  mass and out
  * are fp32 [count, kv_heads, room], room >= the longest kv_lens; mass may be
  * NULL (nothing received before) or out itself.  Sums in fp32 in a fixed
  * order. */

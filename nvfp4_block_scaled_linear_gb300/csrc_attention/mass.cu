@@ -155,7 +155,10 @@ __global__ void __launch_bounds__(kThreads) mass_kernel(const Mass p) {
 #pragma unroll
     for (int i = 0; i < kVec; ++i)
       *reinterpret_cast<uint4*>(&q_sm[b][my_row * kPitch + (i * 8 + my_piece) * 16]) = next[i];
-    if (my_piece == 0) row_sm[b][my_row] = make_float2(c, next_lse * 1.44269504088896f);
+    // (a row of lse -inf has no weight to give)
+    if (my_piece == 0)
+      row_sm[b][my_row] =
+          make_float2(c, next_lse == -INFINITY ? INFINITY : next_lse * 1.44269504088896f);
   };
 
   float sum[kTiles][2];

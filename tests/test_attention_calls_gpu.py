@@ -84,3 +84,21 @@ def test_mass_of_a_key_whose_scores_are_minus_infinity(hq, hk, dim, hint, q_len)
     got = att.attention_mass(b.q.to(DEV), *args, lse.to(DEV), out=torch.empty(1, hk, room, device=DEV)).double().cpu()
     assert not torch.isnan(got).any()
     assert ((got - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("hq,hk,dim", [(24, 4, 256), (8, 2, 128)])
+@pytest.mark.parametrize("hint", [1, 400])
+def test_mass_of_rows_without_a_weight(hq, hk, dim, hint):
+    """A query whose every score is -inf has lse -inf and an output of zeros;
+    no key receives anything from it, by either kernel."""
+    n, q_len = 130, 4
+    b = Batch([n], [q_len], hq, hk, dim, seed=dim, width=9)
+    b.cache.k[..., 3] = float("-inf")
+    b.q[..., 3] = b.q[..., 3].abs() + 0.5
+    q = b.q.to(DEV)
+    args = b.args[:-1] + (hint,)
+    lse = torch.zeros(q.shape[:2], device=DEV)
+    out = att.paged_attention(q, *args, lse=lse)
+    assert (out == 0).all() and (lse == float("-inf")).all()
+    got = att.attention_mass(q, *args, lse)
+    assert (got == 0).all()
