@@ -304,6 +304,9 @@ def paged_attention(q, cache, block_table, kv_lens, q_starts, max_q_len, scale=N
         out = _empty((tokens, hq, dim), torch.bfloat16, dev, stream)
     if workspace is None:
         workspace = _call_workspace(cache, stream)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on %s, got strides %s on %s"
+                         % (dev, workspace.stride(), workspace.device))
     _call("nvfp4_paged_attention", dev, stream, _heads(q, "q", tokens, hq, dim, dev), tokens, hq,
           cache._c, _seqs(cache, block_table, kv_lens, q_starts, max_q_len),
           dim ** -0.5 if scale is None else scale, _heads(out, "out", tokens, hq, dim, dev),

@@ -102,3 +102,14 @@ def test_mass_of_rows_without_a_weight(hq, hk, dim, hint):
     assert (out == 0).all() and (lse == float("-inf")).all()
     got = att.attention_mass(q, *args, lse)
     assert (got == 0).all()
+
+
+def test_a_workspace_elsewhere_is_refused():
+    """Memory of the host, or less memory than the tensor's size says."""
+    b = Batch([70], [2], 8, 2, 128, seed=44)
+    q = b.q.to(DEV)
+    n = att.attention_workspace(b.cache).numel()
+    for workspace in (torch.empty(n, dtype=torch.uint8), torch.empty(1, dtype=torch.uint8, device=DEV).expand(n),
+                      torch.empty(2 * n, dtype=torch.uint8, device=DEV)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            att.paged_attention(q, *b.args, workspace=workspace)
