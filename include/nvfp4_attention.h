@@ -138,7 +138,8 @@ int nvfp4_qk_norm_rope(const nvfp4_heads* q, const nvfp4_heads* k, const nvfp4_h
  *                nvfp4_paged_attention_workspace() bytes; its contents need
  *                no set-up and mean nothing between calls, but calls that
  *                may overlap on the GPU need one each.
- * tokens outside every sequence are left alone. */
+ * tokens outside every sequence are left alone, and so are all tokens where
+ * q_starts descends anywhere (NVFP4_ATTENTION_BAD_INDEX). */
 int nvfp4_paged_attention(const nvfp4_heads* q, int64_t tokens, int32_t q_heads,
                           const nvfp4_kv_cache* cache, const nvfp4_sequences* seqs, float scale,
                           const nvfp4_heads* out, float* lse, void* workspace,

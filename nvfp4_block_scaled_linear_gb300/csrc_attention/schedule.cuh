@@ -69,12 +69,16 @@ struct RangeSmem {
 // warp sums up batches of 32 sequences, and the warp whose batch holds the
 // range's first unit finds its place in it.  Everything is in two passes over
 // the same code, since what runs once per launch costs as much in instruction
-// fetches as in instructions.
+// fetches as in instructions.  Where q_starts descends anywhere, sequences may
+// overlap and have more tokens in all than the units' count allows for
+// (countable), so that no CTA gets a range.
 __device__ inline Range find_range(const Seqs& q, int heads, const Plan& p, uint32_t cta,
                                    uint32_t ctas, RangeSmem* sm, unsigned int* err) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int warps = blockDim.x >> 5, batches = (q.count + 31) / 32;
+  const int warps = blockDim.x >> 5;
+  int batches = (q.count + 31) / 32;
   uint32_t begin = 0;
+  bool descends = false;
   SeqInfo mine{0, 0, 0};
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
@@ -95,6 +99,7 @@ __device__ inline Range find_range(const Seqs& q, int heads, const Plan& p, uint
       const int s = b * 32 + lane;
       if (pass == 0 || batches > 1)
         mine = s < q.count ? load_seq(q, s, err) : SeqInfo{0, 0, 0};
+      descends |= s < q.count && q.q_starts[s + 1] < q.q_starts[s];
       // units of one head of each lane's sequence
       const int tiles = tiles_of(mine, p);
       uint32_t one = tiles == 1 ? tile_units(mine, 0, p) + p.extra : 0;
@@ -147,7 +152,7 @@ __device__ inline Range find_range(const Seqs& q, int heads, const Plan& p, uint
       }
       break;
     }
-    __syncthreads();
+    if (__syncthreads_or(descends)) batches = 0;       // (load_seq has set the error bit)
     if (pass == 0) {
       uint32_t total = 0;
 #pragma unroll 1

@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import _attention_ref as ref
-from test_attention_gpu import BF16, DEV, E4M3, Batch, att, no_device_error, to_dev  # noqa: F401
+from test_attention_gpu import BF16, DEV, E4M3, Batch, att, check_attention, no_device_error, to_dev  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -113,3 +113,19 @@ def test_a_workspace_elsewhere_is_refused():
                       torch.empty(2 * n, dtype=torch.uint8, device=DEV)[::2]):
         with pytest.raises(ValueError, match="workspace"):
             att.paged_attention(q, *b.args, workspace=workspace)
+
+
+@pytest.mark.parametrize("hint", [1, 300])
+@pytest.mark.parametrize("starts", [[0, 4, 0, 4], [0, 4, 2, 4], [4, 0, 4, 4]], ids=str)
+def test_starts_that_descend(hint, starts):
+    """Sequences that would overlap: the error bit, and nothing is written."""
+    b = Batch([90, 64, 33], [2, 1, 1], 4, 2, 128, seed=45)
+    cache, table, kv, good, _ = b.args
+    q, want = b.q.to(DEV), b.reference()
+    out, lse = torch.full_like(q, 3.0), torch.full(q.shape[:2], 7.0, device=DEV)
+    att.paged_attention(q, cache, table, kv, torch.tensor(starts, dtype=torch.int32, device=DEV), hint, out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert att.attention_error() == att.ATTENTION_BAD_INDEX
+    assert (out == 3.0).all() and (lse == 7.0).all()
+    att.paged_attention(q, cache, table, kv, good, hint, out=out, lse=lse)
+    check_attention(out, lse, want)
