@@ -129,3 +129,20 @@ def test_starts_that_descend(hint, starts):
     assert (out == 3.0).all() and (lse == 7.0).all()
     att.paged_attention(q, cache, table, kv, good, hint, out=out, lse=lse)
     check_attention(out, lse, want)
+
+
+def test_norm_rope_values_at_the_edges_of_keys_and_queries():
+    """Rows of zeros, of one large or small value and with a NaN: the same of keys
+    as of queries, and each row to itself."""
+    x = torch.zeros(4, 2, 128, dtype=BF16)
+    x[1, 0, 5], x[2, 1, 7], x[3, 0, 9] = 1e18, float("nan"), 1e-30
+    w = torch.ones(128, dtype=BF16, device=DEV)
+    q, k = (t.float().cpu() for t in att.qk_norm_rope(x.to(DEV), x.to(DEV), w, w, None, None))
+    nan = torch.zeros(4, 2, 128, dtype=torch.bool)
+    nan[2, 1] = True
+    for got in (q, k):
+        assert torch.equal(torch.isnan(got), nan)
+        want = ref.norm_rope(torch.where(nan, torch.zeros_like(x), x), w.cpu(), None, None, 1e-6)
+        off = (got.double() - want).abs()
+        assert (off <= 2.0 ** -8 * want.abs() + 2.0 ** -18 * want.abs().amax(-1, keepdim=True))[~nan].all()
+    assert torch.equal(q.nan_to_num(), k.nan_to_num())
