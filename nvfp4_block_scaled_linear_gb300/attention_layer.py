@@ -112,7 +112,7 @@ def serve(layer, prompt, chunk, tokens, keep, recent=64, page=64, dtype=torch.fl
     small = new_kv_cache(width, page, hk, d, dtype, scale, scale, dev)
     to = torch.arange(width, dtype=torch.int32, device=dev).view(1, -1)
     lens, _, _ = evict(cache, table, torch.tensor([held], dtype=torch.int32, device=dev), mass, keep,
-                       recent, small, to)
+                       min(recent, keep), small, to)
     cut = int(lens)
     whole = [step(cache, table, t, t, 1) for t in range(held, total)]
     short = [step(small, to, cut + i, held + i, 1) for i in range(tokens)]
@@ -122,7 +122,7 @@ def serve(layer, prompt, chunk, tokens, keep, recent=64, page=64, dtype=torch.fl
 def main(argv=None):
     argv = sys.argv[1:] if argv is None else argv
     prompt, chunk, tokens, keep = ([int(v) for v in argv] + [8192, 2048, 16, 4096][len(argv):])[:4]
-    layer = seeded_layer(positions=prompt + 2 * tokens)
+    layer = seeded_layer(positions=max(prompt + 2 * tokens, 256 + 2 * 2))
     serve(layer, min(prompt, 256), 128, 2, 64)                       # warm-up
     torch.cuda.synchronize()
     start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))

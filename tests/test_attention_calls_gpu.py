@@ -146,3 +146,11 @@ def test_norm_rope_values_at_the_edges_of_keys_and_queries():
         off = (got.double() - want).abs()
         assert (off <= 2.0 ** -8 * want.abs() + 2.0 ** -18 * want.abs().amax(-1, keepdim=True))[~nan].all()
     assert torch.equal(q.nan_to_num(), k.nan_to_num())
+
+
+def test_the_example_at_small_sizes(capsys):
+    """One token after a short prompt, cut to fewer keys than are kept as recent by default."""
+    from nvfp4_block_scaled_linear_gb300 import attention_layer
+    attention_layer.main(["100", "64", "1", "32"])
+    assert "cache cut from 101 to 32 keys" in capsys.readouterr().out
+    assert att.attention_error() == 0
