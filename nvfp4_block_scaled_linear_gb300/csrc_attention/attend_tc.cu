@@ -945,33 +945,33 @@ __global__ void __launch_bounds__(Cfg<kDim, kE4m3, kTiles>::kThreads, 1)
         }
         if (valid) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * inv);
-        if (whole) {
-          __nv_bfloat16* dst = a.out.data + token * a.out.ts + head * a.out.hs + i;
-          if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
+          for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * inv);
+          if (whole) {
+            __nv_bfloat16* dst = a.out.data + token * a.out.ts + head * a.out.hs + i;
+            if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 16) {
-              uint32_t y[8];
+              for (int j = 0; j < 32; j += 16) {
+                uint32_t y[8];
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                y[k] = f32x2_to_bf16x2(__uint_as_float(o[j + 2 * k]), __uint_as_float(o[j + 2 * k + 1]));
-              st_global_32(dst + j, y);
+                for (int k = 0; k < 8; ++k)
+                  y[k] = f32x2_to_bf16x2(__uint_as_float(o[j + 2 * k]), __uint_as_float(o[j + 2 * k + 1]));
+                st_global_32(dst + j, y);
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; j += 8)
+                *reinterpret_cast<uint4*>(dst + j) =
+                    make_uint4(f32x2_to_bf16x2(__uint_as_float(o[j]), __uint_as_float(o[j + 1])),
+                               f32x2_to_bf16x2(__uint_as_float(o[j + 2]), __uint_as_float(o[j + 3])),
+                               f32x2_to_bf16x2(__uint_as_float(o[j + 4]), __uint_as_float(o[j + 5])),
+                               f32x2_to_bf16x2(__uint_as_float(o[j + 6]), __uint_as_float(o[j + 7])));
             }
           } else {
+            float* dst = p.parts.out + at_part * kDim + i;
 #pragma unroll
-            for (int j = 0; j < 32; j += 8)
-              *reinterpret_cast<uint4*>(dst + j) =
-                  make_uint4(f32x2_to_bf16x2(__uint_as_float(o[j]), __uint_as_float(o[j + 1])),
-                             f32x2_to_bf16x2(__uint_as_float(o[j + 2]), __uint_as_float(o[j + 3])),
-                             f32x2_to_bf16x2(__uint_as_float(o[j + 4]), __uint_as_float(o[j + 5])),
-                             f32x2_to_bf16x2(__uint_as_float(o[j + 6]), __uint_as_float(o[j + 7])));
+            for (int j = 0; j < 32; j += 8) st_global_32(dst + j, &o[j]);
           }
-        } else {
-          float* dst = p.parts.out + at_part * kDim + i;
-#pragma unroll
-          for (int j = 0; j < 32; j += 8) st_global_32(dst + j, &o[j]);
         }
-  }
         __syncwarp();
       }
       if (fix && valid) {

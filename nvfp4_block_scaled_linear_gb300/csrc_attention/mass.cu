@@ -32,28 +32,13 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStageRows = 32;                // query rows in shared memory at a time
 
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
-  uint32_t d;
-  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}"
-      : "=r"(d)
-      : "r"(v));
-  return d;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 template <int kDim, bool kE4m3>
 __global__ void __launch_bounds__(kThreads) mass_kernel(const Mass p) {
   constexpr int kPitch = kDim * 2 + 16;                    // bytes of a query row
   constexpr int kSteps = kDim / 16;
-  constexpr int kTiles = 1;                                // 16-key tiles of a warp
-  constexpr int kBlockKeys = kWarps * 16 * kTiles;
+  constexpr int kBlockKeys = kWarps * 16;
   __shared__ __align__(16) uint8_t q_sm[2][kStageRows * kPitch];
-  __shared__ float2 row_sm[2][kStageRows];                 // (c, L) of a row
+  __shared__ __align__(16) float2 row_sm[2][kStageRows];   // (c, L) of a row, read in pairs
   griddep_wait();
   griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -62,7 +47,7 @@ __global__ void __launch_bounds__(kThreads) mass_kernel(const Mass p) {
   const SeqInfo si = load_seq(p.seqs, s, p.err);
   const int key0 = blockIdx.x * kBlockKeys;
   const int64_t out0 = (int64_t(s) * p.cache.heads + kvh) * p.room;
-  const int my_key = key0 + warp * 16 * kTiles;
+  const int my_key = key0 + warp * 16;
   const int before = si.kv_len - si.q_len;                 // keys before the first new token
   // the rows of this head's group, token by token; those that see key0 on
   const int rows = si.q_len * p.group;
@@ -70,44 +55,42 @@ __global__ void __launch_bounds__(kThreads) mass_kernel(const Mass p) {
   const bool any = key0 < si.kv_len && row0 < rows;
 
   // ---- the keys: A operands, steps in an order of k that fits 16-byte pieces
-  uint32_t a[kTiles][kSteps][4];
+  uint32_t a[kSteps][4];
   if (any) {
 #pragma unroll
-    for (int m = 0; m < kTiles; ++m)
+    for (int half = 0; half < 2; ++half) {
+      const int key = my_key + half * 8 + g;
+      int64_t page = p.cache.pages;
+      int in_page = 0;
+      if (key < si.kv_len) {
+        const int n = key / p.cache.page_size;
+        page = checked_page(p.seqs.table[int64_t(s) * p.seqs.width + n], p.cache.pages, p.err);
+        in_page = key - n * p.cache.page_size;
+      }
+      const bool valid = page != p.cache.pages;
+      const int64_t off = valid ? page * p.cache.ks[0] + in_page * p.cache.ks[1] + kvh * p.cache.ks[2] : 0;
+      constexpr int kPieces = kDim * (kE4m3 ? 1 : 2) / 64;     // 16-byte pieces of a lane
+      const uint8_t* row = static_cast<const uint8_t*>(p.cache.k) + off * (kE4m3 ? 1 : 2) + t * 16;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int key = my_key + m * 16 + half * 8 + g;
-        int64_t page = p.cache.pages;
-        int in_page = 0;
-        if (key < si.kv_len) {
-          const int n = key / p.cache.page_size;
-          page = checked_page(p.seqs.table[int64_t(s) * p.seqs.width + n], p.cache.pages, p.err);
-          in_page = key - n * p.cache.page_size;
-        }
-        const bool valid = page != p.cache.pages;
-        const int64_t off = valid ? page * p.cache.ks[0] + in_page * p.cache.ks[1] + kvh * p.cache.ks[2] : 0;
-        constexpr int kPieces = kDim * (kE4m3 ? 1 : 2) / 64;     // 16-byte pieces of a lane
-        const uint8_t* row = static_cast<const uint8_t*>(p.cache.k) + off * (kE4m3 ? 1 : 2) + t * 16;
+      for (int i = 0; i < kPieces; ++i) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (valid) v = *reinterpret_cast<const uint4*>(row + i * 64);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        if (kE4m3) {
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (valid) v = *reinterpret_cast<const uint4*>(row + i * 64);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          if (kE4m3) {
+          for (int j = 0; j < 4; ++j) {
+            a[(4 * i + j) % kSteps][half] = e4m3x2_to_f16x2(w[j] & 0xFFFFu);
+            a[(4 * i + j) % kSteps][2 + half] = e4m3x2_to_f16x2(w[j] >> 16);
+          }
+        } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              a[m][(4 * i + j) % kSteps][half] = e4m3x2_to_f16x2(w[j] & 0xFFFFu);
-              a[m][(4 * i + j) % kSteps][2 + half] = e4m3x2_to_f16x2(w[j] >> 16);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              a[m][(2 * i + j) % kSteps][half] = w[2 * j];
-              a[m][(2 * i + j) % kSteps][2 + half] = w[2 * j + 1];
-            }
+          for (int j = 0; j < 2; ++j) {
+            a[(2 * i + j) % kSteps][half] = w[2 * j];
+            a[(2 * i + j) % kSteps][2 + half] = w[2 * j + 1];
           }
         }
       }
+    }
   }
 
   // ---- the rows: 8 threads to each, one stage ahead in registers
@@ -161,9 +144,7 @@ __global__ void __launch_bounds__(kThreads) mass_kernel(const Mass p) {
           make_float2(c, next_lse == -INFINITY ? INFINITY : next_lse * 1.44269504088896f);
   };
 
-  float sum[kTiles][2];
-#pragma unroll
-  for (int m = 0; m < kTiles; ++m) sum[m][0] = sum[m][1] = 0.f;
+  float sum[2] = {0.f, 0.f};
   if (any) {
     fetch(row0 + my_row);
     put(0);
@@ -174,15 +155,11 @@ __global__ void __launch_bounds__(kThreads) mass_kernel(const Mass p) {
       if (more) fetch(r0 + kStageRows + my_row);
       // rows that see this warp's last key, and so all of them, need no mask
       const bool mask = r0 + kStageRows > rows ||
-                        r0 < max(0, my_key + 16 * kTiles - 1 - before) * p.group;
+                        r0 < max(0, my_key + 15 - before) * p.group;
 #pragma unroll 1
       for (int n = 0; n < kStageRows / 8; ++n) {
         if (r0 + n * 8 >= rows) break;
-        float d[kTiles][4];
-#pragma unroll
-        for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) d[m][i] = 0.f;
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
         const uint8_t* qr = &q_sm[b][(n * 8 + g) * kPitch];
 #pragma unroll
         for (int i = 0; i < kSteps; i += kE4m3 ? 4 : 2) {
@@ -195,48 +172,42 @@ __global__ void __launch_bounds__(kThreads) mass_kernel(const Mass p) {
             w[4] = hi.x, w[5] = hi.y, w[6] = hi.z, w[7] = hi.w;
           }
 #pragma unroll
-          for (int j = 0; j < (kE4m3 ? 4 : 2); ++j)
-#pragma unroll
-            for (int m = 0; m < kTiles; ++m) {
-              const uint32_t(&am)[4] = a[m][(i + j) % kSteps];
-              if (kE4m3)
-                mma_f16_16816(d[m], am[0], am[1], am[2], am[3], w[2 * j], w[2 * j + 1]);
-              else
-                mma_bf16_16816(d[m], am[0], am[1], am[2], am[3], w[2 * j], w[2 * j + 1]);
-            }
+          for (int j = 0; j < (kE4m3 ? 4 : 2); ++j) {
+            const uint32_t(&am)[4] = a[(i + j) % kSteps];
+            if (kE4m3)
+              mma_f16_16816(d, am[0], am[1], am[2], am[3], w[2 * j], w[2 * j + 1]);
+            else
+              mma_bf16_16816(d, am[0], am[1], am[2], am[3], w[2 * j], w[2 * j + 1]);
+          }
         }
         // columns 2t, 2t + 1 of this tile: rows of queries
         const float4 cl = *reinterpret_cast<const float4*>(&row_sm[b][n * 8 + 2 * t]);
         const int r = r0 + n * 8 + 2 * t;
 #pragma unroll
-        for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            float e0 = ex2(fmaf(d[m][2 * half], cl.x, -cl.y));
-            float e1 = ex2(fmaf(d[m][2 * half + 1], cl.z, -cl.w));
-            if (mask) {
-              const int least = max(0, my_key + m * 16 + half * 8 + g - before) * p.group;
-              if (r < least || r >= rows) e0 = 0.f;
-              if (r + 1 < least || r + 1 >= rows) e1 = 0.f;
-            }
-            sum[m][half] += e0 + e1;
+        for (int half = 0; half < 2; ++half) {
+          float e0 = ex2(fmaf(d[2 * half], cl.x, -cl.y));
+          float e1 = ex2(fmaf(d[2 * half + 1], cl.z, -cl.w));
+          if (mask) {
+            const int least = max(0, my_key + half * 8 + g - before) * p.group;
+            if (r < least || r >= rows) e0 = 0.f;
+            if (r + 1 < least || r + 1 >= rows) e1 = 0.f;
           }
+          sum[half] += e0 + e1;
+        }
       }
       if (more) put(b ^ 1);
       __syncthreads();
     }
   }
 #pragma unroll
-  for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      float x = sum[m][half];
-      x += __shfl_xor_sync(0xffffffffu, x, 1);
-      x += __shfl_xor_sync(0xffffffffu, x, 2);
-      const int key = my_key + m * 16 + half * 8 + g;
-      if (t == 0 && key < p.room)
-        p.out[out0 + key] = key < si.kv_len ? (p.mass ? p.mass[out0 + key] : 0.f) + x : 0.f;
-    }
+  for (int half = 0; half < 2; ++half) {
+    float x = sum[half];
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    x += __shfl_xor_sync(0xffffffffu, x, 2);
+    const int key = my_key + half * 8 + g;
+    if (t == 0 && key < p.room)
+      p.out[out0 + key] = key < si.kv_len ? (p.mass ? p.mass[out0 + key] : 0.f) + x : 0.f;
+  }
 }
 
 template <int kDim, bool kE4m3>

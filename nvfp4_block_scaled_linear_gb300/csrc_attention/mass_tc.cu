@@ -16,7 +16,7 @@
 // the exponentials, 256 for a thread in the same time, run beside them.
 //
 // Measured at 24 query and 4 key/value heads of 256: 2048 tokens over 16411 keys
-// 304 us, 1276 TFLOP/s, 66% of the burst rate of a matrix product.
+// 308 us, 1256 TFLOP/s, 65% of the burst rate of a matrix product.
 //
 // Warps: 0-3 and 4-7 sum up (tile 0, tile 1); 8 copies K once and then the
 // queries; 9 and 11 MMA (tile 0, tile 1); 10 the rows' log-sums.  An e4m3 K
@@ -385,7 +385,9 @@ int run(const Mass& a, const Device& d, cudaStream_t stream) {
   // Where the new tokens may be half of all, the CTAs of the first keys would see
   // far more queries than those of the last: a cluster of 4 shares them.  8192
   // keys, 8192 new: 302 us against 582 with one CTA; 4096: 244 against 298; 1024,
-  // where each CTA's start counts: 104 against 81.
+  // where each CTA's start counts: 104 against 81.  (The lengths lie on the device:
+  // the rule goes by the room for them, so that a prompt in a wider mass tensor
+  // takes one CTA.)
   const int ctas = 2 * int64_t(a.max_q_len) >= a.room ? 4 : 1;
   if (blocks > INT32_MAX / ctas) return NVFP4_ERR_SHAPE;
   return launch_clusters(ctas, kernel,

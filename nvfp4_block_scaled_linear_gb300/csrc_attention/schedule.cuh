@@ -38,7 +38,7 @@ __device__ __forceinline__ int tile_keys(const SeqInfo& s, int tile, const Plan&
   return max(0, s.kv_len - s.q_len + last);
 }
 
-// Units of an item; with `extra`, what it counts.
+// Units of an item (it counts p.extra more).
 __device__ __forceinline__ int tile_units(const SeqInfo& s, int tile, const Plan& p) {
   return max(1, (tile_keys(s, tile, p) + (1 << p.unit_shift) - 1) >> p.unit_shift);
 }
