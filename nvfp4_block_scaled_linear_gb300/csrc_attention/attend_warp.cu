@@ -32,7 +32,7 @@
 //
 // Measured with the join at 24 query and 4 key/value heads of 256: 32 ragged
 // sequences of one token (451 MB of cache) 77.5 us, 5.83 TB/s, 87% of the copy
-// rate; one token over 4099 keys 13.9 us, of which reading 16.8 MB is 2.5: the
+// rate; one token over 4099 keys 14.2 us, of which reading 16.8 MB is 2.5: the
 // rest is the search for the range, one block's latency and the join.
 #include <algorithm>
 

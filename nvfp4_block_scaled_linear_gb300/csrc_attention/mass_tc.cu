@@ -384,7 +384,7 @@ int run(const Mass& a, const Device& d, cudaStream_t stream) {
     return NVFP4_ERR_LAUNCH;
   // Where the new tokens may be half of all, the CTAs of the first keys would see
   // far more queries than those of the last: a cluster of 4 shares them.  8192
-  // keys, 8192 new: 302 us against 582 with one CTA; 4096: 244 against 298; 1024,
+  // keys, 8192 new: 305 us against 582 with one CTA; 4096: 244 against 298; 1024,
   // where each CTA's start counts: 104 against 81.  (The lengths lie on the device:
   // the rule goes by the room for them, so that a prompt in a wider mass tensor
   // takes one CTA.)
