@@ -3,8 +3,8 @@
     python -m nvfp4_block_scaled_linear_gb300.build [--force] [--verbose]
 
 Output: nvfp4_block_scaled_linear_gb300/_build/libnvfp4_linear.so (ignored by
-git), from the linear layer's translation unit (csrc/) and the attention
-block's (csrc_attention/).  The CUDA runtime is linked as a shared library so
+git), from the linear layer's translation unit (csrc/), the attention block's
+(csrc_attention/) and the NVFP4 x NVFP4 operators' (csrc_w4a4/).  The CUDA runtime is linked as a shared library so
 that the process shares one runtime (current device, streams) with PyTorch.
 """
 import glob
@@ -19,6 +19,7 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libnvfp4_linear.so")
 MAIN = os.path.join(CSRC, "nvfp4_linear.cu")
 CSRC_ATTENTION = os.path.join(HERE, "csrc_attention")
+CSRC_W4A4 = os.path.join(HERE, "csrc_w4a4")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -32,12 +33,16 @@ def _sources():
                   glob.glob(os.path.join(CSRC, "*.cuh")) +
                   glob.glob(os.path.join(CSRC_ATTENTION, "*.cu")) +
                   glob.glob(os.path.join(CSRC_ATTENTION, "*.cuh")) +
+                  glob.glob(os.path.join(CSRC_W4A4, "*.cu")) +
+                  glob.glob(os.path.join(CSRC_W4A4, "*.cuh")) +
                   glob.glob(os.path.join(ROOT, "include", "*.h")))
 
 
 def _units():
-    """The translation units: the linear layer's and the attention block's."""
-    return [MAIN] + sorted(glob.glob(os.path.join(CSRC_ATTENTION, "*.cu")))
+    """The translation units: the linear layer's, the attention block's and the
+    NVFP4 x NVFP4 operators'."""
+    return [MAIN] + sorted(glob.glob(os.path.join(CSRC_ATTENTION, "*.cu")) +
+                           glob.glob(os.path.join(CSRC_W4A4, "*.cu")))
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -54,7 +59,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     try:
         # one nvcc per translation unit, all at once
         for unit in _units():
-            obj = "%s.%s.o" % (tmp, os.path.splitext(os.path.basename(unit))[0])
+            obj = "%s.%s.%s.o" % (tmp, os.path.basename(os.path.dirname(unit)),
+                                  os.path.splitext(os.path.basename(unit))[0])
             objects.append(obj)
             jobs.append(subprocess.Popen([_nvcc(), *flags, "-c", "-o", obj, unit]))
         failed = [j.args for j in jobs if j.wait() != 0]

@@ -1,0 +1,236 @@
+// api.cu -- the C ABI of include/nvfp4_w4a4.h: validation on the host, the
+// per-device set-up and the error word.
+#include <climits>
+#include <cmath>
+#include <mutex>
+
+#include "common.cuh"
+
+namespace {
+
+__device__ unsigned int g_w4a4_error;
+__device__ unsigned int g_w4a4_error_read;
+
+__global__ void read_w4a4_error_kernel(int clear) {
+  g_w4a4_error_read = clear ? atomicExch(&g_w4a4_error, 0u) : atomicOr(&g_w4a4_error, 0u);
+}
+
+using nvfp4::w4a4::kMaxDevices;
+struct Slot {
+  bool ready = false, supported = false;
+  nvfp4::w4a4::Device d;
+};
+Slot g_devices[kMaxDevices];
+std::mutex g_device_mutex;
+
+bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+bool bad_scale(float s) { return !(s > 0.f && s < INFINITY); }
+
+// Largest sizes: offsets stay far inside 64 bits, coordinates inside 32.
+constexpr int64_t kMaxRows = int64_t(1) << 30;
+
+int check_sizes(int64_t M, int64_t K, int64_t unit) {
+  if (M < 0 || K <= 0) return NVFP4_ERR_INVALID;
+  if (K % unit != 0 || M > kMaxRows || K > kMaxRows) return NVFP4_ERR_SHAPE;
+  return NVFP4_OK;
+}
+
+// bf16 rows; the stride counts only where there is more than one.
+int check_matrix(const void* p, int64_t stride, int64_t M, int64_t K) {
+  if (!p) return NVFP4_ERR_INVALID;
+  if (misaligned(p)) return NVFP4_ERR_MISALIGNED;
+  if (M > 1) {
+    if (stride < K) return NVFP4_ERR_INVALID;
+    if (stride % 8 != 0) return NVFP4_ERR_MISALIGNED;
+    if (stride >= (int64_t(1) << 31)) return NVFP4_ERR_SHAPE;
+  }
+  return NVFP4_OK;
+}
+
+int check_rows(const nvfp4_rows* r) {
+  if (!r || !r->codes || !r->scales || bad_scale(r->global_scale)) return NVFP4_ERR_INVALID;
+  if (misaligned(r->codes) || misaligned(r->scales)) return NVFP4_ERR_MISALIGNED;
+  return NVFP4_OK;
+}
+
+}  // namespace
+
+namespace nvfp4 {
+namespace w4a4 {
+
+int device(Device* out) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+    cudaGetLastError();
+    return NVFP4_ERR_DEVICE;
+  }
+  std::lock_guard<std::mutex> lock(g_device_mutex);
+  Slot& s = g_devices[dev];
+  if (!s.ready) {
+    int major = 0, minor = 0, sms = 0;
+    void* err = nullptr;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+      cudaGetLastError();
+      return NVFP4_ERR_DEVICE;
+    }
+    s.supported = major == 10 && minor == 3;
+    if (s.supported && cudaGetSymbolAddress(&err, g_w4a4_error) != cudaSuccess) {
+      cudaGetLastError();
+      return NVFP4_ERR_DEVICE;
+    }
+    s.d.id = dev;
+    s.d.num_sms = sms;
+    s.d.err = static_cast<unsigned int*>(err);
+    s.ready = true;
+  }
+  if (!s.supported) return NVFP4_ERR_DEVICE;
+  *out = s.d;
+  return NVFP4_OK;
+}
+
+}  // namespace w4a4
+}  // namespace nvfp4
+
+using namespace nvfp4::w4a4;
+
+extern "C" {
+
+int64_t nvfp4_w4a4_scale_bytes(int64_t rows, int64_t K) {
+  if (rows < 0 || K <= 0 || K % 256 != 0 || rows > kMaxRows || K > kMaxRows) return 0;
+  return (rows + 127) / 128 * 128 * (K / 16);
+}
+
+int nvfp4_w4a4_scale_layout(const uint8_t* w_scale, int64_t N, int64_t K, uint8_t* blocked,
+                            unsigned int* refused, void* stream) {
+  if (N <= 0) return NVFP4_ERR_INVALID;
+  if (const int st = check_sizes(N, K, 256)) return st;
+  if (N % 128 != 0) return NVFP4_ERR_SHAPE;
+  if (!w_scale || !blocked || !refused) return NVFP4_ERR_INVALID;
+  if (misaligned(w_scale) || misaligned(blocked) || (reinterpret_cast<uintptr_t>(refused) & 3u))
+    return NVFP4_ERR_MISALIGNED;
+  Device d;
+  if (const int st = device(&d)) return st;
+  return run_scale_layout(w_scale, N, K, blocked, refused, d, static_cast<cudaStream_t>(stream));
+}
+
+int nvfp4_quantize_rows(const void* x, int64_t row_stride, int64_t M, int64_t K,
+                        const nvfp4_rows* out, void* stream) {
+  if (const int st = check_sizes(M, K, 256)) return st;
+  if (M == 0) return NVFP4_OK;
+  if (const int st = check_matrix(x, row_stride, M, K)) return st;
+  if (const int st = check_rows(out)) return st;
+  Device d;
+  if (const int st = device(&d)) return st;
+  const Quantize p{static_cast<const __nv_bfloat16*>(x), row_stride, M, K, out->global_scale, out->codes,
+                   out->scales};
+  return run_quantize(p, d, static_cast<cudaStream_t>(stream));
+}
+
+int nvfp4_add_rms_norm(const void* x, int64_t x_stride, const void* residual,
+                       int64_t residual_stride, const void* weight, float eps, int64_t M,
+                       int64_t K, void* residual_out, int64_t residual_out_stride, void* y,
+                       int64_t y_stride, const nvfp4_rows* rows, void* stream) {
+  if (const int st = check_sizes(M, K, rows ? 256 : 16)) return st;
+  if (K > NVFP4_W4A4_MAX_NORM) return NVFP4_ERR_SHAPE;
+  if (!(eps >= 0.f && eps < INFINITY) || !weight) return NVFP4_ERR_INVALID;
+  if (misaligned(weight)) return NVFP4_ERR_MISALIGNED;
+  if (M == 0) return NVFP4_OK;
+  if ((y != nullptr) == (rows != nullptr)) return NVFP4_ERR_INVALID;
+  if (const int st = check_matrix(x, x_stride, M, K)) return st;
+  if (residual)
+    if (const int st = check_matrix(residual, residual_stride, M, K)) return st;
+  if (residual_out)
+    if (const int st = check_matrix(residual_out, residual_out_stride, M, K)) return st;
+  if (const int st = rows ? check_rows(rows) : check_matrix(y, y_stride, M, K)) return st;
+  Device d;
+  if (const int st = device(&d)) return st;
+  Norm p{};
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.residual = static_cast<const __nv_bfloat16*>(residual);
+  p.weight = static_cast<const __nv_bfloat16*>(weight);
+  p.residual_out = static_cast<__nv_bfloat16*>(residual_out);
+  p.y = static_cast<__nv_bfloat16*>(y);
+  p.xs = x_stride;
+  p.rs = residual_stride;
+  p.ros = residual_out_stride;
+  p.ys = y_stride;
+  p.M = M;
+  p.K = K;
+  p.eps = eps;
+  if (rows) {
+    p.gs = rows->global_scale;
+    p.codes = rows->codes;
+    p.scales = rows->scales;
+  }
+  return run_norm(p, d, static_cast<cudaStream_t>(stream));
+}
+
+int nvfp4_linear_w4a4(const nvfp4_rows* a, int64_t M, const nvfp4_weight* w, int32_t swiglu,
+                      void* y, const nvfp4_rows* out, void* stream) {
+  if (!w || w->N <= 0) return NVFP4_ERR_INVALID;
+  if (const int st = check_sizes(M, w->K, 256)) return st;
+  if (w->N > kMaxRows || w->N % (out ? 512 : swiglu ? 256 : 128) != 0) return NVFP4_ERR_SHAPE;
+  if (out && !swiglu) return NVFP4_ERR_INVALID;
+  if (!w->codes || !w->scales) return NVFP4_ERR_INVALID;
+  if (misaligned(w->codes) || misaligned(w->scales)) return NVFP4_ERR_MISALIGNED;
+  if (w->segments < 1 || w->segments > nvfp4::kMaxSegments) return NVFP4_ERR_INVALID;
+  int64_t rows = 0;
+  for (int i = 0; i < w->segments; ++i) {
+    const int64_t n = w->segment_rows[i];
+    if (n <= 0 || n > w->N || bad_scale(w->global_scale[i])) return NVFP4_ERR_INVALID;
+    if (n % 16 != 0) return NVFP4_ERR_SHAPE;
+    rows += n;
+  }
+  if (rows != w->N) return NVFP4_ERR_INVALID;
+  if (M == 0) return NVFP4_OK;
+  if (const int st = check_rows(a)) return st;
+  if ((y != nullptr) == (out != nullptr)) return NVFP4_ERR_INVALID;
+  if (const int st = out ? check_rows(out) : check_matrix(y, w->N, 1, w->N)) return st;
+  Device d;
+  if (const int st = device(&d)) return st;
+  Product p{};
+  p.a_codes = a->codes;
+  p.a_scales = a->scales;
+  p.w_codes = w->codes;
+  p.w_scales = w->scales;
+  p.M = M;
+  p.N = w->N;
+  p.K = w->K;
+  p.seg.n = w->segments;
+  rows = 0;
+  for (int i = 0; i < w->segments; ++i) {
+    rows += w->segment_rows[i];
+    p.seg.end[i] = rows;
+    p.seg.scale[i] = static_cast<float>(1.0 / (double(a->global_scale) * double(w->global_scale[i])));
+  }
+  p.swiglu = swiglu != 0;
+  p.y = static_cast<__nv_bfloat16*>(y);
+  if (out) {
+    p.codes = out->codes;
+    p.scales = out->scales;
+    p.out_gs = out->global_scale;
+  }
+  p.err = d.err;
+  return run_product(p, d, static_cast<cudaStream_t>(stream));
+}
+
+int nvfp4_w4a4_status(unsigned int* bits, int clear) {
+  if (!bits) return NVFP4_ERR_INVALID;
+  Device d;
+  if (const int st = device(&d)) return st;
+  if (cudaDeviceSynchronize() != cudaSuccess) {
+    cudaGetLastError();
+    return NVFP4_ERR_DEVICE;
+  }
+  read_w4a4_error_kernel<<<1, 1>>>(clear);
+  if (cudaGetLastError() != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess ||
+      cudaMemcpyFromSymbol(bits, g_w4a4_error_read, sizeof(*bits)) != cudaSuccess) {
+    cudaGetLastError();
+    return NVFP4_ERR_DEVICE;
+  }
+  return NVFP4_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,60 @@
+// product.cuh -- what the products of NVFP4 rows and NVFP4 weights share: the
+// block-scaled MMA, the copy of scales into TMEM, bulk copies.
+#pragma once
+#include "common.cuh"
+
+namespace nvfp4 {
+namespace w4a4 {
+
+constexpr int kStageK = 256;       // k of one pipeline stage: 128 bytes of codes a row
+constexpr int kMmaK = 64;          // k of one MMA: 32 bytes of codes a row
+constexpr int kScaleBlock = 512;   // the scales of 128 rows x 64 k
+
+// Instruction descriptor, kind::mxf4nvf4: e2m1 A and B, e4m3 scales, K = 64.
+__host__ __device__ constexpr uint32_t idesc_nvfp4(uint32_t m, uint32_t n) {
+  return (1u << 7) | (1u << 10) | ((n >> 3) << 17) | ((m >> 4) << 24);
+}
+
+// D[tmem] (+)= (A . scales) * (B . scales)^T; A and B from shared memory, K-major
+// in 128-byte swizzled rows, the scales from TMEM: row r's four in lane r % 32 of
+// every quarter, column r / 32.
+__device__ __forceinline__ void umma_nvfp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t a_scales, uint32_t b_scales,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], "
+      "[%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(a_scales), "r"(b_scales), "r"(accumulate)
+      : "memory");
+}
+
+// Descriptor of 32 rows of 16 bytes one after another (no swizzle; 8 rows are
+// 128 bytes): a block of scales.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t smem_byte_addr) {
+  return static_cast<uint64_t>((smem_byte_addr >> 4) & 0x3FFFu) |
+         static_cast<uint64_t>(128 >> 4) << 32 | static_cast<uint64_t>(1) << 46;
+}
+
+// 512 bytes of scales -> 4 TMEM columns, the same in each quarter of the lanes.
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_addr(dst)),
+      "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// Tensor map of codes [rows, K/2], boxes of `box` rows by 128 bytes.
+bool codes_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t K, int box);
+
+// Few tokens: 128 tokens by kN weight rows a CTA, k split over a cluster.
+int run_product_few(const Product& p, const Device& d, cudaStream_t stream);
+
+}  // namespace w4a4
+}  // namespace nvfp4
