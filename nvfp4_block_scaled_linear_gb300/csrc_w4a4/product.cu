@@ -35,7 +35,7 @@ bool codes_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t K, 
 }
 
 int run_product(const Product& p, const Device& d, cudaStream_t stream) {
-  return run_product_few(p, d, stream);
+  return p.M > 128 ? run_product_many(p, d, stream) : run_product_few(p, d, stream);
 }
 
 }  // namespace w4a4

@@ -56,5 +56,8 @@ bool codes_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t K, 
 // Few tokens: 128 tokens by kN weight rows a CTA, k split over a cluster.
 int run_product_few(const Product& p, const Device& d, cudaStream_t stream);
 
+// Many tokens: persistent pairs of CTAs, 256 tokens by 256 weight rows.
+int run_product_many(const Product& p, const Device& d, cudaStream_t stream);
+
 }  // namespace w4a4
 }  // namespace nvfp4

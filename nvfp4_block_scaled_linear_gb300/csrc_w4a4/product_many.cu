@@ -1,0 +1,390 @@
+// product_many.cu -- NVFP4 rows times an NVFP4 weight, many rows.
+//
+// Bound by the tensor cores.  A pair of CTAs works on 256 tokens x 256 weight
+// rows as one MMA (cta_group::2): each brings its 128 tokens and half of the
+// weight rows, so that a byte of either is read from shared memory half as often
+// as by a CTA alone.  Of a gate/up pair the first CTA brings the gate's rows and
+// the second the up projection's: both factors of an output are then in one
+// lane, 128 columns apart.
+//
+// Pairs are persistent, one on every two SMs; tiles are taken in order, the
+// token tiles innermost, so that the pairs at work share a few weight tiles.
+//
+// TMEM: the sums of two tiles would take all 512 columns and the scales have 48.
+// The second tile's sums therefore begin in the first one's last 64 columns
+// (kOverlap): the epilogue reads those first, into registers, and the next tile's
+// products start while it works on the rest.
+//
+// Warps: 0 copies, 1 issues the MMAs (in the second CTA: tells the first that a
+// stage has come), 2 TMEM allocation, 4..11 the epilogue, two for each quarter of
+// the lanes, taking every other piece of 16 columns.
+#include "product.cuh"
+
+namespace nvfp4 {
+namespace w4a4 {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kEpilogueWarps = 8;
+constexpr int kTile = 256;                       // tokens and weight rows of a pair's tile
+constexpr int kHalf = 128;
+constexpr int kA = kHalf * 128, kB = kHalf * 128;                 // bytes of codes a stage
+constexpr int kScalesA = 4 * kScaleBlock, kScalesB = 8 * kScaleBlock;
+constexpr int kStage = kA + kB + kScalesA + kScalesB;
+constexpr int kStages = 5;
+constexpr int kSmem = kStages * kStage + 1024;
+constexpr uint32_t kOverlap = 64;
+constexpr uint32_t kSecond = kTile - kOverlap;                    // column of the second tile's sums
+constexpr uint32_t kColA = kSecond + kTile, kColB = kColA + 16;
+static_assert(kColB + 32 <= 512, "TMEM columns");
+static_assert(kStage % 1024 == 0, "stages keep 1024-byte alignment");
+
+enum { kPlain = 0, kGated = 1, kGatedRows = 2 };
+
+__device__ __forceinline__ void umma_nvfp4_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                                uint32_t a_scales, uint32_t b_scales,
+                                                uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], "
+      "[%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(a_scales), "r"(b_scales), "r"(accumulate)
+      : "memory");
+}
+// In both CTAs, each from its own shared memory to its own TMEM.
+__device__ __forceinline__ void copy_scales_pair(uint32_t tmem, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+// Arrive once on `bar` of both CTAs when everything issued so far is over.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], "
+      "%1;" ::"r"(smem_addr(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+__device__ __forceinline__ void arrive_first(uint64_t* bar) {     // on the first CTA's barrier
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                   map_to_rank(smem_addr(bar), 0))
+               : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+// mbar_wait for arrivals from the other CTA.
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+  while (!try_wait_cluster(bar, parity)) {
+    if (*abort_flag) return false;
+    if (global_timer_ns() - t0 > kWaitTimeoutNs) {
+      *abort_flag = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+struct Many {
+  Product p;
+  int token_tiles, tiles, pairs;
+};
+
+// 16 sums of the lane at `col`.
+__device__ __forceinline__ void load16(uint32_t tmem, float (&v)[16]) {
+  uint32_t r[16];
+  __syncwarp();
+  tmem_ld_16cols(tmem, r);
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void store_bf16(__nv_bfloat16* y, const float (&v)[16]) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    reinterpret_cast<uint4*>(y)[k] =
+        make_uint4(f32x2_to_bf16x2(v[8 * k], v[8 * k + 1]), f32x2_to_bf16x2(v[8 * k + 2], v[8 * k + 3]),
+                   f32x2_to_bf16x2(v[8 * k + 4], v[8 * k + 5]), f32x2_to_bf16x2(v[8 * k + 6], v[8 * k + 7]));
+}
+
+template <int kMode>
+__global__ void __launch_bounds__(kThreads, 1)
+    many_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
+                const Many f) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full[kStages], empty[kStages], sums_full[2], sums_free, done;
+  __shared__ int abort_word;
+  __shared__ uint32_t tmem_slot;
+  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  volatile int* abort_flag = &abort_word;
+  const Product& p = f.p;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int pair = blockIdx.x >> 1;
+  const int steps = static_cast<int>(p.K / kStageK);
+  const int my_tiles = (f.tiles - 1 - pair) / f.pairs + 1;        // pair < pairs <= tiles
+  const int64_t scale_row = (p.K / kMmaK) * kScaleBlock;          // bytes of 128 rows' scales
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], rank == 0 ? 2 : 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&sums_full[0], 1);
+    mbar_init(&sums_full[1], 1);
+    mbar_init(&sums_free, 2 * kEpilogueWarps);
+    mbar_init(&done, 1);
+    abort_word = 0;
+    fence_mbar_init();
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_addr(&tmem_slot))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before_sync();
+  __syncwarp();
+  cluster_sync();                                                 // (the other CTA's barriers are set up)
+  tc_fence_after_sync();
+  const uint32_t tmem = tmem_slot;
+  if (threadIdx.x == 0) griddep_launch_dependents();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      prefetch_tensormap(&tm_a);
+      prefetch_tensormap(&tm_w);
+      const int64_t last_a = (p.M - 1) / 128, last_w = p.N / 128 - 1;   // blocks of scales that there are
+      // place of a tile: token row of this CTA's half, weight row of either half
+      struct Place {
+        int tile, m, w[2];
+      };
+      auto place = [&](int tile) {
+        Place q;
+        q.tile = tile;
+        const int n = tile / f.token_tiles;
+        q.m = (tile - n * f.token_tiles) * kTile + rank * kHalf;
+        q.w[0] = kMode == kPlain ? n * kTile : n * kHalf;
+        q.w[1] = kMode == kPlain ? q.w[0] + kHalf : q.w[0] + static_cast<int>(p.N / 2);
+        return q;
+      };
+      auto weights = [&](const Place& q, int it, int slot) {
+        uint8_t* st = smem + slot * kStage;
+        mbar_arrive_expect_tx(&full[slot], kStage);
+        tma_load_2d(st + kA, &tm_w, &full[slot], it * 128, rank ? q.w[1] : q.w[0]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          // (an odd block of 128 weight rows: what its missing half would be is not read back)
+          const int64_t b = min(static_cast<int64_t>(q.w[i] >> 7), last_w);
+          bulk_load(st + kA + kB + kScalesA + i * 4 * kScaleBlock,
+                    p.w_scales + b * scale_row + it * 4 * kScaleBlock, 4 * kScaleBlock, &full[slot]);
+        }
+      };
+      auto tokens = [&](const Place& q, int it, int slot) {
+        uint8_t* st = smem + slot * kStage;
+        tma_load_2d(st, &tm_a, &full[slot], it * 128, q.m);
+        const int64_t b = min(static_cast<int64_t>(q.m >> 7), last_a);
+        bulk_load(st + kA + kB, p.a_scales + b * scale_row + it * 4 * kScaleBlock, kScalesA, &full[slot]);
+      };
+      // weights do not wait for the kernel ahead in the stream, tokens do
+      const int total = my_tiles * steps, pre = steps < kStages ? steps : kStages;
+      Place q = place(pair);
+      for (int it = 0; it < pre; ++it) weights(q, it, it);
+      griddep_wait();
+      for (int it = 0; it < pre; ++it) tokens(q, it, it);
+      int issued = pre, slot = pre == kStages ? 0 : pre, it = pre;
+      uint32_t parity = pre == kStages ? 0 : 1;                  // (slots not used yet are free)
+      for (; issued < total; ++issued) {
+        if (it == steps) it = 0, q = place(q.tile + f.pairs);
+        if (!wait_cluster(&empty[slot], parity, abort_flag)) break;
+        weights(q, it, slot);
+        tokens(q, it, slot);
+        ++it;
+        if (++slot == kStages) slot = 0, parity ^= 1u;
+      }
+      for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i) {
+        volatile int none = 0;
+        if (!mbar_wait(&full[i % kStages], (i / kStages) & 1, &none)) *abort_flag = 1;
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int slot = 0;
+      uint32_t parity = 0;
+      bool ok = true;
+      if (rank == 0) {
+        constexpr uint32_t idesc = idesc_nvfp4(kTile, kTile);
+        for (int i = 0; i < my_tiles && ok; ++i) {
+          // the columns that this tile's sums share with the last one's are read
+          if (i > 0 && !(ok = wait_cluster(&sums_free, (i - 1) & 1, abort_flag))) break;
+          tc_fence_after_sync();
+          const uint32_t d = tmem + (i & 1 ? kSecond : 0);
+          for (int it = 0; it < steps; ++it) {
+            if (!(ok = wait_cluster(&full[slot], parity, abort_flag))) break;
+            tc_fence_after_sync();
+            const uint32_t st = smem_addr(smem + slot * kStage);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              copy_scales_pair(tmem + kColA + 4 * j, scale_desc(st + kA + kB + j * kScaleBlock));
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                copy_scales_pair(tmem + kColB + 8 * j + 4 * h,
+                                 scale_desc(st + kA + kB + kScalesA + (4 * h + j) * kScaleBlock));
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              umma_nvfp4_pair(d, umma_desc_sw128(st + 32 * j), umma_desc_sw128(st + kA + 32 * j), idesc,
+                              tmem + kColA + 4 * j, tmem + kColB + 8 * j, (it | j) != 0);
+            commit_pair(&empty[slot]);
+            if (++slot == kStages) slot = 0, parity ^= 1u;
+          }
+          if (ok) commit_pair(&sums_full[i & 1]);
+        }
+        commit_pair(&done);
+      } else {
+        for (int i = my_tiles * steps; i > 0; --i) {
+          if (!mbar_wait(&full[slot], parity, abort_flag)) break;
+          arrive_first(&full[slot]);
+          if (++slot == kStages) slot = 0, parity ^= 1u;
+        }
+      }
+      // every product is over before TMEM is given back
+      volatile int none = 0;
+      if (!wait_cluster(&done, 0, &none)) *abort_flag = 1;
+    }
+  } else if (warp >= 4) {
+    const int quarter = warp & 3, h = (warp - 4) >> 2;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
+    const int64_t n_out = kMode == kPlain ? p.N : p.N / 2;
+    for (int i = 0; i < my_tiles; ++i) {
+      const int b = i & 1;
+      // (the whole warp together: tcgen05.ld follows)
+      if (!__all_sync(0xffffffffu, wait_cluster(&sums_full[b], (i >> 1) & 1, abort_flag))) break;
+      tc_fence_after_sync();
+      const int tile = pair + i * f.pairs;
+      const int nt = tile / f.token_tiles;
+      const int64_t m = int64_t(tile - nt * f.token_tiles) * kTile + rank * kHalf + 32 * quarter + lane;
+      const uint32_t acc = lanes + (b ? kSecond : 0);
+      // the shared columns first; pieces h and h + 2 of their four
+      uint32_t first[2][16];
+      tmem_ld_16cols(lanes + kSecond + 16 * h, first[0]);
+      tmem_ld_16cols(lanes + kSecond + 32 + 16 * h, first[1]);
+      tmem_ld_wait();
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) arrive_first(&sums_free);
+      const bool inside = m < p.M;
+      if (kMode == kPlain) {
+        auto out = [&](int piece, float (&v)[16]) {
+          const int64_t n = int64_t(nt) * kTile + piece * 16;
+          if (!inside || n >= p.N) return;
+          const float s = seg_scale(p.seg, n);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) v[k] *= s;
+          store_bf16(p.y + m * n_out + n, v);
+        };
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float v[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(first[j][k]);
+          out((b ? 0 : 12) + 2 * j + h, v);
+        }
+#pragma unroll 2
+        for (int j = 0; j < 6; ++j) {
+          const int piece = (b ? 4 : 0) + 2 * j + h;
+          float v[16];
+          load16(acc + 16 * piece, v);
+          out(piece, v);
+        }
+      } else {
+        auto out = [&](int piece, const float (&g)[16], const float (&u)[16]) {
+          const int64_t n = int64_t(nt) * kHalf + piece * 16;
+          if (!inside) return;
+          const float sg = seg_scale(p.seg, n), su = seg_scale(p.seg, n + p.N / 2);
+          float v[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) v[k] = silu_mul(g[k] * sg, u[k] * su);
+          if (kMode == kGatedRows) {
+            uint2 codes;
+            p.scales[scale_at(m, n >> 4, n_out)] = static_cast<uint8_t>(quantize16(v, p.out_gs, codes));
+            *reinterpret_cast<uint2*>(p.codes + m * (n_out >> 1) + (n >> 1)) = codes;
+          } else {
+            store_bf16(p.y + m * n_out + n, v);
+          }
+        };
+        // what was read first: of the first sums the up halves of pieces 4..7, of the
+        // second the gate halves of pieces 0..3
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int piece = (b ? 0 : 4) + 2 * j + h;
+          float x[16], o[16];
+          load16(acc + 16 * piece + (b ? kHalf : 0), o);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(first[j][k]);
+          if (b)
+            out(piece, x, o);
+          else
+            out(piece, o, x);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int piece = (b ? 4 : 0) + 2 * j + h;
+          float g[16], u[16];
+          load16(acc + 16 * piece, g);
+          load16(acc + 16 * piece + kHalf, u);
+          out(piece, g, u);
+        }
+      }
+      // (read before the tile after next is begun: its sums_free comes later)
+      tc_fence_before_sync();
+    }
+  }
+  __syncwarp();
+  if (*abort_flag && lane == 0) atomicOr(p.err, NVFP4_W4A4_TIMEOUT);
+  tc_fence_before_sync();
+  cluster_sync();                                                 // nothing of either is in use any more
+  if (warp == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+template <int kMode>
+int run(const Product& p, const Device& d, cudaStream_t stream) {
+  static std::atomic<bool> ready[kMaxDevices];
+  if (const int st = allow_smem(many_kernel<kMode>, kSmem, d, ready)) return st;
+  CUtensorMap tm_a, tm_w;
+  if (!codes_map(&tm_a, p.a_codes, p.M, p.K, kHalf) || !codes_map(&tm_w, p.w_codes, p.N, p.K, kHalf))
+    return NVFP4_ERR_LAUNCH;
+  const int64_t token_tiles = (p.M + kTile - 1) / kTile;
+  const int64_t tiles = token_tiles * ((p.N + kTile - 1) / kTile);
+  if (tiles > (1 << 30) || tiles * (p.K / kStageK) > (int64_t(1) << 37)) return NVFP4_ERR_SHAPE;
+  Many f{};
+  f.p = p;
+  f.token_tiles = static_cast<int>(token_tiles);
+  f.tiles = static_cast<int>(tiles);
+  f.pairs = static_cast<int>(tiles < d.num_sms / 2 ? tiles : d.num_sms / 2);
+  return launch(2, many_kernel<kMode>, dim3(2 * f.pairs), dim3(kThreads), kSmem, stream, tm_a, tm_w, f);
+}
+
+}  // namespace
+
+int run_product_many(const Product& p, const Device& d, cudaStream_t stream) {
+  return !p.swiglu ? run<kPlain>(p, d, stream)
+         : p.codes ? run<kGatedRows>(p, d, stream)
+                   : run<kGated>(p, d, stream);
+}
+
+}  // namespace w4a4
+}  // namespace nvfp4

@@ -103,10 +103,6 @@ def _scale(value, name):
     return value
 
 
-def _scale_bytes(rows, k):
-    return -(-rows // 128) * 128 * (k // 16)
-
-
 class Fp4Rows:
     """NVFP4 rows [M, K], K a multiple of 256, on one device.
 
@@ -115,7 +111,7 @@ class Fp4Rows:
                   that the product reads (include/nvfp4_w4a4.h).
     global_scale  the values are codes times scales divided by it.
     """
-    __slots__ = ("codes", "scales", "global_scale", "shape", "device", "_c")
+    __slots__ = ("_codes", "_scales", "global_scale", "shape", "device", "_c")
 
     def __init__(self, codes, scales, global_scale=1.0):
         if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
@@ -130,12 +126,26 @@ class Fp4Rows:
                              % ((-(-m // 128), k // 64, 512), tuple(scales.shape)))
         if not (codes.is_contiguous() and scales.is_contiguous()):
             raise ValueError("codes and scales must be contiguous")
-        self._set(codes, scales, _scale(global_scale, "global_scale"), m, k)
-
-    def _set(self, codes, scales, global_scale, m, k):
-        self.codes, self.scales, self.global_scale = codes, scales, global_scale
+        self._codes, self._scales = codes, scales
+        self.global_scale = _scale(global_scale, "global_scale")
         self.shape, self.device = (m, k), codes.device
-        self._c = _pack_rows(codes.data_ptr(), scales.data_ptr(), global_scale)
+        self._c = _pack_rows(codes.data_ptr(), scales.data_ptr(), self.global_scale)
+
+    # (rows that a call makes are one allocation, in _codes; the views of it cost
+    # as much as a small kernel, and no call needs them)
+    @property
+    def codes(self):
+        if self._scales is None:
+            m, k = self.shape
+            return self._codes[:m * (k // 2)].view(m, k // 2)
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            m, k = self.shape
+            return self._codes[m * (k // 2):].view(-(-m // 128), k // 64, 512)
+        return self._scales
 
 
 def new_fp4_rows(m, k, global_scale=1.0, device="cuda", stream=None):
@@ -149,10 +159,16 @@ def new_fp4_rows(m, k, global_scale=1.0, device="cuda", stream=None):
 
 
 def _new_rows(m, k, global_scale, device, stream):
-    split = m * (k // 2)                                   # a multiple of 128: both parts are aligned
-    raw = _empty(split + _scale_bytes(m, k), torch.uint8, device, stream)
+    split = m * (k >> 1)                                   # a multiple of 128: both parts are aligned
+    size = split + (m + 127 >> 7) * 8 * k
+    if stream is None:
+        raw = torch.empty(size, dtype=torch.uint8, device=device)
+    else:
+        raw = _empty(size, torch.uint8, device, stream)
     rows = Fp4Rows.__new__(Fp4Rows)
-    rows._set(raw[:split].view(m, k // 2), raw[split:].view(-(-m // 128), k // 64, 512), global_scale, m, k)
+    rows._codes, rows._scales, rows.global_scale, rows.shape, rows.device = raw, None, global_scale, (m, k), device
+    p = raw.data_ptr()
+    rows._c = _pack_rows(p, p + split, global_scale)
     return rows
 
 
@@ -204,14 +220,16 @@ class Fp4Weight:
 
 
 def _matrix(t, name, shape, device):
-    if t.dtype != torch.bfloat16:
+    """Address and row stride of bfloat16 [M, K]."""
+    if t.dtype is not torch.bfloat16:
         raise TypeError("%s must be bfloat16, got %s" % (name, t.dtype))
     if t.shape != shape or t.device != device:
         raise ValueError("%s must have shape %s on %s, got %s on %s"
                          % (name, tuple(shape), device, tuple(t.shape), t.device))
-    if t.stride(1) != 1 and t.numel():
+    row, one = t.stride()
+    if one != 1:
         raise ValueError("the rows of %s must be dense" % name)
-    return t.data_ptr(), t.stride(0)
+    return t.data_ptr(), row
 
 
 def _rows_out(out, m, k, global_scale, device, stream):
@@ -240,18 +258,33 @@ def quantize_rows(x, global_scale=1.0, out=None, stream=None):
 
 
 def _norm(x, residual, weight, eps, residual_out, y, rows, stream):
-    dev, (m, k) = x.device, x.shape
-    px, sx = _matrix(x, "x", x.shape, dev)
-    pr, sr = (None, 0) if residual is None else _matrix(residual, "residual", x.shape, dev)
-    po, so = (None, 0) if residual_out is None else _matrix(residual_out, "residual_out", x.shape, dev)
-    py, sy = (None, 0) if y is None else _matrix(y, "out", x.shape, dev)
-    if weight.dtype != torch.bfloat16:
+    """The call, on whatever it is given; makes the sum's tensor where that is missing.  Returns the sum."""
+    dev, shape = x.device, x.shape
+    px, sx = _matrix(x, "x", shape, dev)
+    pr, sr = (None, 0) if residual is None else _matrix(residual, "residual", shape, dev)
+    if residual_out is not None:
+        po, so = _matrix(residual_out, "residual_out", shape, dev)
+        total = residual_out
+    elif residual is not None:
+        total = _like(x, stream)
+        po, so = total.data_ptr(), shape[1]
+    else:
+        po, so, total = None, 0, x
+    py, sy = (None, 0) if y is None else _matrix(y, "out", shape, dev)
+    if weight.dtype is not torch.bfloat16:
         raise TypeError("weight must be bfloat16, got %s" % weight.dtype)
-    if weight.shape != (k,) or weight.device != dev or not weight.is_contiguous():
+    if weight.shape != shape[1:] or weight.device != dev or not weight.is_contiguous():
         raise ValueError("weight must be a contiguous tensor of shape %s on %s, got %s on %s"
-                         % ((k,), dev, tuple(weight.shape), weight.device))
-    _call("nvfp4_add_rms_norm", dev, stream, px, sx, pr, sr, weight.data_ptr(), eps, m, k, po, so, py, sy,
-          None if rows is None else rows._c)
+                         % (tuple(shape[1:]), dev, tuple(weight.shape), weight.device))
+    _call("nvfp4_add_rms_norm", dev, stream, px, sx, pr, sr, weight.data_ptr(), eps, shape[0], shape[1], po, so,
+          py, sy, None if rows is None else rows._c)
+    return total
+
+
+def _like(x, stream):
+    if stream is None:
+        return torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+    return _empty(x.shape, torch.bfloat16, x.device, stream)
 
 
 def add_rms_norm(x, residual, weight, eps=1e-6, out=None, residual_out=None, stream=None):
@@ -262,12 +295,9 @@ def add_rms_norm(x, residual, weight, eps=1e-6, out=None, residual_out=None, str
     ``residual_out``)."""
     if not x.is_cuda or x.dim() != 2:
         raise ValueError("x must be a CUDA tensor [M, K]")
-    out = _empty(x.shape, torch.bfloat16, x.device, stream) if out is None else out
-    keep = residual_out
-    if residual_out is None and residual is not None:
-        keep = residual_out = _empty(x.shape, torch.bfloat16, x.device, stream)
-    _norm(x, residual, weight, eps, residual_out, out, None, stream)
-    return out, x if keep is None else keep
+    if out is None:
+        out = _like(x, stream)
+    return out, _norm(x, residual, weight, eps, residual_out, out, None, stream)
 
 
 def add_rms_norm_quantize(x, residual, weight, eps=1e-6, global_scale=1.0, out=None, residual_out=None,
@@ -280,11 +310,7 @@ def add_rms_norm_quantize(x, residual, weight, eps=1e-6, global_scale=1.0, out=N
     if k == 0 or k % 256:
         raise ValueError("K must be a positive multiple of 256, got %d" % k)
     out = _rows_out(out, m, k, global_scale, x.device, stream)
-    keep = residual_out
-    if residual_out is None and residual is not None:
-        keep = residual_out = _empty(x.shape, torch.bfloat16, x.device, stream)
-    _norm(x, residual, weight, eps, residual_out, None, out, stream)
-    return out, x if keep is None else keep
+    return out, _norm(x, residual, weight, eps, residual_out, None, out, stream)
 
 
 def _check_product(a, w):
@@ -296,7 +322,8 @@ def _product(a, w, swiglu, out, stream):
     _check_product(a, w)
     shape = (a.shape[0], w.shape[0] // 2 if swiglu else w.shape[0])
     if out is None:
-        out = _empty(shape, torch.bfloat16, a.device, stream)
+        out = (torch.empty(shape, dtype=torch.bfloat16, device=a.device) if stream is None
+               else _empty(shape, torch.bfloat16, a.device, stream))
     elif out.dtype != torch.bfloat16 or out.shape != shape or not out.is_contiguous() or out.device != a.device:
         raise ValueError("out must be a contiguous bfloat16 tensor of shape %s on %s" % (shape, a.device))
     _call("nvfp4_linear_w4a4", a.device, stream, a._c, a.shape[0], w._c, swiglu, out.data_ptr(), None)
