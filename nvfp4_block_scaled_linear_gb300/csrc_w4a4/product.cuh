@@ -50,8 +50,28 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
+// Wait for the phase with the given parity; given up after 2^31 clock ticks
+// (about a second), or at once when another wait of the block was, with
+// `abort_flag` set and false returned.  (The clock register, not the global
+// timer: reading that takes longer than a stage.)
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint32_t t0 = static_cast<uint32_t>(clock());
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort_flag || static_cast<uint32_t>(clock()) - t0 > 0x7FFFFFFFu) {
+      *abort_flag = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
 // Tensor map of codes [rows, K/2], boxes of `box` rows by 128 bytes.
 bool codes_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t K, int box);
+
+// Tensor map of blocked scales: row (128-row block) * (K / 64) + k / 64, boxes of 4 rows.
+bool scales_map(CUtensorMap* map, const uint8_t* scales, int64_t rows, int64_t K);
 
 // Few tokens: 128 tokens by kN weight rows a CTA, k split over a cluster.
 int run_product_few(const Product& p, const Device& d, cudaStream_t stream);

@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int issued = pre, slot = pre == f.stages ? 0 : pre;
       uint32_t parity = 0;
       for (int it = pre; it < n_steps; ++it) {
-        if (!mbar_wait(&empty[slot], parity, abort_flag)) break;
+        if (!wait(&empty[slot], parity, abort_flag)) break;
         weights(it, slot);
         tokens(it, slot);
         ++issued;
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // nothing is left in flight, whatever became of the others
       for (int it = issued > f.stages ? issued - f.stages : 0; it < issued; ++it) {
         volatile int none = 0;
-        if (!mbar_wait(&full[it % f.stages], (it / f.stages) & 1, &none)) *abort_flag = 1;
+        if (!wait(&full[it % f.stages], (it / f.stages) & 1, &none)) *abort_flag = 1;
       }
     }
   } else if (warp == 1) {
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int slot = 0;
       uint32_t parity = 0;
       for (int it = 0; it < n_steps; ++it) {
-        if (!mbar_wait(&full[slot], parity, abort_flag)) break;
+        if (!wait(&full[slot], parity, abort_flag)) break;
         tc_fence_after_sync();
         const uint32_t st = smem_addr(smem + slot * f.stage_bytes);
 #pragma unroll
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       umma_commit(&done);
       volatile int none = 0;
-      if (!mbar_wait(&done, 0, &none)) *abort_flag = 1;
+      if (!wait(&done, 0, &none)) *abort_flag = 1;
     }
   }
   __syncwarp();

@@ -7,17 +7,20 @@
 // the second the up projection's: both factors of an output are then in one
 // lane, 128 columns apart.
 //
-// Pairs are persistent, one on every two SMs; tiles are taken in order, the
-// token tiles innermost, so that the pairs at work share a few weight tiles.
+// Pairs are persistent, one on every two SMs.
 //
 // TMEM: the sums of two tiles would take all 512 columns and the scales have 48.
 // The second tile's sums therefore begin in the first one's last 64 columns
 // (kOverlap): the epilogue reads those first, into registers, and the next tile's
 // products start while it works on the rest.
 //
-// Warps: 0 copies, 1 issues the MMAs (in the second CTA: tells the first that a
-// stage has come), 2 TMEM allocation, 4..11 the epilogue, two for each quarter of
+// Both CTAs' copies count on the first one's barriers, whose thread issues the
+// MMAs; what it has read is free for both by one commit.
+//
+// Warps: 0 copies, 1 issues the MMAs, 2 TMEM allocation, 4..11 the epilogue, two for each quarter of
 // the lanes, taking every other piece of 16 columns.
+#include <algorithm>
+
 #include "product.cuh"
 
 namespace nvfp4 {
@@ -80,14 +83,13 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity)
       : "memory");
   return done != 0;
 }
-// mbar_wait for arrivals from the other CTA.
+// wait() for arrivals from the other CTA.
 __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   if (try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
+  const uint32_t t0 = static_cast<uint32_t>(clock());
 #pragma unroll 1
   while (!try_wait_cluster(bar, parity)) {
-    if (*abort_flag) return false;
-    if (global_timer_ns() - t0 > kWaitTimeoutNs) {
+    if (*abort_flag || static_cast<uint32_t>(clock()) - t0 > 0x7FFFFFFFu) {
       *abort_flag = 1;
       return false;
     }
@@ -95,10 +97,30 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, vol
   return true;
 }
 
+// A copy into this CTA's shared memory that counts on the first CTA's barrier.
+__device__ __forceinline__ void load_pair(void* dst, const CUtensorMap* map, uint32_t first_bar, int32_t c0,
+                                          int32_t c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(first_bar), "r"(c0), "r"(c1)
+      : "memory");
+}
+
 struct Many {
   Product p;
-  int token_tiles, tiles, pairs;
+  int token_tiles, weight_tiles, tiles, pairs;
 };
+
+// Tile t: bands of kBand token tiles; in a band weight tile by weight tile, its
+// token tiles innermost.  The pairs at work at one time then share few of either.
+constexpr int kBand = 8;
+__device__ __forceinline__ void tile_at(const Many& f, int t, int& token_tile, int& weight_tile) {
+  const int band = t / (kBand * f.weight_tiles), first = band * kBand;
+  const int width = min(kBand, f.token_tiles - first), r = t - band * kBand * f.weight_tiles;
+  weight_tile = r / width;
+  token_tile = first + r - weight_tile * width;
+}
 
 // 16 sums of the lane at `col`.
 __device__ __forceinline__ void load16(uint32_t tmem, float (&v)[16]) {
@@ -121,6 +143,7 @@ __device__ __forceinline__ void store_bf16(__nv_bfloat16* y, const float (&v)[16
 template <int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
     many_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
+                const __grid_constant__ CUtensorMap tm_sa, const __grid_constant__ CUtensorMap tm_sw,
                 const Many f) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[kStages], empty[kStages], sums_full[2], sums_free, done;
@@ -135,11 +158,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int pair = blockIdx.x >> 1;
   const int steps = static_cast<int>(p.K / kStageK);
   const int my_tiles = (f.tiles - 1 - pair) / f.pairs + 1;        // pair < pairs <= tiles
-  const int64_t scale_row = (p.K / kMmaK) * kScaleBlock;          // bytes of 128 rows' scales
+  const int scale_row = static_cast<int>(p.K / kMmaK);            // blocks of 128 rows' scales
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], rank == 0 ? 2 : 1);
+      mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
     mbar_init(&sums_full[0], 1);
@@ -166,7 +189,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       prefetch_tensormap(&tm_a);
       prefetch_tensormap(&tm_w);
-      const int64_t last_a = (p.M - 1) / 128, last_w = p.N / 128 - 1;   // blocks of scales that there are
+      // blocks of scales that there are
+      const int last_a = static_cast<int>((p.M - 1) / 128), last_w = static_cast<int>(p.N / 128) - 1;
+      prefetch_tensormap(&tm_sa);
+      prefetch_tensormap(&tm_sw);
       // place of a tile: token row of this CTA's half, weight row of either half
       struct Place {
         int tile, m, w[2];
@@ -174,29 +200,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto place = [&](int tile) {
         Place q;
         q.tile = tile;
-        const int n = tile / f.token_tiles;
-        q.m = (tile - n * f.token_tiles) * kTile + rank * kHalf;
+        int m, n;
+        tile_at(f, tile, m, n);
+        q.m = m * kTile + rank * kHalf;
         q.w[0] = kMode == kPlain ? n * kTile : n * kHalf;
         q.w[1] = kMode == kPlain ? q.w[0] + kHalf : q.w[0] + static_cast<int>(p.N / 2);
         return q;
       };
       auto weights = [&](const Place& q, int it, int slot) {
         uint8_t* st = smem + slot * kStage;
-        mbar_arrive_expect_tx(&full[slot], kStage);
-        tma_load_2d(st + kA, &tm_w, &full[slot], it * 128, rank ? q.w[1] : q.w[0]);
+        const uint32_t bar = map_to_rank(smem_addr(&full[slot]), 0);
+        if (rank == 0) mbar_arrive_expect_tx(&full[slot], 2 * kStage);
+        load_pair(st + kA, &tm_w, bar, it * 128, rank ? q.w[1] : q.w[0]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           // (an odd block of 128 weight rows: what its missing half would be is not read back)
-          const int64_t b = min(static_cast<int64_t>(q.w[i] >> 7), last_w);
-          bulk_load(st + kA + kB + kScalesA + i * 4 * kScaleBlock,
-                    p.w_scales + b * scale_row + it * 4 * kScaleBlock, 4 * kScaleBlock, &full[slot]);
+          const int b = min(q.w[i] >> 7, last_w);
+          load_pair(st + kA + kB + kScalesA + i * 4 * kScaleBlock, &tm_sw, bar, 0, b * scale_row + it * 4);
         }
       };
       auto tokens = [&](const Place& q, int it, int slot) {
         uint8_t* st = smem + slot * kStage;
-        tma_load_2d(st, &tm_a, &full[slot], it * 128, q.m);
-        const int64_t b = min(static_cast<int64_t>(q.m >> 7), last_a);
-        bulk_load(st + kA + kB, p.a_scales + b * scale_row + it * 4 * kScaleBlock, kScalesA, &full[slot]);
+        const uint32_t bar = map_to_rank(smem_addr(&full[slot]), 0);
+        load_pair(st, &tm_a, bar, it * 128, q.m);
+        load_pair(st + kA + kB, &tm_sa, bar, 0, min(q.m >> 7, last_a) * scale_row + it * 4);
       };
       // weights do not wait for the kernel ahead in the stream, tokens do
       const int total = my_tiles * steps, pre = steps < kStages ? steps : kStages;
@@ -214,10 +241,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++it;
         if (++slot == kStages) slot = 0, parity ^= 1u;
       }
-      for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i) {
-        volatile int none = 0;
-        if (!mbar_wait(&full[i % kStages], (i / kStages) & 1, &none)) *abort_flag = 1;
-      }
+      // nothing is left in flight: the second CTA's copies count on the first's barriers,
+      // which waits for the last of them
+      if (rank == 0)
+        for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i) {
+          volatile int none = 0;
+          if (!wait_cluster(&full[i % kStages], (i / kStages) & 1, &none)) *abort_flag = 1;
+        }
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -253,12 +283,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok) commit_pair(&sums_full[i & 1]);
         }
         commit_pair(&done);
-      } else {
-        for (int i = my_tiles * steps; i > 0; --i) {
-          if (!mbar_wait(&full[slot], parity, abort_flag)) break;
-          arrive_first(&full[slot]);
-          if (++slot == kStages) slot = 0, parity ^= 1u;
-        }
       }
       // every product is over before TMEM is given back
       volatile int none = 0;
@@ -273,9 +297,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (the whole warp together: tcgen05.ld follows)
       if (!__all_sync(0xffffffffu, wait_cluster(&sums_full[b], (i >> 1) & 1, abort_flag))) break;
       tc_fence_after_sync();
-      const int tile = pair + i * f.pairs;
-      const int nt = tile / f.token_tiles;
-      const int64_t m = int64_t(tile - nt * f.token_tiles) * kTile + rank * kHalf + 32 * quarter + lane;
+      int mt, nt;
+      tile_at(f, pair + i * f.pairs, mt, nt);
+      const int64_t m = int64_t(mt) * kTile + rank * kHalf + 32 * quarter + lane;
       const uint32_t acc = lanes + (b ? kSecond : 0);
       // the shared columns first; pieces h and h + 2 of their four
       uint32_t first[2][16];
@@ -364,18 +388,24 @@ template <int kMode>
 int run(const Product& p, const Device& d, cudaStream_t stream) {
   static std::atomic<bool> ready[kMaxDevices];
   if (const int st = allow_smem(many_kernel<kMode>, kSmem, d, ready)) return st;
-  CUtensorMap tm_a, tm_w;
-  if (!codes_map(&tm_a, p.a_codes, p.M, p.K, kHalf) || !codes_map(&tm_w, p.w_codes, p.N, p.K, kHalf))
+  CUtensorMap tm_a, tm_w, tm_sa, tm_sw;
+  if (!codes_map(&tm_a, p.a_codes, p.M, p.K, kHalf) || !codes_map(&tm_w, p.w_codes, p.N, p.K, kHalf) ||
+      !scales_map(&tm_sa, p.a_scales, p.M, p.K) || !scales_map(&tm_sw, p.w_scales, p.N, p.K))
     return NVFP4_ERR_LAUNCH;
   const int64_t token_tiles = (p.M + kTile - 1) / kTile;
   const int64_t tiles = token_tiles * ((p.N + kTile - 1) / kTile);
-  if (tiles > (1 << 30) || tiles * (p.K / kStageK) > (int64_t(1) << 37)) return NVFP4_ERR_SHAPE;
+  // tiles, stages and rows of scales are counted in 32 bits
+  if (tiles > (1 << 30) || (std::max(p.M, p.N) + 127) / 128 * (p.K / kMmaK) > INT32_MAX || 
+      (tiles / (d.num_sms / 2) + 1) * (p.K / kStageK) > INT32_MAX)
+    return NVFP4_ERR_SHAPE;
   Many f{};
   f.p = p;
   f.token_tiles = static_cast<int>(token_tiles);
+  f.weight_tiles = static_cast<int>(tiles / token_tiles);
   f.tiles = static_cast<int>(tiles);
   f.pairs = static_cast<int>(tiles < d.num_sms / 2 ? tiles : d.num_sms / 2);
-  return launch(2, many_kernel<kMode>, dim3(2 * f.pairs), dim3(kThreads), kSmem, stream, tm_a, tm_w, f);
+  return launch(2, many_kernel<kMode>, dim3(2 * f.pairs), dim3(kThreads), kSmem, stream, tm_a, tm_w, tm_sa,
+                tm_sw, f);
 }
 
 }  // namespace
