@@ -152,33 +152,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_nvfp4(128, kN);
-      int slot = 0;
-      uint32_t parity = 0;
-      for (int it = 0; it < n_steps; ++it) {
-        if (!wait(&full[slot], parity, abort_flag)) break;
-        tc_fence_after_sync();
-        const uint32_t st = smem_addr(smem + slot * f.stage_bytes);
+    constexpr uint32_t idesc = idesc_nvfp4(128, kN);
+    int slot = 0;
+    uint32_t parity = 0;
+    for (int it = 0; it < n_steps; ++it) {
+      if (!__all_sync(0xffffffffu, wait(&full[slot], parity, abort_flag))) break;
+      tc_fence_after_sync();
+      if (elect_one()) {
+        const uint32_t st = smem_addr(smem) + slot * f.stage_bytes;
+        const uint64_t a = umma_desc_sw128(st), b = umma_desc_sw128(st + w_off);
+        const uint64_t sa = scale_desc(st + sa_off), sb = scale_desc(st + sb_off);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          copy_scales(tmem + kScaleA + 4 * j, scale_desc(st + sa_off + j * kScaleBlock));
+          copy_scales(tmem + kScaleA + 4 * j, sa + j * (kScaleBlock >> 4));
 #pragma unroll
           for (int i = 0; i < kBlocks; ++i)
-            copy_scales(tmem + kScaleB + 4 * (kBlocks * j + i),
-                        scale_desc(st + sb_off + (4 * i + j) * kScaleBlock));
+            copy_scales(tmem + kScaleB + 4 * (kBlocks * j + i), sb + (4 * i + j) * (kScaleBlock >> 4));
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          umma_nvfp4(tmem, umma_desc_sw128(st + 32 * j), umma_desc_sw128(st + w_off + 32 * j), idesc,
-                     tmem + kScaleA + 4 * j, tmem + kScaleB + 4 * kBlocks * j, (it | j) != 0);
+          umma_nvfp4(tmem, a + 2 * j, b + 2 * j, idesc, tmem + kScaleA + 4 * j, tmem + kScaleB + 4 * kBlocks * j,
+                     (it | j) != 0);
         umma_commit(&empty[slot]);
-        if (++slot == f.stages) slot = 0, parity ^= 1u;
       }
-      umma_commit(&done);
-      volatile int none = 0;
-      if (!wait(&done, 0, &none)) *abort_flag = 1;
+      __syncwarp();
+      if (++slot == f.stages) slot = 0, parity ^= 1u;
     }
+    if (elect_one()) umma_commit(&done);
+    __syncwarp();
+    volatile int none = 0;
+    if (!wait(&done, 0, &none)) *abort_flag = 1;
   }
   __syncwarp();
   // the sums go where the stages were, once every product and copy is over

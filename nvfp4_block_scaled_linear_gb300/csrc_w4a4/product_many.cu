@@ -250,44 +250,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    // The whole warp walks the stages, an elected lane issues.
+    if (rank == 0) {
+      constexpr uint32_t idesc = idesc_nvfp4(kTile, kTile);
       int slot = 0;
       uint32_t parity = 0;
       bool ok = true;
-      if (rank == 0) {
-        constexpr uint32_t idesc = idesc_nvfp4(kTile, kTile);
-        for (int i = 0; i < my_tiles && ok; ++i) {
-          // the columns that this tile's sums share with the last one's are read
-          if (i > 0 && !(ok = wait_cluster(&sums_free, (i - 1) & 1, abort_flag))) break;
+      for (int i = 0; i < my_tiles && ok; ++i) {
+        // the columns that this tile's sums share with the last one's are read
+        if (i > 0) ok = __all_sync(0xffffffffu, wait_cluster(&sums_free, (i - 1) & 1, abort_flag));
+        if (!ok) break;
+        tc_fence_after_sync();
+        const uint32_t d = tmem + (i & 1 ? kSecond : 0);
+        for (int it = 0; it < steps; ++it) {
+          ok = __all_sync(0xffffffffu, wait_cluster(&full[slot], parity, abort_flag));
+          if (!ok) break;
           tc_fence_after_sync();
-          const uint32_t d = tmem + (i & 1 ? kSecond : 0);
-          for (int it = 0; it < steps; ++it) {
-            if (!(ok = wait_cluster(&full[slot], parity, abort_flag))) break;
-            tc_fence_after_sync();
-            const uint32_t st = smem_addr(smem + slot * kStage);
+          if (elect_one()) {
+            const uint32_t st = smem_addr(smem) + slot * kStage;
+            const uint64_t a = umma_desc_sw128(st), b = umma_desc_sw128(st + kA);
+            const uint64_t sa = scale_desc(st + kA + kB), sb = scale_desc(st + kA + kB + kScalesA);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              copy_scales_pair(tmem + kColA + 4 * j, scale_desc(st + kA + kB + j * kScaleBlock));
+              copy_scales_pair(tmem + kColA + 4 * j, sa + j * (kScaleBlock >> 4));
 #pragma unroll
               for (int h = 0; h < 2; ++h)
-                copy_scales_pair(tmem + kColB + 8 * j + 4 * h,
-                                 scale_desc(st + kA + kB + kScalesA + (4 * h + j) * kScaleBlock));
+                copy_scales_pair(tmem + kColB + 8 * j + 4 * h, sb + (4 * h + j) * (kScaleBlock >> 4));
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              umma_nvfp4_pair(d, umma_desc_sw128(st + 32 * j), umma_desc_sw128(st + kA + 32 * j), idesc,
-                              tmem + kColA + 4 * j, tmem + kColB + 8 * j, (it | j) != 0);
+              umma_nvfp4_pair(d, a + 2 * j, b + 2 * j, idesc, tmem + kColA + 4 * j, tmem + kColB + 8 * j,
+                              (it | j) != 0);
             commit_pair(&empty[slot]);
-            if (++slot == kStages) slot = 0, parity ^= 1u;
           }
-          if (ok) commit_pair(&sums_full[i & 1]);
+          __syncwarp();
+          if (++slot == kStages) slot = 0, parity ^= 1u;
         }
-        commit_pair(&done);
+        if (ok && elect_one()) commit_pair(&sums_full[i & 1]);
+        __syncwarp();
       }
-      // every product is over before TMEM is given back
-      volatile int none = 0;
-      if (!wait_cluster(&done, 0, &none)) *abort_flag = 1;
+      if (elect_one()) commit_pair(&done);
+      __syncwarp();
     }
+    // every product is over before TMEM is given back
+    volatile int none = 0;
+    if (!wait_cluster(&done, 0, &none)) *abort_flag = 1;
   } else if (warp >= 4) {
     const int quarter = warp & 3, h = (warp - 4) >> 2;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
