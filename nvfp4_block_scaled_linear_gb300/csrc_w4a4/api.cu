@@ -175,7 +175,7 @@ int nvfp4_linear_w4a4(const nvfp4_rows* a, int64_t M, const nvfp4_weight* w, int
   if (out && !swiglu) return NVFP4_ERR_INVALID;
   if (!w->codes || !w->scales) return NVFP4_ERR_INVALID;
   if (misaligned(w->codes) || misaligned(w->scales)) return NVFP4_ERR_MISALIGNED;
-  if (w->segments < 1 || w->segments > nvfp4::kMaxSegments) return NVFP4_ERR_INVALID;
+  if (w->segments < 1 || w->segments > kMaxSegments) return NVFP4_ERR_INVALID;
   int64_t rows = 0;
   for (int i = 0; i < w->segments; ++i) {
     const int64_t n = w->segment_rows[i];
@@ -202,7 +202,7 @@ int nvfp4_linear_w4a4(const nvfp4_rows* a, int64_t M, const nvfp4_weight* w, int
   rows = 0;
   for (int i = 0; i < w->segments; ++i) {
     rows += w->segment_rows[i];
-    p.seg.end[i] = rows;
+    p.seg.end[i] = static_cast<int>(rows);
     p.seg.scale[i] = static_cast<float>(1.0 / (double(a->global_scale) * double(w->global_scale[i])));
   }
   p.swiglu = swiglu != 0;

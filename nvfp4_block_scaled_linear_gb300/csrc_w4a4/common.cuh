@@ -9,11 +9,12 @@
 #include <cstdint>
 
 #include "../../include/nvfp4_w4a4.h"
-#include "../csrc/dequant.cuh"
 #include "../csrc/ptx.cuh"
 
 namespace nvfp4 {
 namespace w4a4 {
+
+constexpr int kMaxSegments = 8;
 
 // Byte of the scale of row r and 16-block b (of K / 16) in the order of
 // nvfp4_w4a4.h: 512-byte blocks of 128 rows x 4 scales.
@@ -113,7 +114,6 @@ __device__ __forceinline__ uint32_t quantize16(const float (&v)[16], float gs, u
 
 // ---------------------------------------------------------------- host side
 constexpr int kMaxDevices = 64;
-
 struct Device {
   int id = 0;
   int num_sms = 0;
@@ -187,13 +187,38 @@ int run_quantize(const Quantize& p, const Device& d, cudaStream_t stream);
 int run_scale_layout(const uint8_t* scale, int64_t N, int64_t K, uint8_t* blocked,
                      unsigned int* refused, const Device& d, cudaStream_t stream);
 
+// Scales of a stacked weight's segments: outputs below end[i] and not below the
+// one before take scale[i].
+struct Segments {
+  int n;
+  int end[kMaxSegments];
+  float scale[kMaxSegments];
+};
+__device__ __forceinline__ float segment_scale(const Segments& s, int col) {
+  float v = s.scale[0];
+#pragma unroll
+  for (int i = 1; i < kMaxSegments; ++i)
+    if (i < s.n && col >= s.end[i - 1]) v = s.scale[i];
+  return v;
+}
+
+// silu(g) * u = g / (1 + 2^(-g log2 e)) * u, exponential and reciprocal by the
+// hardware's approximations (2^-22 and 2^-23 of the value).  Where the exponential
+// overflows (g < -88) the result is a zero; the exact one is below 1e-36.
+__device__ __forceinline__ float gated(float g, float u) {
+  float e, r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return g * r * u;
+}
+
 struct Product {
   const uint8_t* a_codes;
   const uint8_t* a_scales;
   const uint8_t* w_codes;
   const uint8_t* w_scales;
   int64_t M, N, K;
-  SegScales seg;                     // 1 / (the rows' global scale x the segment's)
+  Segments seg;                      // 1 / (the rows' global scale x the segment's)
   int swiglu;
   __nv_bfloat16* y;                  // or null: codes and scales
   uint8_t* codes;

@@ -217,16 +217,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t at = smem_addr(sums + row * kPitch + c);
     float v[16];
     sum16(at, f.split, v);
-    const float s = seg_scale(p.seg, n);
+    const float s = segment_scale(p.seg, static_cast<int>(n));
     if (kMode == kPlain) {
 #pragma unroll
       for (int k = 0; k < 16; ++k) v[k] *= s;
     } else {
       float u[16];
       sum16(at + 128 * 4, f.split, u);
-      const float su = seg_scale(p.seg, n + p.N / 2);
+      const float su = segment_scale(p.seg, static_cast<int>(n + p.N / 2));
 #pragma unroll
-      for (int k = 0; k < 16; ++k) v[k] = silu_mul(v[k] * s, u[k] * su);
+      for (int k = 0; k < 16; ++k) v[k] = gated(v[k] * s, u[k] * su);
     }
     if (kMode == kGatedRows) {
       uint2 codes;

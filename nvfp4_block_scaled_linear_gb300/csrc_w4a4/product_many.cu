@@ -17,8 +17,10 @@
 // Both CTAs' copies count on the first one's barriers, whose thread issues the
 // MMAs; what it has read is free for both by one commit.
 //
-// Warps: 0 copies, 1 issues the MMAs, 2 TMEM allocation, 4..11 the epilogue, two for each quarter of
-// the lanes, taking every other piece of 16 columns.
+// Warps: 0 copies, 1 issues the MMAs, 2 TMEM allocation, 4..19 the epilogue, four for each quarter of
+// the lanes, taking every fourth piece of 16 columns: a piece's chain (TMEM, the
+// exponentials, the quantisation, the store) is long, and 16 warps hide it where 8
+// took longer than the products.
 #include <algorithm>
 
 #include "product.cuh"
@@ -27,8 +29,8 @@ namespace nvfp4 {
 namespace w4a4 {
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kEpilogueWarps = 8;
+constexpr int kThreads = 640;
+constexpr int kEpilogueWarps = 16;
 constexpr int kTile = 256;                       // tokens and weight rows of a pair's tile
 constexpr int kHalf = 128;
 constexpr int kA = kHalf * 128, kB = kHalf * 128;                 // bytes of codes a stage
@@ -308,46 +310,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       tile_at(f, pair + i * f.pairs, mt, nt);
       const int64_t m = int64_t(mt) * kTile + rank * kHalf + 32 * quarter + lane;
       const uint32_t acc = lanes + (b ? kSecond : 0);
-      // the shared columns first; pieces h and h + 2 of their four
-      uint32_t first[2][16];
-      tmem_ld_16cols(lanes + kSecond + 16 * h, first[0]);
-      tmem_ld_16cols(lanes + kSecond + 32 + 16 * h, first[1]);
-      tmem_ld_wait();
+      // the shared columns first: piece h of their four
+      float first[16];
+      load16(lanes + kSecond + 16 * h, first);
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) arrive_first(&sums_free);
       const bool inside = m < p.M;
       if (kMode == kPlain) {
         auto out = [&](int piece, float (&v)[16]) {
-          const int64_t n = int64_t(nt) * kTile + piece * 16;
+          const int n = nt * kTile + piece * 16;
           if (!inside || n >= p.N) return;
-          const float s = seg_scale(p.seg, n);
+          const float s = segment_scale(p.seg, n);
 #pragma unroll
           for (int k = 0; k < 16; ++k) v[k] *= s;
-          store_bf16(p.y + m * n_out + n, v);
+          store_bf16(p.y + m * p.N + n, v);
         };
+        out((b ? 0 : 12) + h, first);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float v[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(first[j][k]);
-          out((b ? 0 : 12) + 2 * j + h, v);
-        }
-#pragma unroll 2
-        for (int j = 0; j < 6; ++j) {
-          const int piece = (b ? 4 : 0) + 2 * j + h;
-          float v[16];
-          load16(acc + 16 * piece, v);
-          out(piece, v);
+        for (int j = 0; j < 3; ++j) {
+          const int piece = (b ? 4 : 0) + 4 * j + h;
+          load16(acc + 16 * piece, first);
+          out(piece, first);
         }
       } else {
         auto out = [&](int piece, const float (&g)[16], const float (&u)[16]) {
-          const int64_t n = int64_t(nt) * kHalf + piece * 16;
+          const int n = nt * kHalf + piece * 16;
           if (!inside) return;
-          const float sg = seg_scale(p.seg, n), su = seg_scale(p.seg, n + p.N / 2);
+          const float sg = segment_scale(p.seg, n), su = segment_scale(p.seg, n + static_cast<int>(n_out));
           float v[16];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) v[k] = silu_mul(g[k] * sg, u[k] * su);
+          for (int k = 0; k < 16; ++k) v[k] = gated(g[k] * sg, u[k] * su);
           if (kMode == kGatedRows) {
             uint2 codes;
             p.scales[scale_at(m, n >> 4, n_out)] = static_cast<uint8_t>(quantize16(v, p.out_gs, codes));
@@ -356,28 +349,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             store_bf16(p.y + m * n_out + n, v);
           }
         };
-        // what was read first: of the first sums the up halves of pieces 4..7, of the
-        // second the gate halves of pieces 0..3
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int piece = (b ? 0 : 4) + 2 * j + h;
-          float x[16], o[16];
-          load16(acc + 16 * piece + (b ? kHalf : 0), o);
-#pragma unroll
-          for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(first[j][k]);
-          if (b)
-            out(piece, x, o);
-          else
-            out(piece, o, x);
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int piece = (b ? 4 : 0) + 2 * j + h;
-          float g[16], u[16];
-          load16(acc + 16 * piece, g);
-          load16(acc + 16 * piece + kHalf, u);
-          out(piece, g, u);
-        }
+        // what was read first: of the first sums the up half of pieces 4..7, of the
+        // second the gate half of pieces 0..3
+        float other[16];
+        load16(acc + 16 * ((b ? 0 : 4) + h) + (b ? kHalf : 0), other);
+        if (b)
+          out(h, first, other);
+        else
+          out(4 + h, other, first);
+        const int piece = (b ? 4 : 0) + h;
+        load16(acc + 16 * piece, first);
+        load16(acc + 16 * piece + kHalf, other);
+        out(piece, first, other);
       }
       // (read before the tile after next is begun: its sums_free comes later)
       tc_fence_before_sync();
