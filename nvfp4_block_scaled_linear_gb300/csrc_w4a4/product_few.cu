@@ -110,46 +110,53 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) griddep_launch_dependents();
 
   if (warp == 0) {
-    if (lane == 0) {
+    // the whole warp walks the stages, an elected lane issues
+    auto weights = [&](int it, int slot) {
+      uint8_t* st = smem + slot * f.stage_bytes;
+      mbar_arrive_expect_tx(&full[slot], f.stage_bytes);
+#pragma unroll
+      for (int i = 0; i < kBlocks; ++i) {
+        tma_load_2d(st + w_off + i * 128 * 128, &tm_w, &full[slot], (s0 + it) * 128, w_row(i));
+        bulk_load(st + sb_off + i * 4 * kScaleBlock,
+                  p.w_scales + (int64_t(w_row(i) / 128) * (p.K / kMmaK) + (s0 + it) * 4) * kScaleBlock,
+                  4 * kScaleBlock, &full[slot]);
+      }
+    };
+    auto tokens = [&](int it, int slot) {
+      uint8_t* st = smem + slot * f.stage_bytes;
+      tma_load_2d(st, &tm_a, &full[slot], (s0 + it) * 128, m0);
+      bulk_load(st + sa_off,
+                p.a_scales + (int64_t(blockIdx.y) * (p.K / kMmaK) + (s0 + it) * 4) * kScaleBlock,
+                4 * kScaleBlock, &full[slot]);
+    };
+    // weights do not wait for the kernel ahead in the stream, tokens do
+    const int pre = n_steps < f.stages ? n_steps : f.stages;
+    if (elect_one()) {
       prefetch_tensormap(&tm_a);
       prefetch_tensormap(&tm_w);
-      auto weights = [&](int it, int slot) {
-        uint8_t* st = smem + slot * f.stage_bytes;
-        mbar_arrive_expect_tx(&full[slot], f.stage_bytes);
-#pragma unroll
-        for (int i = 0; i < kBlocks; ++i) {
-          tma_load_2d(st + w_off + i * 128 * 128, &tm_w, &full[slot], (s0 + it) * 128, w_row(i));
-          bulk_load(st + sb_off + i * 4 * kScaleBlock,
-                    p.w_scales + (int64_t(w_row(i) / 128) * (p.K / kMmaK) + (s0 + it) * 4) * kScaleBlock,
-                    4 * kScaleBlock, &full[slot]);
-        }
-      };
-      auto tokens = [&](int it, int slot) {
-        uint8_t* st = smem + slot * f.stage_bytes;
-        tma_load_2d(st, &tm_a, &full[slot], (s0 + it) * 128, m0);
-        bulk_load(st + sa_off,
-                  p.a_scales + (int64_t(blockIdx.y) * (p.K / kMmaK) + (s0 + it) * 4) * kScaleBlock,
-                  4 * kScaleBlock, &full[slot]);
-      };
-      // weights do not wait for the kernel ahead in the stream, tokens do
-      const int pre = n_steps < f.stages ? n_steps : f.stages;
       for (int it = 0; it < pre; ++it) weights(it, it);
-      griddep_wait();
+    }
+    __syncwarp();
+    griddep_wait();
+    if (elect_one())
       for (int it = 0; it < pre; ++it) tokens(it, it);
-      int issued = pre, slot = pre == f.stages ? 0 : pre;
-      uint32_t parity = 0;
-      for (int it = pre; it < n_steps; ++it) {
-        if (!wait(&empty[slot], parity, abort_flag)) break;
+    __syncwarp();
+    int issued = pre, slot = pre == f.stages ? 0 : pre;
+    uint32_t parity = 0;
+    for (int it = pre; it < n_steps; ++it) {
+      if (!__all_sync(0xffffffffu, wait(&empty[slot], parity, abort_flag))) break;
+      if (elect_one()) {
         weights(it, slot);
         tokens(it, slot);
-        ++issued;
-        if (++slot == f.stages) slot = 0, parity ^= 1u;
       }
-      // nothing is left in flight, whatever became of the others
-      for (int it = issued > f.stages ? issued - f.stages : 0; it < issued; ++it) {
-        volatile int none = 0;
-        if (!wait(&full[it % f.stages], (it / f.stages) & 1, &none)) *abort_flag = 1;
-      }
+      __syncwarp();
+      ++issued;
+      if (++slot == f.stages) slot = 0, parity ^= 1u;
+    }
+    // nothing is left in flight, whatever became of the others
+    for (int it = issued > f.stages ? issued - f.stages : 0; it < issued; ++it) {
+      volatile int none = 0;
+      if (!wait(&full[it % f.stages], (it / f.stages) & 1, &none)) *abort_flag = 1;
     }
   } else if (warp == 1) {
     constexpr uint32_t idesc = idesc_nvfp4(128, kN);

@@ -70,35 +70,12 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
       : "memory");
 }
 __device__ __forceinline__ void arrive_first(uint64_t* bar) {     // on the first CTA's barrier
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+  // (release in the CTA only: what is handed back is TMEM, ordered by the tcgen05
+  // fence; a release in the cluster waits for the stores of the last tile)
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(
                    map_to_rank(smem_addr(bar), 0))
                : "memory");
 }
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_addr(bar)), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-// wait() for arrivals from the other CTA.
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  if (try_wait_cluster(bar, parity)) return true;
-  const uint32_t t0 = static_cast<uint32_t>(clock());
-#pragma unroll 1
-  while (!try_wait_cluster(bar, parity)) {
-    if (*abort_flag || static_cast<uint32_t>(clock()) - t0 > 0x7FFFFFFFu) {
-      *abort_flag = 1;
-      return false;
-    }
-  }
-  return true;
-}
-
 // A copy into this CTA's shared memory that counts on the first CTA's barrier.
 __device__ __forceinline__ void load_pair(void* dst, const CUtensorMap* map, uint32_t first_bar, int32_t c0,
                                           int32_t c1) {
@@ -188,69 +165,79 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) griddep_launch_dependents();
 
   if (warp == 0) {
-    if (lane == 0) {
+    // The whole warp walks the tiles, an elected lane issues.
+    // blocks of scales that there are
+    const int last_a = static_cast<int>((p.M - 1) / 128), last_w = static_cast<int>(p.N / 128) - 1;
+    // place of a tile: token row of this CTA's half, its weight rows, the first rows of
+    // the scales of its tokens and of either half of the weight rows
+    struct Place {
+      int tile, m, w, sa, sw[2];
+    };
+    auto place = [&](int tile) {
+      Place q;
+      int m, n;
+      tile_at(f, tile, m, n);
+      q.tile = tile;
+      q.m = m * kTile + rank * kHalf;
+      const int w0 = kMode == kPlain ? n * kTile : n * kHalf;
+      const int w1 = kMode == kPlain ? w0 + kHalf : w0 + static_cast<int>(p.N / 2);
+      q.w = rank ? w1 : w0;
+      q.sa = min(q.m >> 7, last_a) * scale_row;
+      // (an odd block of 128 weight rows: what its missing half would be is not read back)
+      q.sw[0] = (w0 >> 7) * scale_row;
+      q.sw[1] = min(w1 >> 7, last_w) * scale_row;
+      return q;
+    };
+    const uint32_t first_full = map_to_rank(smem_addr(full), 0);
+    auto weights = [&](const Place& q, int it, int slot) {
+      uint8_t* st = smem + slot * kStage;
+      const uint32_t bar = first_full + 8 * slot;
+      if (rank == 0) mbar_arrive_expect_tx(&full[slot], 2 * kStage);
+      load_pair(st + kA, &tm_w, bar, it * 128, q.w);
+      load_pair(st + kA + kB + kScalesA, &tm_sw, bar, 0, q.sw[0] + it * 4);
+      load_pair(st + kA + kB + kScalesA + kScalesB / 2, &tm_sw, bar, 0, q.sw[1] + it * 4);
+    };
+    auto tokens = [&](const Place& q, int it, int slot) {
+      uint8_t* st = smem + slot * kStage;
+      const uint32_t bar = first_full + 8 * slot;
+      load_pair(st, &tm_a, bar, it * 128, q.m);
+      load_pair(st + kA + kB, &tm_sa, bar, 0, q.sa + it * 4);
+    };
+    // weights do not wait for the kernel ahead in the stream, tokens do
+    const int total = my_tiles * steps, pre = steps < kStages ? steps : kStages;
+    Place q = place(pair);
+    if (elect_one()) {
       prefetch_tensormap(&tm_a);
       prefetch_tensormap(&tm_w);
-      // blocks of scales that there are
-      const int last_a = static_cast<int>((p.M - 1) / 128), last_w = static_cast<int>(p.N / 128) - 1;
       prefetch_tensormap(&tm_sa);
       prefetch_tensormap(&tm_sw);
-      // place of a tile: token row of this CTA's half, weight row of either half
-      struct Place {
-        int tile, m, w[2];
-      };
-      auto place = [&](int tile) {
-        Place q;
-        q.tile = tile;
-        int m, n;
-        tile_at(f, tile, m, n);
-        q.m = m * kTile + rank * kHalf;
-        q.w[0] = kMode == kPlain ? n * kTile : n * kHalf;
-        q.w[1] = kMode == kPlain ? q.w[0] + kHalf : q.w[0] + static_cast<int>(p.N / 2);
-        return q;
-      };
-      auto weights = [&](const Place& q, int it, int slot) {
-        uint8_t* st = smem + slot * kStage;
-        const uint32_t bar = map_to_rank(smem_addr(&full[slot]), 0);
-        if (rank == 0) mbar_arrive_expect_tx(&full[slot], 2 * kStage);
-        load_pair(st + kA, &tm_w, bar, it * 128, rank ? q.w[1] : q.w[0]);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          // (an odd block of 128 weight rows: what its missing half would be is not read back)
-          const int b = min(q.w[i] >> 7, last_w);
-          load_pair(st + kA + kB + kScalesA + i * 4 * kScaleBlock, &tm_sw, bar, 0, b * scale_row + it * 4);
-        }
-      };
-      auto tokens = [&](const Place& q, int it, int slot) {
-        uint8_t* st = smem + slot * kStage;
-        const uint32_t bar = map_to_rank(smem_addr(&full[slot]), 0);
-        load_pair(st, &tm_a, bar, it * 128, q.m);
-        load_pair(st + kA + kB, &tm_sa, bar, 0, min(q.m >> 7, last_a) * scale_row + it * 4);
-      };
-      // weights do not wait for the kernel ahead in the stream, tokens do
-      const int total = my_tiles * steps, pre = steps < kStages ? steps : kStages;
-      Place q = place(pair);
       for (int it = 0; it < pre; ++it) weights(q, it, it);
-      griddep_wait();
+    }
+    __syncwarp();
+    griddep_wait();
+    if (elect_one())
       for (int it = 0; it < pre; ++it) tokens(q, it, it);
-      int issued = pre, slot = pre == kStages ? 0 : pre, it = pre;
-      uint32_t parity = pre == kStages ? 0 : 1;                  // (slots not used yet are free)
-      for (; issued < total; ++issued) {
-        if (it == steps) it = 0, q = place(q.tile + f.pairs);
-        if (!wait_cluster(&empty[slot], parity, abort_flag)) break;
+    __syncwarp();
+    int issued = pre, slot = pre == kStages ? 0 : pre, it = pre;
+    uint32_t parity = pre == kStages ? 0 : 1;                    // (slots not used yet are free)
+    for (; issued < total; ++issued) {
+      if (it == steps) it = 0, q = place(q.tile + f.pairs);
+      if (!__all_sync(0xffffffffu, wait(&empty[slot], parity, abort_flag))) break;
+      if (elect_one()) {
         weights(q, it, slot);
         tokens(q, it, slot);
-        ++it;
-        if (++slot == kStages) slot = 0, parity ^= 1u;
       }
-      // nothing is left in flight: the second CTA's copies count on the first's barriers,
-      // which waits for the last of them
-      if (rank == 0)
-        for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i) {
-          volatile int none = 0;
-          if (!wait_cluster(&full[i % kStages], (i / kStages) & 1, &none)) *abort_flag = 1;
-        }
+      __syncwarp();
+      ++it;
+      if (++slot == kStages) slot = 0, parity ^= 1u;
     }
+    // nothing is left in flight: the second CTA's copies count on the first's barriers,
+    // which waits for the last of them
+    if (rank == 0)
+      for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i) {
+        volatile int none = 0;
+        if (!wait(&full[i % kStages], (i / kStages) & 1, &none)) *abort_flag = 1;
+      }
   } else if (warp == 1) {
     // The whole warp walks the stages, an elected lane issues.
     if (rank == 0) {
@@ -260,12 +247,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int i = 0; i < my_tiles && ok; ++i) {
         // the columns that this tile's sums share with the last one's are read
-        if (i > 0) ok = __all_sync(0xffffffffu, wait_cluster(&sums_free, (i - 1) & 1, abort_flag));
+        if (i > 0) ok = __all_sync(0xffffffffu, wait(&sums_free, (i - 1) & 1, abort_flag));
         if (!ok) break;
         tc_fence_after_sync();
         const uint32_t d = tmem + (i & 1 ? kSecond : 0);
         for (int it = 0; it < steps; ++it) {
-          ok = __all_sync(0xffffffffu, wait_cluster(&full[slot], parity, abort_flag));
+          ok = __all_sync(0xffffffffu, wait(&full[slot], parity, abort_flag));
           if (!ok) break;
           tc_fence_after_sync();
           if (elect_one()) {
@@ -296,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // every product is over before TMEM is given back
     volatile int none = 0;
-    if (!wait_cluster(&done, 0, &none)) *abort_flag = 1;
+    if (!wait(&done, 0, &none)) *abort_flag = 1;
   } else if (warp >= 4) {
     const int quarter = warp & 3, h = (warp - 4) >> 2;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
@@ -304,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < my_tiles; ++i) {
       const int b = i & 1;
       // (the whole warp together: tcgen05.ld follows)
-      if (!__all_sync(0xffffffffu, wait_cluster(&sums_full[b], (i >> 1) & 1, abort_flag))) break;
+      if (!__all_sync(0xffffffffu, wait(&sums_full[b], (i >> 1) & 1, abort_flag))) break;
       tc_fence_after_sync();
       int mt, nt;
       tile_at(f, pair + i * f.pairs, mt, nt);
