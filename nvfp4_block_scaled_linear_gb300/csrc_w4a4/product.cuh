@@ -77,6 +77,15 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
+// 16 outputs, rounded to bf16.
+__device__ __forceinline__ void store_bf16(__nv_bfloat16* y, const float (&v)[16]) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    reinterpret_cast<uint4*>(y)[k] =
+        make_uint4(f32x2_to_bf16x2(v[8 * k], v[8 * k + 1]), f32x2_to_bf16x2(v[8 * k + 2], v[8 * k + 3]),
+                   f32x2_to_bf16x2(v[8 * k + 4], v[8 * k + 5]), f32x2_to_bf16x2(v[8 * k + 6], v[8 * k + 7]));
+}
+
 // Tensor map of codes [rows, K/2], boxes of `box` rows by 128 bytes.
 bool codes_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t K, int box);
 

@@ -9,12 +9,13 @@
 // Where there are few tokens the tokens' box is only as high as they are, and
 // the MMA's other rows read whatever follows in the stage.
 //
-// A CTA leaves its sums in its own shared memory, [token][column], and, after a
-// cluster barrier, the threads of the cluster take pieces of 16 outputs each,
-// adding the CTAs' sums in their order: no atomics, the same bits on every run.
+// The outputs of a tile are shared out over the cluster in pieces of 16 columns:
+// each CTA stores its sums of a piece in its owner's shared memory, and the owner
+// adds the CTAs' sums in their order: no atomics, the same bits on every run.
 //
-// Warps: 0 copies, 1 MMA, 2 TMEM allocation, 4..7 read the accumulator; all
-// eight write the outputs.
+// Warps: 0 copies, 1 MMA, 2 TMEM allocation; all eight the outputs.
+#include <algorithm>
+
 #include "product.cuh"
 
 namespace nvfp4 {
@@ -22,7 +23,7 @@ namespace w4a4 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kSmem = 227 * 1024;
+constexpr int kAllSmem = 226 * 1024, kHalfSmem = 112 * 1024;
 constexpr int kMaxStages = 12;
 constexpr int kMaxSplit = 8;
 
@@ -32,27 +33,38 @@ struct Few {
   Product p;
   int a_rows;        // rows of a box of tokens
   int split;         // CTAs of a cluster
-  int stages, stage_bytes;
+  int stages, stage_bytes, smem;
 };
 
-__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
+__device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, const float* v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3])
                : "memory");
-  return v;
 }
 
-// The cluster's sums of 16 columns, in the CTAs' order.
-__device__ __forceinline__ void sum16(uint32_t local, int split, float (&v)[16]) {
+// Bytes of the sums that an owner gathers: of every CTA its pieces of the rows.
+constexpr int sums_bytes(int n, int out, int split, int rows) {
+  return split * ((out / 16 + split - 1) / split) * (n / out) * ((rows + 31) / 32 * 32) * 64;
+}
+
+// Where the sums lie in their owner: [CTA][piece of the owner's][four columns][row],
+// so that a warp, a row a lane, stores and loads 512 bytes together.
+struct Sums {
+  int rows;          // of whole warps
+  int pieces;        // of one owner, at most
+  __device__ __forceinline__ uint32_t at(int cta, int piece, int row) const {
+    return static_cast<uint32_t>(((cta * pieces + piece) * 4 * rows + row) * 16);
+  }
+};
+
+// The sum over the CTAs, in their order, of the 16 columns at `at`.
+__device__ __forceinline__ void sum16(const uint8_t* at, int split, int cta_bytes, int four_bytes, float (&v)[16]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = 0.f;
   for (int q = 0; q < split; ++q) {
-    const uint32_t at = map_to_rank(local, q);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 f = ld_cluster_f32x4(at + 16 * i);
+      const float4 f = *reinterpret_cast<const float4*>(at + q * cta_bytes + i * four_bytes);
       v[4 * i] += f.x, v[4 * i + 1] += f.y, v[4 * i + 2] += f.z, v[4 * i + 3] += f.w;
     }
   }
@@ -65,7 +77,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kBlocks = kN / 128;                       // blocks of 128 weight rows
   constexpr uint32_t kCols = kN == 256 ? 512 : 256;       // TMEM: sums, then scales
   constexpr uint32_t kScaleA = kN, kScaleB = kN + 16;     // 4 columns per 64 k and 128 rows
-  constexpr int kPitch = kN + 4;                          // floats of a row of sums
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done;
   __shared__ int abort_word;
@@ -191,87 +202,114 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!wait(&done, 0, &none)) *abort_flag = 1;
   }
   __syncwarp();
-  // the sums go where the stages were, once every product and copy is over
+  // every product and copy of the cluster is over
   tc_fence_before_sync();
-  __syncthreads();
-  tc_fence_after_sync();
-  float* sums = reinterpret_cast<float*>(smem);
-  if (warp >= 4 && (warp - 4) * 32 < rows) {
-    const int row = (warp - 4) * 32 + lane;
-    for (int c = 0; c < kN; c += 32) {
-      uint32_t v[32];
-      tmem_ld_32cols(tmem + (static_cast<uint32_t>((warp - 4) * 32) << 16) + c, v);
-      tmem_ld_wait();
-      if (row < rows)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          reinterpret_cast<uint4*>(sums + row * kPitch + c)[i] =
-              make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    }
-  }
   if (f.split > 1)
     cluster_sync();
   else
     __syncthreads();
-
+  tc_fence_after_sync();
   constexpr int kOut = kMode == kPlain ? kN : 128;        // outputs of a row of the tile
-  constexpr int kPieces = kOut / 16;
-  const int pieces = (kPieces - rank + f.split - 1) / f.split;      // this CTA's: rank, rank + split, ...
-  const int64_t n_out = kMode == kPlain ? p.N : p.N / 2;
-  for (int i = threadIdx.x; i < rows * pieces; i += kThreads) {
-    const int row = i / pieces, c = (rank + (i - row * pieces) * f.split) * 16;
-    const int64_t m = m0 + row, n = int64_t(tile) * kOut + c;
-    const uint32_t at = smem_addr(sums + row * kPitch + c);
-    float v[16];
-    sum16(at, f.split, v);
-    const float s = segment_scale(p.seg, static_cast<int>(n));
+  constexpr int kPieces = kOut / 16, kParts = kN / kOut;  // parts of an output: its sum, or gate and up
+  const int n_out = static_cast<int>(kMode == kPlain ? p.N : p.N / 2);
+  // 16 outputs of a row, from the sums of their parts
+  auto out = [&](int row, int piece, float (&v)[kParts][16]) {
+    const int64_t m = m0 + row;
+    const int n = tile * kOut + piece * 16;
+    const float s = segment_scale(p.seg, n);
     if (kMode == kPlain) {
 #pragma unroll
-      for (int k = 0; k < 16; ++k) v[k] *= s;
+      for (int k = 0; k < 16; ++k) v[0][k] *= s;
     } else {
-      float u[16];
-      sum16(at + 128 * 4, f.split, u);
-      const float su = segment_scale(p.seg, static_cast<int>(n + p.N / 2));
+      const float su = segment_scale(p.seg, n + n_out);
 #pragma unroll
-      for (int k = 0; k < 16; ++k) v[k] = gated(v[k] * s, u[k] * su);
+      for (int k = 0; k < 16; ++k) v[0][k] = gated(v[0][k] * s, v[kParts - 1][k] * su);
     }
     if (kMode == kGatedRows) {
       uint2 codes;
-      p.scales[scale_at(m, n >> 4, n_out)] = static_cast<uint8_t>(quantize16(v, p.out_gs, codes));
+      p.scales[scale_at(m, n >> 4, n_out)] = static_cast<uint8_t>(quantize16(v[0], p.out_gs, codes));
       *reinterpret_cast<uint2*>(p.codes + m * (n_out >> 1) + (n >> 1)) = codes;
     } else {
-      uint4* y = reinterpret_cast<uint4*>(p.y + m * n_out + n);
+      store_bf16(p.y + m * n_out + n, v[0]);
+    }
+  };
+  // two warps for each quarter of the lanes, taking pieces in turn
+  const int quarter = warp & 3, row = quarter * 32 + lane;
+  const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+  auto load = [&](int piece, float (&v)[kParts][16]) {
+    uint32_t r[kParts][16];
+    __syncwarp();
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        y[k] = make_uint4(f32x2_to_bf16x2(v[8 * k], v[8 * k + 1]), f32x2_to_bf16x2(v[8 * k + 2], v[8 * k + 3]),
-                          f32x2_to_bf16x2(v[8 * k + 4], v[8 * k + 5]),
-                          f32x2_to_bf16x2(v[8 * k + 6], v[8 * k + 7]));
+    for (int part = 0; part < kParts; ++part) tmem_ld_16cols(lanes + 16 * piece + kOut * part, r[part]);
+    tmem_ld_wait();
+#pragma unroll
+    for (int part = 0; part < kParts; ++part)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[part][i] = __uint_as_float(r[part][i]);
+  };
+  if (f.split == 1) {
+    if (quarter * 32 < rows)
+      for (int piece = warp >> 2; piece < kPieces; piece += 2) {
+        float v[kParts][16];
+        load(piece, v);
+        if (row < rows) out(row, piece, v);
+      }
+  } else {
+    Sums sums;
+    sums.rows = (rows + 31) & ~31;
+    sums.pieces = (kPieces + f.split - 1) / f.split * kParts;
+    if (quarter * 32 < rows) {
+      const uint32_t here = smem_addr(smem) + sums.at(rank, 0, row);
+      for (int q = 0; q < f.split; ++q) {
+        const uint32_t to = map_to_rank(here, q);
+        int mine = 0;
+        for (int piece = q; piece < kPieces; piece += f.split, ++mine) {
+          if ((piece & 1) != warp >> 2) continue;
+          float v[kParts][16];
+          load(piece, v);
+          if (row < rows)
+#pragma unroll
+            for (int part = 0; part < kParts; ++part)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                st_cluster_f32x4(to + ((mine * kParts + part) * 4 + i) * sums.rows * 16, v[part] + 4 * i);
+        }
+      }
+    }
+    cluster_sync();
+    const int pieces = (kPieces - rank + f.split - 1) / f.split;    // this CTA's: rank, rank + split, ...
+    const int cta_bytes = sums.pieces * sums.rows * 64, four_bytes = sums.rows * 16;
+    for (int i = threadIdx.x; i < sums.rows * pieces; i += kThreads) {
+      const int mine = i / sums.rows, r = i - mine * sums.rows;
+      if (r >= rows) continue;
+      float v[kParts][16];
+#pragma unroll
+      for (int part = 0; part < kParts; ++part)
+        sum16(smem + sums.at(0, mine * kParts + part, r), f.split, cta_bytes, four_bytes, v[part]);
+      out(r, rank + mine * f.split, v);
     }
   }
   if (*abort_flag && threadIdx.x == 0) atomicOr(p.err, NVFP4_W4A4_TIMEOUT);
-  // (peers may still be reading this CTA's sums)
-  if (f.split > 1)
-    cluster_sync();
-  else
-    __syncthreads();
+  tc_fence_before_sync();
+  __syncthreads();
   if (warp == 2) tmem_dealloc(tmem, kCols);
 }
 
 template <int kN, int kMode>
 int run(Few f, const Device& d, cudaStream_t stream) {
   static std::atomic<bool> ready[kMaxDevices];
-  if (const int st = allow_smem(few_kernel<kN, kMode>, kSmem - 1024, d, ready)) return st;
+  if (const int st = allow_smem(few_kernel<kN, kMode>, kAllSmem, d, ready)) return st;
   CUtensorMap tm_a, tm_w;
   if (!codes_map(&tm_a, f.p.a_codes, f.p.M, f.p.K, f.a_rows) ||
       !codes_map(&tm_w, f.p.w_codes, f.p.N, f.p.K, 128))
     return NVFP4_ERR_LAUNCH;
-  f.stage_bytes = f.a_rows * 128 + kN * 128 + 4 * kScaleBlock * (1 + kN / 128);
-  f.stages = (kSmem - 1024 - 1024) / f.stage_bytes;
-  if (f.stages > kMaxStages) f.stages = kMaxStages;
+  if (f.stages < 1 || f.split < 1 || f.split > kMaxSplit ||
+      (f.split > 1 && sums_bytes(kN, 128, f.split, f.a_rows) > f.smem - 1024))
+    return NVFP4_ERR_LAUNCH;
   const unsigned tiles = static_cast<unsigned>(f.p.N / (kMode == kPlain ? kN : 256));
   return launch(f.split, few_kernel<kN, kMode>,
                 dim3(tiles * f.split, static_cast<unsigned>((f.p.M + 127) / 128)), dim3(kThreads),
-                kSmem - 1024, stream, tm_a, tm_w, f);
+                f.smem, stream, tm_a, tm_w, f);
 }
 
 }  // namespace
@@ -281,10 +319,21 @@ int run_product_few(const Product& p, const Device& d, cudaStream_t stream) {
   f.p = p;
   f.a_rows = p.M >= 128 ? 128 : static_cast<int>((p.M + 7) / 8 * 8);
   const int64_t steps = p.K / kStageK, token_tiles = (p.M + 127) / 128;
-  const int64_t tiles = p.N / (p.swiglu ? 256 : 128) * token_tiles;
-  int64_t split = d.num_sms / tiles;
-  split = split < 1 ? 1 : split > kMaxSplit ? kMaxSplit : split;
-  f.split = static_cast<int>(split < steps ? split : steps);
+  const int n = p.swiglu ? 256 : 128;
+  f.stage_bytes = f.a_rows * 128 + n * 128 + 4 * kScaleBlock * (1 + n / 128);
+  int64_t split = d.num_sms / (p.N / n * token_tiles);
+  f.split = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({split, kMaxSplit, steps})));
+  // With half of an SM's shared memory the next kernel's CTAs are resident, with their
+  // first stages on the way, before this one's end; with all of it the ring is twice as
+  // deep.  One token: 10 steps over 8192 rows 7.9 us against 8.4, 23 steps over 5120
+  // 13.0 against 12.4; 128 tokens (stages half as many): 3 steps 10.4 against 13.5, 8
+  // steps 11.5 against 9.1.  A gated tile takes all of TMEM and is alone in any case.
+  const int half = (kHalfSmem - 1024) / f.stage_bytes;
+  f.smem = n == 256 || steps / f.split > 2 * half ? kAllSmem : kHalfSmem;
+  // the sums lie where the stages were (an odd split leaves its owners unequal pieces,
+  // and their sums more room)
+  while (f.split > 1 && sums_bytes(n, 128, f.split, f.a_rows) > f.smem - 1024) --f.split;
+  f.stages = std::min((f.smem - 1024) / f.stage_bytes, kMaxStages);
   if (!p.swiglu) return run<128, kPlain>(f, d, stream);
   return p.codes ? run<256, kGatedRows>(f, d, stream) : run<256, kGated>(f, d, stream);
 }

@@ -111,14 +111,6 @@ __device__ __forceinline__ void load16(uint32_t tmem, float (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-__device__ __forceinline__ void store_bf16(__nv_bfloat16* y, const float (&v)[16]) {
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
-    reinterpret_cast<uint4*>(y)[k] =
-        make_uint4(f32x2_to_bf16x2(v[8 * k], v[8 * k + 1]), f32x2_to_bf16x2(v[8 * k + 2], v[8 * k + 3]),
-                   f32x2_to_bf16x2(v[8 * k + 4], v[8 * k + 5]), f32x2_to_bf16x2(v[8 * k + 6], v[8 * k + 7]));
-}
-
 template <int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
     many_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,

@@ -79,21 +79,24 @@ def w4a4_error(clear: bool = True) -> int:
     return bits.value
 
 
-def _call(function, device, stream, *args):
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
+def _call(name, device, stream, *args):
     """One library call on `stream` (the device's current one by default)."""
     index = device.index
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(index)
+        stream = _raw_stream(index)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    f = getattr(_ready or _library(), function)
-    if index == torch._C._cuda_getDevice():
+    f = getattr(_ready or _library(), name)
+    if index == _current_device():
         st = f(*args, stream)
     else:
         with torch.cuda.device(device):
             st = f(*args, stream)
-    if st != OK:
-        raise Nvfp4Error(st, function)
+    if st:
+        raise Nvfp4Error(st, name)
 
 
 def _scale(value, name):
