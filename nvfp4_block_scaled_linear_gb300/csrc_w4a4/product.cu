@@ -46,7 +46,13 @@ bool scales_map(CUtensorMap* map, const uint8_t* scales, int64_t rows, int64_t K
 }
 
 int run_product(const Product& p, const Device& d, cudaStream_t stream) {
-  return p.M > 128 ? run_product_many(p, d, stream) : run_product_few(p, d, stream);
+  // The kernel for few tokens takes up to 128 by 128 weight rows (of a pair 256) a CTA
+  // and is the faster one as long as every CTA has an SM; beyond that the pairs' 256 by
+  // 256 tiles read half as much.  128 tokens by 5120 rows and 17408 k 14.1 us against
+  // 26.6, 384 24.3 against 27.1; 515 33.5 against 27.8; gated 130 by 12288 and 2048 k
+  // 8.1 against 8.9, by 34816 and 5120 k 34.0 against 22.1.
+  const int64_t few = (p.M + 127) / 128 * (p.N / (p.swiglu ? 256 : 128));
+  return p.M <= 128 || few <= d.num_sms ? run_product_few(p, d, stream) : run_product_many(p, d, stream);
 }
 
 }  // namespace w4a4

@@ -43,8 +43,9 @@ __device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, const float* v) 
 }
 
 // Bytes of the sums that an owner gathers: of every CTA its pieces of the rows.
-constexpr int sums_bytes(int n, int out, int split, int rows) {
-  return split * ((out / 16 + split - 1) / split) * (n / out) * ((rows + 31) / 32 * 32) * 64;
+constexpr int sums_bytes(int n, bool gated, int split, int rows) {
+  const int parts = gated ? 2 : 1, pieces = n / parts / 16;
+  return split * ((pieces + split - 1) / split) * parts * ((rows + 31) / 32 * 32) * 64;
 }
 
 // Where the sums lie in their owner: [CTA][piece of the owner's][four columns][row],
@@ -74,7 +75,10 @@ template <int kN, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
     few_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
                const Few f) {
-  constexpr int kBlocks = kN / 128;                       // blocks of 128 weight rows
+  constexpr int kParts = kMode == kPlain ? 1 : 2;         // parts of an output: its sum, or gate and up
+  constexpr int kOut = kN / kParts;                       // outputs of a row of the tile
+  constexpr int kBlocks = kMode == kPlain ? kN / 128 : 2; // blocks of 128 rows' scales
+  constexpr int kBox = kN / kBlocks;                      // weight rows of a block
   constexpr uint32_t kCols = kN == 256 ? 512 : 256;       // TMEM: sums, then scales
   constexpr uint32_t kScaleA = kN, kScaleB = kN + 16;     // 4 columns per 64 k and 128 rows
   extern __shared__ uint8_t smem_raw[];
@@ -94,9 +98,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int s0 = static_cast<int>(int64_t(steps) * rank / f.split);
   const int s1 = static_cast<int>(int64_t(steps) * (rank + 1) / f.split);
   const int n_steps = s1 - s0;
-  // first weight row of block i of the tile
+  // first weight row of block i of the tile (of a gated tile of 64 outputs the first or
+  // the second half of 128 rows)
   auto w_row = [&](int i) {
-    return kMode == kPlain ? tile * kN + i * 128 : tile * 128 + i * static_cast<int>(p.N / 2);
+    return kMode == kPlain ? tile * kN + i * kBox : tile * kOut + i * static_cast<int>(p.N / 2);
   };
   const int a_bytes = f.a_rows * 128;
   const int w_off = a_bytes, sa_off = w_off + kN * 128, sb_off = sa_off + 4 * kScaleBlock;
@@ -127,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive_expect_tx(&full[slot], f.stage_bytes);
 #pragma unroll
       for (int i = 0; i < kBlocks; ++i) {
-        tma_load_2d(st + w_off + i * 128 * 128, &tm_w, &full[slot], (s0 + it) * 128, w_row(i));
+        tma_load_2d(st + w_off + i * kBox * 128, &tm_w, &full[slot], (s0 + it) * 128, w_row(i));
         bulk_load(st + sb_off + i * 4 * kScaleBlock,
                   p.w_scales + (int64_t(w_row(i) / 128) * (p.K / kMmaK) + (s0 + it) * 4) * kScaleBlock,
                   4 * kScaleBlock, &full[slot]);
@@ -170,7 +175,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait(&full[it % f.stages], (it / f.stages) & 1, &none)) *abort_flag = 1;
     }
   } else if (warp == 1) {
-    constexpr uint32_t idesc = idesc_nvfp4(128, kN);
+    // two halves of 128 rows' scales cannot be one operand: an MMA for each
+    constexpr int kMmas = kBox == 64 ? 2 : 1;
+    constexpr uint32_t idesc = idesc_nvfp4(128, kN / kMmas);
+    const uint32_t half = kMmas == 2 && (tile & 1) ? 2 : 0;
     int slot = 0;
     uint32_t parity = 0;
     for (int it = 0; it < n_steps; ++it) {
@@ -189,8 +197,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          umma_nvfp4(tmem, a + 2 * j, b + 2 * j, idesc, tmem + kScaleA + 4 * j, tmem + kScaleB + 4 * kBlocks * j,
-                     (it | j) != 0);
+#pragma unroll
+          for (int i = 0; i < kMmas; ++i)
+            umma_nvfp4(tmem + kBox * i, a + 2 * j, b + 2 * j + i * (kBox * 128 >> 4), idesc, tmem + kScaleA + 4 * j,
+                       tmem + kScaleB + 4 * (kBlocks * j + i) + half, (it | j) != 0);
         umma_commit(&empty[slot]);
       }
       __syncwarp();
@@ -209,8 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   else
     __syncthreads();
   tc_fence_after_sync();
-  constexpr int kOut = kMode == kPlain ? kN : 128;        // outputs of a row of the tile
-  constexpr int kPieces = kOut / 16, kParts = kN / kOut;  // parts of an output: its sum, or gate and up
+  constexpr int kPieces = kOut / 16;
   const int n_out = static_cast<int>(kMode == kPlain ? p.N : p.N / 2);
   // 16 outputs of a row, from the sums of their parts
   auto out = [&](int row, int piece, float (&v)[kParts][16]) {
@@ -301,15 +310,42 @@ int run(Few f, const Device& d, cudaStream_t stream) {
   if (const int st = allow_smem(few_kernel<kN, kMode>, kAllSmem, d, ready)) return st;
   CUtensorMap tm_a, tm_w;
   if (!codes_map(&tm_a, f.p.a_codes, f.p.M, f.p.K, f.a_rows) ||
-      !codes_map(&tm_w, f.p.w_codes, f.p.N, f.p.K, 128))
+      !codes_map(&tm_w, f.p.w_codes, f.p.N, f.p.K, kMode == kPlain || kN == 256 ? 128 : 64))
     return NVFP4_ERR_LAUNCH;
   if (f.stages < 1 || f.split < 1 || f.split > kMaxSplit ||
-      (f.split > 1 && sums_bytes(kN, 128, f.split, f.a_rows) > f.smem - 1024))
+      (f.split > 1 && sums_bytes(kN, kMode != kPlain, f.split, f.a_rows) > f.smem - 1024))
     return NVFP4_ERR_LAUNCH;
-  const unsigned tiles = static_cast<unsigned>(f.p.N / (kMode == kPlain ? kN : 256));
+  const unsigned tiles = static_cast<unsigned>(f.p.N / kN);
   return launch(f.split, few_kernel<kN, kMode>,
                 dim3(tiles * f.split, static_cast<unsigned>((f.p.M + 127) / 128)), dim3(kThreads),
                 f.smem, stream, tm_a, tm_w, f);
+}
+
+// Clusters of `split` CTAs, one on each SM, that the device holds at one time: not
+// all of its SMs divide by every size (48 clusters of 3, 144 CTAs on 152 SMs, took
+// two rounds, 15 us against 10).  Asked once for each size.
+int most_clusters(int split, const Device& d) {
+  static std::atomic<bool> ready[kMaxDevices];
+  static std::atomic<int> known[kMaxDevices][kMaxSplit + 1];
+  int n = known[d.id][split].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  if (allow_smem(few_kernel<128, kPlain>, kAllSmem, d, ready) != NVFP4_OK) return 0;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(split);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kAllSmem;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = split;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, few_kernel<128, kPlain>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  known[d.id][split].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 }  // namespace
@@ -319,22 +355,30 @@ int run_product_few(const Product& p, const Device& d, cudaStream_t stream) {
   f.p = p;
   f.a_rows = p.M >= 128 ? 128 : static_cast<int>((p.M + 7) / 8 * 8);
   const int64_t steps = p.K / kStageK, token_tiles = (p.M + 127) / 128;
-  const int n = p.swiglu ? 256 : 128;
-  f.stage_bytes = f.a_rows * 128 + n * 128 + 4 * kScaleBlock * (1 + n / 128);
-  int64_t split = d.num_sms / (p.N / n * token_tiles);
-  f.split = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({split, kMaxSplit, steps})));
+  // Gated tiles of 64 outputs leave room in TMEM and shared memory for a second CTA, of
+  // this kernel or the next: one token through 12288 x 2048 7.2 us against 11.5 with
+  // tiles of 128, through 34816 x 5120 18.7 against 19.3.  With many tokens and more of
+  // them than SMs it is the MMAs' operand reads that count: 128 tokens through 34816 x
+  // 5120 21.9 us against 20.4.
+  const int n = p.swiglu && f.a_rows > 64 && p.N / 128 * token_tiles > d.num_sms ? 256 : 128;
+  f.stage_bytes = f.a_rows * 128 + n * 128 + 4 * kScaleBlock * (p.swiglu ? 3 : 2);
+  const int64_t tiles = p.N / n * token_tiles;
+  f.split = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({d.num_sms / tiles, kMaxSplit, steps})));
+  while (f.split > 1 && tiles > most_clusters(f.split, d)) --f.split;
   // With half of an SM's shared memory the next kernel's CTAs are resident, with their
   // first stages on the way, before this one's end; with all of it the ring is twice as
   // deep.  One token: 10 steps over 8192 rows 7.9 us against 8.4, 23 steps over 5120
   // 13.0 against 12.4; 128 tokens (stages half as many): 3 steps 10.4 against 13.5, 8
-  // steps 11.5 against 9.1.  A gated tile takes all of TMEM and is alone in any case.
+  // steps 11.5 against 9.1.  More tiles than SMs: 20 steps over 34816 rows 18.7 against
+  // 26.0.  A gated tile of 128 outputs takes all of TMEM and is alone in any case.
   const int half = (kHalfSmem - 1024) / f.stage_bytes;
-  f.smem = n == 256 || steps / f.split > 2 * half ? kAllSmem : kHalfSmem;
+  f.smem = n == 256 || (steps / f.split > 2 * half && tiles <= d.num_sms) ? kAllSmem : kHalfSmem;
   // the sums lie where the stages were (an odd split leaves its owners unequal pieces,
   // and their sums more room)
-  while (f.split > 1 && sums_bytes(n, 128, f.split, f.a_rows) > f.smem - 1024) --f.split;
+  while (f.split > 1 && sums_bytes(n, p.swiglu, f.split, f.a_rows) > f.smem - 1024) --f.split;
   f.stages = std::min((f.smem - 1024) / f.stage_bytes, kMaxStages);
   if (!p.swiglu) return run<128, kPlain>(f, d, stream);
+  if (n == 128) return p.codes ? run<128, kGatedRows>(f, d, stream) : run<128, kGated>(f, d, stream);
   return p.codes ? run<256, kGatedRows>(f, d, stream) : run<256, kGated>(f, d, stream);
 }
 
