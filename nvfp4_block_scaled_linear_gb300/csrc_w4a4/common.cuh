@@ -16,11 +16,12 @@ namespace w4a4 {
 
 constexpr int kMaxSegments = 8;
 
-// Byte of the scale of row r and 16-block b (of K / 16) in the order of
-// nvfp4_w4a4.h: 512-byte blocks of 128 rows x 4 scales.
-__host__ __device__ __forceinline__ int64_t scale_at(int64_t r, int64_t b, int64_t K) {
-  return ((r >> 7) * (K >> 6) + (b >> 2)) * 512 + (r & 31) * 16 + (r >> 5 & 3) * 4 + (b & 3);
+// Bytes of a row's scales in the order of nvfp4_w4a4.h (512-byte blocks of 128 rows
+// x 4 scales): where row r's begin, and from there to 16-block b's.
+__device__ __forceinline__ int64_t scale_row(int64_t r, int64_t K) {
+  return (r >> 7) * (K >> 6) * 512 + ((r & 31) * 16 + (r >> 5 & 3) * 4);
 }
+__device__ __forceinline__ int64_t scale_in_row(int b) { return (b >> 2) * int64_t(512) + (b & 3); }
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -77,20 +78,21 @@ __device__ __forceinline__ float from_e4m3(uint32_t b) {
   return f;
 }
 
-// A block of 16 values -> 8 code bytes and the scale byte, by the steps of
-// nvfp4_w4a4.h.  The quotient of x = RN(v gs) by the scale s is correctly
-// rounded without a division for each value: with r = RN(1/s), q0 = RN(x r),
-// rem = RN(x - q0 s), q = RN(q0 + rem r) (Markstein's refinement; s has 4
-// significant bits, so r is far from the one case it excepts).  A quotient so
-// small that a step underflows is far below e2m1's first threshold.
-__device__ __forceinline__ uint32_t quantize16(const float (&v)[16], float gs, uint2& codes) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+// A block of 16 values, the largest of magnitude `top` (as bits, which order as the
+// values do and put infinities and NaN above them), -> 8 code bytes and the scale
+// byte, by the steps of nvfp4_w4a4.h.  The quotient of x = RN(v gs) by the scale s is
+// correctly rounded without a division for each value: with r = RN(1/s), q0 = RN(x r),
+// rem = RN(x - q0 s), q = RN(q0 + rem r) (Markstein's refinement; s has 4 significant
+// bits, so r is far from the one case it excepts); the sixth of the largest likewise.
+// A quotient so small that a step underflows is far below the first threshold, of
+// e2m1 or of e4m3.
+__device__ __forceinline__ uint32_t quantize16(const float (&v)[16], uint32_t top, float gs, uint2& codes) {
   const float m = __fmul_rn(__uint_as_float(top), gs);
   codes = make_uint2(0u, 0u);
   if (!(m < __uint_as_float(0x7F800000u))) return 0x7Fu;      // infinity, NaN
-  const uint32_t byte = to_e4m3(__fdiv_rn(m, 6.0f));
+  constexpr float kSixth = 0.16666667163372039794921875f;    // RN(1/6)
+  const float sixth = __fmul_rn(m, kSixth);
+  const uint32_t byte = to_e4m3(__fmaf_rn(__fmaf_rn(sixth, -6.0f, m), kSixth, sixth));
   if (byte == 0u) return 0u;
   const float s = from_e4m3(byte), r = __frcp_rn(s);
   const uint64_t g2 = pack2(gs, gs), r2 = pack2(r, r), ns2 = pack2(-s, -s);
@@ -110,6 +112,13 @@ __device__ __forceinline__ uint32_t quantize16(const float (&v)[16], float gs, u
   }
   codes = make_uint2(c[0], c[1]);
   return byte;
+}
+
+__device__ __forceinline__ uint32_t quantize16(const float (&v)[16], float gs, uint2& codes) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  return quantize16(v, top, gs, codes);
 }
 
 // ---------------------------------------------------------------- host side

@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (kMode == kGatedRows) {
       uint2 codes;
-      p.scales[scale_at(m, n >> 4, n_out)] = static_cast<uint8_t>(quantize16(v[0], p.out_gs, codes));
+      p.scales[scale_row(m, n_out) + scale_in_row(n >> 4)] = static_cast<uint8_t>(quantize16(v[0], p.out_gs, codes));
       *reinterpret_cast<uint2*>(p.codes + m * (n_out >> 1) + (n >> 1)) = codes;
     } else {
       store_bf16(p.y + m * n_out + n, v[0]);

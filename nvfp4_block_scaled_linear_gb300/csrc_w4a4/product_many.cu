@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int pair = blockIdx.x >> 1;
   const int steps = static_cast<int>(p.K / kStageK);
   const int my_tiles = (f.tiles - 1 - pair) / f.pairs + 1;        // pair < pairs <= tiles
-  const int scale_row = static_cast<int>(p.K / kMmaK);            // blocks of 128 rows' scales
+  const int scale_rows = static_cast<int>(p.K / kMmaK);            // blocks of 128 rows' scales
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -174,10 +174,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int w0 = kMode == kPlain ? n * kTile : n * kHalf;
       const int w1 = kMode == kPlain ? w0 + kHalf : w0 + static_cast<int>(p.N / 2);
       q.w = rank ? w1 : w0;
-      q.sa = min(q.m >> 7, last_a) * scale_row;
+      q.sa = min(q.m >> 7, last_a) * scale_rows;
       // (an odd block of 128 weight rows: what its missing half would be is not read back)
-      q.sw[0] = (w0 >> 7) * scale_row;
-      q.sw[1] = min(w1 >> 7, last_w) * scale_row;
+      q.sw[0] = (w0 >> 7) * scale_rows;
+      q.sw[1] = min(w1 >> 7, last_w) * scale_rows;
       return q;
     };
     const uint32_t first_full = map_to_rank(smem_addr(full), 0);
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < 16; ++k) v[k] = gated(g[k] * sg, u[k] * su);
           if (kMode == kGatedRows) {
             uint2 codes;
-            p.scales[scale_at(m, n >> 4, n_out)] = static_cast<uint8_t>(quantize16(v, p.out_gs, codes));
+            p.scales[scale_row(m, n_out) + scale_in_row(n >> 4)] = static_cast<uint8_t>(quantize16(v, p.out_gs, codes));
             *reinterpret_cast<uint2*>(p.codes + m * (n_out >> 1) + (n >> 1)) = codes;
           } else {
             store_bf16(p.y + m * n_out + n, v);

@@ -18,6 +18,17 @@ __device__ __forceinline__ void unpack16(const uint4 (&w)[2], float (&f)[16]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) f[2 * i] = bf16_lo(u[i]), f[2 * i + 1] = bf16_hi(u[i]);
 }
+// The largest magnitude of 16 bf16 numbers, as bits of fp32.
+__device__ __forceinline__ uint32_t largest16(const uint4 (&w)[2]) {
+  constexpr uint32_t kMagnitude = 0x7FFF7FFFu;
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    m = max_u16x2(m, max_u16x2(w[i].x & kMagnitude, w[i].y & kMagnitude));
+    m = max_u16x2(m, max_u16x2(w[i].z & kMagnitude, w[i].w & kMagnitude));
+  }
+  return max(m << 16, m & 0xFFFF0000u);
+}
 __device__ __forceinline__ void pack16(const float (&f)[16], uint4 (&w)[2]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -92,7 +103,7 @@ __global__ void __launch_bounds__(kMaxNormThreads) norm_kernel(const Norm p) {
       store16(p.y + m * p.ys + b * 16, x[v]);
     } else {
       uint2 c;
-      p.scales[scale_at(m, b, p.K)] = static_cast<uint8_t>(quantize16(f, p.gs, c));
+      p.scales[scale_row(m, p.K) + scale_in_row(b)] = static_cast<uint8_t>(quantize16(f, p.gs, c));
       *reinterpret_cast<uint2*>(p.codes + m * (p.K >> 1) + b * 8) = c;
     }
   }
@@ -100,23 +111,32 @@ __global__ void __launch_bounds__(kMaxNormThreads) norm_kernel(const Norm p) {
 
 constexpr int kQuantThreads = 256;
 
-// A thread per block of 16; blockIdx.y walks the rows.
+// blockDim.y rows to a block of threads; of a row a thread takes every blockDim.x-th
+// block of 16, two of them on the way at one time.
 __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const Quantize p) {
   griddep_wait();
   griddep_launch_dependents();
+  const int64_t m = blockIdx.x * static_cast<int64_t>(blockDim.y) + threadIdx.y;
+  if (m >= p.M) return;
   const int blocks = static_cast<int>(p.K >> 4);
-  const int64_t total = p.M * blocks;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kQuantThreads;
-  for (int64_t i = blockIdx.x * static_cast<int64_t>(kQuantThreads) + threadIdx.x; i < total; i += step) {
-    const int64_t m = i / blocks;
-    const int b = static_cast<int>(i - m * blocks);
-    uint4 w[2];
-    load16(p.x + m * p.xs + b * 16, w);
-    float f[16];
-    unpack16(w, f);
-    uint2 c;
-    p.scales[scale_at(m, b, p.K)] = static_cast<uint8_t>(quantize16(f, p.gs, c));
-    *reinterpret_cast<uint2*>(p.codes + m * (p.K >> 1) + b * 8) = c;
+  const __nv_bfloat16* x = p.x + m * p.xs;
+  uint8_t* codes = p.codes + m * (p.K >> 1);
+  uint8_t* scales = p.scales + scale_row(m, p.K);
+  for (int b = threadIdx.x; b < blocks; b += 2 * blockDim.x) {
+    const int b1 = b + blockDim.x;
+    uint4 w[2][2];
+    load16(x + b * 16, w[0]);
+    if (b1 < blocks) load16(x + b1 * 16, w[1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int at = i ? b1 : b;
+      if (at >= blocks) break;
+      float f[16];
+      unpack16(w[i], f);
+      uint2 c;
+      scales[scale_in_row(at)] = static_cast<uint8_t>(quantize16(f, largest16(w[i]), p.gs, c));
+      *reinterpret_cast<uint2*>(codes + at * 8) = c;
+    }
   }
 }
 
@@ -137,15 +157,19 @@ __global__ void __launch_bounds__(256)
       if (b == 0x7Fu || b > 0x80u) atomicOr(refused, 1u);
       out |= (b == 0x80u ? 0u : b) << (8 * k);
     }
-    *reinterpret_cast<uint32_t*>(blocked + scale_at(n, j * 4, K)) = out;
+    *reinterpret_cast<uint32_t*>(blocked + scale_row(n, K) + j * 512) = out;
   }
 }
 
 }  // namespace
 
-int run_norm(const Norm& p, const Device&, cudaStream_t stream) {
+int run_norm(const Norm& p, const Device& d, cudaStream_t stream) {
   const int blocks = static_cast<int>(p.K >> 4);
-  const int v = blocks <= kMaxNormThreads ? 1 : blocks <= 2 * kMaxNormThreads ? 2 : 4;
+  // Few rows: as many threads as blocks of 16.  Many: two blocks a thread, twice the
+  // bytes in flight for the threads that an SM holds.  K = 5120, into NVFP4: one row
+  // 2.5 us against 2.9, 8192 rows 53.0 against 44.4 (into bf16 52.1 against 49.7).
+  const int most = p.M > 2 * d.num_sms ? 128 : kMaxNormThreads;
+  const int v = blocks <= most ? 1 : blocks <= 2 * kMaxNormThreads ? 2 : 4;
   const int threads = ((blocks + v - 1) / v + 31) / 32 * 32;
   const dim3 grid(static_cast<unsigned>(p.M));
   return v == 1   ? launch(1, norm_kernel<1>, grid, dim3(threads), 0, stream, p)
@@ -153,11 +177,13 @@ int run_norm(const Norm& p, const Device&, cudaStream_t stream) {
                   : launch(1, norm_kernel<4>, grid, dim3(threads), 0, stream, p);
 }
 
-int run_quantize(const Quantize& p, const Device& d, cudaStream_t stream) {
-  const int64_t want = (p.M * (p.K >> 4) + kQuantThreads - 1) / kQuantThreads;
-  const int64_t most = int64_t(d.num_sms) * 8;
-  return launch(1, quantize_rows_kernel, dim3(static_cast<unsigned>(want < most ? want : most)),
-                dim3(kQuantThreads), 0, stream, p);
+int run_quantize(const Quantize& p, const Device&, cudaStream_t stream) {
+  // a row's blocks in equal shares of at most kQuantThreads threads, two to a thread
+  // where there are many
+  const int blocks = static_cast<int>(p.K >> 4);
+  const int rounds = (blocks + kQuantThreads - 1) / kQuantThreads, shares = blocks >= 64 && rounds == 1 ? 2 : rounds;
+  const int x = (blocks + shares - 1) / shares, y = kQuantThreads / x;
+  return launch(1, quantize_rows_kernel, dim3(static_cast<unsigned>((p.M + y - 1) / y)), dim3(x, y), 0, stream, p);
 }
 
 int run_scale_layout(const uint8_t* scale, int64_t N, int64_t K, uint8_t* blocked,
