@@ -235,6 +235,19 @@ def _matrix(t, name, shape, device):
     return t.data_ptr(), row
 
 
+def _input(x):
+    """Device, rows, width, address and row stride of the input that decides them."""
+    if not x.is_cuda or x.ndim != 2:
+        raise ValueError("x must be a CUDA tensor [M, K]")
+    if x.dtype is not torch.bfloat16:
+        raise TypeError("x must be bfloat16, got %s" % x.dtype)
+    m, k = x.shape
+    row, one = x.stride()
+    if one != 1:
+        raise ValueError("the rows of x must be dense")
+    return x.device, m, k, x.data_ptr(), row
+
+
 def _rows_out(out, m, k, global_scale, device, stream):
     if out is None:
         return _new_rows(m, k, _scale(global_scale, "global_scale"), device, stream)
@@ -249,45 +262,42 @@ def quantize_rows(x, global_scale=1.0, out=None, stream=None):
     """x (bfloat16 [M, K], rows may be strided, K a multiple of 256) as NVFP4 rows
     with the given global scale (a checkpoint's input_global_scale; 1 keeps what
     lies between about 0.1 and 2688).  Returns Fp4Rows."""
-    if not x.is_cuda or x.dim() != 2:
-        raise ValueError("x must be a CUDA tensor [M, K]")
-    m, k = x.shape
+    dev, m, k, p, stride = _input(x)
     if k == 0 or k % 256:
         raise ValueError("K must be a positive multiple of 256, got %d" % k)
-    p, stride = _matrix(x, "x", x.shape, x.device)
-    out = _rows_out(out, m, k, global_scale, x.device, stream)
-    _call("nvfp4_quantize_rows", x.device, stream, p, stride, m, k, out._c)
+    out = _rows_out(out, m, k, global_scale, dev, stream)
+    _call("nvfp4_quantize_rows", dev, stream, p, stride, m, k, out._c)
     return out
 
 
-def _norm(x, residual, weight, eps, residual_out, y, rows, stream):
-    """The call, on whatever it is given; makes the sum's tensor where that is missing.  Returns the sum."""
-    dev, shape = x.device, x.shape
-    px, sx = _matrix(x, "x", shape, dev)
+def _norm(given, x, residual, weight, eps, residual_out, y, rows, stream):
+    """The call on `given`, the _input of x; makes the sum's tensor where that is missing.  Returns the sum."""
+    dev, m, k, px, sx = given
+    shape = x.shape
     pr, sr = (None, 0) if residual is None else _matrix(residual, "residual", shape, dev)
+    if weight.dtype is not torch.bfloat16:
+        raise TypeError("weight must be bfloat16, got %s" % weight.dtype)
+    if weight.shape != (k,) or weight.device != dev or not weight.is_contiguous():
+        raise ValueError("weight must be a contiguous tensor of shape %s on %s, got %s on %s"
+                         % ((k,), dev, tuple(weight.shape), weight.device))
+    py, sy = (None, 0) if y is None else _matrix(y, "out", shape, dev)
     if residual_out is not None:
         po, so = _matrix(residual_out, "residual_out", shape, dev)
         total = residual_out
     elif residual is not None:
-        total = _like(x, stream)
-        po, so = total.data_ptr(), shape[1]
+        total = _like(shape, dev, stream)
+        po, so = total.data_ptr(), k
     else:
         po, so, total = None, 0, x
-    py, sy = (None, 0) if y is None else _matrix(y, "out", shape, dev)
-    if weight.dtype is not torch.bfloat16:
-        raise TypeError("weight must be bfloat16, got %s" % weight.dtype)
-    if weight.shape != shape[1:] or weight.device != dev or not weight.is_contiguous():
-        raise ValueError("weight must be a contiguous tensor of shape %s on %s, got %s on %s"
-                         % (tuple(shape[1:]), dev, tuple(weight.shape), weight.device))
-    _call("nvfp4_add_rms_norm", dev, stream, px, sx, pr, sr, weight.data_ptr(), eps, shape[0], shape[1], po, so,
-          py, sy, None if rows is None else rows._c)
+    _call("nvfp4_add_rms_norm", dev, stream, px, sx, pr, sr, weight.data_ptr(), eps, m, k, po, so, py, sy,
+          None if rows is None else rows._c)
     return total
 
 
-def _like(x, stream):
+def _like(shape, device, stream):
     if stream is None:
-        return torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
-    return _empty(x.shape, torch.bfloat16, x.device, stream)
+        return torch.empty(shape, dtype=torch.bfloat16, device=device)
+    return _empty(shape, torch.bfloat16, device, stream)
 
 
 def add_rms_norm(x, residual, weight, eps=1e-6, out=None, residual_out=None, stream=None):
@@ -296,24 +306,21 @@ def add_rms_norm(x, residual, weight, eps=1e-6, out=None, residual_out=None, str
     of 16), weight bfloat16 [K].  Without a residual (None) r is x.  Returns
     (normed, r); either may be written over one of the inputs (``out``,
     ``residual_out``)."""
-    if not x.is_cuda or x.dim() != 2:
-        raise ValueError("x must be a CUDA tensor [M, K]")
+    given = _input(x)
     if out is None:
-        out = _like(x, stream)
-    return out, _norm(x, residual, weight, eps, residual_out, out, None, stream)
+        out = _like(x.shape, given[0], stream)
+    return out, _norm(given, x, residual, weight, eps, residual_out, out, None, stream)
 
 
 def add_rms_norm_quantize(x, residual, weight, eps=1e-6, global_scale=1.0, out=None, residual_out=None,
                           stream=None):
     """As ``add_rms_norm``, with the normed rows rounded once, to NVFP4 with the
     given global scale (K a multiple of 256).  Returns (Fp4Rows, r)."""
-    if not x.is_cuda or x.dim() != 2:
-        raise ValueError("x must be a CUDA tensor [M, K]")
-    m, k = x.shape
+    given = dev, m, k, _, _ = _input(x)
     if k == 0 or k % 256:
         raise ValueError("K must be a positive multiple of 256, got %d" % k)
-    out = _rows_out(out, m, k, global_scale, x.device, stream)
-    return out, _norm(x, residual, weight, eps, residual_out, None, out, stream)
+    out = _rows_out(out, m, k, global_scale, dev, stream)
+    return out, _norm(given, x, residual, weight, eps, residual_out, None, out, stream)
 
 
 def _check_product(a, w):
@@ -325,8 +332,7 @@ def _product(a, w, swiglu, out, stream):
     _check_product(a, w)
     shape = (a.shape[0], w.shape[0] // 2 if swiglu else w.shape[0])
     if out is None:
-        out = (torch.empty(shape, dtype=torch.bfloat16, device=a.device) if stream is None
-               else _empty(shape, torch.bfloat16, a.device, stream))
+        out = _like(shape, a.device, stream)
     elif out.dtype != torch.bfloat16 or out.shape != shape or not out.is_contiguous() or out.device != a.device:
         raise ValueError("out must be a contiguous bfloat16 tensor of shape %s on %s" % (shape, a.device))
     _call("nvfp4_linear_w4a4", a.device, stream, a._c, a.shape[0], w._c, swiglu, out.data_ptr(), None)
