@@ -9,7 +9,10 @@
 //
 // Pairs are persistent, one on every two SMs.
 //
-// TMEM: the sums of two tiles would take all 512 columns and the scales have 48.
+// A plain product also has tiles of 192 weight rows, for the numbers of tiles that
+// fill the pairs better so; the sums of two of them are apart in TMEM.
+//
+// TMEM: the sums of two tiles of 256 would take all 512 columns and the scales have 48.
 // The second tile's sums therefore begin in the first one's last 64 columns
 // (kOverlap): the epilogue reads those first, into registers, and the next tile's
 // products start while it works on the rest.
@@ -17,8 +20,8 @@
 // Both CTAs' copies count on the first one's barriers, whose thread issues the
 // MMAs; what it has read is free for both by one commit.
 //
-// Warps: 0 copies, 1 issues the MMAs, 2 TMEM allocation, 4..19 the epilogue, four for each quarter of
-// the lanes, taking every fourth piece of 16 columns: a piece's chain (TMEM, the
+// Warps: 0 copies, 1 issues the MMAs, 2 TMEM allocation, 4..19 the epilogue, four
+// for each quarter of the lanes, taking every fourth piece of 16 columns: a piece's chain (TMEM, the
 // exponentials, the quantisation, the store) is long, and 16 warps hide it where 8
 // took longer than the products.
 #include <algorithm>
@@ -31,18 +34,26 @@ namespace {
 
 constexpr int kThreads = 640;
 constexpr int kEpilogueWarps = 16;
-constexpr int kTile = 256;                       // tokens and weight rows of a pair's tile
+constexpr int kTile = 256;                       // tokens of a pair's tile
 constexpr int kHalf = 128;
-constexpr int kA = kHalf * 128, kB = kHalf * 128;                 // bytes of codes a stage
+constexpr int kA = kHalf * 128;                  // bytes of codes and scales a stage
 constexpr int kScalesA = 4 * kScaleBlock, kScalesB = 8 * kScaleBlock;
-constexpr int kStage = kA + kB + kScalesA + kScalesB;
-constexpr int kStages = 5;
-constexpr int kSmem = kStages * kStage + 1024;
-constexpr uint32_t kOverlap = 64;
-constexpr uint32_t kSecond = kTile - kOverlap;                    // column of the second tile's sums
-constexpr uint32_t kColA = kSecond + kTile, kColB = kColA + 16;
-static_assert(kColB + 32 <= 512, "TMEM columns");
-static_assert(kStage % 1024 == 0, "stages keep 1024-byte alignment");
+
+// What goes by the weight rows of a pair's tile.
+template <int kN>
+struct Shape {
+  static constexpr int kBox = kN / 2;                             // weight rows of a CTA
+  static constexpr int kB = kBox * 128;
+  static constexpr int kStage = kA + kB + kScalesA + kScalesB;
+  static constexpr int kStages = kN == 256 ? 5 : 6;
+  static constexpr int kSmem = kStages * kStage + 1024;
+  // columns of TMEM: where the second tile's sums begin, the scales of tokens and weights
+  static constexpr uint32_t kOverlap = kN == 256 ? 64 : 0;
+  static constexpr uint32_t kSecond = kN - kOverlap, kColA = kSecond + kN, kColB = kColA + 16;
+  static_assert(kColB + 32 <= 512, "TMEM columns");
+  static_assert(kStage % 1024 == 0, "stages keep 1024-byte alignment");
+  static_assert(kSmem <= 226 * 1024, "shared memory");
+};
 
 enum { kPlain = 0, kGated = 1, kGatedRows = 2 };
 
@@ -111,13 +122,16 @@ __device__ __forceinline__ void load16(uint32_t tmem, float (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-template <int kMode>
+template <int kN, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
     many_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
                 const __grid_constant__ CUtensorMap tm_sa, const __grid_constant__ CUtensorMap tm_sw,
                 const Many f) {
+  using S = Shape<kN>;
+  constexpr int kB = S::kB, kStage = S::kStage, kStages = S::kStages;
+  constexpr uint32_t kSecond = S::kSecond, kColA = S::kColA, kColB = S::kColB;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t full[kStages], empty[kStages], sums_full[2], sums_free, done;
+  __shared__ uint64_t full[kStages], empty[kStages], sums_full[2], sums_free[2], done;
   __shared__ int abort_word;
   __shared__ uint32_t tmem_slot;
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -138,7 +152,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&sums_full[0], 1);
     mbar_init(&sums_full[1], 1);
-    mbar_init(&sums_free, 2 * kEpilogueWarps);
+    mbar_init(&sums_free[0], 2 * kEpilogueWarps);
+    mbar_init(&sums_free[1], 2 * kEpilogueWarps);
     mbar_init(&done, 1);
     abort_word = 0;
     fence_mbar_init();
@@ -171,13 +186,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       tile_at(f, tile, m, n);
       q.tile = tile;
       q.m = m * kTile + rank * kHalf;
-      const int w0 = kMode == kPlain ? n * kTile : n * kHalf;
-      const int w1 = kMode == kPlain ? w0 + kHalf : w0 + static_cast<int>(p.N / 2);
+      const int w0 = kMode == kPlain ? n * kN : n * kHalf;
+      const int w1 = kMode == kPlain ? w0 + S::kBox : w0 + static_cast<int>(p.N / 2);
       q.w = rank ? w1 : w0;
       q.sa = min(q.m >> 7, last_a) * scale_rows;
-      // (an odd block of 128 weight rows: what its missing half would be is not read back)
+      // (what the weight rows' last blocks miss of a tile is not read back)
       q.sw[0] = (w0 >> 7) * scale_rows;
-      q.sw[1] = min(w1 >> 7, last_w) * scale_rows;
+      q.sw[1] = min(kMode == kPlain ? (w0 >> 7) + 1 : w1 >> 7, last_w) * scale_rows;
       return q;
     };
     const uint32_t first_full = map_to_rank(smem_addr(full), 0);
@@ -233,14 +248,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // The whole warp walks the stages, an elected lane issues.
     if (rank == 0) {
-      constexpr uint32_t idesc = idesc_nvfp4(kTile, kTile);
+      constexpr uint32_t idesc = idesc_nvfp4(kTile, kN);
       int slot = 0;
       uint32_t parity = 0;
       bool ok = true;
       for (int i = 0; i < my_tiles && ok; ++i) {
-        // the columns that this tile's sums share with the last one's are read
-        if (i > 0) ok = __all_sync(0xffffffffu, wait(&sums_free, (i - 1) & 1, abort_flag));
+        // the columns that this tile's sums share with an earlier one's are read: some of
+        // the last tile's, or all of the one before it
+        const int before = S::kOverlap ? i - 1 : i - 2;
+        if (before >= 0) ok = __all_sync(0xffffffffu, wait(&sums_free[before & 1], (before >> 1) & 1, abort_flag));
         if (!ok) break;
+        // every other tile of 192 weight rows begins in the middle of a block of scales
+        uint32_t col_b = kColB;
+        if (kN == 192) {
+          int mt, nt;
+          tile_at(f, pair + i * f.pairs, mt, nt);
+          col_b += nt & 1 ? 2 : 0;
+        }
         tc_fence_after_sync();
         const uint32_t d = tmem + (i & 1 ? kSecond : 0);
         for (int it = 0; it < steps; ++it) {
@@ -260,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              umma_nvfp4_pair(d, a + 2 * j, b + 2 * j, idesc, tmem + kColA + 4 * j, tmem + kColB + 8 * j,
+              umma_nvfp4_pair(d, a + 2 * j, b + 2 * j, idesc, tmem + kColA + 4 * j, tmem + col_b + 8 * j,
                               (it | j) != 0);
             commit_pair(&empty[slot]);
           }
@@ -289,28 +313,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       tile_at(f, pair + i * f.pairs, mt, nt);
       const int64_t m = int64_t(mt) * kTile + rank * kHalf + 32 * quarter + lane;
       const uint32_t acc = lanes + (b ? kSecond : 0);
-      // the shared columns first: piece h of their four
-      float first[16];
-      load16(lanes + kSecond + 16 * h, first);
+      // the columns that the next sums in line share first: piece h of four, or all of
+      // this warp's
+      float first[16], other[kN == 192 ? 2 : 1][16];
+      load16(S::kOverlap ? lanes + kSecond + 16 * h : acc + 16 * h, first);
+      if (!S::kOverlap)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) load16(acc + 64 * (j + 1) + 16 * h, other[kN == 192 ? j : 0]);
       tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) arrive_first(&sums_free);
+      if (lane == 0) arrive_first(&sums_free[b]);
       const bool inside = m < p.M;
       if (kMode == kPlain) {
         auto out = [&](int piece, float (&v)[16]) {
-          const int n = nt * kTile + piece * 16;
+          const int n = nt * kN + piece * 16;
           if (!inside || n >= p.N) return;
           const float s = segment_scale(p.seg, n);
 #pragma unroll
           for (int k = 0; k < 16; ++k) v[k] *= s;
           store_bf16(p.y + m * p.N + n, v);
         };
-        out((b ? 0 : 12) + h, first);
+        if (!S::kOverlap) {
+          out(h, first);
 #pragma unroll
-        for (int j = 0; j < 3; ++j) {
-          const int piece = (b ? 4 : 0) + 4 * j + h;
-          load16(acc + 16 * piece, first);
-          out(piece, first);
+          for (int j = 0; j < 2; ++j) out(4 * (j + 1) + h, other[kN == 192 ? j : 0]);
+        } else {
+          out((b ? 0 : 12) + h, first);
+#pragma unroll
+          for (int j = 0; j < 3; ++j) {
+            const int piece = (b ? 4 : 0) + 4 * j + h;
+            load16(acc + 16 * piece, first);
+            out(piece, first);
+          }
         }
       } else {
         auto out = [&](int piece, const float (&g)[16], const float (&u)[16]) {
@@ -330,16 +364,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         // what was read first: of the first sums the up half of pieces 4..7, of the
         // second the gate half of pieces 0..3
-        float other[16];
-        load16(acc + 16 * ((b ? 0 : 4) + h) + (b ? kHalf : 0), other);
+        load16(acc + 16 * ((b ? 0 : 4) + h) + (b ? kHalf : 0), other[0]);
         if (b)
-          out(h, first, other);
+          out(h, first, other[0]);
         else
-          out(4 + h, other, first);
+          out(4 + h, other[0], first);
         const int piece = (b ? 4 : 0) + h;
         load16(acc + 16 * piece, first);
-        load16(acc + 16 * piece + kHalf, other);
-        out(piece, first, other);
+        load16(acc + 16 * piece + kHalf, other[0]);
+        out(piece, first, other[0]);
       }
       // (read before the tile after next is begun: its sums_free comes later)
       tc_fence_before_sync();
@@ -353,18 +386,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-template <int kMode>
+template <int kN, int kMode>
 int run(const Product& p, const Device& d, cudaStream_t stream) {
   static std::atomic<bool> ready[kMaxDevices];
-  if (const int st = allow_smem(many_kernel<kMode>, kSmem, d, ready)) return st;
+  constexpr int kSmem = Shape<kN>::kSmem;
+  if (const int st = allow_smem(many_kernel<kN, kMode>, kSmem, d, ready)) return st;
   CUtensorMap tm_a, tm_w, tm_sa, tm_sw;
-  if (!codes_map(&tm_a, p.a_codes, p.M, p.K, kHalf) || !codes_map(&tm_w, p.w_codes, p.N, p.K, kHalf) ||
+  if (!codes_map(&tm_a, p.a_codes, p.M, p.K, kHalf) ||
+      !codes_map(&tm_w, p.w_codes, p.N, p.K, Shape<kN>::kBox) ||
       !scales_map(&tm_sa, p.a_scales, p.M, p.K) || !scales_map(&tm_sw, p.w_scales, p.N, p.K))
     return NVFP4_ERR_LAUNCH;
   const int64_t token_tiles = (p.M + kTile - 1) / kTile;
-  const int64_t tiles = token_tiles * ((p.N + kTile - 1) / kTile);
+  const int64_t tiles = token_tiles * ((p.N + kN - 1) / kN);
   // tiles, stages and rows of scales are counted in 32 bits
-  if (tiles > (1 << 30) || (std::max(p.M, p.N) + 127) / 128 * (p.K / kMmaK) > INT32_MAX || 
+  if (tiles > (1 << 30) || (std::max(p.M, p.N) + 127) / 128 * (p.K / kMmaK) > INT32_MAX ||
       (tiles / (d.num_sms / 2) + 1) * (p.K / kStageK) > INT32_MAX)
     return NVFP4_ERR_SHAPE;
   Many f{};
@@ -373,16 +408,22 @@ int run(const Product& p, const Device& d, cudaStream_t stream) {
   f.weight_tiles = static_cast<int>(tiles / token_tiles);
   f.tiles = static_cast<int>(tiles);
   f.pairs = static_cast<int>(tiles < d.num_sms / 2 ? tiles : d.num_sms / 2);
-  return launch(2, many_kernel<kMode>, dim3(2 * f.pairs), dim3(kThreads), kSmem, stream, tm_a, tm_w, tm_sa,
+  return launch(2, many_kernel<kN, kMode>, dim3(2 * f.pairs), dim3(kThreads), kSmem, stream, tm_a, tm_w, tm_sa,
                 tm_sw, f);
 }
 
 }  // namespace
 
 int run_product_many(const Product& p, const Device& d, cudaStream_t stream) {
-  return !p.swiglu ? run<kPlain>(p, d, stream)
-         : p.codes ? run<kGatedRows>(p, d, stream)
-                   : run<kGated>(p, d, stream);
+  if (p.swiglu) return p.codes ? run<256, kGatedRows>(p, d, stream) : run<256, kGated>(p, d, stream);
+  const int64_t pairs = d.num_sms / 2, token_tiles = (p.M + kTile - 1) / kTile;
+  auto rounds = [&](int n) { return (token_tiles * ((p.N + n - 1) / n) + pairs - 1) / pairs; };
+  // Tiles of 192 weight rows where they need no more rounds of the pairs: a round of
+  // them takes 0.79 to 0.91 of one of 256 (a fourth less work, and nothing shared in
+  // TMEM, but more copies for each product).  1111 tokens by 8192 rows and 5120 k, 3
+  // rounds of either: 23.1 us against 25.7; 2048 by 5120 and 17408 60.3 against 68.9;
+  // 8192 by 5120 and 17408, 12 rounds of 192 against 9: 224 against 207.
+  return 87 * rounds(192) < 100 * rounds(256) ? run<192, kPlain>(p, d, stream) : run<256, kPlain>(p, d, stream);
 }
 
 }  // namespace w4a4

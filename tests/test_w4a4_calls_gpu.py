@@ -249,6 +249,16 @@ def test_a_row_does_not_depend_on_the_others(m):
     assert bool((byte[1::2] == 0x7F).all()) and bool((byte[::2] < 0x7F).all())
 
 
+def test_tokens_verified_together_are_those_decoded_alone():
+    """Up to 8 rows share one schedule: a row's bits are the same alone and among them."""
+    for n, k in ((5120, 6144), (1024, 17408), (640, 512)):
+        w, _, _ = weight(n, k, 12)
+        x = hidden(8, k, 13).to(DEV)
+        y = pkg.linear_w4a4(pkg.quantize_rows(x, 30.0), w)
+        for m in (1, 3, 7):
+            assert torch.equal(pkg.linear_w4a4(pkg.quantize_rows(x[:m], 30.0), w), y[:m])
+
+
 def test_offsets_beyond_32_bits():
     """Inputs, codes and results whose last rows lie more than 2^32 bytes behind their first."""
     m, k = 70_000, 32768                                            # bf16: 4.6 GB
@@ -277,7 +287,7 @@ def test_offsets_beyond_32_bits():
 
 
 def test_many_tiles_turn_the_ring_many_times():
-    for m, n, k in ((1500, 16384, 256), (3000, 256, 16384), (777, 4224, 4352)):
+    for m, n, k in ((1500, 16384, 256), (3000, 256, 16384), (777, 4224, 4352), (1111, 8192, 4096), (2048, 5120, 2048)):
         rows = pkg.quantize_rows(hidden(m, k, 10).to(DEV), 64.0)
         w, w64, per_row = weight(n, k, 11)
         y = pkg.linear_w4a4(rows, w)

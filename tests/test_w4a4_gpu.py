@@ -177,7 +177,7 @@ def product64(rows, w64, per_row, gs):
 SHAPES = [(1, 128, 256), (1, 5120, 6144), (2, 256, 512), (7, 640, 1280), (8, 8192, 5120), (9, 128, 17408), (32, 384, 2560),
           (64, 1024, 2048), (65, 128, 256), (100, 2560, 3840), (127, 256, 768), (128, 256, 512), (129, 128, 512),
           (255, 512, 1024), (256, 256, 256), (257, 768, 1536), (300, 2560, 5120), (515, 640, 2048), (1111, 8192, 1024),
-          (2048, 5120, 512)]
+          (2048, 5120, 512), (600, 5504, 256), (1300, 3968, 768), (1030, 8064, 1536), (900, 128, 256), (3500, 384, 512)]
 
 
 @pytest.mark.parametrize("m, n, k", SHAPES, ids=str)
