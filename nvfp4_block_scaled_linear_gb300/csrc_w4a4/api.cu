@@ -188,8 +188,6 @@ int nvfp4_linear_w4a4(const nvfp4_rows* a, int64_t M, const nvfp4_weight* w, int
   if (const int st = check_rows(a)) return st;
   if ((y != nullptr) == (out != nullptr)) return NVFP4_ERR_INVALID;
   if (const int st = out ? check_rows(out) : check_matrix(y, w->N, 1, w->N)) return st;
-  Device d;
-  if (const int st = device(&d)) return st;
   Product p{};
   p.a_codes = a->codes;
   p.a_scales = a->scales;
@@ -204,7 +202,10 @@ int nvfp4_linear_w4a4(const nvfp4_rows* a, int64_t M, const nvfp4_weight* w, int
     rows += w->segment_rows[i];
     p.seg.end[i] = static_cast<int>(rows);
     p.seg.scale[i] = static_cast<float>(1.0 / (double(a->global_scale) * double(w->global_scale[i])));
+    if (bad_scale(p.seg.scale[i])) return NVFP4_ERR_INVALID;
   }
+  Device d;
+  if (const int st = device(&d)) return st;
   p.swiglu = swiglu != 0;
   p.y = static_cast<__nv_bfloat16*>(y);
   if (out) {

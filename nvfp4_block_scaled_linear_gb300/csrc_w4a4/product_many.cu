@@ -20,6 +20,11 @@
 // Both CTAs' copies count on the first one's barriers, whose thread issues the
 // MMAs; what it has read is free for both by one commit.
 //
+// Measured: 8192 x 34816 x 5120 gated into NVFP4 428 us, 6.8 PFLOP/s; 8192 x 5120 x
+// 17408 205 us, 7.1 PFLOP/s, 0.94 of four times the measured bf16 rate.  A stage's
+// products take 512 clocks; a tile of 20 stages takes some 1.3 times its products
+// (the sums handed over, 0.8 us, and the epilogue's own issue slots and stores).
+//
 // Warps: 0 copies, 1 issues the MMAs, 2 TMEM allocation, 4..19 the epilogue, four
 // for each quarter of the lanes, taking every fourth piece of 16 columns: a piece's chain (TMEM, the
 // exponentials, the quantisation, the store) is long, and 16 warps hide it where 8

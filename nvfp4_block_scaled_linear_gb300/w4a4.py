@@ -179,7 +179,9 @@ class Fp4Weight:
     """An NVFP4 weight [N, K] as ``linear_w4a4`` takes it, kept as long as the
     layer: N a multiple of 128, K of 256.
 
-    w_packed      uint8 [N, K/2], as ``linear`` takes it; referred to, not copied.
+    w_packed      uint8 [N, K/2], as ``linear`` takes it; referred to, not copied, and
+                  read before the kernel ahead of a call has ended: that kernel must
+                  not write it.
     w_scale       uint8 (or float8_e4m3fn) [N, K/16], as ``linear`` takes it; its
                   scales are laid out anew once, here, which synchronises.  None may
                   be negative or NaN.

@@ -122,6 +122,7 @@ def test_linear_rejects(lib):
     assert call(w=weight(parts=[496])) == INVALID and call(w=weight(parts=[500])) == SHAPE and call(w=weight(gs=(1, 1), parts=[256, 128])) == INVALID
     assert call(w=weight(gs=(1, 1), parts=[504, 8])) == SHAPE and call(w=weight(gs=(1, 1), parts=[512, 0])) == INVALID
     assert call(w=weight(gs=(), parts=[])) == INVALID
+    assert call(a=rows(gs=1e-30), w=weight(gs=(1e-30,))) == INVALID and call(a=rows(gs=1e30), w=weight(gs=(1e30,))) == INVALID
     w = weight()
     w.segments = 9
     assert call(w=w) == INVALID
