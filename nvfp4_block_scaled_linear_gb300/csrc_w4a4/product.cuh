@@ -86,13 +86,44 @@ __device__ __forceinline__ void store_bf16(__nv_bfloat16* y, const float (&v)[16
                    f32x2_to_bf16x2(v[8 * k + 4], v[8 * k + 5]), f32x2_to_bf16x2(v[8 * k + 6], v[8 * k + 7]));
 }
 
+enum { kPlain = 0, kGated = 1, kGatedRows = 2 };
+
+// 16 outputs n .. n + 15 of row m from their sums (of a gated product gate and up),
+// scaled, gated and rounded.
+template <int kMode, int kParts>
+__device__ __forceinline__ void outputs16(const Product& p, int64_t m, int n, float (&v)[kParts][16]) {
+  const int n_out = static_cast<int>(kMode == kPlain ? p.N : p.N / 2);
+  const float s = segment_scale(p.seg, n);
+  if (kMode == kPlain) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[0][k] *= s;
+  } else {
+    const float su = segment_scale(p.seg, n + n_out);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[0][k] = gated(v[0][k] * s, v[kParts - 1][k] * su);
+  }
+  if (kMode == kGatedRows) {
+    uint2 codes;
+    p.scales[scale_row(m, n_out) + scale_in_row(n >> 4)] = static_cast<uint8_t>(quantize16(v[0], p.out_gs, codes));
+    *reinterpret_cast<uint2*>(p.codes + m * (n_out >> 1) + (n >> 1)) = codes;
+  } else {
+    store_bf16(p.y + m * n_out + n, v[0]);
+  }
+}
+
 // Tensor map of codes [rows, K/2], boxes of `box` rows by 128 bytes.
 bool codes_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t K, int box);
 
 // Tensor map of blocked scales: row (128-row block) * (K / 64) + k / 64, boxes of 4 rows.
 bool scales_map(CUtensorMap* map, const uint8_t* scales, int64_t rows, int64_t K);
 
-// Few tokens: 128 tokens by kN weight rows a CTA, k split over a cluster.
+// Clusters of `split` CTAs, one on each SM, that the device holds at one time.
+int most_clusters(int split, const Device& d);
+
+// Up to 32 tokens: 128 weight rows (gated 128 of each) a CTA, the MMA's rows.
+int run_product_narrow(const Product& p, const Device& d, cudaStream_t stream);
+
+// 33 tokens and more: 128 tokens by 128 (gated 64 or 128 of each) weight rows a CTA.
 int run_product_few(const Product& p, const Device& d, cudaStream_t stream);
 
 // Many tokens: persistent pairs of CTAs, 256 tokens by 256 weight rows.

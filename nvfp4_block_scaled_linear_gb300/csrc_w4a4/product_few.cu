@@ -1,4 +1,4 @@
-// product_few.cu -- NVFP4 rows times an NVFP4 weight, up to 128 rows a CTA.
+// product_few.cu -- NVFP4 rows times an NVFP4 weight, 33 rows and more, 128 a CTA.
 //
 //   y[m, n] = scale * sum_k a[m, k] w[n, k]
 //
@@ -13,13 +13,11 @@
 // each CTA stores its sums of a piece in its owner's shared memory, and the owner
 // adds the CTAs' sums in their order: no atomics, the same bits on every run.
 //
-// Bound by the weights' bytes where there are many, by latency where there are few:
-// what one call needs beyond its bytes is the tokens' copy after the kernel ahead has
-// ended (some 1.5 us to the first product), the exchange (1.3 us and more for more
-// rows) and the outputs (0.9 us).  Measured back to back, weights from memory, one
-// token: 34816 x 5120 gated 18.6 us, 5.4 TB/s; 5120 x 17408 12.4 us, 4.1 TB/s; 8192 x
-// 5120 7.6 us; 5120 x 6144 6.8 us; 128 tokens: 20.3, 14.1, 9.4, 9.0 us.  The MMA's
-// idle rows cost nothing: the tensor pipe is 13 to 20% busy.
+// Between bytes and products: 128 tokens need 0.28 us a stage of 256 k for 18 KB of
+// weights, and beyond them the tokens' copy after the kernel ahead has ended, the
+// exchange (1.3 us and more with more rows) and the outputs.  Measured back to back,
+// weights from memory, 128 tokens: 34816 x 5120 gated 20.3 us, 5.0 TB/s; 5120 x 17408
+// 14.1 us; 8192 x 5120 9.4 us; 5120 x 6144 9.0 us.
 //
 // Warps: 0 copies, 1 MMA, 2 TMEM allocation; all eight the outputs.
 #include <algorithm>
@@ -34,8 +32,6 @@ constexpr int kThreads = 256;
 constexpr int kAllSmem = 226 * 1024, kHalfSmem = 112 * 1024;
 constexpr int kMaxStages = 12;
 constexpr int kMaxSplit = 8;
-
-enum { kPlain = 0, kGated = 1, kGatedRows = 2 };
 
 struct Few {
   Product p;
@@ -228,27 +224,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
   tc_fence_after_sync();
   constexpr int kPieces = kOut / 16;
-  const int n_out = static_cast<int>(kMode == kPlain ? p.N : p.N / 2);
-  // 16 outputs of a row, from the sums of their parts
   auto out = [&](int row, int piece, float (&v)[kParts][16]) {
-    const int64_t m = m0 + row;
-    const int n = tile * kOut + piece * 16;
-    const float s = segment_scale(p.seg, n);
-    if (kMode == kPlain) {
-#pragma unroll
-      for (int k = 0; k < 16; ++k) v[0][k] *= s;
-    } else {
-      const float su = segment_scale(p.seg, n + n_out);
-#pragma unroll
-      for (int k = 0; k < 16; ++k) v[0][k] = gated(v[0][k] * s, v[kParts - 1][k] * su);
-    }
-    if (kMode == kGatedRows) {
-      uint2 codes;
-      p.scales[scale_row(m, n_out) + scale_in_row(n >> 4)] = static_cast<uint8_t>(quantize16(v[0], p.out_gs, codes));
-      *reinterpret_cast<uint2*>(p.codes + m * (n_out >> 1) + (n >> 1)) = codes;
-    } else {
-      store_bf16(p.y + m * n_out + n, v[0]);
-    }
+    outputs16<kMode>(p, m0 + row, tile * kOut + piece * 16, v);
   };
   // two warps for each quarter of the lanes, taking pieces in turn
   const int quarter = warp & 3, row = quarter * 32 + lane;
@@ -329,6 +306,8 @@ int run(Few f, const Device& d, cudaStream_t stream) {
                 f.smem, stream, tm_a, tm_w, f);
 }
 
+}  // namespace
+
 // Clusters of `split` CTAs, one on each SM, that the device holds at one time: not
 // all of its SMs divide by every size (48 clusters of 3, 144 CTAs on 152 SMs, took
 // two rounds, 15 us against 10).  Asked once for each size.
@@ -356,26 +335,23 @@ int most_clusters(int split, const Device& d) {
   return n;
 }
 
-}  // namespace
-
 int run_product_few(const Product& p, const Device& d, cudaStream_t stream) {
   Few f{};
   f.p = p;
   f.a_rows = p.M >= 128 ? 128 : static_cast<int>((p.M + 7) / 8 * 8);
   const int64_t steps = p.K / kStageK, token_tiles = (p.M + 127) / 128;
   // Gated tiles of 64 outputs leave room in TMEM and shared memory for a second CTA, of
-  // this kernel or the next: one token through 12288 x 2048 7.2 us against 11.5 with
-  // tiles of 128, through 34816 x 5120 18.7 against 19.3.  With many tokens and more of
-  // them than SMs it is the MMAs' operand reads that count: 128 tokens through 34816 x
-  // 5120 21.9 us against 20.4.
+  // this kernel or the next: 128 tokens through 12288 x 2048 7.1 us against 17.7 with
+  // tiles of 128.  With many tokens and more of them than SMs it is the MMAs' operand
+  // reads that count: 128 tokens through 34816 x 5120 21.9 us against 20.3.
   const int n = p.swiglu && f.a_rows > 64 && p.N / 128 * token_tiles > d.num_sms ? 256 : 128;
   f.stage_bytes = f.a_rows * 128 + n * 128 + 4 * kScaleBlock * (p.swiglu ? 3 : 2);
   const int64_t tiles = p.N / n * token_tiles;
   // Of the splits that the device holds at one time the one with the least time, in ns
   // as measured: 280 a step (gated, with twice the MMAs and more scales, 400), and
   // where sums are exchanged 1300, 30 a CTA of the cluster and 3 more for each row.
-  // 128 tokens by 2048 rows, 24 steps: one CTA 9.8 us, 3 7.6, 8 9.8; 16 tokens 9.0, 6.0,
-  // 5.4; 1024 rows and 4 steps: one 3.3, 4 3.9.
+  // 128 tokens by 2048 rows, 24 steps: one CTA 9.8 us, 3 7.6, 8 9.8; 64 tokens 9.2, 6.3,
+  // 6.9; 1024 rows and 4 steps: one 3.4, 4 4.4.
   f.split = 1;
   int64_t least = INT64_MAX;
   for (int split = 1; split <= kMaxSplit && split <= steps && split * tiles <= std::max<int64_t>(d.num_sms, tiles);
@@ -387,10 +363,8 @@ int run_product_few(const Product& p, const Device& d, cudaStream_t stream) {
   }
   // With half of an SM's shared memory the next kernel's CTAs are resident, with their
   // first stages on the way, before this one's end; with all of it the ring is twice as
-  // deep.  One token: 10 steps over 8192 rows 7.9 us against 8.4, 23 steps over 5120
-  // 13.0 against 12.4; 128 tokens (stages half as many): 3 steps 10.4 against 13.5, 8
-  // steps 11.5 against 9.1.  More tiles than SMs: 20 steps over 34816 rows 18.7 against
-  // 26.0.  A gated tile of 128 outputs takes all of TMEM and is alone in any case.
+  // deep.  128 tokens: 3 steps 10.4 us against 13.5, 8 steps 11.5 against 9.1.  A gated
+  // tile of 128 outputs takes all of TMEM and is alone in any case.
   const int half = (kHalfSmem - 1024) / f.stage_bytes;
   f.smem = n == 256 || (steps / f.split > 2 * half && tiles <= d.num_sms) ? kAllSmem : kHalfSmem;
   // the sums lie where the stages were (an odd split leaves its owners unequal pieces,

@@ -60,8 +60,6 @@ struct Shape {
   static_assert(kSmem <= 226 * 1024, "shared memory");
 };
 
-enum { kPlain = 0, kGated = 1, kGatedRows = 2 };
-
 __device__ __forceinline__ void umma_nvfp4_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                                 uint32_t a_scales, uint32_t b_scales,
                                                 uint32_t accumulate) {

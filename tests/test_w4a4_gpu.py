@@ -177,7 +177,8 @@ def product64(rows, w64, per_row, gs):
 SHAPES = [(1, 128, 256), (1, 5120, 6144), (2, 256, 512), (7, 640, 1280), (8, 8192, 5120), (9, 128, 17408), (32, 384, 2560),
           (64, 1024, 2048), (65, 128, 256), (100, 2560, 3840), (127, 256, 768), (128, 256, 512), (129, 128, 512),
           (255, 512, 1024), (256, 256, 256), (257, 768, 1536), (300, 2560, 5120), (515, 640, 2048), (1111, 8192, 1024),
-          (2048, 5120, 512), (600, 5504, 256), (1300, 3968, 768), (1030, 8064, 1536), (900, 128, 256), (3500, 384, 512)]
+          (2048, 5120, 512), (600, 5504, 256), (1300, 3968, 768), (1030, 8064, 1536), (900, 128, 256), (3500, 384, 512),
+          (16, 128, 256), (17, 1024, 4352), (24, 640, 1024), (31, 256, 17408), (33, 640, 1024), (32, 16640, 256), (40, 20608, 512)]
 
 
 @pytest.mark.parametrize("m, n, k", SHAPES, ids=str)
@@ -232,7 +233,8 @@ def gated64(rows, w64, per_row, gs, k):
 
 
 GATED = [(1, 512, 256), (1, 34816, 512), (3, 1024, 2560), (32, 512, 5120), (100, 2048, 512), (128, 512, 512),
-         (129, 1024, 256), (515, 1536, 1024), (700, 512, 3840)]
+         (129, 1024, 256), (515, 1536, 1024), (700, 512, 3840),
+         (8, 512, 17408), (17, 1536, 1024), (32, 34816, 512), (33, 1024, 1024), (40, 512, 256), (2, 40960, 256), (90, 20480, 768)]
 
 
 @pytest.mark.parametrize("m, n, k", GATED + [(5, 256, 512), (200, 768, 512)], ids=str)
