@@ -179,6 +179,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait(&full[it % f.stages], (it / f.stages) & 1, &none)) *abort_flag = 1;
     }
   } else if (warp == 1) {
+    // (before any wait with a limit: the kernel ahead may take its time)
+    griddep_wait();
     // two halves of 128 rows' scales cannot be one operand: an MMA for each
     constexpr int kMmas = kBox == 64 ? 2 : 1;
     constexpr uint32_t idesc = idesc_nvfp4(128, kN / kMmas);

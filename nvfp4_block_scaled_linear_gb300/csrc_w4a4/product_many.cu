@@ -250,6 +250,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
   } else if (warp == 1) {
     // The whole warp walks the stages, an elected lane issues.
+    // (before any wait with a limit: the kernel ahead may take its time)
+    griddep_wait();
     if (rank == 0) {
       constexpr uint32_t idesc = idesc_nvfp4(kTile, kN);
       int slot = 0;
@@ -304,6 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int none = 0;
     if (!wait(&done, 0, &none)) *abort_flag = 1;
   } else if (warp >= 4) {
+    griddep_wait();
     const int quarter = warp & 3, h = (warp - 4) >> 2;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
     const int64_t n_out = kMode == kPlain ? p.N : p.N / 2;

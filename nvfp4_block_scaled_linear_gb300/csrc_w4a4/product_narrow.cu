@@ -161,6 +161,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait(&full[it % f.stages], (it / f.stages) & 1, &none)) *abort_flag = 1;
     }
   } else if (warp == 1) {
+    // (before any wait with a limit: the kernel ahead may take its time)
+    griddep_wait();
     const uint32_t idesc = idesc_nvfp4(128, f.cols);
     int slot = 0;
     uint32_t parity = 0;

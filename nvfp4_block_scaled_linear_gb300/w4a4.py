@@ -326,6 +326,8 @@ def add_rms_norm_quantize(x, residual, weight, eps=1e-6, global_scale=1.0, out=N
 
 
 def _check_product(a, w):
+    if not (isinstance(a, Fp4Rows) and isinstance(w, Fp4Weight)):
+        raise TypeError("a product is of Fp4Rows and an Fp4Weight, got %s and %s" % (type(a).__name__, type(w).__name__))
     if a.shape[1] != w.shape[1] or a.device != w.device:
         raise ValueError("rows %s on %s do not fit a weight %s on %s" % (a.shape, a.device, w.shape, w.device))
 

@@ -52,6 +52,10 @@ def test_binding_refuses():
         pkg.quantize_rows(x, 2.0, out=pkg.new_fp4_rows(4, 512, 1.0))
     with pytest.raises(ValueError):
         pkg.quantize_rows(x, out=pkg.new_fp4_rows(5, 512))
+    for bad in ((x, w), (rows, w.codes), (w, w), (rows, rows)):
+        for call in (pkg.linear_w4a4, pkg.linear_w4a4_swiglu, pkg.linear_w4a4_swiglu_quantize):
+            with pytest.raises(TypeError):
+                call(*bad)
     with pytest.raises(ValueError):
         pkg.linear_w4a4(pkg.quantize_rows(x[:, :256]), w)
     with pytest.raises(ValueError):
