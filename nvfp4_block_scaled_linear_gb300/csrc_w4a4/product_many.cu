@@ -1,6 +1,6 @@
 // product_many.cu -- NVFP4 rows times an NVFP4 weight, many rows.
 //
-// Bound by the tensor cores.  A pair of CTAs works on 256 tokens x 256 weight
+// Bound by the copies and the tensor cores alike.  A pair of CTAs works on 256 tokens x 256 weight
 // rows as one MMA (cta_group::2): each brings its 128 tokens and half of the
 // weight rows, so that a byte of either is read from shared memory half as often
 // as by a CTA alone.  Of a gate/up pair the first CTA brings the gate's rows and
@@ -22,7 +22,9 @@
 //
 // Measured: 8192 x 34816 x 5120 gated into NVFP4 428 us, 6.8 PFLOP/s; 8192 x 5120 x
 // 17408 205 us, 7.1 PFLOP/s, 0.94 of four times the measured bf16 rate.  A stage's
-// products take 512 clocks; a tile of 20 stages takes some 1.3 times its products
+// products take 512 clocks; its 38 KB take 600 through an SM's port to L2 (64 bytes a
+// clock, which no kernel here got more out of): that is what a pair's tile is bound by,
+// and its copies of scales cost nothing.  A tile of 20 stages takes some 1.2 times that
 // (the sums handed over, 0.8 us, and the epilogue's own issue slots and stores).
 //
 // Warps: 0 copies, 1 issues the MMAs, 2 TMEM allocation, 4..19 the epilogue, four
