@@ -20,7 +20,7 @@
 // Both CTAs' copies count on the first one's barriers, whose thread issues the
 // MMAs; what it has read is free for both by one commit.
 //
-// Measured: 8192 x 34816 x 5120 gated into NVFP4 428 us, 6.8 PFLOP/s; 8192 x 5120 x
+// Measured: 8192 x 34816 x 5120 gated into NVFP4 424 us, 6.9 PFLOP/s; 8192 x 5120 x
 // 17408 205 us, 7.1 PFLOP/s, 0.94 of four times the measured bf16 rate.  A stage's
 // products take 512 clocks; its 38 KB take 600 through an SM's port to L2 (64 bytes a
 // clock, which no kernel here got more out of): that is what a pair's tile is bound by,
@@ -105,14 +105,14 @@ __device__ __forceinline__ void load_pair(void* dst, const CUtensorMap* map, uin
 struct Many {
   Product p;
   int token_tiles, weight_tiles, tiles, pairs;
+  int band;          // token tiles of a band of the tile order
 };
 
-// Tile t: bands of kBand token tiles; in a band weight tile by weight tile, its
-// token tiles innermost.  The pairs at work at one time then share few of either.
-constexpr int kBand = 8;
+// Tile t: bands of token tiles; in a band weight tile by weight tile, its token tiles
+// innermost.  The weights then pass by once for each band, whose tokens stay in L2.
 __device__ __forceinline__ void tile_at(const Many& f, int t, int& token_tile, int& weight_tile) {
-  const int band = t / (kBand * f.weight_tiles), first = band * kBand;
-  const int width = min(kBand, f.token_tiles - first), r = t - band * kBand * f.weight_tiles;
+  const int band = t / (f.band * f.weight_tiles), first = band * f.band;
+  const int width = min(f.band, f.token_tiles - first), r = t - band * f.band * f.weight_tiles;
   weight_tile = r / width;
   token_tile = first + r - weight_tile * width;
 }
@@ -415,6 +415,10 @@ int run(const Product& p, const Device& d, cudaStream_t stream) {
   f.token_tiles = static_cast<int>(token_tiles);
   f.weight_tiles = static_cast<int>(tiles / token_tiles);
   f.tiles = static_cast<int>(tiles);
+  // Up to 32 token tiles, of at most 24 MB, but 8.  8192 tokens x 34816 x 5120 gated:
+  // bands of 8 435 us, of 16 428, of 32 (21 MB) 423; x 5120 x 17408 8 (18 MB) 213, 16
+  // 216, 32 233.
+  f.band = static_cast<int>(std::max<int64_t>(8, std::min<int64_t>(32, (24 << 20) / (kTile / 2 * p.K))));
   f.pairs = static_cast<int>(tiles < d.num_sms / 2 ? tiles : d.num_sms / 2);
   return launch(2, many_kernel<kN, kMode>, dim3(2 * f.pairs), dim3(kThreads), kSmem, stream, tm_a, tm_w, tm_sa,
                 tm_sw, f);

@@ -184,6 +184,34 @@ def test_captured_and_replayed(m):
                 assert torch.equal(a, b)
 
 
+_FIRST = """
+import torch, nvfp4_block_scaled_linear_gb300 as pkg
+dev = torch.device("cuda:0")
+w = pkg.Fp4Weight(torch.full((512, 512), 0x22, dtype=torch.uint8, device=dev),
+                  torch.full((512, 64), 0x38, dtype=torch.uint8, device=dev), 1.0)
+xs = [torch.ones((m, 1024), dtype=torch.bfloat16, device=dev) for m in (1, 100, 1000)]
+nw = torch.ones(1024, dtype=torch.bfloat16, device=dev)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    ys = [pkg.linear_w4a4(pkg.quantize_rows(x), w) for x in xs]
+    zs = [pkg.linear_w4a4_swiglu_quantize(pkg.add_rms_norm_quantize(x, x, nw)[0], w) for x in xs]
+g.replay()
+torch.cuda.synchronize()
+assert all(bool((y == 1024.0).all()) for y in ys), ys
+assert pkg.w4a4_error() == 0
+"""
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _FIRST], cwd=root, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stderr[-1500:]
+
+
 def test_back_to_back_over_the_same_buffers():
     """A chain of products whose rows and results live in the same memory, with nothing between them: each reads
     what the one before wrote."""

@@ -153,6 +153,25 @@ def test_norm_in_place_and_strided():
     assert torch.equal(other, base)                                # nothing around it was written
 
 
+@pytest.mark.parametrize("m, k", [(1, 512), (40, 1536), (700, 4096)])
+def test_outputs_over_either_input(m, k):
+    x, res = hidden(m, k, 14).to(DEV), hidden(m, k, 15).to(DEV)
+    w = (1 + 0.1 * torch.randn(k, generator=torch.Generator().manual_seed(3))).to(BF16).to(DEV)
+    want_y, want_r = pkg.add_rms_norm(x, res, w)
+    rows, _ = pkg.add_rms_norm_quantize(x, res, w, 1e-6, 150.0)
+    for swap in (False, True):
+        a, b = x.clone(), res.clone()
+        y, r = pkg.add_rms_norm(a, b, w, out=b if swap else a, residual_out=a if swap else b)
+        assert torch.equal(y, want_y) and torch.equal(r, want_r)
+        a, b = x.clone(), res.clone()
+        q, r = pkg.add_rms_norm_quantize(a, b, w, 1e-6, 150.0, residual_out=a if swap else b)
+        assert torch.equal(r, want_r) and torch.equal(q.codes, rows.codes)
+        assert torch.equal(ref.plain_scales(q), ref.plain_scales(rows))
+    a = x.clone()
+    y, r = pkg.add_rms_norm(a, None, w, out=a, residual_out=res)    # no residual: the sum is x, copied
+    assert torch.equal(r, x) and torch.equal(y, pkg.add_rms_norm(x, None, w)[0])
+
+
 def test_norm_not_finite_rows_stay_apart():
     x = hidden(4, 512, 11)
     x[1, 3], x[2, 5] = float("nan"), float("inf")
