@@ -194,7 +194,8 @@ nw = torch.ones(1024, dtype=torch.bfloat16, device=dev)
 torch.cuda.synchronize()
 g = torch.cuda.CUDAGraph()
 with torch.cuda.graph(g):
-    ys = [pkg.linear_w4a4(pkg.quantize_rows(x), w) for x in xs]
+    # (ones with the global scale 6: block scales of one, codes of 6, without a rounding)
+    ys = [pkg.linear_w4a4(pkg.quantize_rows(x, 6.0), w) for x in xs]
     zs = [pkg.linear_w4a4_swiglu_quantize(pkg.add_rms_norm_quantize(x, x, nw)[0], w) for x in xs]
 g.replay()
 torch.cuda.synchronize()
