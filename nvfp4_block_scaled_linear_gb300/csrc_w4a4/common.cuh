@@ -83,7 +83,8 @@ __device__ __forceinline__ float from_e4m3(uint32_t b) {
 // byte, by the steps of nvfp4_w4a4.h.  The quotient of x = RN(v gs) by the scale s is
 // correctly rounded without a division for each value: with r = RN(1/s), q0 = RN(x r),
 // rem = RN(x - q0 s), q = RN(q0 + rem r) (Markstein's refinement; s has 4 significant
-// bits, so r is far from the one case it excepts); the sixth of the largest likewise.
+// bits, so r is far from the one case it excepts; checked for every significand in
+// tests/test_quantize_division.py); the sixth of the largest likewise.
 // A quotient so small that a step underflows is far below the first threshold, of
 // e2m1 or of e4m3.
 __device__ __forceinline__ uint32_t quantize16(const float (&v)[16], uint32_t top, float gs, uint2& codes) {
