@@ -63,11 +63,12 @@ __device__ __forceinline__ void st_cluster_b32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-template <int kMode>
+// kPer: parts of an output (its sum, or gate and up) that a stage brings weights for.
+template <int kMode, int kPer>
 __global__ void __launch_bounds__(kThreads, 1)
     narrow_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
                   const Narrow f) {
-  constexpr int kParts = kMode == kPlain ? 1 : 2;         // parts of an output: its sum, or gate and up
+  constexpr int kParts = kMode == kPlain ? 1 : 2, kRuns = kParts / kPer;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done;
   __shared__ int abort_word;
@@ -83,10 +84,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int steps = static_cast<int>(p.K / kStageK);
   const int s0 = static_cast<int>(int64_t(steps) * rank / f.split);
   const int s1 = static_cast<int>(int64_t(steps) * (rank + 1) / f.split);
-  const int n_steps = s1 - s0;
+  const int n_stages = (s1 - s0) * kRuns;
   auto w_row = [&](int i) { return tile * kTile + i * static_cast<int>(p.N / 2); };
-  const int a_off = kParts * kWeights, sw_off = a_off + f.cols * 128;
-  const int sa_off = sw_off + kParts * 4 * kScaleBlock;
+  const int a_off = kPer * kWeights, sw_off = a_off + f.cols * 128;
+  const int sa_off = sw_off + kPer * 4 * kScaleBlock;
   float* sums = reinterpret_cast<float*>(smem + f.stages * f.stage_bytes);
 
   if (threadIdx.x == 0) {
@@ -115,24 +116,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // the whole warp walks the stages, an elected lane issues
-    auto weights = [&](int it, int slot) {
+    // stage g: k step g / kRuns, parts from g % kRuns on
+    auto weights = [&](int g, int slot) {
+      const int it = s0 + g / kRuns;
       uint8_t* st = smem + slot * f.stage_bytes;
       mbar_arrive_expect_tx(&full[slot], f.stage_bytes);
 #pragma unroll
-      for (int i = 0; i < kParts; ++i) {
-        tma_load_2d(st + i * kWeights, &tm_w, &full[slot], (s0 + it) * 128, w_row(i));
+      for (int i = 0; i < kPer; ++i) {
+        const int w = w_row(g % kRuns + i);
+        tma_load_2d(st + i * kWeights, &tm_w, &full[slot], it * 128, w);
         bulk_load(st + sw_off + i * 4 * kScaleBlock,
-                  p.w_scales + (int64_t(w_row(i) / 128) * (p.K / kMmaK) + (s0 + it) * 4) * kScaleBlock,
-                  4 * kScaleBlock, &full[slot]);
+                  p.w_scales + (int64_t(w / 128) * (p.K / kMmaK) + it * 4) * kScaleBlock, 4 * kScaleBlock,
+                  &full[slot]);
       }
     };
-    auto tokens = [&](int it, int slot) {
+    auto tokens = [&](int g, int slot) {
+      const int it = s0 + g / kRuns;
       uint8_t* st = smem + slot * f.stage_bytes;
-      tma_load_2d(st + a_off, &tm_a, &full[slot], (s0 + it) * 128, 0);
-      bulk_load(st + sa_off, p.a_scales + int64_t(s0 + it) * 4 * kScaleBlock, 4 * kScaleBlock, &full[slot]);
+      tma_load_2d(st + a_off, &tm_a, &full[slot], it * 128, 0);
+      bulk_load(st + sa_off, p.a_scales + int64_t(it) * 4 * kScaleBlock, 4 * kScaleBlock, &full[slot]);
     };
     // weights do not wait for the kernel ahead in the stream, tokens do
-    const int pre = n_steps < f.stages ? n_steps : f.stages;
+    const int pre = n_stages < f.stages ? n_stages : f.stages;
     if (elect_one()) {
       prefetch_tensormap(&tm_a);
       prefetch_tensormap(&tm_w);
@@ -145,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     int issued = pre, slot = pre == f.stages ? 0 : pre;
     uint32_t parity = 0;
-    for (int it = pre; it < n_steps; ++it) {
+    for (int it = pre; it < n_stages; ++it) {
       if (!__all_sync(0xffffffffu, wait(&empty[slot], parity, abort_flag))) break;
       if (elect_one()) {
         weights(it, slot);
@@ -166,26 +171,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t idesc = idesc_nvfp4(128, f.cols);
     int slot = 0;
     uint32_t parity = 0;
-    for (int it = 0; it < n_steps; ++it) {
+    for (int g = 0; g < n_stages; ++g) {
       if (!__all_sync(0xffffffffu, wait(&full[slot], parity, abort_flag))) break;
       tc_fence_after_sync();
       if (elect_one()) {
-        const uint32_t st = smem_addr(smem) + slot * f.stage_bytes;
+        const uint32_t st = smem_addr(smem) + slot * f.stage_bytes, d = tmem + 32 * (g % kRuns);
         const uint64_t w = umma_desc_sw128(st), a = umma_desc_sw128(st + a_off);
         const uint64_t sw = scale_desc(st + sw_off), sa = scale_desc(st + sa_off);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
 #pragma unroll
-          for (int i = 0; i < kParts; ++i)
-            copy_scales(tmem + kColW + 4 * (kParts * j + i), sw + (4 * i + j) * (kScaleBlock >> 4));
+          for (int i = 0; i < kPer; ++i)
+            copy_scales(tmem + kColW + 4 * (kPer * j + i), sw + (4 * i + j) * (kScaleBlock >> 4));
           copy_scales(tmem + kColA + 4 * j, sa + j * (kScaleBlock >> 4));
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int i = 0; i < kParts; ++i)
-            umma_nvfp4(tmem + 32 * i, w + 2 * j + i * (kWeights >> 4), a + 2 * j, idesc,
-                       tmem + kColW + 4 * (kParts * j + i), tmem + kColA + 4 * j, (it | j) != 0);
+          for (int i = 0; i < kPer; ++i)
+            umma_nvfp4(d + 32 * i, w + 2 * j + i * (kWeights >> 4), a + 2 * j, idesc,
+                       tmem + kColW + 4 * (kPer * j + i), tmem + kColA + 4 * j, (g / kRuns | j) != 0);
         umma_commit(&empty[slot]);
       }
       __syncwarp();
@@ -250,10 +255,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 2) tmem_dealloc(tmem, kCols);
 }
 
-template <int kMode>
+template <int kMode, int kPer>
 int run(const Narrow& f, const Device& d, cudaStream_t stream) {
   static std::atomic<bool> ready[kMaxDevices];
-  if (const int st = allow_smem(narrow_kernel<kMode>, kAllSmem, d, ready)) return st;
+  if (const int st = allow_smem(narrow_kernel<kMode, kPer>, kAllSmem, d, ready)) return st;
   CUtensorMap tm_a, tm_w;
   if (!codes_map(&tm_a, f.p.a_codes, f.p.M, f.p.K, f.cols) || !codes_map(&tm_w, f.p.w_codes, f.p.N, f.p.K, kTile))
     return NVFP4_ERR_LAUNCH;
@@ -261,7 +266,7 @@ int run(const Narrow& f, const Device& d, cudaStream_t stream) {
   if (f.stages < 1 || f.split < 1 || f.split > kMaxSplit ||
       f.stages * f.stage_bytes + sums_bytes(kParts, f.split, f.cols) > f.smem - 1024)
     return NVFP4_ERR_LAUNCH;
-  return launch(f.split, narrow_kernel<kMode>, dim3(static_cast<unsigned>(f.p.N / (kTile * kParts)) * f.split),
+  return launch(f.split, narrow_kernel<kMode, kPer>, dim3(static_cast<unsigned>(f.p.N / (kTile * kParts)) * f.split),
                 dim3(kThreads), f.smem, stream, tm_a, tm_w, f);
 }
 
@@ -272,8 +277,13 @@ int run_product_narrow(const Product& p, const Device& d, cudaStream_t stream) {
   f.p = p;
   f.cols = static_cast<int>((p.M + 7) / 8 * 8);
   const int parts = p.swiglu ? 2 : 1;
-  f.stage_bytes = parts * kWeights + f.cols * 128 + 4 * kScaleBlock * (parts + 1);
   const int64_t steps = p.K / kStageK, tiles = p.N / (kTile * parts);
+  // A stage for each of gate and up where there are more tiles than SMs: half of an SM's
+  // shared memory then holds four, and two CTAs an SM are one round.  One token through
+  // 40960 x 5120 22.0 us against 28.6 (two rounds of CTAs with both in a stage); where a
+  // tile has an SM for itself 34816 x 5120 18.9 against 18.3.
+  const int per = tiles > d.num_sms ? 1 : parts;
+  f.stage_bytes = per * kWeights + f.cols * 128 + 4 * kScaleBlock * (per + 1);
   // Of the splits that the device holds at one time the one with the least time, in ns
   // as measured: 180 a step (gated 310), and where sums are exchanged 900 and 60 a CTA.
   f.split = 1;
@@ -288,12 +298,14 @@ int run_product_narrow(const Product& p, const Device& d, cudaStream_t stream) {
   // With half of an SM's shared memory the next kernel's CTAs are resident, with their
   // first stages on the way, before this one's end; with all of it the ring is twice as
   // deep.  8192 x 5120, 10 steps: 7.0 us against 7.9; 5120 x 17408, 23 steps, 32 tokens:
-  // 13.7 against 12.1.  Half holds two gated stages, too few: 34816 x 5120 22.1 us
+  // 13.7 against 12.1.  Half holds two stages of both gate and up, too few: 34816 x 5120 22.1 us
   // against 18.3, 12288 x 2048 6.6 against 6.0.
   const int half = (kHalfSmem - 1024 - sums) / f.stage_bytes;
-  f.smem = p.swiglu || (steps / f.split > 2 * half && tiles <= d.num_sms) ? kAllSmem : kHalfSmem;
+  f.smem = per == 2 || (steps / f.split > 2 * half && tiles <= d.num_sms) ? kAllSmem : kHalfSmem;
   f.stages = std::min((f.smem - 1024 - sums) / f.stage_bytes, kMaxStages);
-  return !p.swiglu ? run<kPlain>(f, d, stream) : p.codes ? run<kGatedRows>(f, d, stream) : run<kGated>(f, d, stream);
+  if (!p.swiglu) return run<kPlain, 1>(f, d, stream);
+  if (per == 1) return p.codes ? run<kGatedRows, 1>(f, d, stream) : run<kGated, 1>(f, d, stream);
+  return p.codes ? run<kGatedRows, 2>(f, d, stream) : run<kGated, 2>(f, d, stream);
 }
 
 }  // namespace w4a4

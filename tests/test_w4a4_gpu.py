@@ -253,7 +253,7 @@ def gated64(rows, w64, per_row, gs, k):
 
 GATED = [(1, 512, 256), (1, 34816, 512), (3, 1024, 2560), (32, 512, 5120), (100, 2048, 512), (128, 512, 512),
          (129, 1024, 256), (515, 1536, 1024), (700, 512, 3840),
-         (8, 512, 17408), (17, 1536, 1024), (32, 34816, 512), (33, 1024, 1024), (40, 512, 256), (2, 40960, 256), (90, 20480, 768)]
+         (8, 512, 17408), (17, 1536, 1024), (32, 34816, 512), (33, 1024, 1024), (40, 512, 256), (2, 40960, 256), (32, 40960, 1280), (9, 39424, 768), (90, 20480, 768)]
 
 
 @pytest.mark.parametrize("m, n, k", GATED + [(5, 256, 512), (200, 768, 512)], ids=str)
