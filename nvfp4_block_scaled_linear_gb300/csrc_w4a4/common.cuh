@@ -213,13 +213,37 @@ __device__ __forceinline__ float segment_scale(const Segments& s, int col) {
 }
 
 // silu(g) * u = g / (1 + 2^(-g log2 e)) * u, exponential and reciprocal by the
-// hardware's approximations (2^-22 and 2^-23 of the value).  Where the exponential
-// overflows (g < -88) the result is a zero; the exact one is below 1e-36.
+// hardware's approximations (2^-22 and 2^-23 of the value); the exponent's rounding
+// to fp32 is |g| 2^-24 of the exponential more, 2^-18 at g = -80.  From g >= -80 the sum
+// and its reciprocal stay in fp32's normal range, and an exponential below it is
+// nothing beside 1.
 __device__ __forceinline__ float gated(float g, float u) {
   float e, r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
   return g * r * u;
+}
+
+// Below, where 1 is nothing beside the exponential: silu(g) = g e^g, in fp32's normal
+// range down to about g = -92 and smoothly to zero from there.
+constexpr float kSiluTail = -80.f;
+__device__ __forceinline__ float gated_tail(float g, float u) { return g * expf(g) * u; }
+
+// g[i] = silu(g[i] sg) * (u[i] su).  One comparison for the sixteen: so low a gate is rare.
+__device__ __forceinline__ void gated16(float (&g)[16], const float (&u)[16], float sg, float su) {
+  float low = 0.f;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    g[k] *= sg;
+    low = fminf(low, g[k]);
+  }
+  if (low >= kSiluTail) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) g[k] = gated(g[k], u[k] * su);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) g[k] = g[k] < kSiluTail ? gated_tail(g[k], u[k] * su) : gated(g[k], u[k] * su);
+  }
 }
 
 struct Product {

@@ -98,9 +98,7 @@ __device__ __forceinline__ void outputs16(const Product& p, int64_t m, int n, fl
 #pragma unroll
     for (int k = 0; k < 16; ++k) v[0][k] *= s;
   } else {
-    const float su = segment_scale(p.seg, n + n_out);
-#pragma unroll
-    for (int k = 0; k < 16; ++k) v[0][k] = gated(v[0][k] * s, v[kParts - 1][k] * su);
+    gated16(v[0], v[kParts - 1], s, segment_scale(p.seg, n + n_out));
   }
   if (kMode == kGatedRows) {
     uint2 codes;

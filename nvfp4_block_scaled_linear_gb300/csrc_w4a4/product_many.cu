@@ -355,13 +355,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       } else {
-        auto out = [&](int piece, const float (&g)[16], const float (&u)[16]) {
+        auto out = [&](int piece, float (&v)[16], const float (&u)[16]) {     // (v: the gate's sums)
           const int n = nt * kHalf + piece * 16;
           if (!inside) return;
-          const float sg = segment_scale(p.seg, n), su = segment_scale(p.seg, n + static_cast<int>(n_out));
-          float v[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) v[k] = gated(g[k] * sg, u[k] * su);
+          gated16(v, u, segment_scale(p.seg, n), segment_scale(p.seg, n + static_cast<int>(n_out)));
           if (kMode == kGatedRows) {
             uint2 codes;
             p.scales[scale_row(m, n_out) + scale_in_row(n >> 4)] = static_cast<uint8_t>(quantize16(v, p.out_gs, codes));
