@@ -303,10 +303,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (elect_one()) commit_pair(&done);
       __syncwarp();
+      // every product is over before TMEM is given back
+      volatile int none = 0;
+      if (!wait(&done, 0, &none)) *abort_flag = 1;
     }
-    // every product is over before TMEM is given back
-    volatile int none = 0;
-    if (!wait(&done, 0, &none)) *abort_flag = 1;
   } else if (warp >= 4) {
     griddep_wait();
     const int quarter = warp & 3, h = (warp - 4) >> 2;
@@ -381,6 +381,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // (read before the tile after next is begun: its sums_free comes later)
       tc_fence_before_sync();
+    }
+    // The second CTA learns here that every product is over: with its last tile read, the
+    // limit is of what the first one still commits.  (From the kernel's start it would be
+    // of the whole kernel, and more than a second of products would end unfinished.)
+    if (rank == 1 && warp == 4) {
+      volatile int none = 0;
+      if (!wait(&done, 0, &none)) *abort_flag = 1;
     }
   }
   __syncwarp();
