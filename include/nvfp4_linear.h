@@ -38,7 +38,9 @@
  * the tail of the kernel before it in the stream, while the activations are
  * read, and the output written, only after that kernel has completed.  So
  * the weights and scales must not be written by the kernel immediately
- * before the call in the same stream.  Calls may be captured into a CUDA
+ * before the call in the same stream, nor, where that is a call of this
+ * library too (which may itself have started early), by the one before that,
+ * and so on.  Calls may be captured into a CUDA
  * graph; a captured call keeps the pointers it was given.  A device-side failure (a pipeline wait that timed out)
  * does not fault the context: the kernel winds down and sets a bit in the
  * library's device error word, readable with nvfp4_device_status().

@@ -18,7 +18,12 @@
  * and return an NVFP4_* status.  Kernels are launched with programmatic
  * dependent launch; nvfp4_linear_w4a4 reads the weight's codes and scales
  * before the kernel ahead of it in the stream has completed, so that kernel
- * must not write them.  Everything else is read and written after it.
+ * must not write them; and where it is a call of this library too, which may
+ * itself have started early, nor may the call ahead of that one, and so on up
+ * to a kernel of another kind, a copy or a wait on the host.
+ * nvfp4_w4a4_scale_layout is the exception: it lets nothing start before its
+ * own end and may stand anywhere ahead, directly as well.  Everything else is
+ * read and written after the kernel ahead.
  *
  * NVFP4 rows [M, K] stand for  e2m1(code[m,k]) * e4m3(scale[m, k/16]) /
  * global_scale.  Codes: uint8 [M, K/2], the low nibble holding the even k.

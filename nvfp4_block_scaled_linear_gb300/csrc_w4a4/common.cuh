@@ -133,8 +133,10 @@ struct Device {
 // The current device's set-up (NVFP4_ERR_DEVICE where it is not sm_103).
 int device(Device* out);
 
-// Launch, in clusters of `cluster` CTAs, with programmatic stream
-// serialization.
+// Launch, in clusters of `cluster` CTAs, with programmatic stream serialization.
+// A kernel lets the next one start (griddep_launch_dependents) only after its own
+// griddep_wait: what runs then is that kernel and no earlier one, so that a product's
+// early reads of its weight can meet no writes but the kernel's directly ahead.
 template <typename... P, typename... A>
 int launch(int cluster, void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
            cudaStream_t stream, const A&... args) {

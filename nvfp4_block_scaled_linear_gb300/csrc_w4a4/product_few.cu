@@ -127,7 +127,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = tmem_slot;
-  if (threadIdx.x == 0) griddep_launch_dependents();
 
   if (warp == 0) {
     // the whole warp walks the stages, an elected lane issues
@@ -158,8 +157,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     griddep_wait();
-    if (elect_one())
+    if (elect_one()) {
+      griddep_launch_dependents();                               // (after the wait: see launch())
       for (int it = 0; it < pre; ++it) tokens(it, it);
+    }
     __syncwarp();
     int issued = pre, slot = pre == f.stages ? 0 : pre;
     uint32_t parity = 0;

@@ -174,7 +174,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync();                                                 // (the other CTA's barriers are set up)
   tc_fence_after_sync();
   const uint32_t tmem = tmem_slot;
-  if (threadIdx.x == 0) griddep_launch_dependents();
 
   if (warp == 0) {
     // The whole warp walks the tiles, an elected lane issues.
@@ -227,8 +226,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     griddep_wait();
-    if (elect_one())
+    if (elect_one()) {
+      griddep_launch_dependents();                               // (after the wait: see launch())
       for (int it = 0; it < pre; ++it) tokens(q, it, it);
+    }
     __syncwarp();
     int issued = pre, slot = pre == kStages ? 0 : pre, it = pre;
     uint32_t parity = pre == kStages ? 0 : 1;                    // (slots not used yet are free)

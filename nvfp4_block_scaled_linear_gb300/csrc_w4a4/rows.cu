@@ -149,8 +149,8 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const Quan
 __global__ void __launch_bounds__(256)
     scale_layout_kernel(const uint8_t* scale, int64_t N, int64_t K, uint8_t* blocked,
                         unsigned int* refused) {
+  // No early start of the kernel behind: a product reads scales before it waits.
   griddep_wait();
-  griddep_launch_dependents();
   const int64_t words = K >> 6, total = N * words;
   for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
     const int64_t n = i / words, j = i - n * words;
@@ -164,6 +164,7 @@ __global__ void __launch_bounds__(256)
     }
     *reinterpret_cast<uint32_t*>(blocked + scale_row(n, K) + j * 512) = out;
   }
+  __threadfence();
 }
 
 }  // namespace

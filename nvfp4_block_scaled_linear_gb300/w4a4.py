@@ -180,8 +180,9 @@ class Fp4Weight:
     layer: N a multiple of 128, K of 256.
 
     w_packed      uint8 [N, K/2], as ``linear`` takes it; referred to, not copied, and
-                  read before the kernel ahead of a call has ended: that kernel must
-                  not write it.
+                  read before the kernel ahead of a call has ended: neither that kernel
+                  nor, where it is one of this library's, one of those that it follows
+                  directly may write it.
     w_scale       uint8 (or float8_e4m3fn) [N, K/16], as ``linear`` takes it; its
                   scales are laid out anew once, here, which synchronises.  None may
                   be negative or NaN.
