@@ -287,7 +287,8 @@ def _norm(given, x, residual, weight, eps, residual_out, y, rows, stream):
     if residual_out is not None:
         po, so = _matrix(residual_out, "residual_out", shape, dev)
         total = residual_out
-    elif residual is not None:
+    elif residual is not None or (m and py == px):
+        # (without a residual the sum is x, unless that is written over)
         total = _like(shape, dev, stream)
         po, so = total.data_ptr(), k
     else:
@@ -306,9 +307,9 @@ def _like(shape, device, stream):
 def add_rms_norm(x, residual, weight, eps=1e-6, out=None, residual_out=None, stream=None):
     """r = x + residual (rounded to bfloat16) and its RMS norm, r * rsqrt(mean(r^2)
     + eps) * weight: x, residual bfloat16 [M, K] (rows may be strided, K a multiple
-    of 16), weight bfloat16 [K].  Without a residual (None) r is x.  Returns
-    (normed, r); either may be written over one of the inputs (``out``,
-    ``residual_out``)."""
+    of 16), weight bfloat16 [K].  Without a residual (None) r is x, or a copy of it
+    where the normed rows go over x.  Returns (normed, r); either may be written over
+    one of the inputs (``out``, ``residual_out``)."""
     given = _input(x)
     if out is None:
         out = _like(x.shape, given[0], stream)
