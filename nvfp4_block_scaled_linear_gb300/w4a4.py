@@ -113,8 +113,11 @@ class Fp4Rows:
     scales        uint8 [ceil(M/128), K/64, 512]: the e4m3 scales in the order
                   that the product reads (include/nvfp4_w4a4.h).
     global_scale  the values are codes times scales divided by it.
+
+    What rows are is fixed when they are made: another scale or other memory are
+    other Fp4Rows.  Copies (``copy.deepcopy``, ``torch.save``) have memory of their own.
     """
-    __slots__ = ("_codes", "_scales", "global_scale", "shape", "device", "_c")
+    __slots__ = ("_codes", "_scales", "_global_scale", "_shape", "_device", "_c")
 
     def __init__(self, codes, scales, global_scale=1.0):
         if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
@@ -129,26 +132,34 @@ class Fp4Rows:
                              % ((-(-m // 128), k // 64, 512), tuple(scales.shape)))
         if not (codes.is_contiguous() and scales.is_contiguous()):
             raise ValueError("codes and scales must be contiguous")
-        self._codes, self._scales = codes, scales
-        self.global_scale = _scale(global_scale, "global_scale")
-        self.shape, self.device = (m, k), codes.device
-        self._c = _pack_rows(codes.data_ptr(), scales.data_ptr(), self.global_scale)
+        # (tensors of its own: the memory whose addresses _c holds stays, whatever the caller's are set to)
+        self._codes, self._scales = codes.detach(), scales.detach()
+        self._global_scale = _scale(global_scale, "global_scale")
+        self._shape, self._device = (m, k), codes.device
+        self._c = _pack_rows(codes.data_ptr(), scales.data_ptr(), self._global_scale)
+
+    global_scale = property(lambda self: self._global_scale)
+    shape = property(lambda self: self._shape)
+    device = property(lambda self: self._device)
 
     # (rows that a call makes are one allocation, in _codes; the views of it cost
     # as much as a small kernel, and no call needs them)
     @property
     def codes(self):
         if self._scales is None:
-            m, k = self.shape
+            m, k = self._shape
             return self._codes[:m * (k // 2)].view(m, k // 2)
         return self._codes
 
     @property
     def scales(self):
         if self._scales is None:
-            m, k = self.shape
+            m, k = self._shape
             return self._codes[m * (k // 2):].view(-(-m // 128), k // 64, 512)
         return self._scales
+
+    def __reduce__(self):
+        return type(self), (self.codes, self.scales, self._global_scale)
 
 
 def new_fp4_rows(m, k, global_scale=1.0, device="cuda", stream=None):
@@ -169,7 +180,7 @@ def _new_rows(m, k, global_scale, device, stream):
     else:
         raw = _empty(size, torch.uint8, device, stream)
     rows = Fp4Rows.__new__(Fp4Rows)
-    rows._codes, rows._scales, rows.global_scale, rows.shape, rows.device = raw, None, global_scale, (m, k), device
+    rows._codes, rows._scales, rows._global_scale, rows._shape, rows._device = raw, None, global_scale, (m, k), device
     p = raw.data_ptr()
     rows._c = _pack_rows(p, p + split, global_scale)
     return rows
@@ -188,6 +199,10 @@ class Fp4Weight:
                   be negative or NaN.
     global_scale  the weight's, or a list of one for each of up to 8 stacked segments
                   of segment_rows rows (multiples of 16).
+
+    Its scales and segments are fixed when it is made; what is copied into ``codes`` later
+    is read by later calls.  Copies (``copy.deepcopy``, ``torch.save``) have memory of
+    their own.
     """
 
     def __init__(self, w_packed, w_scale, global_scale, segment_rows=None):
@@ -217,12 +232,38 @@ class Fp4Weight:
               refused.data_ptr())
         if int(refused):
             raise ValueError("w_scale holds a negative scale or a NaN")
-        self.codes, self.scales = w_packed, blocked
-        self.global_scales, self.segment_rows = scales, rows
-        self.shape, self.device = (n, k), dev
+        self._set(w_packed.detach(), blocked, scales, rows)
+
+    def _set(self, codes, blocked, scales, rows):
+        """Fill in from checked arguments, the scales in the product's order."""
+        # (tensors of its own: the memory whose addresses _c holds stays, whatever the caller's are set to)
+        n, k = codes.shape[0], codes.shape[1] * 2
+        self._codes, self._scales, self._global_scales, self._segment_rows = codes, blocked, scales, rows
+        self._shape, self._device = (n, k), codes.device
         pad = MAX_SEGMENTS - len(rows)
-        self._c = _pack_weight(w_packed.data_ptr(), blocked.data_ptr(), n, k, len(rows), *scales,
+        self._c = _pack_weight(codes.data_ptr(), blocked.data_ptr(), n, k, len(rows), *scales,
                                *[0.0] * pad, *rows, *[0] * pad)
+
+    codes = property(lambda self: self._codes)
+    scales = property(lambda self: self._scales)
+    global_scales = property(lambda self: list(self._global_scales))
+    segment_rows = property(lambda self: list(self._segment_rows))
+    shape = property(lambda self: self._shape)
+    device = property(lambda self: self._device)
+
+    def __reduce__(self):
+        own = {"_codes", "_scales", "_global_scales", "_segment_rows", "_shape", "_device", "_c"}
+        rest = {name: value for name, value in self.__dict__.items() if name not in own}
+        return _copied_weight, (type(self), self._codes, self._scales, self.global_scales, self.segment_rows), rest or None
+
+
+def _copied_weight(kind, codes, blocked, scales, rows):
+    """The Fp4Weight of a copy's tensors."""
+    if not (codes.is_cuda and codes.device == blocked.device and codes.is_contiguous() and blocked.is_contiguous()):
+        raise ValueError("an Fp4Weight's codes and scales must be contiguous CUDA tensors on one device")
+    w = kind.__new__(kind)
+    w._set(codes, blocked, scales, rows)
+    return w
 
 
 def _matrix(t, name, shape, device):
@@ -254,9 +295,9 @@ def _input(x):
 def _rows_out(out, m, k, global_scale, device, stream):
     if out is None:
         return _new_rows(m, k, _scale(global_scale, "global_scale"), device, stream)
-    if out.shape != (m, k) or out.device != device:
+    if out._shape != (m, k) or out._device != device:
         raise ValueError("out must hold rows %s on %s, got %s on %s" % ((m, k), device, out.shape, out.device))
-    if out.global_scale != global_scale:
+    if out._global_scale != global_scale:
         raise ValueError("out has the global scale %s, the call %s" % (out.global_scale, global_scale))
     return out
 
@@ -330,18 +371,18 @@ def add_rms_norm_quantize(x, residual, weight, eps=1e-6, global_scale=1.0, out=N
 def _check_product(a, w):
     if not (isinstance(a, Fp4Rows) and isinstance(w, Fp4Weight)):
         raise TypeError("a product is of Fp4Rows and an Fp4Weight, got %s and %s" % (type(a).__name__, type(w).__name__))
-    if a.shape[1] != w.shape[1] or a.device != w.device:
+    if a._shape[1] != w._shape[1] or a._device != w._device:
         raise ValueError("rows %s on %s do not fit a weight %s on %s" % (a.shape, a.device, w.shape, w.device))
 
 
 def _product(a, w, swiglu, out, stream):
     _check_product(a, w)
-    shape = (a.shape[0], w.shape[0] // 2 if swiglu else w.shape[0])
+    shape = (a._shape[0], w._shape[0] // 2 if swiglu else w._shape[0])
     if out is None:
-        out = _like(shape, a.device, stream)
-    elif out.dtype != torch.bfloat16 or out.shape != shape or not out.is_contiguous() or out.device != a.device:
-        raise ValueError("out must be a contiguous bfloat16 tensor of shape %s on %s" % (shape, a.device))
-    _call("nvfp4_linear_w4a4", a.device, stream, a._c, a.shape[0], w._c, swiglu, out.data_ptr(), None)
+        out = _like(shape, a._device, stream)
+    elif out.dtype != torch.bfloat16 or out.shape != shape or not out.is_contiguous() or out.device != a._device:
+        raise ValueError("out must be a contiguous bfloat16 tensor of shape %s on %s" % (shape, a._device))
+    _call("nvfp4_linear_w4a4", a._device, stream, a._c, a._shape[0], w._c, swiglu, out.data_ptr(), None)
     return out
 
 
@@ -361,9 +402,9 @@ def linear_w4a4_swiglu_quantize(a, w, global_scale=1.0, out=None, stream=None):
     """As ``linear_w4a4_swiglu``, its fp32 results rounded once, to NVFP4 with the
     given global scale (N a multiple of 512).  Returns Fp4Rows [M, N/2]."""
     _check_product(a, w)
-    n = w.shape[0]
+    n = w._shape[0]
     if n % 512:
         raise ValueError("N must be a multiple of 512, got %d" % n)
-    out = _rows_out(out, a.shape[0], n // 2, global_scale, a.device, stream)
-    _call("nvfp4_linear_w4a4", a.device, stream, a._c, a.shape[0], w._c, 1, None, out._c)
+    out = _rows_out(out, a._shape[0], n // 2, global_scale, a._device, stream)
+    _call("nvfp4_linear_w4a4", a._device, stream, a._c, a._shape[0], w._c, 1, None, out._c)
     return out
