@@ -72,12 +72,14 @@ int64_t nvfp4_w4a4_scale_bytes(int64_t rows, int64_t K);
  * order above (blocked, 16-byte aligned, nvfp4_w4a4_scale_bytes(N, K) bytes).
  * *refused (device) is set to 1 where a scale is below zero or NaN, which the
  * product has no meaning for (its scales are unsigned), and left alone
- * otherwise; -0 becomes 0.  N % 128 == 0, K % 256 == 0. */
+ * otherwise; -0 becomes 0.  blocked overlaps nothing.  N % 128 == 0, K % 256
+ * == 0. */
 int nvfp4_w4a4_scale_layout(const uint8_t* w_scale, int64_t N, int64_t K, uint8_t* blocked,
                             unsigned int* refused, void* stream);
 
 /* out = x (bf16 [M, K], row_stride elements from row to row, a multiple of 8;
- * 16-byte aligned) in NVFP4 with out->global_scale.  K % 256 == 0. */
+ * 16-byte aligned) in NVFP4 with out->global_scale, apart from x.  K % 256
+ * == 0. */
 int nvfp4_quantize_rows(const void* x, int64_t row_stride, int64_t M, int64_t K,
                         const nvfp4_rows* out, void* stream);
 
@@ -87,7 +89,8 @@ int nvfp4_quantize_rows(const void* x, int64_t row_stride, int64_t M, int64_t K,
  * into y (bf16) or, where `rows` is given, into NVFP4 rows; exactly one of the
  * two is.  x, residual, residual_out, y: bf16 [M, K], 16-byte aligned, strides
  * in elements, multiples of 8; weight: bf16 [K].  An output may be one of the
- * inputs (same pointer and stride); they must not overlap otherwise.
+ * inputs (same pointer and stride); otherwise outputs overlap neither inputs
+ * nor one another (NVFP4_ERR_INVALID).
  * K % 16 == 0 (into NVFP4 rows K % 256 == 0), K <= NVFP4_W4A4_MAX_NORM. */
 int nvfp4_add_rms_norm(const void* x, int64_t x_stride, const void* residual,
                        int64_t residual_stride, const void* weight, float eps, int64_t M,
@@ -112,9 +115,9 @@ typedef struct nvfp4_weight {
  * silu(g) * u, silu(g) = g / (1 + exp(-g)) in fp32, from the products
  * before any rounding; into y, or into NVFP4 rows `out` where that is given
  * (N % 512 == 0).  y: row-major, contiguous, 16-byte aligned.  Outputs must
- * not overlap inputs.  The products of the global scales must have reciprocals
- * in fp32's range.  Sums are fp32, in an order that depends on the sizes (M
- * rounded up to 8 among them) and nothing else. */
+ * not overlap inputs (NVFP4_ERR_INVALID).  The products of the global scales
+ * must have reciprocals in fp32's range.  Sums are fp32, in an order that
+ * depends on the sizes (M rounded up to 8 among them) and nothing else. */
 int nvfp4_linear_w4a4(const nvfp4_rows* a, int64_t M, const nvfp4_weight* w, int32_t swiglu,
                       void* y, const nvfp4_rows* out, void* stream);
 

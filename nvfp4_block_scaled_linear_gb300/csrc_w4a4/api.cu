@@ -53,6 +53,46 @@ int check_rows(const nvfp4_rows* r) {
   return NVFP4_OK;
 }
 
+// Memory that a call touches: `rows` pieces of `width` bytes, `stride` bytes apart.
+struct Memory {
+  uintptr_t p;
+  int64_t rows, width, stride;
+};
+Memory bytes_of(const void* p, int64_t bytes) { return {reinterpret_cast<uintptr_t>(p), 1, bytes, bytes}; }
+Memory matrix_of(const void* p, int64_t stride, int64_t M, int64_t K) {
+  if (M == 1 || stride == K) return bytes_of(p, M * K * 2);
+  return {reinterpret_cast<uintptr_t>(p), M, K * 2, stride * 2};
+}
+int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b < 0); }
+
+// Whether a byte is in both, exactly: views of one tensor may lie between one another.
+bool overlap(const Memory& a, const Memory& b) {
+  const int64_t d = static_cast<int64_t>(b.p - a.p);
+  if (d >= (a.rows - 1) * a.stride + a.width || -d >= (b.rows - 1) * b.stride + b.width) return false;
+  if (a.rows > b.rows) return overlap(b, a);
+  if (a.stride == b.stride) {
+    // row i of a meets row j of b where (i - j) strides lie in (d - a.width, d + b.width)
+    const int64_t first = floor_div(d - a.width, a.stride) + 1, n = first < 1 - b.rows ? 1 - b.rows : first;
+    return n < a.rows && n * a.stride < d + b.width;
+  }
+  for (int64_t i = 0; i < a.rows; ++i) {
+    // the first row of b that ends behind this row's begin
+    const int64_t at = i * a.stride - d, first = floor_div(at - b.width, b.stride) + 1, j = first < 0 ? 0 : first;
+    if (j < b.rows && j * b.stride < at + a.width) return true;
+  }
+  return false;
+}
+
+// Codes and scales of rows [M, K].
+struct RowsMemory {
+  Memory codes, scales;
+};
+RowsMemory memory_of(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t K) {
+  return {bytes_of(codes, M * (K / 2)), bytes_of(scales, nvfp4_w4a4_scale_bytes(M, K))};
+}
+bool overlap(const RowsMemory& r, const Memory& m) { return overlap(r.codes, m) || overlap(r.scales, m); }
+bool overlap(const RowsMemory& r, const RowsMemory& s) { return overlap(r, s.codes) || overlap(r, s.scales); }
+
 }  // namespace
 
 namespace nvfp4 {
@@ -110,6 +150,8 @@ int nvfp4_w4a4_scale_layout(const uint8_t* w_scale, int64_t N, int64_t K, uint8_
   if (!w_scale || !blocked || !refused) return NVFP4_ERR_INVALID;
   if (misaligned(w_scale) || misaligned(blocked) || (reinterpret_cast<uintptr_t>(refused) & 3u))
     return NVFP4_ERR_MISALIGNED;
+  const Memory laid = bytes_of(blocked, N * (K / 16)), flag = bytes_of(refused, 4);
+  if (overlap(laid, bytes_of(w_scale, N * (K / 16))) || overlap(laid, flag)) return NVFP4_ERR_INVALID;
   Device d;
   if (const int st = device(&d)) return st;
   return run_scale_layout(w_scale, N, K, blocked, refused, d, static_cast<cudaStream_t>(stream));
@@ -121,6 +163,8 @@ int nvfp4_quantize_rows(const void* x, int64_t row_stride, int64_t M, int64_t K,
   if (M == 0) return NVFP4_OK;
   if (const int st = check_matrix(x, row_stride, M, K)) return st;
   if (const int st = check_rows(out)) return st;
+  const RowsMemory o = memory_of(out->codes, out->scales, M, K);
+  if (overlap(o, matrix_of(x, row_stride, M, K)) || overlap(o.codes, o.scales)) return NVFP4_ERR_INVALID;
   Device d;
   if (const int st = device(&d)) return st;
   const Quantize p{static_cast<const __nv_bfloat16*>(x), row_stride, M, K, out->global_scale, out->codes,
@@ -144,6 +188,27 @@ int nvfp4_add_rms_norm(const void* x, int64_t x_stride, const void* residual,
   if (residual_out)
     if (const int st = check_matrix(residual_out, residual_out_stride, M, K)) return st;
   if (const int st = rows ? check_rows(rows) : check_matrix(y, y_stride, M, K)) return st;
+  // an output is one of the inputs, or apart from all of them; the outputs are apart
+  auto apart = [&](const void* out, int64_t stride) {
+    const Memory o = matrix_of(out, stride, M, K);
+    auto clear = [&](const void* in, int64_t in_stride) {
+      return !in || (in == out && (M == 1 || in_stride == stride)) || !overlap(o, matrix_of(in, in_stride, M, K));
+    };
+    return clear(x, x_stride) && clear(residual, residual_stride) && !overlap(o, bytes_of(weight, K * 2));
+  };
+  if (residual_out && !apart(residual_out, residual_out_stride)) return NVFP4_ERR_INVALID;
+  if (y) {
+    if (!apart(y, y_stride)) return NVFP4_ERR_INVALID;
+    if (residual_out && overlap(matrix_of(y, y_stride, M, K), matrix_of(residual_out, residual_out_stride, M, K)))
+      return NVFP4_ERR_INVALID;
+  } else {
+    const RowsMemory o = memory_of(rows->codes, rows->scales, M, K);
+    if (overlap(o, matrix_of(x, x_stride, M, K)) || overlap(o, bytes_of(weight, K * 2)) ||
+        (residual && overlap(o, matrix_of(residual, residual_stride, M, K))) ||
+        (residual_out && overlap(o, matrix_of(residual_out, residual_out_stride, M, K))) ||
+        overlap(o.codes, o.scales))
+      return NVFP4_ERR_INVALID;
+  }
   Device d;
   if (const int st = device(&d)) return st;
   Norm p{};
@@ -204,6 +269,15 @@ int nvfp4_linear_w4a4(const nvfp4_rows* a, int64_t M, const nvfp4_weight* w, int
     p.seg.end[i] = static_cast<int>(rows);
     p.seg.scale[i] = static_cast<float>(1.0 / (double(a->global_scale) * double(w->global_scale[i])));
     if (bad_scale(p.seg.scale[i])) return NVFP4_ERR_INVALID;
+  }
+  const RowsMemory in[2] = {memory_of(a->codes, a->scales, M, w->K), memory_of(w->codes, w->scales, w->N, w->K)};
+  const int64_t n_out = swiglu ? w->N / 2 : w->N;
+  if (out) {
+    const RowsMemory o = memory_of(out->codes, out->scales, M, n_out);
+    if (overlap(o, in[0]) || overlap(o, in[1]) || overlap(o.codes, o.scales)) return NVFP4_ERR_INVALID;
+  } else {
+    const Memory o = bytes_of(y, M * n_out * 2);
+    if (overlap(in[0], o) || overlap(in[1], o)) return NVFP4_ERR_INVALID;
   }
   Device d;
   if (const int st = device(&d)) return st;
