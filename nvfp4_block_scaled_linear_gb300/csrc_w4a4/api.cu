@@ -224,7 +224,7 @@ int nvfp4_add_rms_norm(const void* x, int64_t x_stride, const void* residual,
   p.M = M;
   p.K = K;
   p.eps = eps;
-  p.per_k = 1.0f / static_cast<float>(K);
+  p.width = static_cast<float>(K);
   if (rows) {
     p.gs = rows->global_scale;
     p.codes = rows->codes;

@@ -182,7 +182,7 @@ struct Norm {
   __nv_bfloat16* y;                  // or null: codes and scales
   int64_t xs, rs, ros, ys;
   int64_t M, K;
-  float eps, gs, per_k;              // per_k: 1 / K
+  float eps, gs, width;              // width: K
   uint8_t* codes;
   uint8_t* scales;
 };

@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kMaxNormThreads) norm_kernel(const Norm p) {
   __syncthreads();
   sum = 0.f;
   for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) sum += part[i];
-  const float scale = rsqrtf(sum * p.per_k + p.eps);
+  const float scale = rsqrtf(__fdiv_rn(sum, p.width) + p.eps);
 #pragma unroll
   for (int v = 0; v < kV; ++v) {
     const int b = threadIdx.x + v * blockDim.x;
