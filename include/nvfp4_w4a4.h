@@ -116,8 +116,9 @@ typedef struct nvfp4_weight {
  * before any rounding; into y, or into NVFP4 rows `out` where that is given
  * (N % 512 == 0).  y: row-major, contiguous, 16-byte aligned.  Outputs must
  * not overlap inputs (NVFP4_ERR_INVALID).  The products of the global scales
- * must have reciprocals in fp32's range.  Sums are fp32, in an order that
- * depends on the sizes (M rounded up to 8 among them) and nothing else. */
+ * must have reciprocals in fp32's normal range (NVFP4_ERR_INVALID).  Sums are
+ * fp32, in an order that depends on the sizes (M rounded up to 8 among them)
+ * and nothing else. */
 int nvfp4_linear_w4a4(const nvfp4_rows* a, int64_t M, const nvfp4_weight* w, int32_t swiglu,
                       void* y, const nvfp4_rows* out, void* stream);
 

@@ -1,5 +1,6 @@
 // api.cu -- the C ABI of include/nvfp4_w4a4.h: validation on the host, the
 // per-device set-up and the error word.
+#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <mutex>
@@ -268,7 +269,8 @@ int nvfp4_linear_w4a4(const nvfp4_rows* a, int64_t M, const nvfp4_weight* w, int
     rows += w->segment_rows[i];
     p.seg.end[i] = static_cast<int>(rows);
     p.seg.scale[i] = static_cast<float>(1.0 / (double(a->global_scale) * double(w->global_scale[i])));
-    if (bad_scale(p.seg.scale[i])) return NVFP4_ERR_INVALID;
+    // (below fp32's normal range it would be left with fewer bits than a result)
+    if (bad_scale(p.seg.scale[i]) || p.seg.scale[i] < FLT_MIN) return NVFP4_ERR_INVALID;
   }
   const RowsMemory in[2] = {memory_of(a->codes, a->scales, M, w->K), memory_of(w->codes, w->scales, w->N, w->K)};
   const int64_t n_out = swiglu ? w->N / 2 : w->N;

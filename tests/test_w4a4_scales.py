@@ -1,0 +1,23 @@
+"""Global scales at the ends of fp32, on the host (made-up addresses: what is let through ends at the missing device)."""
+import ctypes
+
+import pytest
+import torch
+
+from test_w4a4_abi import INVALID, lib, rows, weight  # noqa: F401
+
+DEVICE = -5
+X, R, W, O, Y = (0x10000000 * i for i in range(1, 6))
+
+
+def product(lib, gs_a, gs_w):
+    w = weight(W, O, 512, 512, gs_w, [512 // len(gs_w)] * len(gs_w))
+    return lib.nvfp4_linear_w4a4(rows(X, R, gs_a), 4, ctypes.byref(w), 0, Y, None, None)
+
+
+def test_reciprocals_below_the_normal_range(lib):
+    for a, w in ((2.0 ** 64, 2.0 ** 63), (3e20, 3e20), (2.0 ** 100, 2.0 ** 48), (3e38, 1.0)):
+        assert product(lib, a, [w]) == INVALID and product(lib, a, [1e-3, w]) == INVALID
+    if not torch.cuda.is_available():
+        for a, w in ((2.0 ** 63, 2.0 ** 63), (1.0, 8e37), (2.0 ** -64, 2.0 ** -63), (1e-20, 3e-19)):
+            assert product(lib, a, [w]) == DEVICE, (a, w)
