@@ -20,7 +20,6 @@ or a raw handle).  What a call makes itself belongs to the stream that it runs o
 as under ``torch.cuda.stream(stream)``.
 """
 import ctypes
-import math
 import os
 import re
 import struct
@@ -101,8 +100,9 @@ def _call(name, device, stream, *args):
 
 def _scale(value, name):
     value = float(value)
-    if not 0.0 < value < math.inf:
-        raise ValueError("%s must be positive and finite, got %s" % (name, value))
+    # (what fp32 rounds neither to zero nor to infinity)
+    if not 2.0 ** -150 < value < 2.0 ** 128 - 2.0 ** 103:
+        raise ValueError("%s must be positive and finite in fp32, got %s" % (name, value))
     return value
 
 
