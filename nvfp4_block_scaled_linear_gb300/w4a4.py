@@ -167,6 +167,8 @@ def new_fp4_rows(m, k, global_scale=1.0, device="cuda", stream=None):
     if m < 0 or k <= 0 or k % 256:
         raise ValueError("rows must be [M, K], K a positive multiple of 256, got [%d, %d]" % (m, k))
     device = torch.device(device)
+    if device.type != "cuda":
+        raise ValueError("rows are of a CUDA device, got %s" % device)
     if device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
     return _new_rows(m, k, _scale(global_scale, "global_scale"), device, stream)

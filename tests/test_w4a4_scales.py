@@ -38,3 +38,9 @@ def test_the_binding_takes_what_fp32_holds(value):
     assert w4a4._scale(value, "global_scale") == value
     gs = struct.unpack("f", w4a4._pack_rows(X, R, value)[16:20])[0]
     assert 0.0 < gs < float("inf")
+
+
+@pytest.mark.parametrize("device", ["cpu", "meta"])
+def test_rows_are_of_a_cuda_device(device):
+    with pytest.raises(ValueError):
+        w4a4.new_fp4_rows(4, 256, device=device)
