@@ -297,6 +297,8 @@ def _input(x):
 def _rows_out(out, m, k, global_scale, device, stream):
     if out is None:
         return _new_rows(m, k, _scale(global_scale, "global_scale"), device, stream)
+    if not isinstance(out, Fp4Rows):
+        raise TypeError("out must be Fp4Rows, got %s" % type(out).__name__)
     if out._shape != (m, k) or out._device != device:
         raise ValueError("out must hold rows %s on %s, got %s on %s" % ((m, k), device, out.shape, out.device))
     if out._global_scale != global_scale:

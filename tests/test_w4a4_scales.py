@@ -44,3 +44,9 @@ def test_the_binding_takes_what_fp32_holds(value):
 def test_rows_are_of_a_cuda_device(device):
     with pytest.raises(ValueError):
         w4a4.new_fp4_rows(4, 256, device=device)
+
+
+def test_out_is_rows():
+    for out in (torch.empty((4, 256)), (1, 2), "rows"):
+        with pytest.raises(TypeError):
+            w4a4._rows_out(out, 4, 256, 1.0, torch.device("cuda:0"), None)
