@@ -39,6 +39,8 @@
  *   zeros where the scale rounds to 0 (a zero's sign is not kept);
  *   where max|v| * global_scale is not finite the scale is NaN and the codes
  *   are zeros: every product of that row is NaN.
+ * Scales are never negative; rows from elsewhere must not hold negative ones
+ * either (the product takes scales as unsigned).
  */
 #ifndef NVFP4_W4A4_H
 #define NVFP4_W4A4_H
@@ -86,6 +88,8 @@ int nvfp4_quantize_rows(const void* x, int64_t row_stride, int64_t M, int64_t K,
 /* r = x + residual (rounded to bf16; x itself where residual is NULL), into
  * residual_out (may be NULL), and
  *   y = r * rsqrt(mean(r^2) + eps) * weight      (fp32, rounded once)
+ * (the mean: the fp32 sum over K, rounded once; a finite row whose squares pass
+ * fp32's range, magnitudes from 1.8e19 / sqrt(K) on, gives zeros)
  * into y (bf16) or, where `rows` is given, into NVFP4 rows; exactly one of the
  * two is.  x, residual, residual_out, y: bf16 [M, K], 16-byte aligned, strides
  * in elements, multiples of 8; weight: bf16 [K].  An output may be one of the

@@ -47,14 +47,18 @@ bool scales_map(CUtensorMap* map, const uint8_t* scales, int64_t rows, int64_t K
 
 int run_product(const Product& p, const Device& d, cudaStream_t stream) {
   // Up to 32 tokens: the weights as the MMA's rows.  One token by 5120 rows and 6144 k
-  // 6.2 us against 6.9 with the tokens there, gated by 12288 and 2048 k 6.0 against 7.2;
-  // 24 tokens 6.9 against 7.2, 6.5 against 7.2; 32 7.5 against 7.5, 6.7 against 7.2.
+  // 6.5 us against 7.2 with the tokens there, by 2048 rows 4.0 against 5.2, gated by 12288
+  // and 2048 k 5.9 against 6.5; 24 tokens 6.9 against 7.4, 4.7 against 5.5, 6.4 against 6.5;
+  // 32 7.5 against 7.2, 4.9 against 5.5, 6.7 against 6.6, gated by 40960 and 5120 k 26.6
+  // against 30.0.
   if (p.M <= 32) return run_product_narrow(p, d, stream);
   // The kernel for few tokens takes up to 128 by 128 weight rows (of a pair 256) a CTA
   // and is the faster one as long as every CTA has an SM; beyond that the pairs' 256 by
-  // 256 tiles read half as much.  128 tokens by 5120 rows and 17408 k 14.1 us against
-  // 26.6, 384 24.3 against 27.1; 515 33.5 against 27.8; gated 130 by 12288 and 2048 k
-  // 8.1 against 8.9, by 34816 and 5120 k 34.0 against 22.1.
+  // 256 tiles read half as much.  128 tokens by 5120 rows and 17408 k 14.2 us against
+  // 22.7, 384 24.3 against 23.5; 515 33.5 against 27.4; gated 130 by 12288 and 2048 k
+  // 7.9 against 8.8, by 34816 and 5120 k 34.0 against 22.0.  Up to 128 tokens always:
+  // gated by 34816 and 5120 k 128 20.5 against 22.1, 64 19.8 against 21.7, but by 40960,
+  // where its CTAs take two rounds, 32.4 against 29.6 and 31.4 against 29.0.
   const int64_t few = (p.M + 127) / 128 * (p.N / (p.swiglu ? 256 : 128));
   return p.M <= 128 || few <= d.num_sms ? run_product_few(p, d, stream) : run_product_many(p, d, stream);
 }

@@ -16,8 +16,8 @@
 // Bound by an SM's port to L2 (64 bytes a clock): 128 tokens need 0.28 us a stage of 256
 // k, 18 KB of tokens beside 18 KB of weights; and beyond the stages by the tokens' copy after the kernel ahead has ended, the
 // exchange (1.3 us and more with more rows) and the outputs.  Measured back to back,
-// weights from memory, 128 tokens: 34816 x 5120 gated 20.3 us, 5.0 TB/s; 5120 x 17408
-// 14.1 us; 8192 x 5120 9.4 us; 5120 x 6144 9.0 us.
+// weights from memory, 128 tokens: 34816 x 5120 gated 20.5 us, 4.9 TB/s (40960 x 5120,
+// 160 tiles on 152 SMs, 32.4); 5120 x 17408 14.2 us; 8192 x 5120 9.4 us; 5120 x 6144 9.0 us.
 //
 // Warps: 0 copies, 1 MMA, 2 TMEM allocation; all eight the outputs.
 #include <algorithm>
@@ -344,17 +344,17 @@ int run_product_few(const Product& p, const Device& d, cudaStream_t stream) {
   f.a_rows = p.M >= 128 ? 128 : static_cast<int>((p.M + 7) / 8 * 8);
   const int64_t steps = p.K / kStageK, token_tiles = (p.M + 127) / 128;
   // Gated tiles of 64 outputs leave room in TMEM and shared memory for a second CTA, of
-  // this kernel or the next: 128 tokens through 12288 x 2048 7.1 us against 17.7 with
+  // this kernel or the next: 128 tokens through 12288 x 2048 7.2 us against 7.7 with
   // tiles of 128.  With many tokens and more of them than SMs it is the MMAs' operand
-  // reads that count: 128 tokens through 34816 x 5120 21.9 us against 20.3.
+  // reads that count: 128 tokens through 34816 x 5120 21.7 us against 20.5.
   const int n = p.swiglu && f.a_rows > 64 && p.N / 128 * token_tiles > d.num_sms ? 256 : 128;
   f.stage_bytes = f.a_rows * 128 + n * 128 + 4 * kScaleBlock * (p.swiglu ? 3 : 2);
   const int64_t tiles = p.N / n * token_tiles;
   // Of the splits that the device holds at one time the one with the least time, in ns
   // as measured: 280 a step (gated, with twice the MMAs and more scales, 400), and
   // where sums are exchanged 1300, 30 a CTA of the cluster and 3 more for each row.
-  // 128 tokens by 2048 rows, 24 steps: one CTA 9.8 us, 3 7.6, 8 9.8; 64 tokens 9.2, 6.3,
-  // 6.9; 1024 rows and 4 steps: one 3.4, 4 4.4.
+  // 128 tokens by 2048 rows, 24 steps: one CTA 9.7 us, 3 7.4, 4 7.1, 8 9.6; 64 tokens 9.2,
+  // 6.3, 5.8, 6.5; 128 by 1024 rows, 4 steps: one 4.4, 4 5.6.
   f.split = 1;
   int64_t least = INT64_MAX;
   for (int split = 1; split <= kMaxSplit && split <= steps && split * tiles <= std::max<int64_t>(d.num_sms, tiles);
@@ -366,8 +366,9 @@ int run_product_few(const Product& p, const Device& d, cudaStream_t stream) {
   }
   // With half of an SM's shared memory the next kernel's CTAs are resident, with their
   // first stages on the way, before this one's end; with all of it the ring is twice as
-  // deep.  128 tokens: 3 steps 10.4 us against 13.5, 8 steps 11.5 against 9.1.  A gated
-  // tile of 128 outputs takes all of TMEM and is alone in any case.
+  // deep.  64 tokens: 2048 x 6144, 6 steps, 5.9 us against 6.2, 34816 x 5120 gated 19.8
+  // against 25.7; 128 tokens by 5120 rows: 8 steps 9.8 against 9.1, 23 16.2 against 14.2.  A
+  // gated tile of 128 outputs takes all of TMEM and is alone in any case.
   const int half = (kHalfSmem - 1024) / f.stage_bytes;
   f.smem = n == 256 || (steps / f.split > 2 * half && tiles <= d.num_sms) ? kAllSmem : kHalfSmem;
   // the sums lie where the stages were (an odd split leaves its owners unequal pieces,

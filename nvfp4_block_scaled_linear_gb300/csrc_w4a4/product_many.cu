@@ -20,8 +20,9 @@
 // Both CTAs' copies count on the first one's barriers, whose thread issues the
 // MMAs; what it has read is free for both by one commit.
 //
-// Measured: 8192 x 34816 x 5120 gated into NVFP4 424 us, 6.9 PFLOP/s; 8192 x 5120 x
-// 17408 205 us, 7.1 PFLOP/s, 0.94 of four times the measured bf16 rate.  A stage's
+// Measured: 8192 x 34816 x 5120 gated into NVFP4 414 us, 7.1 PFLOP/s, into bf16 413; 8192 x
+// 5120 x 17408 203 us, 7.2 PFLOP/s, 0.95 of four times the measured bf16 rate (the rate of
+// this MMA, of 64 k; sm_103a has one of 96 k as well, which is not used here).  A stage's
 // products take 512 clocks; its 38 KB take 600 through an SM's port to L2 (64 bytes a
 // clock, which no kernel here got more out of): that is what a pair's tile is bound by,
 // and its copies of scales cost nothing.  A tile of 20 stages takes some 1.2 times that

@@ -18,9 +18,9 @@
 // Bound by the weights' bytes where there are many, by latency where there are few:
 // beyond its bytes a call needs the tokens' copy after the kernel ahead has ended (some
 // 1.5 us to the first product), the exchange (1 us) and the outputs (0.7 us).  Measured
-// back to back, weights from memory, one token: 34816 x 5120 gated 18.3 us, 5.5 TB/s;
-// 5120 x 17408 11.7 us, 4.3 TB/s; 8192 x 5120 7.0 us; 5120 x 6144 6.2 us; 32 tokens 19.6,
-// 12.1, 8.0, 7.5.
+// back to back, weights from memory, one token: 34816 x 5120 gated 18.2 us, 5.5 TB/s;
+// 5120 x 17408 11.5 us, 4.4 TB/s; 8192 x 5120 7.0 us; 5120 x 6144 6.5 us; 32 tokens 19.5,
+// 12.0, 8.0, 7.5.
 //
 // Warps: 0 copies, 1 MMA, 2 TMEM allocation; all eight the outputs.
 #include <algorithm>
@@ -281,8 +281,8 @@ int run_product_narrow(const Product& p, const Device& d, cudaStream_t stream) {
   const int64_t steps = p.K / kStageK, tiles = p.N / (kTile * parts);
   // A stage for each of gate and up where there are more tiles than SMs: half of an SM's
   // shared memory then holds four, and two CTAs an SM are one round.  One token through
-  // 40960 x 5120 22.0 us against 28.6 (two rounds of CTAs with both in a stage); where a
-  // tile has an SM for itself 34816 x 5120 18.9 against 18.3.
+  // 40960 x 5120 22.7 us against 28.9 (two rounds of CTAs with both in a stage); where a
+  // tile has an SM for itself 34816 x 5120 19.0 against 18.2.
   const int per = tiles > d.num_sms ? 1 : parts;
   f.stage_bytes = per * kWeights + f.cols * 128 + 4 * kScaleBlock * (per + 1);
   // Of the splits that the device holds at one time the one with the least time, in ns
@@ -298,9 +298,9 @@ int run_product_narrow(const Product& p, const Device& d, cudaStream_t stream) {
   const int sums = sums_bytes(parts, f.split, f.cols);
   // With half of an SM's shared memory the next kernel's CTAs are resident, with their
   // first stages on the way, before this one's end; with all of it the ring is twice as
-  // deep.  8192 x 5120, 10 steps: 7.0 us against 7.9; 5120 x 17408, 23 steps, 32 tokens:
-  // 13.7 against 12.1.  Half holds two stages of both gate and up, too few: 34816 x 5120 22.1 us
-  // against 18.3, 12288 x 2048 6.6 against 6.0.
+  // deep.  8192 x 5120, 10 steps: 7.0 us against 7.6; 5120 x 17408, 23 steps, 32 tokens:
+  // 13.7 against 12.0.  Half holds two stages of both gate and up, too few: 34816 x 5120 22.5 us
+  // against 18.2, 12288 x 2048 6.7 against 5.9.
   const int half = (kHalfSmem - 1024 - sums) / f.stage_bytes;
   f.smem = per == 2 || (steps / f.split > 2 * half && tiles <= d.num_sms) ? kAllSmem : kHalfSmem;
   f.stages = std::min((f.smem - 1024 - sums) / f.stage_bytes, kMaxStages);

@@ -8,8 +8,8 @@
 // block of 16 (and so its scale) in one thread.
 //
 // Measured, 8192 x 5120: addition and norm into bf16 49.7 us, 6.8 TB/s, into NVFP4
-// 43.8 us, 6.3 TB/s; quantisation 17.6 us, 6.1 TB/s (8192 x 17408 56.5 us, 6.5 TB/s);
-// one row 2.3, 2.5 and 1.7 us, one trip to memory and the launch.
+// 43.7 us, 6.3 TB/s; quantisation 17.4 us, 6.2 TB/s (8192 x 17408 56.5 us, 6.5 TB/s);
+// one row 2.4, 2.6 and 1.7 us, one trip to memory and the launch.
 #include "common.cuh"
 
 namespace nvfp4 {
