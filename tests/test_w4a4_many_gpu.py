@@ -21,7 +21,7 @@ def rows_for_pairs(outputs, extra):
 
 # outputs, k and rows into the last 128: single rows behind a tile, halves of a pair's tile without a row, one
 # stage and more than the ring has, several tiles for a pair
-SHAPES = [(1024, 512, 1), (2048, 256, 127), (4096, 512, 128), (1536, 1280, 70), (768, 1536, 5), (256, 768, 33)]
+SHAPES = [(1024, 512, 1), (2048, 256, 127), (4096, 512, 128), (1792, 1280, 70), (768, 1536, 5), (256, 768, 33)]
 
 
 @pytest.mark.parametrize("outputs, k, extra", SHAPES, ids=str)

@@ -23,5 +23,5 @@ def test_the_mean_is_exact_where_it_can_be(gs):
         assert bool((s == s[:, :1]).all())
         return s[:, 0]
     want = scales(256)
-    for j in range(3, 129):
+    for j in range(3, 129, 2):
         assert torch.equal(scales(256 * j), want), j
